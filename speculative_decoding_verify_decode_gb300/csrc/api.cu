@@ -12,12 +12,7 @@
 
 using namespace sdv;
 
-namespace {
-
-constexpr size_t kAlign = 256;
-size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
-
-sd_status fill_batch(int batch, const int* indptr, BatchDesc* bd) {
+sd_status sdv::fill_batch(int batch, const int* indptr, BatchDesc* bd) {
   if (batch < 1 || batch > kMaxBatch || indptr == nullptr) return SD_ERR_INVALID_ARG;
   if (indptr[0] != 0) return SD_ERR_INVALID_ARG;
   bd->batch = batch;
@@ -32,6 +27,11 @@ sd_status fill_batch(int batch, const int* indptr, BatchDesc* bd) {
   bd->total_nodes = indptr[batch];
   return SD_OK;
 }
+
+namespace {
+
+constexpr size_t kAlign = 256;
+size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 
 sd_status check_shape(const sd_shape* s, BatchDesc* bd) {
   if (s == nullptr) return SD_ERR_INVALID_ARG;

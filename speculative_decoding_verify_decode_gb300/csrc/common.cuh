@@ -2,6 +2,7 @@
 // kernels.  Internal to the library (the public interface is sd_verify.h).
 #pragma once
 
+#include <climits>
 #include <utility>
 
 #include <cstdint>
@@ -9,6 +10,7 @@
 #include <cuda_bf16.h>
 
 #include "../../include/sd_verify.h"
+#include "../../include/sd_kv8.h"
 
 namespace sdv {
 
@@ -21,6 +23,7 @@ constexpr int kTileTokens = 128; // context tokens per attention tile (the MMA's
 constexpr int kMaxNodes = SD_MAX_NODES;
 constexpr int kMaxBatch = SD_MAX_BATCH;
 constexpr int kMaxLayers = SD_MAX_LAYERS;
+constexpr int kSMs = 152;        // SMs of a GB300
 
 // log2(e) / sqrt(256): scores are kept in base 2 so exp becomes ex2.
 constexpr float kScaleLog2 = 1.4426950408889634f / 16.0f;

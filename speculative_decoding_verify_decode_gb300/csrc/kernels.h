@@ -31,6 +31,9 @@ size_t tc_smem_bytes(int nq);
 cudaError_t launch_attn_tc8(const AttnParams& p, const BatchDesc& bd, cudaStream_t st);
 cudaError_t launch_attn_tc16(const AttnParams& p, const BatchDesc& bd, cudaStream_t st);
 
+// The batch description of a host q_indptr (SD_OK, or the status of what is wrong with it).
+sd_status fill_batch(int batch, const int* indptr, BatchDesc* bd);
+
 // Host-side validation of a verify-attention shape (the status sd_verify_attn returns for it).
 sd_status verify_shape_status(const sd_shape* s);
 
@@ -160,5 +163,69 @@ size_t gdn_smem_bytes(int max_nodes);
 cudaError_t launch_gdn_tree(const GdnParams& p, const BatchDesc& bd, cudaStream_t st);
 cudaError_t launch_gdn_commit(const GdnCommitParams& p, const BatchDesc& bd, cudaStream_t st);
 cudaError_t launch_conv_tree(const ConvTreeParams& p, const BatchDesc& bd, cudaStream_t st);
+
+// Page tables and slot maps from request lengths; pages back on the free list.
+struct PagesParams {
+  const int* ctx_lens;       // [B]; pages_release: the tokens to keep
+  const int* add_lens;       // [B]
+  const int* path;           // [B][max_path], nullable
+  int* page_table;           // [B][max_pages]
+  const int* held;           // [B]
+  int* new_held;
+  const int* free_list;      // [num_pool_pages]
+  int* free_list_out;        // pages_release: the same list, written behind the first *free_count entries
+  const int* free_count;
+  int* new_free_count;
+  int* slots;                // [max_rows]
+  int* rows;                 // [max_rows], nullable
+  int* row_indptr;           // [B + 1], nullable
+  int* new_ctx_lens;         // [B], nullable
+  int* dev_status;           // nullable
+  int batch, max_pages, num_pool_pages, max_path, max_rows;
+  int vec;                   // slots and rows start on 16 bytes
+};
+cudaError_t launch_pages_extend(const PagesParams& p, const BatchDesc& bd, cudaStream_t st);
+cudaError_t launch_pages_release(const PagesParams& p, cudaStream_t st);
+
+// Quantising append into the block-scaled cache.
+struct Kv8AppendParams {
+  uint8_t* k_cache[kMaxLayers];
+  uint8_t* v_cache[kMaxLayers];
+  float* k_scale[kMaxLayers];
+  float* v_scale[kMaxLayers];
+  const __nv_bfloat16* k_new[kMaxLayers];
+  const __nv_bfloat16* v_new[kMaxLayers];
+  const int* slots;
+  const int* rows;           // nullable
+  int* dev_status;           // nullable
+  long long new_stride;      // elements between source rows
+  int num_layers, heads, dim, num_pool_pages, num_src_rows, max_rows;
+};
+cudaError_t launch_kv8_append(const Kv8AppendParams& p, cudaStream_t st);
+
+// Verify attention over the block-scaled cache (one layer).
+struct Kv8AttnParams {
+  const __nv_bfloat16* q;
+  const uint8_t* k_cache;
+  const uint8_t* v_cache;
+  const float* k_scales;     // [num_pool_pages][hkv]
+  const float* v_scales;
+  const __nv_bfloat16* k_new;
+  const __nv_bfloat16* v_new;
+  const int* page_table;
+  const int* ctx_lens;
+  const int* parents;
+  const float* slopes;       // [hq], nullable
+  __nv_bfloat16* out;
+  float* lse;                // nullable
+  int* dev_status;           // nullable
+  long long q_stride, k_stride, v_stride;   // elements between rows
+  float scale, softcap;      // softcap 0: none
+  int hq, hkv, dim, max_pages, num_pool_pages, window;
+  void* workspace;
+};
+constexpr int kMaxKvHeads = 64, kMaxGroup = 16;   // of the block-scaled cache's calls
+size_t kv8_attn_workspace(int hq, int hkv, int dim, const BatchDesc& bd);
+cudaError_t launch_kv8_attn(const Kv8AttnParams& p, const BatchDesc& bd, cudaStream_t st);
 
 }  // namespace sdv

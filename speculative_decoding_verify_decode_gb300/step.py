@@ -4,7 +4,8 @@ The three C-ABI calls run in order on one CUDA stream with no host
 synchronisation between them, so a step can also be captured into a CUDA
 graph (``VerifyStep.capture``).  This module owns the output buffers and the
 workspaces; the inputs (queries, draft K/V, caches, logits, tree, page
-table) belong to the caller.
+table) belong to the caller.  ``Kv8Cache`` and ``Kv8Step`` are the same over
+the 8-bit block-scaled cache, with its pages allocated on the GPU.
 """
 from __future__ import annotations
 
@@ -107,6 +108,94 @@ class VerifyStep:
                 self.run(*args, stream=s, **kwargs)
         torch.cuda.current_stream(self.device).wait_stream(s)
         return g
+
+
+class Kv8Cache:
+    """A pool of 8-bit block-scaled K/V pages for every layer, its page tables, and the free list, all on the GPU.
+
+    ``extend`` takes pages for joining tokens and appends their K/V, ``release`` gives pages back; both only
+    launch kernels, so a step that contains them can be captured into a CUDA graph and replayed.
+    """
+
+    def __init__(self, batch: int, max_pages_per_seq: int, num_pool_pages: int, num_layers: int,
+                 num_kv_heads: int = 4, head_dim: int = 256, device="cuda"):
+        dev = self.device = torch.device(device)
+        self.num_pool_pages = int(num_pool_pages)
+        codes = (num_layers, num_pool_pages, num_kv_heads, 16, head_dim)
+        self.k, self.v = (torch.zeros(codes, dtype=torch.uint8, device=dev) for _ in "kv")
+        self.k_scales, self.v_scales = (torch.ones(codes[:3], dtype=torch.float32, device=dev) for _ in "kv")
+        ints = lambda *s: torch.zeros(s, dtype=torch.int32, device=dev)
+        self.page_table = torch.full((batch, max_pages_per_seq), -1, dtype=torch.int32, device=dev)
+        self.ctx_lens, self.held, self.free_count = ints(batch), ints(batch), ints(1)
+        self.free_list = torch.arange(num_pool_pages - 1, -1, -1, dtype=torch.int32, device=dev)
+        self.free_count.fill_(num_pool_pages)
+        self._new = ints(batch), ints(batch), ints(1)
+        self.dev_status = ints(1)
+
+    def _settle(self, ctx: bool):
+        new_ctx, new_held, new_count = self._new
+        if ctx:
+            self.ctx_lens.copy_(new_ctx)
+        self.held.copy_(new_held)
+        self.free_count.copy_(new_count)
+
+    def extend(self, add_lens, k_new, v_new, slots, rows=None, q_indptr=None, path=None, stream=None):
+        """``add_lens`` tokens join every sequence: their pages, then their rows of every layer's ``k_new`` and
+        ``v_new`` into the cache.  ``slots`` (and ``rows`` with a path) are int32 scratch with room for all rows."""
+        with torch.cuda.stream(stream):
+            new_ctx, new_held, new_count = self._new
+            native.sd_pages_extend(self.ctx_lens, add_lens, self.page_table, self.held, new_held, self.free_list,
+                                   self.free_count, new_count, slots, rows=rows, new_ctx_lens=new_ctx,
+                                   q_indptr=q_indptr, path=path, dev_status=self.dev_status)
+            native.sd_kv8_append(self.k, self.v, self.k_scales, self.v_scales, k_new, v_new, slots, rows,
+                                 self.dev_status)
+            self._settle(ctx=True)
+
+    def release(self, keep_lens, stream=None):
+        """Every sequence keeps its first ``keep_lens`` tokens at most; the pages behind them become free."""
+        with torch.cuda.stream(stream):
+            _, new_held, new_count = self._new
+            native.sd_pages_release(keep_lens, self.page_table, self.held, new_held, self.free_list, self.free_count,
+                                    new_count, self.dev_status)
+            self._settle(ctx=False)
+            torch.minimum(self.ctx_lens, keep_lens, out=self.ctx_lens)
+
+
+class Kv8Step:
+    """One verify step over a Kv8Cache: every layer's attention, accept, the accepted path's pages and append."""
+
+    def __init__(self, cache: Kv8Cache, q_indptr, vocab: int, num_q_heads: int = 24, window: int = 0,
+                 softcap: float = 0.0, slopes=None, max_path: int | None = None):
+        self.cache, self.vocab, self.softcap, self.slopes = cache, int(vocab), softcap, slopes
+        self.q_indptr = np.asarray(q_indptr, dtype=np.int32)
+        layers, pool, heads, _, dim = cache.k.shape
+        batch, total, dev = len(self.q_indptr) - 1, int(self.q_indptr[-1]), cache.device
+        self.shape = native.Shape(self.q_indptr, cache.page_table.shape[1], pool, window=window,
+                                  num_q_heads=num_q_heads, num_kv_heads=heads, head_dim=dim)
+        self.max_path = int(max_path or int(np.diff(self.q_indptr).max()))
+        byte = lambda n: torch.empty(max(n, 16), dtype=torch.uint8, device=dev)
+        self.attn_ws = byte(native.sd_kv8_attn_workspace_size(self.shape))
+        self.acc_ws = byte(native.sd_accept_workspace_size(self.q_indptr, self.vocab))
+        ints = lambda *s: torch.empty(s, dtype=torch.int32, device=dev)
+        self.out = torch.empty((layers, total, num_q_heads, dim), dtype=torch.bfloat16, device=dev)
+        self.accept_len, self.target_tokens = ints(batch), ints(total)
+        self.path, self.out_tokens = ints(batch, self.max_path), ints(batch, self.max_path)
+        self.slots, self.rows = ints(total), ints(total)
+
+    def attention(self, layer, q, k_new, v_new, parents, stream=None):
+        c = self.cache
+        native.sd_kv8_attn(self.shape, q, c.k[layer], c.v[layer], c.k_scales[layer], c.v_scales[layer], k_new, v_new,
+                           c.page_table, c.ctx_lens, parents, self.out[layer], softcap=self.softcap,
+                           slopes=self.slopes, workspace=self.attn_ws, dev_status=c.dev_status, stream=stream)
+
+    def run(self, q, k_new, v_new, parents, draft_tokens, logits, stream=None):
+        """q, k_new and v_new are per-layer lists (or tensors with a leading layer dimension)."""
+        for layer in range(len(q)):
+            self.attention(layer, q[layer], k_new[layer], v_new[layer], parents, stream)
+        native.sd_accept(self.q_indptr, self.vocab, logits, parents, draft_tokens, self.accept_len, self.path,
+                         self.out_tokens, self.target_tokens, self.max_path, self.acc_ws, self.cache.dev_status,
+                         stream)
+        self.cache.extend(self.accept_len, k_new, v_new, self.slots, self.rows, self.q_indptr, self.path, stream)
 
 
 def device_inputs(w, device="cuda"):
