@@ -223,9 +223,15 @@ struct Kv8AttnParams {
   float scale, softcap;      // softcap 0: none
   int hq, hkv, dim, max_pages, num_pool_pages, window;
   void* workspace;
+  int group;                 // query heads per KV head
+  // filled in by the launch: the plan and the workspace's parts
+  int hpc, hparts, nq, grid;
+  int* cum;                  // [batch + 1] first unit of each sequence (written for the merge)
+  __nv_bfloat16* o_part;     // [piece + segment][nq][dim] partial outputs
+  float* lse_part;           // [piece + segment][nq] base-2 log-sum-exps
 };
 constexpr int kMaxKvHeads = 64, kMaxGroup = 16;   // of the block-scaled cache's calls
 size_t kv8_attn_workspace(int hq, int hkv, int dim, const BatchDesc& bd);
-cudaError_t launch_kv8_attn(const Kv8AttnParams& p, const BatchDesc& bd, cudaStream_t st);
+cudaError_t launch_kv8_attn(Kv8AttnParams p, const BatchDesc& bd, cudaStream_t st);
 
 }  // namespace sdv

@@ -44,6 +44,10 @@ sd_status check_kv8_shape(const sd_shape* s, BatchDesc* bd) {
   if (s->num_splits != 0) return SD_ERR_UNSUPPORTED;
   st = check_pages(s->batch < 1 ? 1 : s->batch, s->max_pages_per_seq, s->num_pool_pages);
   if (st != SD_OK) return st;
+  // a half page of one head is a tensor-map coordinate; tiles are counted in 32 bits over the whole batch
+  if ((long long)s->num_pool_pages * s->num_kv_heads * 2 > INT_MAX) return SD_ERR_UNSUPPORTED;
+  const long long tiles = ((long long)s->max_pages_per_seq * kPage + kTileTokens - 1) / kTileTokens + 1;
+  if (tiles * s->num_q_heads * (s->batch < 1 ? 1 : s->batch) > INT_MAX / 2) return SD_ERR_UNSUPPORTED;
   return fill_batch(s->batch, s->q_indptr_h, bd);
 }
 
@@ -213,6 +217,7 @@ sd_status sd_kv8_attn(const sd_shape* shape, const sd_kv8_opts* opts, const void
   p.softcap = o.softcap;
   p.hq = shape->num_q_heads;
   p.hkv = shape->num_kv_heads;
+  p.group = p.hq / p.hkv;
   p.dim = shape->head_dim;
   p.max_pages = shape->max_pages_per_seq;
   p.num_pool_pages = shape->num_pool_pages;

@@ -1,154 +1,211 @@
-// Verify attention over the 8-bit block-scaled cache (include/sd_kv8.h:
-// sd_kv8_attn), the plain kernel: one CTA per (node row, query head), one warp
-// per key at a time, fp32 throughout, one pass with each warp's running
-// maximum and sum, the eight warps joined at the end.
-#include <cuda_fp16.h>
+// Host side of the verify attention over the 8-bit block-scaled cache: the
+// query-column plan, the workspace, the page tensor map, the merge of split
+// segments, and the launches.  The kernel is in kv8_attn_kernel.cuh.
+#include <cudaTypedefs.h>
 
-#include "common.cuh"
-#include "kernels.h"
+#include "kv8_attn_launch.cuh"
 
 namespace sdv {
 namespace {
 
-constexpr int kThreads = 256;
-
-__device__ __forceinline__ float2 e4m3x2_value(uint32_t codes) {
-  uint32_t h;
-  asm("{ .reg .b16 t; cvt.u16.u32 t, %1; cvt.rn.f16x2.e4m3x2 %0, t; }" : "=r"(h) : "r"(codes & 0xffffu));
-  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      ptr = nullptr;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+  }();
+  return fn;
 }
 
+// The codes viewed as 4-D: x = 128 codes of a row, y = slot within an 8-slot half page, z = 128-dim block,
+// w = half page of one KV head.  A box of {128, 8, D / 128, 2} is one page of one head, landing as
+// [half][block][8 slots][128 B] with the 128-byte swizzle: two 8-row groups of a K tile or a V half tile.
+bool page_map(CUtensorMap* map, const void* cache, const Kv8AttnParams& p) {
+  auto fn = tensor_map_fn();
+  if (fn == nullptr) return false;
+  const cuuint32_t blocks = (cuuint32_t)(p.dim / 128);
+  cuuint64_t dims[4] = {128, 8, blocks, (cuuint64_t)p.num_pool_pages * p.hkv * 2};
+  cuuint64_t strides[3] = {(cuuint64_t)p.dim, 128, (cuuint64_t)p.dim * 8};
+  cuuint32_t box[4] = {128, 8, blocks, 2};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(cache), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int sm_count() {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1) {
+    cudaGetLastError();   // no device here
+    return kSMs;
+  }
+  return sms;
+}
+
+// Log-sum-exp merge of the segments that piece borders cut: o = sum 2^(lse_s - M) o_s / sum 2^(lse_s - M).
+// One block per (node row, query head): four warps each take every fourth partial, a lane D / 32 dims, with the
+// loads of kBatch partials in flight per warp (40 partials in one round of latency).
+constexpr int kMergeThreads = 128, kMergeWarps = 4, kBatch = 10;
+
 template <int D>
-__global__ void __launch_bounds__(kThreads) kv8_attn_plain_kernel(const Kv8AttnParams p, const BatchDesc bd) {
-  constexpr int E = D / 32;   // values per lane
-  const int r = blockIdx.x, h = blockIdx.y, g = h / (p.hq / p.hkv);
+__global__ void __launch_bounds__(kMergeThreads) kv8_merge_kernel(const Kv8AttnParams p, const BatchDesc bd) {
+  constexpr int E = D / 32;   // dims per lane
+  const int r = blockIdx.x, h = blockIdx.y;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int b = 0, hi = bd.batch - 1;
   while (b < hi) {
     const int mid = (b + hi + 1) >> 1;
     if (bd.q_indptr[mid] <= r) b = mid; else hi = mid - 1;
   }
-  const int q0 = bd.q_indptr[b], node = r - q0;
-  int L = p.ctx_lens[b];
-  if (L < 0 || L > p.max_pages * kPage) {
-    if (threadIdx.x == 0) report(p.dev_status, SD_DEV_BAD_CTX);
-    L = L < 0 ? 0 : p.max_pages * kPage;
-  }
-  // the root path
-  unsigned long long see = 1ull << node;
-  int depth = 0;
-  for (int u = node; u >= 0;) {
-    const int up = p.parents[q0 + u];
-    if (u == 0 ? up != -1 : (up < 0 || up >= u)) {
-      if (threadIdx.x == 0) report(p.dev_status, SD_DEV_BAD_PARENTS);
-      see = 1ull << node;
-      depth = 0;
-      break;
+  const int g = h / p.group, c = (h % p.group) / p.hpc, part0 = c * p.hpc;
+  const int hpc = min(p.hpc, p.group - part0);
+  const int col = (r - bd.q_indptr[b]) * hpc + h % p.group - part0;
+  const int parts = p.hkv * p.hparts, s = g * p.hparts + c;
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // the attention kernel's partials and unit sums
+  const int cum = p.cum[b], units = (p.cum[b + 1] - cum) / parts;
+  const int per = (p.cum[bd.batch] + p.grid - 1) / p.grid;
+  const int u0 = cum + s * units, k0 = u0 / per, n = (u0 + units - 1) / per - k0 + 1;
+  if (n == 1) return;   // written directly
+  const size_t slot0 = (size_t)k0 + b * parts + s;
+  float mx = -INFINITY, den = 0.f, acc[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) acc[e] = 0.f;
+  for (int base = warp; base < n; base += kMergeWarps * kBatch) {
+    float w[kBatch];
+    uint32_t o[kBatch][E / 2];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int i = base + k * kMergeWarps;
+      const size_t at = (slot0 + min(i, n - 1)) * p.nq + col;
+      w[k] = i < n ? p.lse_part[at] : -INFINITY;
+      const uint32_t* src = reinterpret_cast<const uint32_t*>(p.o_part + at * D + lane * E);
+#pragma unroll
+      for (int e = 0; e < E / 2; ++e) o[k][e] = src[e];
     }
-    if (u == 0) break;
-    see |= 1ull << up;
-    ++depth;
-    u = up;
-  }
-  float q[E], acc[E];
+    float bm = mx;
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    q[e] = __bfloat162float(p.q[(long long)r * p.q_stride + h * D + lane * E + e]) * p.scale;
-    acc[e] = 0.f;
-  }
-  const float slope = p.slopes != nullptr ? p.slopes[h] : 0.f;
-  float m = -INFINITY, l = 0.f;
-  auto take = [&](const float (&k)[E], const float (&v)[E], int away) {
-    float s = 0.f;
+    for (int k = 0; k < kBatch; ++k) bm = fmaxf(bm, w[k]);
+    const float a = mx == -INFINITY ? 0.f : fast_exp2(mx - bm);
+    den *= a;
 #pragma unroll
-    for (int e = 0; e < E; ++e) s = fmaf(q[e], k[e], s);
+    for (int e = 0; e < E; ++e) acc[e] *= a;
+    mx = bm;
 #pragma unroll
-    for (int d = 16; d >= 1; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-    if (p.softcap > 0.f) s = p.softcap * tanhf(s / p.softcap);
-    if (p.slopes != nullptr) s += slope * (float)away;
-    const float mn = fmaxf(m, s);
-    const float a = m == -INFINITY ? 0.f : expf(m - mn), w = expf(s - mn);
-    l = l * a + w;
+    for (int k = 0; k < kBatch; ++k) {
+      if (w[k] == -INFINITY) continue;                   // nothing visible there, or padding (a NaN goes on)
+      const float f = fast_exp2(w[k] - mx);
+      den += f;
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = acc[e] * a + w * v[e];
-    m = mn;
-  };
-  const int q_pos = L + depth;
-  const int t_first = p.window > 0 ? max(0, q_pos - p.window + 1) : 0;
-  for (int t = t_first + warp; t < L; t += kThreads / 32) {
-    const int page = p.page_table[(size_t)b * p.max_pages + t / kPage];
-    float k[E], v[E];
-    if (page < 0 || page >= p.num_pool_pages) {
-      report(p.dev_status, SD_DEV_BAD_PAGE);
-#pragma unroll
-      for (int e = 0; e < E; ++e) k[e] = v[e] = 0.f;
-    } else {
-      const size_t block = (size_t)page * p.hkv + g;
-      float sk = p.k_scales[block], sv = p.v_scales[block];
-      const float lo = 0x1p-100f, up = 0x1p100f;
-      if (!(sk >= lo && sk <= up) || !(sv >= lo && sv <= up)) {
-        report(p.dev_status, SD_DEV_BAD_SCALE);
-        sk = fminf(fmaxf(sk, lo), up);
-        sv = fminf(fmaxf(sv, lo), up);
-      }
-      const size_t at = (block * kPage + t % kPage) * D + lane * E;
-#pragma unroll
-      for (int e = 0; e < E; e += 2) {
-        const float2 a = e4m3x2_value(*reinterpret_cast<const uint16_t*>(p.k_cache + at + e));
-        const float2 c = e4m3x2_value(*reinterpret_cast<const uint16_t*>(p.v_cache + at + e));
-        k[e] = a.x * sk; k[e + 1] = a.y * sk;
-        v[e] = c.x * sv; v[e + 1] = c.y * sv;
+      for (int e = 0; e < E / 2; ++e) {
+        const float2 v = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&o[k][e]));
+        acc[2 * e] += f * v.x;
+        acc[2 * e + 1] += f * v.y;
       }
     }
-    take(k, v, t - q_pos);
   }
-  int up = depth;   // the path's nodes from the deepest: depth of the next one
-  if (warp == 0) {
-    for (int n = node; n >= 0; --n) {
-      if (!((see >> n) & 1ull)) continue;
-      const int away = up - depth;
-      --up;
-      if (p.window > 0 && away <= -p.window) continue;
-      float k[E], v[E];
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        k[e] = __bfloat162float(p.k_new[(long long)(q0 + n) * p.k_stride + g * D + lane * E + e]);
-        v[e] = __bfloat162float(p.v_new[(long long)(q0 + n) * p.v_stride + g * D + lane * E + e]);
-      }
-      take(k, v, away);
-    }
-  }
-  __shared__ float s_m[kThreads / 32], s_l[kThreads / 32], s_acc[kThreads / 32][D];
-  if (lane == 0) { s_m[warp] = m; s_l[warp] = l; }
+  __shared__ float s_m[kMergeWarps], s_d[kMergeWarps], s_acc[kMergeWarps][D];
+  if (lane == 0) { s_m[warp] = mx; s_d[warp] = den; }
 #pragma unroll
   for (int e = 0; e < E; ++e) s_acc[warp][lane * E + e] = acc[e];
   __syncthreads();
-  float mm = s_m[0];
-  for (int w = 1; w < kThreads / 32; ++w) mm = fmaxf(mm, s_m[w]);
-  for (int d = threadIdx.x; d < D; d += kThreads) {
-    float sum = 0.f, den = 0.f;
-    for (int w = 0; w < kThreads / 32; ++w) {
-      if (s_m[w] == -INFINITY) continue;
-      const float f = expf(s_m[w] - mm);
-      sum += f * s_acc[w][d];
-      den += f * s_l[w];
-    }
-    p.out[((size_t)r * p.hq + h) * D + d] = __float2bfloat16_rn(sum / den);
-    if (p.lse != nullptr && d == 0) p.lse[(size_t)r * p.hq + h] = mm + logf(den);
+  float m = s_m[0];
+#pragma unroll
+  for (int w = 1; w < kMergeWarps; ++w) m = fmaxf(m, s_m[w]);
+  float f[kMergeWarps], d = 0.f;
+#pragma unroll
+  for (int w = 0; w < kMergeWarps; ++w) {
+    f[w] = s_m[w] == -INFINITY && s_d[w] == 0.f ? 0.f : fast_exp2(s_m[w] - m);
+    d += f[w] * s_d[w];
   }
+  const float inv = 1.f / d;
+  constexpr int T = D / 2;    // threads that write a pair of dims
+  if (threadIdx.x < T) {
+    float x = 0.f, y = 0.f;
+#pragma unroll
+    for (int w = 0; w < kMergeWarps; ++w) {
+      const float2 v = *reinterpret_cast<const float2*>(&s_acc[w][2 * threadIdx.x]);
+      x += f[w] * v.x;
+      y += f[w] * v.y;
+    }
+    *reinterpret_cast<__nv_bfloat162*>(p.out + ((size_t)r * p.hq + h) * D + 2 * threadIdx.x) =
+        __floats2bfloat162_rn(x * inv, y * inv);
+  }
+  if (p.lse != nullptr && threadIdx.x == 0) p.lse[(size_t)r * p.hq + h] = (m + fast_log2(d)) * kLn2;
+}
+
+constexpr size_t kAlign = 256;
+size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
+
+struct Layout {
+  size_t o, lse, total;   // cum at 0
+};
+Layout layout_of(const Kv8Plan& pl, int hkv, int dim, const BatchDesc& bd, int sms) {
+  // a piece and a segment name a partial; along the line of units their numbers rise together
+  const size_t slots = (size_t)sms + (size_t)bd.batch * hkv * pl.hparts;
+  Layout l;
+  l.o = align_up((kMaxBatch + 1) * sizeof(int));
+  l.lse = l.o + align_up(slots * pl.nq * dim * sizeof(__nv_bfloat16));
+  l.total = l.lse + align_up(slots * pl.nq * sizeof(float));
+  return l;
 }
 
 }  // namespace
 
-size_t kv8_attn_workspace(int, int, int, const BatchDesc&) { return 0; }
+// Query columns of a CTA: as many heads of a KV group as fit, so that the cache is read as few times as can be.
+Kv8Plan kv8_plan(int group, int max_nodes, bool mod) {
+  const int most = mod ? 128 : 144;
+  Kv8Plan pl;
+  pl.hparts = 1;
+  while ((group + pl.hparts - 1) / pl.hparts * max_nodes > most) ++pl.hparts;
+  pl.hpc = (group + pl.hparts - 1) / pl.hparts;
+  pl.hparts = (group + pl.hpc - 1) / pl.hpc;
+  const int cols = pl.hpc * max_nodes;
+  pl.hc = cols <= 32 ? 1 : cols <= 64 ? 2 : cols <= 96 ? 3 : mod ? 4 : 5;
+  pl.nq = pl.hc == 5 ? 144 : 32 * pl.hc;
+  return pl;
+}
 
-cudaError_t launch_kv8_attn(const Kv8AttnParams& p, const BatchDesc& bd, cudaStream_t st) {
+size_t kv8_attn_workspace(int hq, int hkv, int dim, const BatchDesc& bd) {
+  // the query does not know whether scores will be capped or biased
+  const int sms = sm_count();
+  const size_t a = layout_of(kv8_plan(hq / hkv, bd.max_nodes, false), hkv, dim, bd, sms).total;
+  const size_t b = layout_of(kv8_plan(hq / hkv, bd.max_nodes, true), hkv, dim, bd, sms).total;
+  return a > b ? a : b;
+}
+
+cudaError_t launch_kv8_attn(Kv8AttnParams p, const BatchDesc& bd, cudaStream_t st) {
+  const bool mod = p.softcap > 0.f || p.slopes != nullptr;
+  const Kv8Plan pl = kv8_plan(p.group, bd.max_nodes, mod);
+  p.hpc = pl.hpc;
+  p.hparts = pl.hparts;
+  p.nq = pl.nq;
+  p.grid = sm_count();
+  const Layout l = layout_of(pl, p.hkv, p.dim, bd, p.grid);
+  char* ws = static_cast<char*>(p.workspace);
+  p.cum = reinterpret_cast<int*>(ws);
+  p.o_part = reinterpret_cast<__nv_bfloat16*>(ws + l.o);
+  p.lse_part = reinterpret_cast<float*>(ws + l.lse);
+  CUtensorMap mk, mv;
+  if (!page_map(&mk, p.k_cache, p) || !page_map(&mv, p.v_cache, p)) return cudaErrorInvalidValue;
+  cudaError_t e = p.dim == 256 ? (mod ? launch_kv8_256_mod(mk, mv, p, bd, pl.hc, st) : launch_kv8_256(mk, mv, p, bd, pl.hc, st))
+                               : (mod ? launch_kv8_128_mod(mk, mv, p, bd, pl.hc, st) : launch_kv8_128(mk, mv, p, bd, pl.hc, st));
+  if (e != cudaSuccess) return e;
   const dim3 grid(bd.total_nodes, p.hq);
-  if (p.dim == 256)
-    kv8_attn_plain_kernel<256><<<grid, kThreads, 0, st>>>(p, bd);
-  else
-    kv8_attn_plain_kernel<128><<<grid, kThreads, 0, st>>>(p, bd);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(kMergeThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return p.dim == 256 ? cudaLaunchKernelEx(&cfg, kv8_merge_kernel<256>, p, bd)
+                      : cudaLaunchKernelEx(&cfg, kv8_merge_kernel<128>, p, bd);
 }
 
 }  // namespace sdv

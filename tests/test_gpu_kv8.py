@@ -5,8 +5,10 @@ Tolerance of the attention, per output element, derived from its roundings (half
   2^-8 A              each split's partial output in bf16; A = sum of p |v| / sum of p bounds any convex mix
   2^-7 A              the softmax weights as an e4m3 value (2^-4) and an e5m2 rest (2^-3 of at most 2^-4)
   2 ds A              an absolute error ds of the scores changes a weight by at most e^ds - 1, in sum and in share
-with ds the error of q as two e4m3 terms: at most 2^-10 of the step in which the row's amax is 224..448, so
-2^-17 amax |k|_1 scale, and 2^-20 of the score scale |q|_1 |k|_inf for fp32 products and sums.
+  2^-17 max|v_new|    the draft values as two e4m3 terms: a row is scaled so that its amax is 224..448, and what the
+                      two terms leave is at most half of e4m3's smallest step 2^-9, so 2^-10 / 224 of amax < 2^-17
+with ds the same error of q (2^-17 amax |k|_1 scale) and of the draft keys (2^-17 amax |q|_1 scale), and 2^-20 of
+the score scale |q|_1 |k|_inf for fp32 products and sums.
 The log-sum-exp is off by at most ds plus fp32 rounding of sums and logarithm (2^-20 of its size).
 """
 import numpy as np
@@ -124,7 +126,8 @@ class Case:
         k1, kinf = max(k1, kn.sum(-1).max()), max(kinf, kn.max())
         scale = self.scale or self.dim ** -0.5
         bias = 0.0 if self.slopes is None else 2.0 ** -23 * float(np.abs(self.slopes).max()) * (float(self.ctx.max()) + 64)
-        return (2.0 ** -17 * q.max() * k1 + 2.0 ** -20 * q.sum(-1).max() * kinf) * scale + bias
+        q1 = q.sum(-1).max()
+        return (2.0 ** -17 * (q.max() * k1 + kn.max() * q1) + 2.0 ** -20 * q1 * kinf) * scale + bias
 
     def check(self, only=None):
         torch.cuda.synchronize()
@@ -133,7 +136,8 @@ class Case:
         at = ~np.isnan(lse)
         got, got_lse, ds = np64(self.out[:-1]), np64(self.lse), self.score_error()
         assert ds < 0.25, ds
-        bound = 2.0 ** -8 * np.abs(ref) + (2.0 ** -8 + 2.0 ** -7 + 2 * np.expm1(ds)) * spread + 1e-30
+        bound = 2.0 ** -8 * np.abs(ref) + (2.0 ** -8 + 2.0 ** -7 + 2 * np.expm1(ds)) * spread + \
+            2.0 ** -17 * float(self.vn.abs().max()) + 1e-30
         over = (np.abs(got - ref) / bound)[at]
         assert np.isfinite(got[at]).all() and over.max() <= 1.0, (over.max(), ds)
         assert np.all(np.abs(got_lse - lse)[at] <= ds + 2.0 ** -20 * (np.abs(lse[at]) + 1)), np.abs(got_lse - lse)[at].max()
@@ -622,8 +626,9 @@ def test_prompt_then_verify_steps(graph):
             ref, _, spread = kv8.attention(np64(q[layer]), codes[0][layer], codes[1][layer], scales[0][layer], scales[1][layer],
                                            np64(kn[layer]), np64(vn[layer]), table, ctx, indptr, parents, softcap=20.0)
             got = np64(step.out[layer])
-            ds = 2.0 ** -17 * float(q.abs().max()) * 256 * 4 * 2.0 ** it / 16       # |k|_1 <= 256 values of up to 4 * 2^it
-            assert np.all(np.abs(got - ref) <= 2.0 ** -8 * np.abs(ref) + (2.0 ** -8 + 2.0 ** -7 + 2 * np.expm1(ds)) * spread)
+            ds = 2.0 ** -16 * float(q.abs().max()) * 256 * 4 * 2.0 ** it / 16       # |k|_1 <= 256 values of up to 4 * 2^it
+            assert np.all(np.abs(got - ref) <= 2.0 ** -8 * np.abs(ref) + (2.0 ** -8 + 2.0 ** -7 + 2 * np.expm1(ds)) * spread +
+                          2.0 ** -17 * float(vn.abs().max()))
         table, held, free, sl, rows, _, ctx = kv8.pages_extend(ctx, alen, table, held, free, total, indptr, paths)
         assert list(step.slots.cpu().numpy()) == sl and list(step.rows.cpu().numpy()) == rows
         done = put([list(kn), list(vn)], sl, rows)
