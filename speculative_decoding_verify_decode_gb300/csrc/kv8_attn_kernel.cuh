@@ -40,7 +40,8 @@
 // Warps: 0-7 softmax (lane quarter = warp % 4, column half = warp / 4; thread =
 // token row), which also stage Q and the draft block and write the results; 8
 // loads K and the block scales, 9 loads V, 10 issues QK, 11 issues PV.
-// Every wait is bounded; on expiry the kernel reports SD_DEV_TIMEOUT and ends.
+// Every wait on a barrier is bounded; on expiry the kernel reports
+// SD_DEV_TIMEOUT and runs out.
 #pragma once
 
 #include <cstddef>
@@ -56,9 +57,9 @@ namespace {
 constexpr int kKvThreads = 384;
 constexpr int kWarpK = 8, kWarpV = 9, kWarpQK = 10, kWarpPV = 11;
 constexpr int kTile = kTileTokens;
-constexpr float kHead = 6.0f;          // the largest weight sits at 2^6 when m is exact
+constexpr float kHead = 5.0f;          // the largest weight sits at 2^5 when m is exact
 constexpr float kTop = 448.0f;         // weights beyond it move m
-constexpr float kNone = -1.0e30f;      // m before any visible key
+constexpr float kDown = 0x1p-8f;       // weights are formed times 2^-8 (see split4)
 constexpr float kScaleLo = 0x1p-100f, kScaleHi = 0x1p100f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kSmemBytes = 232448;     // 227 KB of dynamic shared memory per CTA
@@ -82,7 +83,7 @@ struct KvSmall {
   int scan[8];
   int8_t par[kMaxNodes];
   int8_t depth[kMaxNodes];
-  int flag[2][2][4];       // [column half][tile parity][lane quarter]: a weight passed kTop
+  alignas(16) int flag[2][2][4];   // [column half][tile parity][lane quarter]: chunks where a weight passes kTop
   uint32_t tmem;
   int abort;
 };
@@ -113,6 +114,28 @@ struct Kv {
 
 // ------------------------------------------------------------ small pieces
 
+// A bounded wait, kept short (every instruction of this kernel's loops comes through a small instruction cache):
+// false, with the CTA's abort flag set, if the phase never completes.  The kernel's end reports the flag.
+__device__ __forceinline__ bool wait8(uint32_t bar, uint32_t parity, volatile int* abort) {
+  long long t0 = 0;
+#pragma unroll 1
+  while (!mbar_try(bar, parity)) {
+    const long long now = clock64();
+    if (t0 == 0) t0 = now;
+    if (now - t0 > kWaitCycles || *abort) {
+      *abort = 1;
+      return false;
+    }
+  }
+  return true;
+}
+// One lane of a converged warp.  The tensor core's and TMA's instructions take uniform operands: issued by an elected
+// lane of a warp that runs as one they cost a few instructions, issued under a plain lane test several dozen each.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(ok));
+  return ok != 0;
+}
 __device__ __forceinline__ uint64_t noswz_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
   return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) |
          ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46);
@@ -122,10 +145,18 @@ __device__ __forceinline__ uint32_t f8_idesc(int n, int a_mn, int b_mn, bool b_e
   return (1u << 4) | (b_e5m2 ? 1u << 10 : 0u) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) |
          ((uint32_t)(n >> 3) << 17) | (8u << 24);
 }
-__device__ __forceinline__ void umma8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{ .reg .pred p; setp.ne.b32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p; }"
-      ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc));
+// ACC: 0 overwrites D, 1 adds to it, 2 as `acc` says.  One lane issues some thirty of these per tile, so their
+// operands are a descriptor plus a constant and nothing is decided at run time that need not be.
+template <int ACC>
+__device__ __forceinline__ void umma8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc = 1) {
+  if (ACC == 2)
+    asm volatile(
+        "{ .reg .pred p; setp.ne.b32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p; }"
+        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc));
+  else
+    asm volatile(
+        "{ .reg .pred p; setp.ne.b32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p; }"
+        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "n"(ACC));
 }
 __device__ __forceinline__ void tma_page8(uint32_t dst, const CUtensorMap* map, int w, uint32_t bar, uint64_t policy) {
   asm volatile(
@@ -161,44 +192,52 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
       : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)), "l"(*reinterpret_cast<uint64_t*>(&c)));
   return *reinterpret_cast<float2*>(&r);
 }
-// Four weights (two pairs, columns in order) as four e4m3 codes and four e5m2 codes of the rest.
+// Four weights w (two pairs, columns in order, each times 2^-8) as four e4m3 codes and four e5m2 codes of the
+// rest, w in [0, 448].  The 8-bit conversions share a slow pipe with exp2, so they are done on f16 bits: w * 2^-8
+// has e4m3's exponent bias in f16, subnormals included, so the code is the rounded top byte below the sign; e5m2
+// is the top byte of f16.  Both round half away (off by at most half a step, like any nearest rounding; a tie
+// costs a weight nothing that its rest does not give back).  A NaN weight loses itself here and is carried by the
+// column's sum.
 __device__ __forceinline__ void split4(float2 w0, float2 w1, uint32_t& hi, uint32_t& lo) {
-  asm("{ .reg .b32 a, b, c, d; .reg .b16 s, t, u, v;\n\t"
-      "cvt.rn.f16x2.f32 a, %3, %2;\n\t"
-      "cvt.rn.f16x2.f32 b, %5, %4;\n\t"
-      "cvt.rn.satfinite.e4m3x2.f16x2 s, a;\n\t"
-      "cvt.rn.satfinite.e4m3x2.f16x2 t, b;\n\t"
-      "cvt.rn.f16x2.e4m3x2 c, s;\n\t"
-      "cvt.rn.f16x2.e4m3x2 d, t;\n\t"
-      "sub.rn.f16x2 c, a, c;\n\t"
-      "sub.rn.f16x2 d, b, d;\n\t"
-      "cvt.rn.satfinite.e5m2x2.f16x2 u, c;\n\t"
-      "cvt.rn.satfinite.e5m2x2.f16x2 v, d;\n\t"
-      "mov.b32 %0, {s, t};\n\t"
-      "mov.b32 %1, {u, v}; }"
-      : "=r"(hi), "=r"(lo)
-      : "f"(w0.x), "f"(w0.y), "f"(w1.x), "f"(w1.y));
+  const __half2 a = __floats2half2_rn(w0.x, w0.y), b = __floats2half2_rn(w1.x, w1.y);
+  const uint32_t ta = *reinterpret_cast<const uint32_t*>(&a) + 0x00400040u;
+  const uint32_t tb = *reinterpret_cast<const uint32_t*>(&b) + 0x00400040u;
+  hi = __byte_perm(ta >> 7, tb >> 7, 0x6420);
+  const uint32_t ha = ta & 0x7f807f80u, hb = tb & 0x7f807f80u;
+  const __half2 up = __halves2half2(__ushort_as_half(0x5c00), __ushort_as_half(0x5c00));   // 2^8
+  const __half2 ra = __hmul2(__hsub2(a, *reinterpret_cast<const __half2*>(&ha)), up);
+  const __half2 rb = __hmul2(__hsub2(b, *reinterpret_cast<const __half2*>(&hb)), up);
+  lo = __byte_perm(*reinterpret_cast<const uint32_t*>(&ra) + 0x00800080u,
+                   *reinterpret_cast<const uint32_t*>(&rb) + 0x00800080u, 0x7531);
 }
 __device__ __forceinline__ float fast_rcp(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// Reduce 16 values per lane over the warp: lane L ends with the result for value L % 16.
-template <bool MAX>
-__device__ __forceinline__ float reduce16(float (&v)[16], int lane) {
+// Maxima of 16 values (each lane's plus `plus`) over the warp's lanes: lane L ends with that of value L % 16.
+__device__ __forceinline__ float warp_max16(const float (&v)[16], float plus, int lane) {
+  float r = 0.f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    float x;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(x) : "f"(v[i] + plus));
+    r = (lane & 15) == i ? x : r;
+  }
+  return r;
+}
+// Sums of 16 values over the warp's lanes: lane L ends with that of value L % 16.
+__device__ __forceinline__ float warp_sum16(float (&v)[16], int lane) {
 #pragma unroll
   for (int half = 8; half >= 1; half >>= 1) {
     const bool up = (lane & half) != 0;
 #pragma unroll
     for (int i = 0; i < half; ++i) {
       const float send = up ? v[i] : v[i + half], keep = up ? v[i + half] : v[i];
-      const float got = __shfl_xor_sync(0xffffffffu, send, half);
-      v[i] = MAX ? fmaxf(keep, got) : keep + got;
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, send, half);
     }
   }
-  const float got = __shfl_xor_sync(0xffffffffu, v[0], 16);
-  return MAX ? fmaxf(v[0], got) : v[0] + got;
+  return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 16);
 }
 
 // Eight bf16 as two e4m3 terms (hi + lo) of x * 2^-e.
@@ -245,9 +284,8 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
   constexpr int NQ = K::NQ, MH = K::MH, NS = K::NS, KS = K::KS, VS = K::VS;
   using Sm = typename K::Small;
   constexpr int B_KF = 0, B_KE = KS, B_VF = 2 * KS, B_VE = B_VF + VS, B_SC = B_VE + VS, B_SF = B_SC + KS + NS,
-                B_SE = B_SF + NS, B_PF = B_SE + NS, B_OD = B_PF + 1, B_Q = B_PF + 2, B_G0 = B_PF + 3, B_G1 = B_PF + 4,
-                B_ALL = B_PF + 5;
-  constexpr int kNumBars = B_ALL + 1;
+                B_SE = B_SF + NS, B_PF = B_SE + NS, B_OD = B_PF + 1, B_Q = B_PF + 2;
+  constexpr int kNumBars = B_Q + 1;
   static_assert(kNumBars <= Sm::kBars, "barriers");
   constexpr int SC = KS + NS;   // scale stages: see the K producer
   extern __shared__ __align__(1024) uint8_t smem8[];
@@ -256,7 +294,7 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
   uint8_t* sV = sK + KS * K::kTileBytes;
   uint8_t* sP = sV + VS * K::kHalf;
   Sm* sm = reinterpret_cast<Sm*>(sP + K::kPBytes);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   if (smem_u32(smem8) & 1023u) {   // not expected; refuse rather than mis-swizzle
     if (tid == 0) report(p.dev_status, SD_DEV_TIMEOUT);
     return;
@@ -269,9 +307,9 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     return L < 0 ? 0 : min(L, p.max_pages * kPage);
   };
   if (tid == 0) {
+#pragma unroll 1
     for (int i = 0; i < kNumBars; ++i)
-      mbar_init(smem_u32(&sm->bar[i]), i == B_PF || i == B_ALL || (i >= B_SE && i < B_SE + NS) ? 8u
-                                       : i == B_G0 || i == B_G1 ? 4u : 1u);
+      mbar_init(smem_u32(&sm->bar[i]), i == B_PF || (i >= B_SE && i < B_SE + NS) ? 8u : 1u);
     sm->abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -293,6 +331,7 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     }
     __syncthreads();
     if (warp < 8) {
+#pragma unroll 1
       for (int w = 0; w < warp; ++w) incl += sm->scan[w];
       if (tid == 0) sm->cum[0] = 0;
       if (tid < bd.batch) sm->cum[tid + 1] = incl;
@@ -310,12 +349,14 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
   const int per = (total + gridDim.x - 1) / gridDim.x;
   const int u_begin = min(total, (int)blockIdx.x * per), u_end = min(total, u_begin + per);
   if (blockIdx.x == 0) {   // for the merge
+#pragma unroll 1
     for (int i = tid; i <= bd.batch; i += kKvThreads) p.cum[i] = sm->cum[i];
   }
   // The piece that begins at unit u.
   auto piece_at = [&](int u) {
     Piece pc;
     int lo = 0, hi = bd.batch - 1;
+#pragma unroll 1
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
       if (sm->cum[mid] <= u) lo = mid; else hi = mid - 1;
@@ -331,248 +372,333 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     pc.whole = pc.tiles == units;
     pc.L = ctx_of(lo);
     pc.base = window_base(pc.L, p.window, kTile);
+    // the same for every lane, and known to be
+    pc.b = __shfl_sync(0xffffffffu, pc.b, 0);
+    pc.g = __shfl_sync(0xffffffffu, pc.g, 0);
+    pc.c = __shfl_sync(0xffffffffu, pc.c, 0);
+    pc.first = __shfl_sync(0xffffffffu, pc.first, 0);
+    pc.tiles = __shfl_sync(0xffffffffu, pc.tiles, 0);
+    pc.L = __shfl_sync(0xffffffffu, pc.L, 0);
+    pc.base = __shfl_sync(0xffffffffu, pc.base, 0);
     return pc;
   };
   const uint32_t bars = smem_u32(&sm->bar[0]);
   auto bar = [&](int i) { return bars + 8u * (uint32_t)i; };
-  auto wait = [&](int i, int n) { return mbar_wait(bar(i), (uint32_t)n & 1u, &sm->abort, p.dev_status); };
-  // for whole warps: one answer, so that a warp leaves as one
+  auto wait = [&](int i, int n) { return wait8(bar(i), (uint32_t)n & 1u, &sm->abort); };
+  // The softmax warps do not leave early: after an expired wait no other one waits, and they run through, so that
+  // their named barriers always find all of them.
   auto spin = [&](int i, int n) {
-    return __all_sync(0xffffffffu, mbar_spin(bar(i), (uint32_t)n & 1u, &sm->abort, p.dev_status)) != 0;
+    wait(i, n);
+    __syncwarp();
   };
   const uint32_t tmem = sm->tmem;
   const uint32_t kColO = NS * NQ;   // O^T behind the S buffers
 
-  if (warp == kWarpK || warp == kWarpV) {
-    // ------------------------------------------------------------ producers
-    const bool is_k = warp == kWarpK;
-    const CUtensorMap* map = is_k ? &tm_k : &tm_v;
-    const uint64_t policy = l2_evict_first();
-    int it = 0;         // tiles so far (the draft block's among them: staged by the softmax warps)
-    bool ok = true;
-    for (int u = u_begin; u < u_end && ok;) {
-      const Piece pc = piece_at(u);
-      u += pc.tiles;
-      const int* row = p.page_table + (size_t)pc.b * p.max_pages;
-      // page id of lane l's page of the tile that begins at t0 (-1: behind the context)
-      auto fetch = [&](int t0) {
-        const int pos = t0 + (lane & 7) * kPage;
-        return pos < pc.L && (lane < 8 || is_k) && lane < 16 ? row[pos / kPage] : -1;
-      };
-      auto t0_of = [&](int i) { return pc.base + (pc.first + i - 1) * kTile; };
-      const int i0 = pc.first == 0 ? 1 : 0;
-      if (i0) {
-        // the draft tile is staged by the softmax warps: its scale stage passes by empty, in its turn
-        if (is_k) {
-          ok = __all_sync(0xffffffffu, wait(B_KE + it % KS, it / KS + 1));
-          if (!ok) break;
-          if (lane == 0) mbar_arrive(bar(B_SC + it % SC));
-        }
-        ++it;
-      }
-      int page_next = i0 < pc.tiles ? fetch(t0_of(i0)) : -1;
-      for (int i = i0; i < pc.tiles && ok; ++i, ++it) {
-        const int t0 = t0_of(i);
-        const int valid = min(kTile, pc.L - t0);
-        int page = page_next;
-        page_next = i + 1 < pc.tiles ? fetch(t0_of(i + 1)) : -1;
-        const bool in_ctx = lane < 16 && (lane & 7) * kPage < valid;
-        const bool bad = in_ctx && (page < 0 || page >= p.num_pool_pages);
-        if (bad) {
-          if (is_k && lane < 8) report(p.dev_status, SD_DEV_BAD_PAGE);
-          page = -1;
-        }
-        if (is_k) {
-          // Block scales: lanes 0-7 those of K, 8-15 those of V.  A stage may be rewritten once the
-          // softmax has read the scores of the tile KS + NS before, which the wait on K_EMPTY implies
-          // (that tile's successor by NS has been multiplied).
-          float sc = 1.f;
-          if (in_ctx && page >= 0) {
-            sc = __ldg((lane < 8 ? p.k_scales : p.v_scales) + (size_t)page * p.hkv + pc.g);
-            if (!(sc >= kScaleLo && sc <= kScaleHi)) {
-              report(p.dev_status, SD_DEV_BAD_SCALE);
-              sc = sc > kScaleHi ? kScaleHi : kScaleLo;
-            }
-          }
-          const int slot = it % KS;
-          ok = wait(B_KE + slot, it / KS + 1);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          uint8_t* dst = sK + slot * K::kTileBytes;
-          const uint32_t zero = __ballot_sync(0xffffffffu, lane < 8 && bad);
-          if (zero != 0u) {
-            for (uint32_t z = zero; z != 0u; z &= z - 1u)
-              for (int e = lane; e < K::kPageBytes / 16; e += 32)
-                reinterpret_cast<uint4*>(dst + (__ffs(z) - 1) * K::kPageBytes)[e] = make_uint4(0, 0, 0, 0);
-            fence_async_smem();
-            __syncwarp();
-          }
-          const bool load = lane < 8 && page >= 0;
-          const uint32_t mask = __ballot_sync(0xffffffffu, load);
-          if (lane == 0) mbar_expect_tx(bar(B_KF + slot), (uint32_t)__popc(mask) * (uint32_t)K::kPageBytes);
-          __syncwarp();
-          if (load) tma_page8(smem_u32(dst + lane * K::kPageBytes), map, (page * p.hkv + pc.g) * 2, bar(B_KF + slot), policy);
-          if (lane < 16) sm->scale[it % SC][lane] = sc;
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(B_SC + it % SC));
-        } else {
-          // V: two halves of 64 tokens.  Rows that nobody sees must be zeros, not whatever lies there (a weight
-          // of 0 times a NaN code is NaN): pages with such rows, and those that only some nodes of a tree see
-          // through a window, go through plain loads, the rest by TMA.
-          const int lo = p.window > 0 ? pc.L - p.window + 1 : 0;          // the root's oldest visible position
-          for (int h = 0; h < 2; ++h) {
-            const int fill = 2 * it + h, slot = fill % VS;
-            ok = wait(B_VE + slot, fill / VS + 1);
-            ok = __all_sync(0xffffffffu, ok);
+  // Positions in the rings, counted along: an index and the parity of its round.
+  struct Ring {
+    int at = 0;
+    uint32_t round = 0;
+    __device__ __forceinline__ void next(int n) {
+      if (++at == n) { at = 0; round ^= 1u; }
+    }
+  };
+  auto wait_full = [&](int first, const Ring& r) { return wait(first + r.at, (int)r.round); };
+  auto wait_empty = [&](int first, const Ring& r) { return wait(first + r.at, (int)r.round ^ 1); };
+
+  // The softmax warps of the wide tiles need more registers than an even share: 2 x 208 + 88 per thread triple is what
+  // the block was launched with (3 x 168).
+  if (warp >= 8) {
+    if (HC >= 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if (warp <= kWarpV) {
+      // ---------------------------------------------------------- producers
+      // Page ids come a group of four tiles at a time (lane l: page l % 8 of the group's tile l / 8), two groups ahead of
+      // their use, block scales one: under a full memory system a load takes as long as a tile or two.
+      const bool is_k = warp == kWarpK;
+      const CUtensorMap* map = is_k ? &tm_k : &tm_v;
+      const uint64_t policy = l2_evict_first();
+      Ring ring, sc_ring;   // K tiles or V half tiles; scale stages
+      bool ok = true;
+#pragma unroll 1
+      for (int u = u_begin; u < u_end && ok;) {
+        const Piece pc = piece_at(u);
+        u += pc.tiles;
+        const int* row = p.page_table + (size_t)pc.b * p.max_pages;
+        int t0 = pc.base + (pc.first - 1) * kTile, left = pc.tiles;
+        if (pc.first == 0) {
+          // the draft tile is staged by the softmax warps: its slots, and its scale stage, pass by in their turn
+          if (is_k) {
+            ok = __all_sync(0xffffffffu, wait_empty(B_KE, ring));
             if (!ok) break;
-            uint8_t* dst = sV + slot * K::kHalf;
-            const int rows = min(64, valid - h * 64);
-            const int steps = rows > 0 ? (rows + 31) / 32 * 2 : 0;        // pages up to the last 32-token step
-            const int j = lane - 4 * h;
-            const bool mine = lane >= 4 * h && j < steps && lane < 4 * h + 4;
-            const int pos = t0 + lane * kPage;
-            const bool plain = mine && (page < 0 || pos + kPage > pc.L || pos < lo + (p.window > 0 ? kMaxNodes : 0));
-            const uint32_t slow = __ballot_sync(0xffffffffu, plain);
-            for (uint32_t z = slow; z != 0u; z &= z - 1u) {
-              const int l = __ffs(z) - 1;
-              const int pg = __shfl_sync(0xffffffffu, page, l);
-              for (int e = lane; e < kPage * D / 16; e += 32) {
-                const int r = e / (D / 16), ch = e % (D / 16), t = t0 + l * kPage + r;
-                uint4 v = make_uint4(0, 0, 0, 0);
-                if (pg >= 0 && t >= lo && t < pc.L) {
-                  v = __ldg(reinterpret_cast<const uint4*>(p.v_cache + (((size_t)pg * p.hkv + pc.g) * kPage + r) * D) + ch);
-                  if (p.window > 0 && t < lo + kMaxNodes) {   // NaN codes: the softmax makes the row's scores NaN instead
-                    uint32_t* w = reinterpret_cast<uint32_t*>(&v);
-#pragma unroll
-                    for (int i4 = 0; i4 < 4; ++i4) w[i4] &= ~__vcmpeq4(w[i4] & 0x7f7f7f7fu, 0x7f7f7f7fu);
-                  }
-                }
-                *reinterpret_cast<uint4*>(dst + ((l - 4 * h) * 2 + (r >> 3)) * K::kGroupBytes + (ch >> 3) * 1024 +
-                                          (r & 7) * 128 + (((ch & 7) ^ (r & 7)) << 4)) = v;
+            if (elect_one()) mbar_arrive(bar(B_SC + sc_ring.at));
+            sc_ring.next(SC);
+            ring.next(KS);
+          } else {
+            ring.next(VS);
+            ring.next(VS);
+          }
+          t0 += kTile;
+          --left;
+        }
+        const int t_end = min(pc.L, t0 + left * kTile);   // tokens of this piece
+        auto ids_from = [&](int t) {
+          t += lane * kPage;
+          return t < t_end ? row[t / kPage] : -1;
+        };
+        auto in_pool = [&](int page) { return (unsigned)page < (unsigned)p.num_pool_pages; };
+        auto scales_of = [&](const float* s, int page) {
+          return is_k && in_pool(page) ? __ldg(s + (size_t)page * p.hkv + pc.g) : 1.f;
+        };
+        int ids_next = ids_from(t0), ids_after = ids_from(t0 + 4 * kTile), ids = -1;
+        float ks_next = scales_of(p.k_scales, ids_next), vs_next = scales_of(p.v_scales, ids_next), ks_now = 1.f, vs_now = 1.f;
+        uint32_t good = 0;    // pages of the group that can be loaded
+#pragma unroll 1
+        for (int n = 0; n < left; ++n, t0 += kTile) {
+          const int sub = (n & 3) * 8;
+          if (sub == 0) {
+            ids = ids_next;
+            ks_now = ks_next;
+            vs_now = vs_next;
+            ids_next = ids_after;
+            ids_after = ids_from(t0 + 8 * kTile);
+            ks_next = scales_of(p.k_scales, ids_next);
+            vs_next = scales_of(p.v_scales, ids_next);
+            good = __ballot_sync(0xffffffffu, in_pool(ids));
+            if (is_k) {
+              if (t0 + lane * kPage < t_end && !in_pool(ids)) report(p.dev_status, SD_DEV_BAD_PAGE);
+              if (!(ks_now >= kScaleLo && ks_now <= kScaleHi && vs_now >= kScaleLo && vs_now <= kScaleHi)) {
+                report(p.dev_status, SD_DEV_BAD_SCALE);
+                ks_now = ks_now > kScaleHi ? kScaleHi : ks_now >= kScaleLo ? ks_now : kScaleLo;
+                vs_now = vs_now > kScaleHi ? kScaleHi : vs_now >= kScaleLo ? vs_now : kScaleLo;
               }
             }
-            if (slow != 0u) fence_async_smem();
+          }
+          const uint32_t have = (good >> sub) & 0xffu;
+          const int valid = min(kTile, t_end - t0);
+          const uint32_t need = (1u << ((valid + kPage - 1) / kPage)) - 1u;
+          const int half_page = (ids * p.hkv + pc.g) * 2;   // the tensor map's outer coordinate
+          if (is_k) {
+            ok = __all_sync(0xffffffffu, wait_empty(B_KE, ring));
+            if (!ok) break;
+            uint8_t* dst = sK + ring.at * K::kTileBytes;
+            if (need & ~have) {   // ids out of range count as zeros (they cannot be read)
+#pragma unroll 1
+              for (int e = lane; e < 8 * (K::kPageBytes / 16); e += 32)
+                if (((need & ~have) >> (e / (K::kPageBytes / 16))) & 1u)
+                  reinterpret_cast<uint4*>(dst)[e] = make_uint4(0, 0, 0, 0);
+              fence_async_smem();
+              __syncwarp();
+            }
+            int w[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) w[j] = __shfl_sync(0xffffffffu, half_page, sub + j);
+            if (elect_one()) {
+              mbar_expect_tx(bar(B_KF + ring.at), (uint32_t)__popc(have) * (uint32_t)K::kPageBytes);
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                if ((have >> j) & 1u) tma_page8(smem_u32(dst) + j * K::kPageBytes, map, w[j], bar(B_KF + ring.at), policy);
+            }
+            // A scale stage may be rewritten once the softmax has read the scores of the tile KS + NS before, which the
+            // wait on K_EMPTY implies (that tile's successor by NS has been multiplied).
+            const float k_sc = __shfl_sync(0xffffffffu, ks_now, sub + (lane & 7));
+            const float v_sc = __shfl_sync(0xffffffffu, vs_now, sub + (lane & 7));
+            if (lane < 16) sm->scale[sc_ring.at][lane] = lane < 8 ? k_sc : v_sc;
             __syncwarp();
-            const bool load = mine && !plain;
-            const uint32_t mask = __ballot_sync(0xffffffffu, load);
-            if (lane == 0) mbar_expect_tx(bar(B_VF + slot), (uint32_t)__popc(mask) * (uint32_t)K::kPageBytes);
-            __syncwarp();
-            if (load) tma_page8(smem_u32(dst + j * K::kPageBytes), map, (page * p.hkv + pc.g) * 2, bar(B_VF + slot), policy);
-            __syncwarp();
+            if (elect_one()) mbar_arrive(bar(B_SC + sc_ring.at));
+            sc_ring.next(SC);
+            ring.next(KS);
+          } else {
+            // V: two halves of 64 tokens, issued together where the ring holds two tiles.  Rows that nobody sees must be
+            // zeros, not whatever lies there (a weight of 0 times a NaN code is NaN): pages with such rows, and those
+            // that only some nodes of a tree see through a window, go through plain loads, the rest by TMA.
+            constexpr int kJoint = VS >= 4 ? 2 : 1;
+            const int lo = p.window > 0 ? pc.L - p.window + 1 : 0;          // the root's oldest visible position
+            const int seen = p.window > 0 ? lo + kMaxNodes : 0;             // from here on every node sees every token
+            uint32_t fast = have, slow = 0;
+            if (have != 0xffu || valid < kTile || t0 < seen) {
+              const int at = t0 + lane * kPage;
+              // pages up to the last 32-token step of their half
+              const int steps = lane < 4 ? (min(64, valid) + 31) / 32 * 2 : (max(0, valid - 64) + 31) / 32 * 2;
+              const bool used = lane < 8 && (lane & 3) < steps;
+              const bool plain = used && (!((have >> lane) & 1u) || at + kPage > pc.L || at < seen);
+              slow = __ballot_sync(0xffffffffu, plain);
+              fast = __ballot_sync(0xffffffffu, used && !plain);
+            }
+            int w[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) w[j] = __shfl_sync(0xffffffffu, half_page, sub + j);
+#pragma unroll
+            for (int h = 0; h < 2; h += kJoint) {
+              Ring other = ring;
+              other.next(VS);
+              ok = wait_empty(B_VE, ring);
+              if (kJoint == 2) ok = ok && wait_empty(B_VE, other);
+              ok = __all_sync(0xffffffffu, ok);
+              if (!ok) break;
+              const uint32_t sel = kJoint == 2 ? 0xffu : 0xfu << (4 * h);
+              uint8_t* base[2] = {sV + ring.at * K::kHalf, sV + (kJoint == 2 ? other.at : ring.at) * K::kHalf};
+              if (slow & sel) {
+#pragma unroll 1
+                for (int e = lane; e < 8 * kPage * (D / 16); e += 32) {
+                  const int pg = e / (kPage * (D / 16)), r = e / (D / 16) % kPage, ch = e % (D / 16);
+                  const int id = __shfl_sync(0xffffffffu, ids, sub + pg);
+                  if (!(((slow & sel) >> pg) & 1u)) continue;
+                  const int t = t0 + pg * kPage + r;
+                  uint4 v = make_uint4(0, 0, 0, 0);
+                  if (in_pool(id) && t >= lo && t < pc.L) {
+                    v = __ldg(reinterpret_cast<const uint4*>(p.v_cache + (((size_t)id * p.hkv + pc.g) * kPage + r) * D) + ch);
+                    if (t < seen) {   // NaN codes: the softmax makes the row's scores NaN instead
+                      uint32_t* x = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+                      for (int k = 0; k < 4; ++k) x[k] &= ~__vcmpeq4(x[k] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                    }
+                  }
+                  *reinterpret_cast<uint4*>((pg < 4 ? base[0] : base[1]) + (pg & 3) * K::kPageBytes +
+                                            (r >> 3) * K::kGroupBytes + (ch >> 3) * 1024 + (r & 7) * 128 +
+                                            (((ch & 7) ^ (r & 7)) << 4)) = v;
+                }
+                fence_async_smem();
+                __syncwarp();
+              }
+              if (elect_one()) {
+#pragma unroll
+                for (int hh = h; hh < h + kJoint; ++hh) {
+                  const uint32_t full = bar(B_VF + (hh > h ? other.at : ring.at));
+                  const uint32_t mine = (fast >> (4 * hh)) & 0xfu;
+                  mbar_expect_tx(full, (uint32_t)__popc(mine) * (uint32_t)K::kPageBytes);
+#pragma unroll
+                  for (int j = 0; j < 4; ++j)
+                    if ((mine >> j) & 1u)
+                      tma_page8(smem_u32(base[hh > h ? 1 : 0]) + j * K::kPageBytes, map, w[4 * hh + j], full, policy);
+                }
+              }
+              __syncwarp();
+              for (int k = 0; k < kJoint; ++k) ring.next(VS);
+            }
+            if (!ok) break;
           }
         }
       }
-    }
-    // After an abort no copy may still be landing when the CTA ends: wait, bounded, for the last fills.
-    if (lane == 0 && *(volatile int*)&sm->abort) {
-      const int slots = is_k ? KS : VS, fills = is_k ? it : 2 * it;
-      for (int s = 0; s < slots; ++s) {
-        for (int back = 0; back < 2; ++back) {   // the last fill of the slot, and the one that may be under way
-          const int n = (fills + 1 - s) / slots - back;
-          if (n < 0) continue;
-          const long long t0 = clock64();
-          while (!mbar_test(bar((is_k ? B_KF : B_VF) + s), (uint32_t)n & 1u) && clock64() - t0 < kWaitCycles / 64) {
+      // After an abort no copy may still be landing when the CTA ends: wait, bounded, for both rounds of every slot.
+      if (lane == 0 && *(volatile int*)&sm->abort) {
+#pragma unroll 1
+        for (int s = 0; s < 2 * (is_k ? KS : VS); ++s) {
+          const long long begin = clock64();
+          while (!mbar_test(bar((is_k ? B_KF : B_VF) + (s >> 1)), (uint32_t)s & 1u) && clock64() - begin < kWaitCycles / 64) {
           }
         }
       }
-    }
-  } else if (warp == kWarpQK) {
-    // ------------------------------------------------------------ QK issuer
-    if (lane == 0) {
-      int it = 0, np = 0;
+    } else if (warp == kWarpQK) {
+      // ---------------------------------------------------------- QK issuer
+      Ring s_ring, k_ring;
+      int np = 0;
       bool ok = true;
+      const uint64_t q_desc = sw128_desc(smem_u32(sQ), 16, 1024);
+#pragma unroll 1
       for (int u = u_begin; u < u_end && ok; ++np) {
         const Piece pc = piece_at(u);
         u += pc.tiles;
         const int n_nodes = bd.q_indptr[pc.b + 1] - bd.q_indptr[pc.b];
         const int nq = (min(p.hpc, p.group - pc.c * p.hpc) * n_nodes + 15) & ~15;
         const uint32_t idesc = f8_idesc(nq, 0, 0, false);
-        ok = wait(B_Q, np);
-        for (int i = 0; i < pc.tiles && ok; ++i, ++it) {
-          ok = wait(B_SE + it % NS, it / NS + 1) && wait(B_KF + it % KS, it / KS);
+        ok = __all_sync(0xffffffffu, wait(B_Q, np));
+#pragma unroll 1
+        for (int i = 0; i < pc.tiles && ok; ++i) {
+          ok = wait_empty(B_SE, s_ring) && wait_full(B_KF, k_ring);
+          ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t k0 = smem_u32(sK + it % KS * K::kTileBytes), q0 = smem_u32(sQ);
-          const uint32_t d = tmem + (it % NS) * NQ;
-          // the draft block: rows 0-63 the keys' first terms, rows 64-127 the second (both onto rows 0-63 of S; the
-          // other rows of S then hold nothing and are masked)
-          const int terms = pc.first + i == 0 ? 2 : 1;
-          for (int kt = 0; kt < terms; ++kt) {
+          const uint64_t a0 = sw128_desc(smem_u32(sK + k_ring.at * K::kTileBytes), 16, K::kGroupBytes);
+          const uint32_t d = tmem + s_ring.at * NQ;
+          if (elect_one()) {
 #pragma unroll
             for (int kk = 0; kk < D / 32; ++kk) {
-              const uint32_t off = (kk & 3) * 32;
-              const uint64_t a = sw128_desc(k0 + kt * 8 * K::kGroupBytes + (kk >> 2) * 1024 + off, 16, K::kGroupBytes);
-#pragma unroll
-              for (int t = 0; t < 2; ++t)
-                umma8(d, a, sw128_desc(q0 + t * K::kQTerm + (kk >> 2) * NQ * 128 + off, 16, 1024), idesc,
-                      kt + kk + t > 0 ? 1u : 0u);
+              const uint64_t a = a0 + (((kk >> 2) * 1024 + (kk & 3) * 32) >> 4);
+              const uint64_t b = q_desc + (((kk >> 2) * NQ * 128 + (kk & 3) * 32) >> 4);
+              if (kk == 0) umma8<0>(d, a, b, idesc); else umma8<1>(d, a, b, idesc);
+              umma8<1>(d, a, b + (K::kQTerm >> 4), idesc);
             }
+            // The draft block: rows 0-63 hold the keys' first terms, rows 64-127 the second; both go to rows 0-63 of S
+            // (its other rows then hold nothing and are masked).
+            if (pc.first + i == 0) {
+#pragma unroll 1
+              for (int kk = 0; kk < D / 32; ++kk) {
+                const uint32_t off = (kk & 3) * 32;
+                const uint64_t a = a0 + ((8 * K::kGroupBytes + (kk >> 2) * 1024 + off) >> 4);
+                const uint64_t b = q_desc + (((kk >> 2) * NQ * 128 + off) >> 4);
+                umma8<1>(d, a, b, idesc);
+                umma8<1>(d, a, b + (K::kQTerm >> 4), idesc);
+              }
+            }
+            umma_commit(bar(B_KE + k_ring.at));
+            umma_commit(bar(B_SF + s_ring.at));
           }
-          umma_commit(bar(B_KE + it % KS));
-          umma_commit(bar(B_SF + it % NS));
+          __syncwarp();
+          s_ring.next(NS);
+          k_ring.next(KS);
         }
       }
-    }
-  } else if (warp == kWarpPV) {
-    // ------------------------------------------------------------ PV issuer
-    if (lane == 0) {
+    } else {
+      // ---------------------------------------------------------- PV issuer
+      Ring v_ring;
       int it = 0;
       bool ok = true;
+      // P: 16-column chunks of 128 token rows x 16 bytes; MN-major without a swizzle
+      const uint64_t p_desc = noswz_desc(smem_u32(sP), 128, kTile * 16);
+#pragma unroll 1
       for (int u = u_begin; u < u_end && ok;) {
         const Piece pc = piece_at(u);
         u += pc.tiles;
         const int n_nodes = bd.q_indptr[pc.b + 1] - bd.q_indptr[pc.b];
         const int nq = (min(p.hpc, p.group - pc.c * p.hpc) * n_nodes + 15) & ~15;
         const uint32_t id_hi = f8_idesc(nq, 1, 1, false), id_lo = f8_idesc(nq, 1, 1, true);
+#pragma unroll 1
         for (int i = 0; i < pc.tiles && ok; ++i, ++it) {
           const bool draft = pc.first + i == 0;
           const int valid = draft ? n_nodes : min(kTile, pc.L - (pc.base + (pc.first + i - 1) * kTile));
-          ok = wait(B_PF, it);
+          ok = __all_sync(0xffffffffu, wait(B_PF, it));
+#pragma unroll 1
           for (int h = 0; h < 2 && ok; ++h) {
-            const int fill = 2 * it + h, slot = fill % VS;
-            ok = wait(B_VF + slot, fill / VS);
+            ok = __all_sync(0xffffffffu, wait_full(B_VF, v_ring));
             if (!ok) break;
             tc_fence_after();
             // the draft block: half 0 the values' first terms, half 1 the second, both weighed by rows 0-63 of P
-            const int rows = draft ? valid : min(64, valid - h * 64);
-            const uint32_t v0 = smem_u32(sV + slot * K::kHalf);
-            const uint32_t p0 = smem_u32(sP) + (draft ? 0 : h * 64 * 16);
-            for (int ks = 0; ks * 32 < rows; ++ks) {
-              const uint32_t first = i > 0 || h > 0 || ks > 0 ? 1u : 0u;
+            const int rows = draft ? valid : valid - h * 64;
+            const uint64_t v0 = sw128_desc(smem_u32(sV + v_ring.at * K::kHalf), 1024, K::kGroupBytes);
+            const uint64_t p0 = p_desc + (draft ? 0 : (h * 64 * 16) >> 4);
+            if (elect_one()) {
+              // two 32-token steps: the weights' first term and their rest on each 128-dim block
 #pragma unroll
-              for (int mb = 0; mb < MH; ++mb) {
-                const uint64_t a = sw128_desc(v0 + ks * 4 * K::kGroupBytes + mb * 1024, 1024, K::kGroupBytes);
-                // P: 16-column chunks of 128 token rows x 16 bytes; MN-major without a swizzle
-                const uint32_t d = tmem + kColO + mb * NQ;
-                umma8(d, a, noswz_desc(p0 + ks * 512, 128, kTile * 16), id_hi, first);
-                umma8(d, a, noswz_desc(p0 + K::kPTerm + ks * 512, 128, kTile * 16), id_lo, 1u);
+              for (int ks = 0; ks < 2; ++ks) {
+                if (rows > ks * 32) {
+#pragma unroll
+                  for (int mb = 0; mb < MH; ++mb) {
+                    const uint64_t a = v0 + ((ks * 4 * K::kGroupBytes + mb * 1024) >> 4);
+                    const uint64_t b = p0 + ((ks * 512) >> 4);
+                    umma8<2>(tmem + kColO + mb * NQ, a, b, id_hi, i > 0 || h > 0 || ks > 0 ? 1u : 0u);
+                    umma8<1>(tmem + kColO + mb * NQ, a, b + (K::kPTerm >> 4), id_lo);
+                  }
+                }
               }
+              umma_commit(bar(B_VE + v_ring.at));
+              if (h == 1) umma_commit(bar(B_OD));
             }
-            umma_commit(bar(B_VE + slot));
+            __syncwarp();
+            v_ring.next(VS);
           }
-          if (ok) umma_commit(bar(B_OD));
         }
       }
     }
   } else {
     // ------------------------------------------------------------ softmax warps
+    if (HC >= 4) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     const int half = warp >> 2, quarter = warp & 3;
     const int row = quarter * 32 + lane;                       // token row of S; dim (mod 128) of O^T
     const uint32_t lane_addr = (uint32_t)(quarter * 32) << 16;
-    int n_all = 0, n_grp = 0;
-    auto sync_all = [&]() -> bool {      // the eight softmax warps
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(B_ALL));
-      return spin(B_ALL, n_all++);
-    };
-    auto sync_half = [&]() -> bool {     // the four warps of this column half
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(B_G0 + half));
-      return spin(B_G0 + half, n_grp++);
-    };
+    auto sync_all = [] { asm volatile("bar.sync 3, 256;" ::: "memory"); };                          // the eight warps
+    auto sync_half = [&] { asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory"); };      // the column half's four
     int it = 0;
-    bool ok = true;
-    for (int u = u_begin; u < u_end && ok;) {
+#pragma unroll 1
+    for (int u = u_begin; u < u_end;) {
       const Piece pc = piece_at(u);
       u += pc.tiles;
       const int q0 = bd.q_indptr[pc.b], n_nodes = bd.q_indptr[pc.b + 1] - q0;
@@ -589,76 +715,98 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         sm->par[tid] = (int8_t)(up < -1 || up >= kMaxNodes ? -2 : up);
       }
       {
+        // Rows by warp, U at a time with the next U's loads under way.  The code runs once per piece: it is kept short,
+        // since its first run waits for its own instructions.
         constexpr int LPR = D / 8, RPW = 32 / LPR;      // lanes per row, rows per warp and load
-        constexpr int U = 6;
+        constexpr int U = 3, kStep = 8 * RPW * U;
         const int sub = lane / LPR, ch = lane % LPR;    // 8-value chunk of the row
         const int n_draft = has_draft ? n_nodes : 0;
         const int n_q = nc * 16, n_stage = n_q + 2 * n_draft;
+        const float inv_hpc = 1.0f / (float)hpc;
         if (has_draft) {
           // the ring slots of the draft tile, once their previous contents have been multiplied
-          ok = spin(B_KE + it % KS, it / KS + 1) && spin(B_VE + 2 * it % VS, 2 * it / VS + 1) &&
-               spin(B_VE + (2 * it + 1) % VS, (2 * it + 1) / VS + 1);
-          const int z_end = (n_nodes + 31) & ~31;       // V rows up to the 32-token step: zeros
-          for (int e = tid; e < (z_end - n_nodes) * (D / 16) * 2; e += 256) {
-            const int t = e / (z_end - n_nodes), r = n_nodes + e % (z_end - n_nodes);
-            const int h = t & 1, c16 = t >> 1;
-            *reinterpret_cast<uint4*>(sV + (2 * it + h) % VS * K::kHalf + (r >> 3) * K::kGroupBytes + (c16 >> 3) * 1024 +
-                                      (r & 7) * 128 + (((c16 & 7) ^ (r & 7)) << 4)) = make_uint4(0, 0, 0, 0);
+          spin(B_KE + it % KS, it / KS + 1);
+          spin(B_VE + 2 * it % VS, 2 * it / VS + 1);
+          spin(B_VE + (2 * it + 1) % VS, (2 * it + 1) / VS + 1);
+          const int n_zero = ((n_nodes + 31) & ~31) - n_nodes;       // V rows up to the 32-token step: zeros
+#pragma unroll 1
+          for (int e = tid; e < n_zero * (D / 16) * 2; e += 256) {
+            const int c16 = (e >> 1) % (D / 16), r = n_nodes + (e >> 1) / (D / 16);
+            *reinterpret_cast<uint4*>(sV + (2 * it + (e & 1)) % VS * K::kHalf + (r >> 3) * K::kGroupBytes +
+                                      (c16 >> 3) * 1024 + (r & 7) * 128 + (((c16 & 7) ^ (r & 7)) << 4)) =
+                make_uint4(0, 0, 0, 0);
           }
         }
-        for (int base = warp * RPW; base < n_stage; base += 8 * RPW * U) {
+        auto load = [&](int r) {
+          const __nv_bfloat16* src = nullptr;
+          if (r < n_q) {
+            const int node = __float2int_rz(((float)r + 0.5f) * inv_hpc);   // r / hpc, exact for r < 2^20
+            if (r < rows) src = p.q + (long long)(q0 + node) * p.q_stride + (head0 + r - node * hpc) * D;
+          } else if (r < n_stage) {
+            const bool is_v = r >= n_q + n_draft;
+            const long long t = q0 + r - n_q - (is_v ? n_draft : 0);
+            src = (is_v ? p.v_new + t * p.v_stride : p.k_new + t * p.k_stride) + pc.g * D;
+          }
+          return src != nullptr ? __ldg(reinterpret_cast<const uint4*>(src) + ch) : make_uint4(0, 0, 0, 0);
+        };
+        uint4 next[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i) next[i] = load(warp * RPW + sub + i * 8 * RPW);
+#pragma unroll 1
+        for (int base = warp * RPW; base < n_stage; base += kStep) {
           uint4 x[U];
 #pragma unroll
           for (int i = 0; i < U; ++i) {
-            const int r = base + i * 8 * RPW + sub;
-            const __nv_bfloat16* src = nullptr;
-            if (r < rows) src = p.q + (long long)(q0 + r / hpc) * p.q_stride + (head0 + r % hpc) * D;
-            else if (r >= n_q && r < n_q + n_draft) src = p.k_new + (long long)(q0 + r - n_q) * p.k_stride + pc.g * D;
-            else if (r >= n_q && r < n_stage) src = p.v_new + (long long)(q0 + r - n_q - n_draft) * p.v_stride + pc.g * D;
-            x[i] = src != nullptr ? __ldg(reinterpret_cast<const uint4*>(src) + ch) : make_uint4(0, 0, 0, 0);
+            x[i] = next[i];
+            next[i] = load(base + kStep + sub + i * 8 * RPW);
           }
 #pragma unroll
           for (int i = 0; i < U; ++i) {
             const int r = base + i * 8 * RPW + sub;
             uint32_t a = amax_bits(x[i]);
+            if (RPW == 1) {
+              a = __reduce_max_sync(0xffffffffu, a);
+            } else {
 #pragma unroll
-            for (int d = LPR / 2; d >= 1; d >>= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, d));
+              for (int d = LPR / 2; d >= 1; d >>= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, d));
+            }
             const bool wild = a >= 0x7f80u;             // a NaN or an infinity: zeros, and a NaN scale
             if (wild) { x[i] = make_uint4(0, 0, 0, 0); a = 0; }
             const int e = exp_of(a);
             uint2 hi, lo;
             split8(x[i], exp2i(-e), hi, lo);
             const float s = wild ? __int_as_float(0x7fc00000) : exp2i(e);
-            const uint32_t in_row = (uint32_t)((((ch >> 1) & 7) << 4) | ((ch & 1) << 3));   // before the swizzle
-            if (r < n_q) {
-              uint8_t* at = sQ + (ch >> 4) * NQ * 128 + r * 128 + (in_row ^ ((r & 7) << 4));
-              *reinterpret_cast<uint2*>(at) = hi;
-              *reinterpret_cast<uint2*>(at + K::kQTerm) = lo;
-              if (ch == 0) {
-                sm->f[r] = s * p.scale * (MOD && p.softcap > 0.f ? 2.f * kLog2e / p.softcap : kLog2e);
-                sm->m[r] = kNone;
-                if (MOD) sm->slope[r] = p.slopes != nullptr && r < rows ? p.slopes[head0 + r % hpc] * kLog2e : 0.f;
-              }
-            } else if (r < n_stage) {
-              const bool is_v = r >= n_q + n_draft;
-              const int t = r - n_q - (is_v ? n_draft : 0);
-              const uint32_t off = (uint32_t)((t >> 3) * K::kGroupBytes + (ch >> 4) * 1024 + (t & 7) * 128) + (in_row ^ ((t & 7) << 4));
-              uint8_t* d_hi = is_v ? sV + 2 * it % VS * K::kHalf : sK + it % KS * K::kTileBytes;
-              uint8_t* d_lo = is_v ? sV + (2 * it + 1) % VS * K::kHalf : d_hi + 8 * K::kGroupBytes;
-              *reinterpret_cast<uint2*>(d_hi + off) = hi;
-              *reinterpret_cast<uint2*>(d_lo + off) = lo;
-              if (ch == 0) (is_v ? sm->row_v : sm->row_k)[t] = s;
+            const bool is_q = r < n_q, is_v = r >= n_q + n_draft;
+            const int t = is_q ? r : r - n_q - (is_v ? n_draft : 0);
+            const uint32_t in_row = (uint32_t)(((((ch >> 1) ^ t) & 7) << 4) | ((ch & 1) << 3));   // swizzled
+            uint8_t* at = is_q ? sQ + (ch >> 4) * NQ * 128 + t * 128
+                               : (is_v ? sV + 2 * it % VS * K::kHalf : sK + it % KS * K::kTileBytes) +
+                                     (t >> 3) * K::kGroupBytes + (ch >> 4) * 1024 + (t & 7) * 128;
+            uint8_t* at_lo = is_q ? at + K::kQTerm
+                             : is_v ? at + (sV + (2 * it + 1) % VS * K::kHalf - (sV + 2 * it % VS * K::kHalf))
+                                    : at + 8 * K::kGroupBytes;
+            if (r < n_stage) {
+              *reinterpret_cast<uint2*>(at + in_row) = hi;
+              *reinterpret_cast<uint2*>(at_lo + in_row) = lo;
+              if (ch == 0) (is_q ? sm->f : is_v ? sm->row_v : sm->row_k)[t] = s;
             }
           }
         }
       }
       fence_async_smem();
-      if (!sync_all()) break;
+      sync_all();
+#pragma unroll 1
+      for (int q = tid; q < nc * 16; q += 256) {
+        sm->f[q] *= p.scale * (MOD && p.softcap > 0.f ? 2.f * kLog2e / p.softcap : kLog2e);
+        sm->m[q] = 0.f;     // no reference yet
+        if (MOD) sm->slope[q] = p.slopes != nullptr && q < rows ? p.slopes[head0 + q % hpc] * kLog2e : 0.f;
+      }
       // the tree: root paths and depths
       if (tid < n_nodes) {
         unsigned long long a = 1ull << tid;
         int d = 0;
         bool good = sm->par[tid] >= -1 && (tid > 0 || sm->par[0] == -1);
+#pragma unroll 1
         for (int v = tid; good && v > 0; ++d) {
           const int up = sm->par[v];
           good = up >= 0 && up < v;
@@ -674,10 +822,11 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         sm->depth[tid] = d;
         if (has_draft && sm->row_v[tid] != sm->row_v[tid]) sm->row_k[tid] = sm->row_v[tid];   // NaN: to the scores
       }
-      if (!sync_all()) break;
+      sync_all();
       if (MOD) {
+#pragma unroll 1
         for (int q = tid; q < nc * 16; q += 256) sm->dep[q] = q < rows ? (float)sm->depth[q / hpc] : 0.f;
-        if (!sync_all()) break;
+        sync_all();
       }
       if (tid == 0) {
         mbar_arrive(bar(B_Q));
@@ -695,6 +844,9 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         for (int e = 0; e < 8; ++e) sum[c][e] = make_float2(0.f, 0.f);
       const int lo_root = p.window > 0 ? pc.L - p.window + 1 : 0;
 
+      // Until a tile that every column sees something of has passed, columns may have no reference.
+      bool settled = false;
+#pragma unroll 1
       for (int i = 0; i < pc.tiles; ++i, ++it) {
         const bool draft = pc.first + i == 0;
         const int t0 = pc.base + (pc.first + i - 1) * kTile;
@@ -705,8 +857,7 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         if (draft) {
           if (row < n_nodes) { ks = sm->row_k[row]; vs = sm->row_v[row]; if (vs != vs) vs = 1.f; }
         } else {
-          ok = spin(B_SC + it % SC, it / SC);
-          if (!ok) break;
+          spin(B_SC + it % SC, it / SC);
           ks = sm->scale[it % SC][row >> 4];
           vs = sm->scale[it % SC][8 + (row >> 4)];
           if (band && t0 + row >= lo_root && t0 + row < min(pc.L, lo_root + kMaxNodes)) {
@@ -716,6 +867,7 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
               const uint4* src = reinterpret_cast<const uint4*>(
                   p.v_cache + (((size_t)pg * p.hkv + pc.g) * kPage + (t0 + row) % kPage) * D);
               uint32_t nan = 0;
+#pragma unroll 1
               for (int e = 0; e < D / 16; ++e) {
                 const uint4 v = __ldg(src + e);
                 nan |= __vcmpeq4(v.x & 0x7f7f7f7fu, 0x7f7f7f7fu) | __vcmpeq4(v.y & 0x7f7f7f7fu, 0x7f7f7f7fu) |
@@ -725,180 +877,153 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             }
           }
         }
-        // Which of this thread's columns see its token row: one bit per column of the half.
-        constexpr int VW = (HC * 16 + 31) / 32;
-        uint32_t vis[VW];
-#pragma unroll
-        for (int w = 0; w < VW; ++w) vis[w] = row < valid ? 0xffffffffu : 0u;
-        if (draft || band) {
-          const int pos = t0 + row;
-#pragma unroll
-          for (int w = 0; w < VW; ++w) {
-            uint32_t bits = 0u;
-#pragma unroll 1
-            for (int e = 0; e < 32; ++e) {
-              const int q = col0 + w * 32 + e;
-              if (w * 32 + e >= mine * 16) break;
-              const int dq = q < rows ? sm->depth[q / hpc] : 0;
-              bool see = true;
-              if (draft) {
-                const int node = q < rows ? q / hpc : 0;
-                see = row < n_nodes && ((sm->anc[node] >> row) & 1ull);
-                if (p.window > 0 && see) see = dq - sm->depth[row] < p.window;
-              } else {
-                see = pos >= lo_root + dq;
-              }
-              bits |= (see ? 1u : 0u) << e;
-            }
-            vis[w] &= bits;
-          }
-        }
-        const float rel = draft ? (row < n_nodes ? (float)sm->depth[row] : 0.f) : (float)(t0 + row - pc.L);
-        ok = spin(B_SF + it % NS, it / NS);
-        if (!ok) break;
+        const float lv = fast_log2(vs), vd = vs * kDown;
+        // ---- the scores of this token row, and S is free for the tile after the next
+        spin(B_SF + it % NS, it / NS);
         tc_fence_after();
-        const uint32_t s_addr = tmem + lane_addr + (it % NS) * NQ + col0;
-        uint32_t hi[HC][4], lo[HC][4];
-        // base-2 score of a column pair from the raw product
-        auto score2 = [&](float2 a, float2 f, int q) -> float2 {
-          float2 s = mul2(a, mul2(f, make_float2(ks, ks)));
-          if (MOD) {
-            if (p.softcap > 0.f) {
-              // c tanh(x / c) = c - 2 c / (1 + 2^(2 log2e x / c)); f holds the factor of the exponent
-              const float cl = p.softcap * kLog2e;
-              s.x = fmaf(-2.f * cl, fast_rcp(1.f + fast_exp2(s.x)), cl);
-              s.y = fmaf(-2.f * cl, fast_rcp(1.f + fast_exp2(s.y)), cl);
-            }
-            if (p.slopes != nullptr) {
-              s.x = fmaf(sm->slope[q], rel - sm->dep[q], s.x);
-              s.y = fmaf(sm->slope[q + 1], rel - sm->dep[q + 1], s.y);
-            }
-          }
-          return s;
-        };
-        uint32_t added = 0;      // chunks whose weights are in `sum` already
-        bool over = i == 0 || masked;
-        if (!over) {
-          // One pass with the reference as it stands.
+        float a[HC][16];
+        {
+          const uint32_t s_addr = tmem + lane_addr + (it % NS) * NQ + col0;
 #pragma unroll
-          for (int c = 0; c < HC; ++c) {
-            if (c < mine) {
-              float a[16];
-              tmem_ld16(s_addr + c * 16, a);
-              tmem_wait_ld();
-              const int q = col0 + c * 16;
-              float2 w[8];
-              float top = 0.f;
-              float2 e2[8];
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const float2 f = *reinterpret_cast<const float2*>(&sm->f[q + 2 * e]);
-                const float2 m = *reinterpret_cast<const float2*>(&sm->m[q + 2 * e]);
-                float2 d;
-                if (MOD) {
-                  const float2 s = score2(make_float2(a[2 * e], a[2 * e + 1]), f, q + 2 * e);
-                  d = make_float2(s.x - m.x, s.y - m.y);
-                } else {
-                  d = fma2(make_float2(a[2 * e], a[2 * e + 1]), mul2(f, make_float2(ks, ks)), make_float2(-m.x, -m.y));
-                }
-                e2[e] = make_float2(fast_exp2(d.x), fast_exp2(d.y));
-                w[e] = mul2(e2[e], make_float2(vs, vs));
-                top = fmaxf(top, fmaxf(w[e].x, w[e].y));
-              }
-              if (__any_sync(0xffffffffu, top > kTop)) {
-                over = true;
-              } else {
-                added |= 1u << c;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) sum[c][e] = add2(sum[c][e], e2[e]);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) split4(w[2 * k], w[2 * k + 1], hi[c][k], lo[c][k]);
-              }
-            }
-          }
-          if (lane == 0) sm->flag[half][it & 1][quarter] = over ? 1 : 0;
-          ok = sync_half();
-          if (!ok) break;
-          const int* fl = sm->flag[half][it & 1];
-          over = (fl[0] | fl[1] | fl[2] | fl[3]) != 0;
+          for (int c = 0; c < HC; ++c)
+            if (c < mine) tmem_ld16(s_addr + c * 16, a[c]);
+          tmem_wait_ld();
         }
-        if (over) {
-          // The exact maxima of this tile, new references and rescale factors, then the weights.
-          const float lv = fast_log2(vs);
-#pragma unroll
-          for (int c = 0; c < HC; ++c) {
-            if (c < mine) {
-              float a[16];
-              tmem_ld16(s_addr + c * 16, a);
-              tmem_wait_ld();
-              const int q = col0 + c * 16;
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const float2 s = score2(make_float2(a[2 * e], a[2 * e + 1]), *reinterpret_cast<const float2*>(&sm->f[q + 2 * e]), q + 2 * e);
-                const uint32_t v = vis[c / 2] >> ((c & 1) * 16 + 2 * e);
-                a[2 * e] = v & 1u ? s.x + lv : -INFINITY;
-                a[2 * e + 1] = v & 2u ? s.y + lv : -INFINITY;
-              }
-              const float mx = reduce16<true>(a, lane);
-              if (lane < 16) sm->red[quarter][q + lane] = mx;
-            }
-          }
-          ok = sync_half();
-          if (!ok) break;
-          const int q = col0 + quarter * 32 + lane;
-          if (quarter * 32 + lane < mine * 16) {
-            const float mt = fmaxf(fmaxf(sm->red[0][q], sm->red[1][q]), fmaxf(sm->red[2][q], sm->red[3][q]));
-            const float old = sm->m[q], now = fmaxf(old, mt - kHead);
-            sm->alpha[q] = fast_exp2(old - now);
-            sm->m[q] = now;
-          }
-          ok = sync_half();
-          if (!ok) break;
-#pragma unroll
-          for (int c = 0; c < HC; ++c) {
-            if (c < mine) {
-              float a[16];
-              tmem_ld16(s_addr + c * 16, a);
-              tmem_wait_ld();
-              const int qc = col0 + c * 16;
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                float2 w[2];
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                  const int e = 2 * k + h;
-                  const float2 s = score2(make_float2(a[2 * e], a[2 * e + 1]), *reinterpret_cast<const float2*>(&sm->f[qc + 2 * e]), qc + 2 * e);
-                  const float2 m = *reinterpret_cast<const float2*>(&sm->m[qc + 2 * e]);
-                  const float2 al = *reinterpret_cast<const float2*>(&sm->alpha[qc + 2 * e]);
-                  const uint32_t v = vis[c / 2] >> ((c & 1) * 16 + 2 * e);
-                  float2 ex;
-                  ex.x = v & 1u ? fast_exp2(s.x - m.x) : 0.f;
-                  ex.y = v & 2u ? fast_exp2(s.y - m.y) : 0.f;
-                  sum[c][e] = mul2(sum[c][e], al);
-                  if (!((added >> c) & 1u)) sum[c][e] = add2(sum[c][e], ex);
-                  w[h].x = v & 1u ? ex.x * vs : 0.f;
-                  w[h].y = v & 2u ? ex.y * vs : 0.f;
-                }
-                split4(w[0], w[1], hi[c][k], lo[c][k]);
-              }
-            }
-          }
-        }
-        // S is read
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(B_SE + it % NS));
-        // P and O belong to the previous tile's PV until it has finished
-        if (it > 0) {
-          ok = spin(B_OD, it - 1);
-          if (!ok) break;
+        // ---- exponents against the references as they stand (base 2), and the chunks where a weight would pass kTop
+        uint32_t missed = 0;
+        const float limit = 8.807354922f - lv;       // log2(kTop)
+        const float rel = draft ? (row < n_nodes ? (float)sm->depth[row] : 0.f) : (float)(t0 + row - pc.L);
+#pragma unroll
+        for (int c = 0; c < HC; ++c) {
+          if (c < mine) {
+            const int q = col0 + c * 16;
+            float top = -INFINITY;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float4 f = *reinterpret_cast<const float4*>(&sm->f[q + 4 * k]);
+              const float4 m = *reinterpret_cast<const float4*>(&sm->m[q + 4 * k]);
+              float* v = &a[c][4 * k];
+              const float2 kk = make_float2(ks, ks), f0 = mul2(make_float2(f.x, f.y), kk), f1 = mul2(make_float2(f.z, f.w), kk);
+              float2 d0, d1;
+              if (MOD) {
+                float s[4] = {v[0] * f0.x, v[1] * f0.y, v[2] * f1.x, v[3] * f1.y};
+                if (p.softcap > 0.f) {
+                  // c tanh(x / c) = c - 2 c / (1 + 2^(2 log2e x / c)); f holds the factor of the exponent
+                  const float cl = p.softcap * kLog2e;
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) s[e] = fmaf(-2.f * cl, fast_rcp(1.f + fast_exp2(s[e])), cl);
+                }
+                const float4 sl = *reinterpret_cast<const float4*>(&sm->slope[q + 4 * k]);
+                const float4 dp = *reinterpret_cast<const float4*>(&sm->dep[q + 4 * k]);
+                d0 = make_float2(fmaf(sl.x, rel - dp.x, s[0]) - m.x, fmaf(sl.y, rel - dp.y, s[1]) - m.y);
+                d1 = make_float2(fmaf(sl.z, rel - dp.z, s[2]) - m.z, fmaf(sl.w, rel - dp.w, s[3]) - m.w);
+              } else {
+                d0 = fma2(make_float2(v[0], v[1]), f0, make_float2(-m.x, -m.y));
+                d1 = fma2(make_float2(v[2], v[3]), f1, make_float2(-m.z, -m.w));
+              }
+              v[0] = d0.x; v[1] = d0.y; v[2] = d1.x; v[3] = d1.y;
+              top = fmaxf(fmaxf(top, fmaxf(d0.x, d0.y)), fmaxf(d1.x, d1.y));
+            }
+            missed |= __any_sync(0xffffffffu, top > limit) ? 1u << c : 0u;
+          }
         }
+        const uint32_t all = (1u << mine) - 1u;
+        if (masked) {
+          // Which columns see this row: one bit each.  Masked exponents are -inf whatever the product was.
+          constexpr int VW = (HC * 16 + 31) / 32;
+          uint32_t vis[VW];
+#pragma unroll
+          for (int w = 0; w < VW; ++w) vis[w] = row < valid && !draft && !band ? 0xffffffffu : 0u;
+          if (row < valid && (draft || band)) {
+            // node by node: a node's columns see this row, or none of them does
+#pragma unroll 1
+            for (int n = 0; n < n_nodes; ++n) {
+              const int dn = sm->depth[n];
+              const bool see = draft ? ((sm->anc[n] >> row) & 1ull) && (p.window <= 0 || dn - sm->depth[row] < p.window)
+                                     : t0 + row >= lo_root + dn;
+              if (see) {
+#pragma unroll
+                for (int w = 0; w < VW; ++w) vis[w] |= bit_range(n * hpc - col0 - w * 32, hpc);
+              }
+            }
+          }
+#pragma unroll
+          for (int c = 0; c < HC; ++c)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) a[c][e] = (vis[c / 2] >> ((c & 1) * 16 + e)) & 1u ? a[c][e] : -INFINITY;
+        }
+        // (The barrier also keeps red[] of this tile behind the last tile's readers.)
+        uint32_t todo = all;                          // chunks whose references move
+        if (lane == 0) sm->flag[half][it & 1][quarter] = (int)missed;
+        sync_half();
+        if (settled && !masked) {
+          const int4 fl = *reinterpret_cast<const int4*>(sm->flag[half][it & 1]);
+          todo = (uint32_t)(fl.x | fl.y | fl.z | fl.w);
+        }
+        settled = settled || draft || !band;
+        if (todo != 0u) {
+          // The exact maxima of these chunks' columns, new references (unset ones are 0, set ones never are),
+          // and the exponents and sums against them.
+#pragma unroll
+          for (int c = 0; c < HC; ++c) {
+            if ((todo >> c) & 1u) {
+              const float mx = warp_max16(a[c], lv, lane);
+              if (lane < 16) sm->red[quarter][col0 + c * 16 + lane] = mx;
+            }
+          }
+          sync_half();
+          const int mine_col = quarter * 32 + lane, q = col0 + mine_col;
+          if (mine_col < mine * 16 && ((todo >> (mine_col >> 4)) & 1u)) {
+            const float old = sm->m[q];
+            const float mt = old + fmaxf(fmaxf(sm->red[0][q], sm->red[1][q]), fmaxf(sm->red[2][q], sm->red[3][q])) - kHead;
+            float now = mt == -INFINITY ? old : old == 0.f ? mt : fmaxf(old, mt);
+            if (now == 0.f && mt != -INFINITY) now = 1e-30f;
+            sm->alpha[q] = old == 0.f ? 1.f : fast_exp2(old - now);
+            sm->m[q] = now;
+            sm->red[0][q] = old - now;
+          }
+          sync_half();
+#pragma unroll
+          for (int c = 0; c < HC; ++c) {
+            if ((todo >> c) & 1u) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const float2 al = *reinterpret_cast<const float2*>(&sm->alpha[col0 + c * 16 + 2 * e]);
+                const float2 dl = *reinterpret_cast<const float2*>(&sm->red[0][col0 + c * 16 + 2 * e]);
+                sum[c][e] = mul2(sum[c][e], al);
+                a[c][2 * e] += dl.x;
+                a[c][2 * e + 1] += dl.y;
+              }
+            }
+          }
+        }
+        // ---- the weights
+        uint32_t hi[HC][4], lo[HC][4];
+#pragma unroll
+        for (int c = 0; c < HC; ++c) {
+          if (c < mine) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float2 e0 = make_float2(fast_exp2(a[c][4 * k]), fast_exp2(a[c][4 * k + 1]));
+              const float2 e1 = make_float2(fast_exp2(a[c][4 * k + 2]), fast_exp2(a[c][4 * k + 3]));
+              sum[c][2 * k] = add2(sum[c][2 * k], e0);
+              sum[c][2 * k + 1] = add2(sum[c][2 * k + 1], e1);
+              split4(mul2(e0, make_float2(vd, vd)), mul2(e1, make_float2(vd, vd)), hi[c][k], lo[c][k]);
+            }
+          }
+        }
+        // P and O belong to the previous tile's PV until it has finished
+        if (it > 0) spin(B_OD, it - 1);
         tc_fence_after();
-        if (over && i > 0) {
+        if (todo != 0u && i > 0) {
 #pragma unroll 1
-          for (int mb = 0; mb < MH; ++mb) {
+          for (int c = 0; c < mine; ++c) {
+            if (!((todo >> c) & 1u)) continue;
 #pragma unroll 1
-            for (int c = 0; c < mine; ++c) {
+            for (int mb = 0; mb < MH; ++mb) {
               float v[16];
               const uint32_t ad = tmem + lane_addr + kColO + mb * NQ + col0 + c * 16;
               tmem_ld16(ad, v);
@@ -923,22 +1048,22 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(B_PF));
       }
-      if (!ok) break;
 
       // ---------------------------------------------------------- results
       // Column sums over the tile's 128 token rows: the lanes, then the quarters.
+      sync_half();      // the last tile's readers of red[] are done
 #pragma unroll
       for (int c = 0; c < HC; ++c) {
         if (c < mine) {
           float v[16];
 #pragma unroll
           for (int e = 0; e < 8; ++e) { v[2 * e] = sum[c][e].x; v[2 * e + 1] = sum[c][e].y; }
-          const float s = reduce16<false>(v, lane);
+          const float s = warp_sum16(v, lane);
           if (lane < 16) sm->red[quarter][col0 + c * 16 + lane] = s;
         }
       }
-      ok = sync_half() && spin(B_OD, it - 1);
-      if (!ok) break;
+      sync_half();
+      spin(B_OD, it - 1);
       tc_fence_after();
       const size_t slot = (size_t)blockIdx.x + pc.seg;      // rises by at least one along the pieces: unique
       {
@@ -946,47 +1071,52 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         if (quarter * 32 + lane < mine * 16) {
           const float l = sm->red[0][q] + sm->red[1][q] + sm->red[2][q] + sm->red[3][q];
           sm->alpha[q] = l == 0.f ? 0.f : 1.f / l;
+          // the column's output row; the score factors are not needed any more
+          int* out_row = reinterpret_cast<int*>(sm->f);
+          out_row[q] = -1;
           if (q < rows) {
+            const int node = q / hpc, at = (q0 + node) * p.hq + head0 + q - node * hpc;
+            out_row[q] = pc.whole ? at : q;
             const float lse2 = l == 0.f ? -INFINITY : sm->m[q] + fast_log2(l);
             if (!pc.whole) p.lse_part[slot * NQ + q] = lse2;
-            else if (p.lse != nullptr) p.lse[(size_t)(q0 + q / hpc) * p.hq + head0 + q % hpc] = lse2 * kLn2;
+            else if (p.lse != nullptr) p.lse[at] = lse2 * kLn2;
           }
         }
       }
-      ok = sync_half();
-      if (!ok) break;
+      sync_half();
       const bool odd = lane & 1;
+      __nv_bfloat16* dst = (pc.whole ? p.out : p.o_part + slot * NQ * D) + (row & ~1);
 #pragma unroll 1
       for (int c = 0; c < mine; ++c) {
+        float v[MH][16];
 #pragma unroll
-        for (int mb = 0; mb < MH; ++mb) {
-          float v[16];
-          tmem_ld16(tmem + lane_addr + kColO + mb * NQ + col0 + c * 16, v);
-          tmem_wait_ld();
+        for (int mb = 0; mb < MH; ++mb) tmem_ld16(tmem + lane_addr + kColO + mb * NQ + col0 + c * 16, v[mb]);
+        tmem_wait_ld();
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const int qe = col0 + c * 16 + 2 * k;
-            const float ev = v[2 * k] * sm->alpha[qe], od = v[2 * k + 1] * sm->alpha[qe + 1];
+        for (int k = 0; k < 8; ++k) {
+          const int qe = col0 + c * 16 + 2 * k;
+          const float2 inv = *reinterpret_cast<const float2*>(&sm->alpha[qe]);
+          const int2 at = *reinterpret_cast<const int2*>(&sm->f[qe]);
+          const int r = odd ? at.y : at.x;
+#pragma unroll
+          for (int mb = 0; mb < MH; ++mb) {
+            const float ev = v[mb][2 * k] * inv.x, od = v[mb][2 * k + 1] * inv.y;
             // even lanes keep the even column and take the odd lane's dim of it; odd lanes the reverse
             const float got = __shfl_xor_sync(0xffffffffu, odd ? ev : od, 1);
             const __nv_bfloat162 h = __floats2bfloat162_rn(odd ? got : ev, odd ? od : got);
-            const int q = qe + (odd ? 1 : 0);
-            if (q < rows) {
-              __nv_bfloat16* dst = pc.whole ? p.out + ((size_t)(q0 + q / hpc) * p.hq + head0 + q % hpc) * D
-                                            : p.o_part + (slot * NQ + q) * D;
-              *reinterpret_cast<__nv_bfloat162*>(dst + mb * 128 + (row & ~1)) = h;
-            }
+            if (r >= 0) *reinterpret_cast<__nv_bfloat162*>(dst + (size_t)r * D + mb * 128) = h;
           }
         }
       }
       tc_fence_before();
       // every warp is done with the columns' arrays and O before the next piece is staged
-      ok = sync_all();
+      sync_all();
       tc_fence_after();
     }
   }
   tc_fence_before();
   __syncthreads();
+  if (tid == 0 && sm->abort) report(p.dev_status, SD_DEV_TIMEOUT);
   if (warp == kWarpQK) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(K::kTmem));
