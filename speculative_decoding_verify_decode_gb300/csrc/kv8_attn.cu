@@ -156,30 +156,29 @@ Layout layout_of(const Kv8Plan& pl, int hkv, int dim, const BatchDesc& bd, int s
 }  // namespace
 
 // Query columns of a CTA: as many heads of a KV group as fit, so that the cache is read as few times as can be.
-Kv8Plan kv8_plan(int group, int max_nodes, bool mod) {
-  const int most = mod ? 128 : 144;
+Kv8Plan kv8_plan(int group, int max_nodes, int dim, bool mod) {
+  const int most = mod && dim == 256 ? 128 : 144;
   Kv8Plan pl;
   pl.hparts = 1;
   while ((group + pl.hparts - 1) / pl.hparts * max_nodes > most) ++pl.hparts;
   pl.hpc = (group + pl.hparts - 1) / pl.hparts;
   pl.hparts = (group + pl.hpc - 1) / pl.hpc;
   const int cols = pl.hpc * max_nodes;
-  pl.hc = cols <= 32 ? 1 : cols <= 64 ? 2 : cols <= 96 ? 3 : mod ? 4 : 5;
-  pl.nq = pl.hc == 5 ? 144 : 32 * pl.hc;
+  pl.nq = cols <= 16 ? 16 : cols <= 48 ? 48 : cols <= 96 ? 96 : most;
   return pl;
 }
 
 size_t kv8_attn_workspace(int hq, int hkv, int dim, const BatchDesc& bd) {
   // the query does not know whether scores will be capped or biased
   const int sms = sm_count();
-  const size_t a = layout_of(kv8_plan(hq / hkv, bd.max_nodes, false), hkv, dim, bd, sms).total;
-  const size_t b = layout_of(kv8_plan(hq / hkv, bd.max_nodes, true), hkv, dim, bd, sms).total;
+  const size_t a = layout_of(kv8_plan(hq / hkv, bd.max_nodes, dim, false), hkv, dim, bd, sms).total;
+  const size_t b = layout_of(kv8_plan(hq / hkv, bd.max_nodes, dim, true), hkv, dim, bd, sms).total;
   return a > b ? a : b;
 }
 
 cudaError_t launch_kv8_attn(Kv8AttnParams p, const BatchDesc& bd, cudaStream_t st) {
   const bool mod = p.softcap > 0.f || p.slopes != nullptr;
-  const Kv8Plan pl = kv8_plan(p.group, bd.max_nodes, mod);
+  const Kv8Plan pl = kv8_plan(p.group, bd.max_nodes, p.dim, mod);
   p.hpc = pl.hpc;
   p.hparts = pl.hparts;
   p.nq = pl.nq;
@@ -191,8 +190,8 @@ cudaError_t launch_kv8_attn(Kv8AttnParams p, const BatchDesc& bd, cudaStream_t s
   p.lse_part = reinterpret_cast<float*>(ws + l.lse);
   CUtensorMap mk, mv;
   if (!page_map(&mk, p.k_cache, p) || !page_map(&mv, p.v_cache, p)) return cudaErrorInvalidValue;
-  cudaError_t e = p.dim == 256 ? (mod ? launch_kv8_256_mod(mk, mv, p, bd, pl.hc, st) : launch_kv8_256(mk, mv, p, bd, pl.hc, st))
-                               : (mod ? launch_kv8_128_mod(mk, mv, p, bd, pl.hc, st) : launch_kv8_128(mk, mv, p, bd, pl.hc, st));
+  cudaError_t e = p.dim == 256 ? (mod ? launch_kv8_256_mod(mk, mv, p, bd, st) : launch_kv8_256(mk, mv, p, bd, st))
+                               : (mod ? launch_kv8_128_mod(mk, mv, p, bd, st) : launch_kv8_128(mk, mv, p, bd, st));
   if (e != cudaSuccess) return e;
   const dim3 grid(bd.total_nodes, p.hq);
   cudaLaunchConfig_t cfg = {};

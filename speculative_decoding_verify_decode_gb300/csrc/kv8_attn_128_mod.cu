@@ -5,9 +5,9 @@
 
 namespace sdv {
 
-cudaError_t launch_kv8_128_mod(const CUtensorMap& mk, const CUtensorMap& mv, const Kv8AttnParams& p, const BatchDesc& bd, int hc,
+cudaError_t launch_kv8_128_mod(const CUtensorMap& mk, const CUtensorMap& mv, const Kv8AttnParams& p, const BatchDesc& bd,
                            cudaStream_t st) {
-  return launch_kv8_kind(mk, mv, p, bd, hc, st);
+  return launch_kv8_kind(mk, mv, p, bd, st);
 }
 
 }  // namespace sdv

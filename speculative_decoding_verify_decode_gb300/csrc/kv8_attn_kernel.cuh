@@ -37,9 +37,10 @@
 // Per tile (tokens are the MMA's M; NQ columns):
 //   S[128 tok][NQ]     = K_tile . (Qhi + Qlo)^T      K-major, K = 32 a step
 //   O^T[D][NQ]        += V_tile^T . (Phi + Plo)^T    M = 128 dims a product, MN-major
-// Warps: 0-7 softmax (lane quarter = warp % 4, column half = warp / 4; thread =
-// token row), which also stage Q and the draft block and write the results; 8
-// loads K and the block scales, 9 loads V, 10 issues QK, 11 issues PV.
+// Warps: NG groups of four softmax warps (lane quarter = warp % 4, a share of the
+// columns per group; thread = token row), which also stage Q and the draft block
+// and write the results; then one warp each that loads K and the block scales,
+// loads V, issues QK, issues PV.
 // Every wait on a barrier is bounded; on expiry the kernel reports
 // SD_DEV_TIMEOUT and runs out.
 #pragma once
@@ -54,8 +55,6 @@
 namespace sdv {
 namespace {
 
-constexpr int kKvThreads = 384;
-constexpr int kWarpK = 8, kWarpV = 9, kWarpQK = 10, kWarpPV = 11;
 constexpr int kTile = kTileTokens;
 constexpr float kHead = 5.0f;          // the largest weight sits at 2^5 when m is exact
 constexpr float kTop = 448.0f;         // weights beyond it move m
@@ -83,15 +82,17 @@ struct KvSmall {
   int scan[8];
   int8_t par[kMaxNodes];
   int8_t depth[kMaxNodes];
-  alignas(16) int flag[2][2][4];   // [column half][tile parity][lane quarter]: chunks where a weight passes kTop
+  alignas(16) int flag[3][2][4];   // [group][tile parity][lane quarter]: chunks where a weight passes kTop
   uint32_t tmem;
   int abort;
 };
 
-template <int D, int HC, bool MOD>
+// D: head dim.  NG groups of softmax warps, of up to CC 16-column chunks each.  MOD: capped scores or a distance bias.
+template <int D, int NG, int CC, bool MOD>
 struct Kv {
-  using Small = KvSmall<HC == 5 ? 144 : 32 * HC, MOD, HC == 5 && D == 256>;
-  static constexpr int NQ = HC == 5 ? 144 : 32 * HC;      // query columns
+  static constexpr int NQ = NG * CC * 16 == 144 && MOD && D == 256 ? 128 : NG * CC * 16;   // query columns
+  static constexpr int kWarps = NG * 4, kThreads = (kWarps + 4) * 32;
+  using Small = KvSmall<NQ, MOD, NQ == 144 && D == 256>;
   static constexpr int MH = D / 128;                      // 128-dim blocks
   static constexpr int NS = (2 + MH) * NQ <= 512 ? 2 : 1; // S buffers in tensor memory
   static constexpr int kCols = (NS + MH) * NQ;
@@ -276,16 +277,18 @@ struct Piece {
   bool whole;          // the segment lies in this piece alone
 };
 
-template <int D, int HC, bool MOD>
-__global__ void __launch_bounds__(kKvThreads, 1)
+template <int D, int NG, int CC, bool MOD>
+__global__ void __launch_bounds__((NG + 1) * 128, 1)
 kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                 const Kv8AttnParams p, const BatchDesc bd) {
-  using K = Kv<D, HC, MOD>;
+  using K = Kv<D, NG, CC, MOD>;
   constexpr int NQ = K::NQ, MH = K::MH, NS = K::NS, KS = K::KS, VS = K::VS;
+  constexpr int kWarps = K::kWarps, kKvThreads = K::kThreads;      // softmax warps; all threads
+  constexpr int kWarpK = kWarps, kWarpV = kWarps + 1, kWarpQK = kWarps + 2;
   using Sm = typename K::Small;
   constexpr int B_KF = 0, B_KE = KS, B_VF = 2 * KS, B_VE = B_VF + VS, B_SC = B_VE + VS, B_SF = B_SC + KS + NS,
-                B_SE = B_SF + NS, B_PF = B_SE + NS, B_OD = B_PF + 1, B_Q = B_PF + 2;
-  constexpr int kNumBars = B_Q + 1;
+                B_SE = B_SF + NS, B_PF = B_SE + NS, B_OD = B_PF + 1, B_Q = B_PF + 2, B_G = B_PF + 3;
+  constexpr int kNumBars = B_G + NG;
   static_assert(kNumBars <= Sm::kBars, "barriers");
   constexpr int SC = KS + NS;   // scale stages: see the K producer
   extern __shared__ __align__(1024) uint8_t smem8[];
@@ -309,7 +312,7 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
   if (tid == 0) {
 #pragma unroll 1
     for (int i = 0; i < kNumBars; ++i)
-      mbar_init(smem_u32(&sm->bar[i]), i == B_PF || (i >= B_SE && i < B_SE + NS) ? 8u : 1u);
+      mbar_init(smem_u32(&sm->bar[i]), i == B_PF || (i >= B_SE && i < B_SE + NS) ? (uint32_t)kWarps : i >= B_G ? 4u : 1u);
     sm->abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -405,10 +408,11 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
   auto wait_full = [&](int first, const Ring& r) { return wait(first + r.at, (int)r.round); };
   auto wait_empty = [&](int first, const Ring& r) { return wait(first + r.at, (int)r.round ^ 1); };
 
-  // The softmax warps of the wide tiles need more registers than an even share: 2 x 208 + 88 per thread triple is what
-  // the block was launched with (3 x 168).
-  if (warp >= 8) {
-    if (HC >= 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+  // The softmax warps of the wider tiles need more registers than an even share: 3 x 144 + 80 is what the block was
+  // launched with (4 x 128 per warp).
+  constexpr bool kShare = CC >= 2;
+  if (warp >= kWarps) {
+    if (kShare) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
     if (warp <= kWarpV) {
       // ---------------------------------------------------------- producers
       // Page ids come a group of four tiles at a time (lane l: page l % 8 of the group's tile l / 8), two groups ahead of
@@ -690,12 +694,13 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     }
   } else {
     // ------------------------------------------------------------ softmax warps
-    if (HC >= 4) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-    const int half = warp >> 2, quarter = warp & 3;
+    if (kShare) asm volatile("setmaxnreg.inc.sync.aligned.u32 144;");
+    const int group = warp >> 2, quarter = warp & 3;
     const int row = quarter * 32 + lane;                       // token row of S; dim (mod 128) of O^T
     const uint32_t lane_addr = (uint32_t)(quarter * 32) << 16;
-    auto sync_all = [] { asm volatile("bar.sync 3, 256;" ::: "memory"); };                          // the eight warps
-    auto sync_half = [&] { asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory"); };      // the column half's four
+    auto sync_all = [] { asm volatile("bar.sync 7, %0;" ::"n"(kWarps * 32) : "memory"); };        // the softmax warps
+    auto sync_group = [&] { asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory"); };     // the group's four
+    Ring s_ring, sc_ring;
     int it = 0;
 #pragma unroll 1
     for (int u = u_begin; u < u_end;) {
@@ -705,7 +710,8 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
       const int hpc = min(p.hpc, p.group - pc.c * p.hpc);
       const int head0 = pc.g * p.group + pc.c * p.hpc;
       const int rows = hpc * n_nodes, nc = (rows + 15) / 16;
-      const int c_first = half ? (nc + 1) / 2 : 0, mine = half ? nc / 2 : (nc + 1) / 2;   // 16-column chunks
+      const int mine = nc / NG + (group < nc % NG ? 1 : 0);                       // 16-column chunks of this group
+      const int c_first = group * (nc / NG) + min(group, nc % NG);
       const int col0 = c_first * 16;
       const bool has_draft = pc.first == 0;
       // ---------------------------------------------------------- staging: Q, the tree, the draft block
@@ -718,7 +724,7 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         // Rows by warp, U at a time with the next U's loads under way.  The code runs once per piece: it is kept short,
         // since its first run waits for its own instructions.
         constexpr int LPR = D / 8, RPW = 32 / LPR;      // lanes per row, rows per warp and load
-        constexpr int U = 3, kStep = 8 * RPW * U;
+        constexpr int U = 3, kStep = kWarps * RPW * U;
         const int sub = lane / LPR, ch = lane % LPR;    // 8-value chunk of the row
         const int n_draft = has_draft ? n_nodes : 0;
         const int n_q = nc * 16, n_stage = n_q + 2 * n_draft;
@@ -730,7 +736,7 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
           spin(B_VE + (2 * it + 1) % VS, (2 * it + 1) / VS + 1);
           const int n_zero = ((n_nodes + 31) & ~31) - n_nodes;       // V rows up to the 32-token step: zeros
 #pragma unroll 1
-          for (int e = tid; e < n_zero * (D / 16) * 2; e += 256) {
+          for (int e = tid; e < n_zero * (D / 16) * 2; e += kWarps * 32) {
             const int c16 = (e >> 1) % (D / 16), r = n_nodes + (e >> 1) / (D / 16);
             *reinterpret_cast<uint4*>(sV + (2 * it + (e & 1)) % VS * K::kHalf + (r >> 3) * K::kGroupBytes +
                                       (c16 >> 3) * 1024 + (r & 7) * 128 + (((c16 & 7) ^ (r & 7)) << 4)) =
@@ -751,18 +757,18 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         };
         uint4 next[U];
 #pragma unroll
-        for (int i = 0; i < U; ++i) next[i] = load(warp * RPW + sub + i * 8 * RPW);
+        for (int i = 0; i < U; ++i) next[i] = load(warp * RPW + sub + i * kWarps * RPW);
 #pragma unroll 1
         for (int base = warp * RPW; base < n_stage; base += kStep) {
           uint4 x[U];
 #pragma unroll
           for (int i = 0; i < U; ++i) {
             x[i] = next[i];
-            next[i] = load(base + kStep + sub + i * 8 * RPW);
+            next[i] = load(base + kStep + sub + i * kWarps * RPW);
           }
 #pragma unroll
           for (int i = 0; i < U; ++i) {
-            const int r = base + i * 8 * RPW + sub;
+            const int r = base + i * kWarps * RPW + sub;
             uint32_t a = amax_bits(x[i]);
             if (RPW == 1) {
               a = __reduce_max_sync(0xffffffffu, a);
@@ -796,7 +802,7 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
       fence_async_smem();
       sync_all();
 #pragma unroll 1
-      for (int q = tid; q < nc * 16; q += 256) {
+      for (int q = tid; q < nc * 16; q += kWarps * 32) {
         sm->f[q] *= p.scale * (MOD && p.softcap > 0.f ? 2.f * kLog2e / p.softcap : kLog2e);
         sm->m[q] = 0.f;     // no reference yet
         if (MOD) sm->slope[q] = p.slopes != nullptr && q < rows ? p.slopes[head0 + q % hpc] * kLog2e : 0.f;
@@ -825,7 +831,7 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
       sync_all();
       if (MOD) {
 #pragma unroll 1
-        for (int q = tid; q < nc * 16; q += 256) sm->dep[q] = q < rows ? (float)sm->depth[q / hpc] : 0.f;
+        for (int q = tid; q < nc * 16; q += kWarps * 32) sm->dep[q] = q < rows ? (float)sm->depth[q / hpc] : 0.f;
         sync_all();
       }
       if (tid == 0) {
@@ -837,9 +843,9 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         }
       }
 
-      float2 sum[HC][8];
+      float2 sum[CC][8];
 #pragma unroll
-      for (int c = 0; c < HC; ++c)
+      for (int c = 0; c < CC; ++c)
 #pragma unroll
         for (int e = 0; e < 8; ++e) sum[c][e] = make_float2(0.f, 0.f);
       const int lo_root = p.window > 0 ? pc.L - p.window + 1 : 0;
@@ -857,9 +863,10 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         if (draft) {
           if (row < n_nodes) { ks = sm->row_k[row]; vs = sm->row_v[row]; if (vs != vs) vs = 1.f; }
         } else {
-          spin(B_SC + it % SC, it / SC);
-          ks = sm->scale[it % SC][row >> 4];
-          vs = sm->scale[it % SC][8 + (row >> 4)];
+          wait_full(B_SC, sc_ring);
+          __syncwarp();
+          ks = sm->scale[sc_ring.at][row >> 4];
+          vs = sm->scale[sc_ring.at][8 + (row >> 4)];
           if (band && t0 + row >= lo_root && t0 + row < min(pc.L, lo_root + kMaxNodes)) {
             // a token that a window may hide from some nodes: its NaN codes of V become NaN scores
             const int pg = p.page_table[(size_t)pc.b * p.max_pages + (t0 + row) / kPage];
@@ -877,27 +884,30 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             }
           }
         }
+        sc_ring.next(SC);
         const float lv = fast_log2(vs), vd = vs * kDown;
         // ---- the scores of this token row, and S is free for the tile after the next
-        spin(B_SF + it % NS, it / NS);
+        wait_full(B_SF, s_ring);
+        __syncwarp();
         tc_fence_after();
-        float a[HC][16];
+        float a[CC][16];
         {
-          const uint32_t s_addr = tmem + lane_addr + (it % NS) * NQ + col0;
+          const uint32_t s_addr = tmem + lane_addr + s_ring.at * NQ + col0;
 #pragma unroll
-          for (int c = 0; c < HC; ++c)
+          for (int c = 0; c < CC; ++c)
             if (c < mine) tmem_ld16(s_addr + c * 16, a[c]);
           tmem_wait_ld();
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(B_SE + it % NS));
+        if (lane == 0) mbar_arrive(bar(B_SE + s_ring.at));
+        s_ring.next(NS);
         // ---- exponents against the references as they stand (base 2), and the chunks where a weight would pass kTop
         uint32_t missed = 0;
         const float limit = 8.807354922f - lv;       // log2(kTop)
         const float rel = draft ? (row < n_nodes ? (float)sm->depth[row] : 0.f) : (float)(t0 + row - pc.L);
 #pragma unroll
-        for (int c = 0; c < HC; ++c) {
+        for (int c = 0; c < CC; ++c) {
           if (c < mine) {
             const int q = col0 + c * 16;
             float top = -INFINITY;
@@ -933,7 +943,7 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         const uint32_t all = (1u << mine) - 1u;
         if (masked) {
           // Which columns see this row: one bit each.  Masked exponents are -inf whatever the product was.
-          constexpr int VW = (HC * 16 + 31) / 32;
+          constexpr int VW = (CC * 16 + 31) / 32;
           uint32_t vis[VW];
 #pragma unroll
           for (int w = 0; w < VW; ++w) vis[w] = row < valid && !draft && !band ? 0xffffffffu : 0u;
@@ -951,30 +961,49 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             }
           }
 #pragma unroll
-          for (int c = 0; c < HC; ++c)
+          for (int c = 0; c < CC; ++c)
 #pragma unroll
             for (int e = 0; e < 16; ++e) a[c][e] = (vis[c / 2] >> ((c & 1) * 16 + e)) & 1u ? a[c][e] : -INFINITY;
         }
-        // (The barrier also keeps red[] of this tile behind the last tile's readers.)
-        uint32_t todo = all;                          // chunks whose references move
-        if (lane == 0) sm->flag[half][it & 1][quarter] = (int)missed;
-        sync_half();
-        if (settled && !masked) {
-          const int4 fl = *reinterpret_cast<const int4*>(sm->flag[half][it & 1]);
-          todo = (uint32_t)(fl.x | fl.y | fl.z | fl.w);
+        // ---- the weights, on the assumption that no warp of the group has to move a reference; what they need to know
+        // of each other is under way meanwhile.  (The barrier also keeps red[] of this tile behind the last one's readers.)
+        uint32_t hi[CC][4], lo[CC][4];
+        auto weigh = [&](int c, float add) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float2 e0 = make_float2(fast_exp2(a[c][4 * k]), fast_exp2(a[c][4 * k + 1]));
+            const float2 e1 = make_float2(fast_exp2(a[c][4 * k + 2]), fast_exp2(a[c][4 * k + 3]));
+            sum[c][2 * k] = fma2(e0, make_float2(add, add), sum[c][2 * k]);
+            sum[c][2 * k + 1] = fma2(e1, make_float2(add, add), sum[c][2 * k + 1]);
+            split4(mul2(e0, make_float2(vd, vd)), mul2(e1, make_float2(vd, vd)), hi[c][k], lo[c][k]);
+          }
+        };
+        const bool plain = settled && !masked;
+        if (!plain) missed = all;
+        if (lane == 0) {
+          sm->flag[group][it & 1][quarter] = (int)missed;
+          mbar_arrive(bar(B_G + group));
+        }
+        if (plain) {
+#pragma unroll
+          for (int c = 0; c < CC; ++c)
+            if (c < mine && !((missed >> c) & 1u)) weigh(c, 1.f);
         }
         settled = settled || draft || !band;
+        spin(B_G + group, it);
+        const int4 fl = *reinterpret_cast<const int4*>(sm->flag[group][it & 1]);
+        const uint32_t todo = (uint32_t)(fl.x | fl.y | fl.z | fl.w);     // chunks whose references move
         if (todo != 0u) {
           // The exact maxima of these chunks' columns, new references (unset ones are 0, set ones never are),
-          // and the exponents and sums against them.
+          // and the weights and sums against them.
 #pragma unroll
-          for (int c = 0; c < HC; ++c) {
+          for (int c = 0; c < CC; ++c) {
             if ((todo >> c) & 1u) {
               const float mx = warp_max16(a[c], lv, lane);
               if (lane < 16) sm->red[quarter][col0 + c * 16 + lane] = mx;
             }
           }
-          sync_half();
+          sync_group();
           const int mine_col = quarter * 32 + lane, q = col0 + mine_col;
           if (mine_col < mine * 16 && ((todo >> (mine_col >> 4)) & 1u)) {
             const float old = sm->m[q];
@@ -985,9 +1014,9 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             sm->m[q] = now;
             sm->red[0][q] = old - now;
           }
-          sync_half();
+          sync_group();
 #pragma unroll
-          for (int c = 0; c < HC; ++c) {
+          for (int c = 0; c < CC; ++c) {
             if ((todo >> c) & 1u) {
 #pragma unroll
               for (int e = 0; e < 8; ++e) {
@@ -997,21 +1026,7 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                 a[c][2 * e] += dl.x;
                 a[c][2 * e + 1] += dl.y;
               }
-            }
-          }
-        }
-        // ---- the weights
-        uint32_t hi[HC][4], lo[HC][4];
-#pragma unroll
-        for (int c = 0; c < HC; ++c) {
-          if (c < mine) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const float2 e0 = make_float2(fast_exp2(a[c][4 * k]), fast_exp2(a[c][4 * k + 1]));
-              const float2 e1 = make_float2(fast_exp2(a[c][4 * k + 2]), fast_exp2(a[c][4 * k + 3]));
-              sum[c][2 * k] = add2(sum[c][2 * k], e0);
-              sum[c][2 * k + 1] = add2(sum[c][2 * k + 1], e1);
-              split4(mul2(e0, make_float2(vd, vd)), mul2(e1, make_float2(vd, vd)), hi[c][k], lo[c][k]);
+              weigh(c, (missed >> c) & 1u ? 1.f : 0.f);     // 0: this tile's weights are in the sum
             }
           }
         }
@@ -1036,7 +1051,7 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
           tmem_wait_st();
         }
 #pragma unroll
-        for (int c = 0; c < HC; ++c) {
+        for (int c = 0; c < CC; ++c) {
           if (c < mine) {
             uint8_t* at = sP + (c_first + c) * kTile * 16 + row * 16;
             *reinterpret_cast<uint4*>(at) = make_uint4(hi[c][0], hi[c][1], hi[c][2], hi[c][3]);
@@ -1051,9 +1066,9 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
 
       // ---------------------------------------------------------- results
       // Column sums over the tile's 128 token rows: the lanes, then the quarters.
-      sync_half();      // the last tile's readers of red[] are done
+      sync_group();      // the last tile's readers of red[] are done
 #pragma unroll
-      for (int c = 0; c < HC; ++c) {
+      for (int c = 0; c < CC; ++c) {
         if (c < mine) {
           float v[16];
 #pragma unroll
@@ -1062,7 +1077,7 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
           if (lane < 16) sm->red[quarter][col0 + c * 16 + lane] = s;
         }
       }
-      sync_half();
+      sync_group();
       spin(B_OD, it - 1);
       tc_fence_after();
       const size_t slot = (size_t)blockIdx.x + pc.seg;      // rises by at least one along the pieces: unique
@@ -1083,7 +1098,7 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
           }
         }
       }
-      sync_half();
+      sync_group();
       const bool odd = lane & 1;
       __nv_bfloat16* dst = (pc.whole ? p.out : p.o_part + slot * NQ * D) + (row & ~1);
 #pragma unroll 1
