@@ -226,7 +226,7 @@ struct Kv8AttnParams {
   int group;                 // query heads per KV head
   // filled in by the launch: the plan and the workspace's parts
   int hpc, hparts, nq, grid;
-  int* cum;                  // [batch + 1] first unit of each sequence (written for the merge)
+  int* cum;                  // [kMaxBatch + 3] first unit of each sequence, then the plan (written for the merge)
   __nv_bfloat16* o_part;     // [piece + segment][nq][dim] partial outputs
   float* lse_part;           // [piece + segment][nq] base-2 log-sum-exps
 };

@@ -65,10 +65,13 @@ __global__ void __launch_bounds__(kMergeThreads) kv8_merge_kernel(const Kv8AttnP
   const int hpc = min(p.hpc, p.group - part0);
   const int col = (r - bd.q_indptr[b]) * hpc + h % p.group - part0;
   const int parts = p.hkv * p.hparts, s = g * p.hparts + c;
+  int L = p.ctx_lens[b];
+  L = L < 0 ? 0 : min(L, p.max_pages * kPage);
   asm volatile("griddepcontrol.wait;" ::: "memory");   // the attention kernel's partials and unit sums
-  const int cum = p.cum[b], units = (p.cum[b + 1] - cum) / parts;
-  const int per = (p.cum[bd.batch] + p.grid - 1) / p.grid;
-  const int u0 = cum + s * units, k0 = u0 / per, n = (u0 + units - 1) / per - k0 + 1;
+  const int per = p.cum[kMaxBatch + 1], extra = p.cum[kMaxBatch + 2];
+  const int cum = p.cum[b], line = (p.cum[b + 1] - cum) / parts;
+  const int units = extra < 0 ? line : 1 + extra + (L - window_base(L, p.window, kTileTokens) + kTileTokens - 1) / kTileTokens;
+  const int u0 = cum + s * line, k0 = u0 / per, n = (u0 + units - 1) / per - k0 + 1;
   if (n == 1) return;   // written directly
   const size_t slot0 = (size_t)k0 + b * parts + s;
   float mx = -INFINITY, den = 0.f, acc[E];
@@ -147,7 +150,7 @@ Layout layout_of(const Kv8Plan& pl, int hkv, int dim, const BatchDesc& bd, int s
   // a piece and a segment name a partial; along the line of units their numbers rise together
   const size_t slots = (size_t)sms + (size_t)bd.batch * hkv * pl.hparts;
   Layout l;
-  l.o = align_up((kMaxBatch + 1) * sizeof(int));
+  l.o = align_up((kMaxBatch + 3) * sizeof(int));
   l.lse = l.o + align_up(slots * pl.nq * dim * sizeof(__nv_bfloat16));
   l.total = l.lse + align_up(slots * pl.nq * sizeof(float));
   return l;

@@ -30,9 +30,13 @@
 // Work split.  The 128-token tiles of every (sequence, KV head, head part)
 // segment, its draft block in front as one more tile, form one line of units
 // that is cut into equal pieces, one per CTA, on the device from ctx_lens: no
-// host knowledge of the lengths, no idle CTA on a ragged batch.  A segment cut
-// by piece borders leaves bf16 partial outputs and fp32 log-sum-exps for the
-// merge; one that lies in a single piece is written directly.
+// host knowledge of the lengths.  Where every segment can have CTAs of its own
+// for at most an eighth more units per CTA, it does (a second piece costs a CTA
+// another staging and epilogue); else the line is cut where it falls, and no CTA
+// idles on a ragged batch.  A segment in several pieces leaves bf16 partial
+// outputs and fp32 log-sum-exps for the merge; one in a single piece is written
+// directly.  Context tiles go from the last to the first: a bias that falls with
+// distance then has its largest scores first, and m moves once.
 //
 // Per tile (tokens are the MMA's M; NQ columns):
 //   S[128 tok][NQ]     = K_tile . (Qhi + Qlo)^T      K-major, K = 32 a step
@@ -69,7 +73,7 @@ template <int NQ, bool MOD, bool TIGHT>
 struct KvSmall {
   static constexpr int kBars = TIGHT ? 24 : 40;
   float f[NQ];             // score factor of a column: its query scale times the softmax scale, base 2
-  float m[NQ];             // the column's reference m
+  float m[NQ];             // the column's reference, negated: -m
   float alpha[NQ];         // rescale factor of the current tile; 1 / l in the epilogue
   float slope[MOD ? NQ : 4];   // distance bias (base 2) and depth of the column's node
   float dep[MOD ? NQ : 4];
@@ -166,16 +170,6 @@ __device__ __forceinline__ void tma_page8(uint32_t dst, const CUtensorMap* map, 
       ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(w), "r"(bar), "l"(policy)
       : "memory");
 }
-__device__ __forceinline__ uint32_t e4m3x2_of(float lo, float hi) {
-  uint32_t r;
-  asm("{ .reg .b16 t; cvt.rn.satfinite.e4m3x2.f32 t, %1, %2; cvt.u32.u16 %0, t; }" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-__device__ __forceinline__ float2 e4m3x2_val(uint32_t codes) {
-  uint32_t h;
-  asm("{ .reg .b16 t; cvt.u16.u32 t, %1; cvt.rn.f16x2.e4m3x2 %0, t; }" : "=r"(h) : "r"(codes));
-  return __half22float2(*reinterpret_cast<const __half2*>(&h));
-}
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
   uint64_t r;
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)));
@@ -241,21 +235,26 @@ __device__ __forceinline__ float warp_sum16(float (&v)[16], int lane) {
   return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 16);
 }
 
-// Eight bf16 as two e4m3 terms (hi + lo) of x * 2^-e.
+// Eight bf16 as two e4m3 terms (hi + lo) of x * 2^-e.  In f16 on the way: 8 significant bits survive it wherever the
+// two terms could hold them.
+__device__ __forceinline__ uint32_t split2(uint32_t w, float inv) {   // hi pair below, lo pair above
+  const float2 v = mul2(__bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w)), make_float2(inv, inv));
+  uint32_t r;
+  asm("{ .reg .b32 a, b; .reg .b16 s, t;\n\t"
+      "cvt.rn.f16x2.f32 a, %2, %1;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 s, a;\n\t"
+      "cvt.rn.f16x2.e4m3x2 b, s;\n\t"
+      "sub.rn.f16x2 a, a, b;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 t, a;\n\t"
+      "mov.b32 %0, {s, t}; }"
+      : "=r"(r)
+      : "f"(v.x), "f"(v.y));
+  return r;
+}
 __device__ __forceinline__ void split8(const uint4 x, float inv, uint2& hi, uint2& lo) {
-  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-  uint32_t h[4], l[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float2 v = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]));
-    v.x *= inv;
-    v.y *= inv;
-    h[i] = e4m3x2_of(v.x, v.y);
-    const float2 b = e4m3x2_val(h[i]);
-    l[i] = e4m3x2_of(v.x - b.x, v.y - b.y);
-  }
-  hi = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
-  lo = make_uint2(l[0] | (l[1] << 16), l[2] | (l[3] << 16));
+  const uint32_t a = split2(x.x, inv), b = split2(x.y, inv), c = split2(x.z, inv), d = split2(x.w, inv);
+  hi = make_uint2(__byte_perm(a, b, 0x5410), __byte_perm(c, d, 0x5410));
+  lo = make_uint2(__byte_perm(a, b, 0x7632), __byte_perm(c, d, 0x7632));
 }
 // Largest bf16 magnitude of a chunk, as bits (infinities and NaN sort above the finite values).
 __device__ __forceinline__ uint32_t amax_bits(const uint4 x) {
@@ -272,9 +271,11 @@ __device__ __forceinline__ float exp2i(int e) { return __int_as_float((e + 127) 
 struct Piece {
   int b, g, c;         // sequence, KV head, head part
   int seg;
-  int L, base;         // context length; first position the tiles cover
-  int first, tiles;    // first tile of the segment (0: the draft block) and how many
+  int L, base, nt;     // context length; first position the context tiles cover, and how many there are
+  int first, tiles;    // first tile of the segment (0: the draft block, i: the i-th context tile from the end), how many
+  int span;            // units of the line that the piece takes
   bool whole;          // the segment lies in this piece alone
+  __device__ __forceinline__ int t0(int i) const { return base + (nt - i) * kTile; }   // position of context tile i
 };
 
 template <int D, int NG, int CC, bool MOD>
@@ -316,14 +317,40 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     sm->abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  int per, extra;   // units per CTA; >= 0: every segment has CTAs of its own, its draft tile counting 1 + extra units
   {
-    int n = 0;
+    int units = 0;
     if (tid < bd.batch) {
       const int raw = p.ctx_lens[tid], L = ctx_of(tid);
       if (blockIdx.x == 0 && raw != L) report(p.dev_status, SD_DEV_BAD_CTX);
-      n = (1 + (L - window_base(L, p.window, kTile) + kTile - 1) / kTile) * parts;
+      units = 1 + (L - window_base(L, p.window, kTile) + kTile - 1) / kTile;
+      sm->cum[tid] = units;
     }
-    int incl = n;
+    __syncthreads();
+    // Eight warps try eight piece sizes, from the even share up.
+    if (warp < 8) {
+      int sum = 0;
+#pragma unroll 1
+      for (int b = lane; b < bd.batch; b += 32) sum += sm->cum[b];
+      sum = __reduce_add_sync(0xffffffffu, sum);
+      const int even = (sum * parts + (int)gridDim.x - 1) / (int)gridDim.x;
+      const int more = even >= 12 ? 2 : even >= 5 ? 1 : 0;
+      const int size = even + warp * max(1, even / 56);
+      int need = 0;
+#pragma unroll 1
+      for (int b = lane; b < bd.batch; b += 32) need += (sm->cum[b] + more + size - 1) / size;
+      need = __reduce_add_sync(0xffffffffu, need) * parts;
+      if (lane == 0) sm->scan[warp] = need <= (int)gridDim.x ? size : 0;
+      if (tid == 0) { sm->flag[0][0][0] = even; sm->flag[0][0][1] = more; }
+    }
+    __syncthreads();
+    per = 0;
+#pragma unroll
+    for (int w = 7; w >= 0; --w) per = sm->scan[w] > 0 ? sm->scan[w] : per;
+    extra = per > 0 ? sm->flag[0][0][1] : -1;
+    if (per == 0) per = sm->flag[0][0][0];
+    __syncthreads();
+    int incl = (extra >= 0 ? (units + (units > 0 ? extra : 0) + per - 1) / per * per : units) * parts;
     if (warp < 8) {
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
@@ -349,11 +376,11 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
   __syncthreads();
   tc_fence_after();
   const int total = sm->cum[bd.batch];
-  const int per = (total + gridDim.x - 1) / gridDim.x;
   const int u_begin = min(total, (int)blockIdx.x * per), u_end = min(total, u_begin + per);
   if (blockIdx.x == 0) {   // for the merge
 #pragma unroll 1
     for (int i = tid; i <= bd.batch; i += kKvThreads) p.cum[i] = sm->cum[i];
+    if (tid == 0) { p.cum[kMaxBatch + 1] = per; p.cum[kMaxBatch + 2] = extra; }
   }
   // The piece that begins at unit u.
   auto piece_at = [&](int u) {
@@ -364,17 +391,24 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
       const int mid = (lo + hi + 1) >> 1;
       if (sm->cum[mid] <= u) lo = mid; else hi = mid - 1;
     }
-    const int units = (sm->cum[lo + 1] - sm->cum[lo]) / parts;
-    const int rem = u - sm->cum[lo], s = rem / units;
+    const int line = (sm->cum[lo + 1] - sm->cum[lo]) / parts;     // units of one of the sequence's segments
+    const int rem = u - sm->cum[lo], s = rem / line, at = rem - s * line;
     pc.b = lo;
     pc.g = s / p.hparts;
     pc.c = s - pc.g * p.hparts;
     pc.seg = lo * parts + s;
-    pc.first = rem - s * units;
-    pc.tiles = min(units - pc.first, u_end - u);
-    pc.whole = pc.tiles == units;
     pc.L = ctx_of(lo);
     pc.base = window_base(pc.L, p.window, kTile);
+    pc.nt = (pc.L - pc.base + kTile - 1) / kTile;
+    if (extra >= 0) {
+      pc.first = max(0, at - extra);
+      pc.tiles = min(pc.nt + 1, at + per - extra) - pc.first;
+      pc.span = per;
+    } else {
+      pc.first = at;
+      pc.tiles = pc.span = min(line - at, u_end - u);
+    }
+    pc.whole = pc.tiles == pc.nt + 1;
     // the same for every lane, and known to be
     pc.b = __shfl_sync(0xffffffffu, pc.b, 0);
     pc.g = __shfl_sync(0xffffffffu, pc.g, 0);
@@ -383,6 +417,8 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     pc.tiles = __shfl_sync(0xffffffffu, pc.tiles, 0);
     pc.L = __shfl_sync(0xffffffffu, pc.L, 0);
     pc.base = __shfl_sync(0xffffffffu, pc.base, 0);
+    pc.nt = __shfl_sync(0xffffffffu, pc.nt, 0);
+    pc.span = __shfl_sync(0xffffffffu, pc.span, 0);
     return pc;
   };
   const uint32_t bars = smem_u32(&sm->bar[0]);
@@ -425,9 +461,9 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
 #pragma unroll 1
       for (int u = u_begin; u < u_end && ok;) {
         const Piece pc = piece_at(u);
-        u += pc.tiles;
+        u += pc.span;
         const int* row = p.page_table + (size_t)pc.b * p.max_pages;
-        int t0 = pc.base + (pc.first - 1) * kTile, left = pc.tiles;
+        int left = pc.tiles;
         if (pc.first == 0) {
           // the draft tile is staged by the softmax warps: its slots, and its scale stage, pass by in their turn
           if (is_k) {
@@ -440,35 +476,35 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             ring.next(VS);
             ring.next(VS);
           }
-          t0 += kTile;
           --left;
         }
-        const int t_end = min(pc.L, t0 + left * kTile);   // tokens of this piece
-        auto ids_from = [&](int t) {
-          t += lane * kPage;
-          return t < t_end ? row[t / kPage] : -1;
+        int t0 = pc.t0(max(pc.first, 1));
+        auto ids_from = [&](int n) {     // of the piece's context tiles n .. n + 3
+          const int t = t0 - (lane >> 3) * kTile + (lane & 7) * kPage;
+          return n + (lane >> 3) < left && t - n * kTile < pc.L ? row[(t - n * kTile) / kPage] : -1;
         };
         auto in_pool = [&](int page) { return (unsigned)page < (unsigned)p.num_pool_pages; };
         auto scales_of = [&](const float* s, int page) {
           return is_k && in_pool(page) ? __ldg(s + (size_t)page * p.hkv + pc.g) : 1.f;
         };
-        int ids_next = ids_from(t0), ids_after = ids_from(t0 + 4 * kTile), ids = -1;
+        int ids_next = ids_from(0), ids_after = ids_from(4), ids = -1;
         float ks_next = scales_of(p.k_scales, ids_next), vs_next = scales_of(p.v_scales, ids_next), ks_now = 1.f, vs_now = 1.f;
         uint32_t good = 0;    // pages of the group that can be loaded
 #pragma unroll 1
-        for (int n = 0; n < left; ++n, t0 += kTile) {
+        for (int n = 0; n < left; ++n) {
           const int sub = (n & 3) * 8;
           if (sub == 0) {
             ids = ids_next;
             ks_now = ks_next;
             vs_now = vs_next;
             ids_next = ids_after;
-            ids_after = ids_from(t0 + 8 * kTile);
+            ids_after = ids_from(n + 8);
             ks_next = scales_of(p.k_scales, ids_next);
             vs_next = scales_of(p.v_scales, ids_next);
             good = __ballot_sync(0xffffffffu, in_pool(ids));
             if (is_k) {
-              if (t0 + lane * kPage < t_end && !in_pool(ids)) report(p.dev_status, SD_DEV_BAD_PAGE);
+              const int at = t0 - (n + (lane >> 3)) * kTile + (lane & 7) * kPage;
+              if (n + (lane >> 3) < left && at < pc.L && !in_pool(ids)) report(p.dev_status, SD_DEV_BAD_PAGE);
               if (!(ks_now >= kScaleLo && ks_now <= kScaleHi && vs_now >= kScaleLo && vs_now <= kScaleHi)) {
                 report(p.dev_status, SD_DEV_BAD_SCALE);
                 ks_now = ks_now > kScaleHi ? kScaleHi : ks_now >= kScaleLo ? ks_now : kScaleLo;
@@ -477,7 +513,8 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             }
           }
           const uint32_t have = (good >> sub) & 0xffu;
-          const int valid = min(kTile, t_end - t0);
+          const int tile = t0 - n * kTile;
+          const int valid = min(kTile, pc.L - tile);
           const uint32_t need = (1u << ((valid + kPage - 1) / kPage)) - 1u;
           const int half_page = (ids * p.hkv + pc.g) * 2;   // the tensor map's outer coordinate
           if (is_k) {
@@ -518,8 +555,8 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             const int lo = p.window > 0 ? pc.L - p.window + 1 : 0;          // the root's oldest visible position
             const int seen = p.window > 0 ? lo + kMaxNodes : 0;             // from here on every node sees every token
             uint32_t fast = have, slow = 0;
-            if (have != 0xffu || valid < kTile || t0 < seen) {
-              const int at = t0 + lane * kPage;
+            if (have != 0xffu || valid < kTile || tile < seen) {
+              const int at = tile + lane * kPage;
               // pages up to the last 32-token step of their half
               const int steps = lane < 4 ? (min(64, valid) + 31) / 32 * 2 : (max(0, valid - 64) + 31) / 32 * 2;
               const bool used = lane < 8 && (lane & 3) < steps;
@@ -546,7 +583,7 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                   const int pg = e / (kPage * (D / 16)), r = e / (D / 16) % kPage, ch = e % (D / 16);
                   const int id = __shfl_sync(0xffffffffu, ids, sub + pg);
                   if (!(((slow & sel) >> pg) & 1u)) continue;
-                  const int t = t0 + pg * kPage + r;
+                  const int t = tile + pg * kPage + r;
                   uint4 v = make_uint4(0, 0, 0, 0);
                   if (in_pool(id) && t >= lo && t < pc.L) {
                     v = __ldg(reinterpret_cast<const uint4*>(p.v_cache + (((size_t)id * p.hkv + pc.g) * kPage + r) * D) + ch);
@@ -600,7 +637,7 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
 #pragma unroll 1
       for (int u = u_begin; u < u_end && ok; ++np) {
         const Piece pc = piece_at(u);
-        u += pc.tiles;
+        u += pc.span;
         const int n_nodes = bd.q_indptr[pc.b + 1] - bd.q_indptr[pc.b];
         const int nq = (min(p.hpc, p.group - pc.c * p.hpc) * n_nodes + 15) & ~15;
         const uint32_t idesc = f8_idesc(nq, 0, 0, false);
@@ -651,14 +688,14 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
 #pragma unroll 1
       for (int u = u_begin; u < u_end && ok;) {
         const Piece pc = piece_at(u);
-        u += pc.tiles;
+        u += pc.span;
         const int n_nodes = bd.q_indptr[pc.b + 1] - bd.q_indptr[pc.b];
         const int nq = (min(p.hpc, p.group - pc.c * p.hpc) * n_nodes + 15) & ~15;
         const uint32_t id_hi = f8_idesc(nq, 1, 1, false), id_lo = f8_idesc(nq, 1, 1, true);
 #pragma unroll 1
         for (int i = 0; i < pc.tiles && ok; ++i, ++it) {
           const bool draft = pc.first + i == 0;
-          const int valid = draft ? n_nodes : min(kTile, pc.L - (pc.base + (pc.first + i - 1) * kTile));
+          const int valid = draft ? n_nodes : min(kTile, pc.L - pc.t0(pc.first + i));
           ok = __all_sync(0xffffffffu, wait(B_PF, it));
 #pragma unroll 1
           for (int h = 0; h < 2 && ok; ++h) {
@@ -705,7 +742,7 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
 #pragma unroll 1
     for (int u = u_begin; u < u_end;) {
       const Piece pc = piece_at(u);
-      u += pc.tiles;
+      u += pc.span;
       const int q0 = bd.q_indptr[pc.b], n_nodes = bd.q_indptr[pc.b + 1] - q0;
       const int hpc = min(p.hpc, p.group - pc.c * p.hpc);
       const int head0 = pc.g * p.group + pc.c * p.hpc;
@@ -743,6 +780,10 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                 make_uint4(0, 0, 0, 0);
           }
         }
+        uint8_t* const k_hi = sK + it % KS * K::kTileBytes;
+        uint8_t* const v_hi = sV + 2 * it % VS * K::kHalf;
+        const int v_lo = (int)(sV + (2 * it + 1) % VS * K::kHalf - v_hi);
+        const uint32_t ch_off = (uint32_t)((ch & 1) << 3), ch_chunk = (uint32_t)(ch >> 1) & 7u;
         auto load = [&](int r) {
           const __nv_bfloat16* src = nullptr;
           if (r < n_q) {
@@ -784,16 +825,13 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             const float s = wild ? __int_as_float(0x7fc00000) : exp2i(e);
             const bool is_q = r < n_q, is_v = r >= n_q + n_draft;
             const int t = is_q ? r : r - n_q - (is_v ? n_draft : 0);
-            const uint32_t in_row = (uint32_t)(((((ch >> 1) ^ t) & 7) << 4) | ((ch & 1) << 3));   // swizzled
-            uint8_t* at = is_q ? sQ + (ch >> 4) * NQ * 128 + t * 128
-                               : (is_v ? sV + 2 * it % VS * K::kHalf : sK + it % KS * K::kTileBytes) +
-                                     (t >> 3) * K::kGroupBytes + (ch >> 4) * 1024 + (t & 7) * 128;
-            uint8_t* at_lo = is_q ? at + K::kQTerm
-                             : is_v ? at + (sV + (2 * it + 1) % VS * K::kHalf - (sV + 2 * it % VS * K::kHalf))
-                                    : at + 8 * K::kGroupBytes;
+            uint8_t* at = (is_q ? sQ + (ch >> 4) * NQ * 128 + t * 128
+                                : (is_v ? v_hi : k_hi) + (t >> 3) * K::kGroupBytes + (ch >> 4) * 1024 + (t & 7) * 128) +
+                          (((ch_chunk ^ t) & 7u) << 4) + ch_off;     // swizzled
+            const int lo_off = is_q ? K::kQTerm : is_v ? v_lo : 8 * K::kGroupBytes;
             if (r < n_stage) {
-              *reinterpret_cast<uint2*>(at + in_row) = hi;
-              *reinterpret_cast<uint2*>(at_lo + in_row) = lo;
+              *reinterpret_cast<uint2*>(at) = hi;
+              *reinterpret_cast<uint2*>(at + lo_off) = lo;
               if (ch == 0) (is_q ? sm->f : is_v ? sm->row_v : sm->row_k)[t] = s;
             }
           }
@@ -855,7 +893,7 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
 #pragma unroll 1
       for (int i = 0; i < pc.tiles; ++i, ++it) {
         const bool draft = pc.first + i == 0;
-        const int t0 = pc.base + (pc.first + i - 1) * kTile;
+        const int t0 = pc.t0(pc.first + i);
         const int valid = draft ? n_nodes : min(kTile, pc.L - t0);
         const bool band = !draft && p.window > 0 && t0 < lo_root + kMaxNodes;
         const bool masked = draft || valid < kTile || band;
@@ -910,7 +948,7 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         for (int c = 0; c < CC; ++c) {
           if (c < mine) {
             const int q = col0 + c * 16;
-            float top = -INFINITY;
+            float top = -INFINITY;      // of this chunk
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               const float4 f = *reinterpret_cast<const float4*>(&sm->f[q + 4 * k]);
@@ -928,18 +966,19 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                 }
                 const float4 sl = *reinterpret_cast<const float4*>(&sm->slope[q + 4 * k]);
                 const float4 dp = *reinterpret_cast<const float4*>(&sm->dep[q + 4 * k]);
-                d0 = make_float2(fmaf(sl.x, rel - dp.x, s[0]) - m.x, fmaf(sl.y, rel - dp.y, s[1]) - m.y);
-                d1 = make_float2(fmaf(sl.z, rel - dp.z, s[2]) - m.z, fmaf(sl.w, rel - dp.w, s[3]) - m.w);
+                d0 = make_float2(fmaf(sl.x, rel - dp.x, s[0]) + m.x, fmaf(sl.y, rel - dp.y, s[1]) + m.y);
+                d1 = make_float2(fmaf(sl.z, rel - dp.z, s[2]) + m.z, fmaf(sl.w, rel - dp.w, s[3]) + m.w);
               } else {
-                d0 = fma2(make_float2(v[0], v[1]), f0, make_float2(-m.x, -m.y));
-                d1 = fma2(make_float2(v[2], v[3]), f1, make_float2(-m.z, -m.w));
+                d0 = fma2(make_float2(v[0], v[1]), f0, make_float2(m.x, m.y));
+                d1 = fma2(make_float2(v[2], v[3]), f1, make_float2(m.z, m.w));
               }
               v[0] = d0.x; v[1] = d0.y; v[2] = d1.x; v[3] = d1.y;
               top = fmaxf(fmaxf(top, fmaxf(d0.x, d0.y)), fmaxf(d1.x, d1.y));
             }
-            missed |= __any_sync(0xffffffffu, top > limit) ? 1u << c : 0u;
+            missed |= top > limit ? 1u << c : 0u;
           }
         }
+        if (__any_sync(0xffffffffu, missed != 0u)) missed = __reduce_or_sync(0xffffffffu, missed);
         const uint32_t all = (1u << mine) - 1u;
         if (masked) {
           // Which columns see this row: one bit each.  Masked exponents are -inf whatever the product was.
@@ -1006,12 +1045,12 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
           sync_group();
           const int mine_col = quarter * 32 + lane, q = col0 + mine_col;
           if (mine_col < mine * 16 && ((todo >> (mine_col >> 4)) & 1u)) {
-            const float old = sm->m[q];
+            const float old = -sm->m[q];
             const float mt = old + fmaxf(fmaxf(sm->red[0][q], sm->red[1][q]), fmaxf(sm->red[2][q], sm->red[3][q])) - kHead;
             float now = mt == -INFINITY ? old : old == 0.f ? mt : fmaxf(old, mt);
             if (now == 0.f && mt != -INFINITY) now = 1e-30f;
             sm->alpha[q] = old == 0.f ? 1.f : fast_exp2(old - now);
-            sm->m[q] = now;
+            sm->m[q] = -now;
             sm->red[0][q] = old - now;
           }
           sync_group();
@@ -1092,7 +1131,7 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
           if (q < rows) {
             const int node = q / hpc, at = (q0 + node) * p.hq + head0 + q - node * hpc;
             out_row[q] = pc.whole ? at : q;
-            const float lse2 = l == 0.f ? -INFINITY : sm->m[q] + fast_log2(l);
+            const float lse2 = l == 0.f ? -INFINITY : fast_log2(l) - sm->m[q];
             if (!pc.whole) p.lse_part[slot * NQ + q] = lse2;
             else if (p.lse != nullptr) p.lse[at] = lse2 * kLn2;
           }
