@@ -160,14 +160,15 @@ Layout layout_of(const Kv8Plan& pl, int hkv, int dim, const BatchDesc& bd, int s
 
 // Query columns of a CTA: as many heads of a KV group as fit, so that the cache is read as few times as can be.
 Kv8Plan kv8_plan(int group, int max_nodes, int dim, bool mod) {
-  const int most = mod && dim == 256 ? 128 : 144;
+  // capped or biased scores over 256 dims: the wider columns' slopes and depths find no room beside the operands
+  const int most = mod && dim == 256 ? 96 : 144;
   Kv8Plan pl;
   pl.hparts = 1;
   while ((group + pl.hparts - 1) / pl.hparts * max_nodes > most) ++pl.hparts;
   pl.hpc = (group + pl.hparts - 1) / pl.hparts;
   pl.hparts = (group + pl.hpc - 1) / pl.hpc;
   const int cols = pl.hpc * max_nodes;
-  pl.nq = cols <= 16 ? 16 : cols <= 48 ? 48 : cols <= 96 ? 96 : most;
+  pl.nq = cols <= 16 ? 16 : cols <= 48 ? 48 : cols <= 96 ? 96 : 144;
   return pl;
 }
 

@@ -14,8 +14,9 @@
 // kTop, the largest e4m3 value.
 //
 // The 8-bit operands.  K and V are exact as they lie.  A bf16 query is two
-// e4m3 terms (a power-of-two scale per row, then the rounded value and the
-// rounded rest: 8 significant bits, off by at most 2^-18 of the row's amax);
+// e4m3 terms (a power-of-two scale for all the CTA's queries, then the rounded
+// value and the rounded rest: 8 significant bits, off by at most 2^-18 of the
+// largest query's amax, so a score is off by no more than that query's);
 // both multiply the same K tile into the same accumulator.  A weight is an
 // e4m3 term and an e5m2 rest (2^-4 times 2^-3: at most 2^-7 off, about 2^-9.5
 // in the mean square; e5m2 so that the rest of small weights keeps its
@@ -72,7 +73,6 @@ constexpr int kScaleStages = 6;
 template <int NQ, bool MOD, bool TIGHT>
 struct KvSmall {
   static constexpr int kBars = TIGHT ? 24 : 40;
-  float f[NQ];             // score factor of a column: its query scale times the softmax scale, base 2
   float m[NQ];             // the column's reference, negated: -m
   float alpha[NQ];         // rescale factor of the current tile; 1 / l in the epilogue
   float slope[MOD ? NQ : 4];   // distance bias (base 2) and depth of the column's node
@@ -84,6 +84,7 @@ struct KvSmall {
   uint64_t bar[kBars];
   int cum[kMaxBatch + 1];  // first unit of each sequence
   int scan[8];
+  uint32_t q_amax[2];      // bf16 bits of the largest finite query magnitude of this piece, and of the next
   int8_t par[kMaxNodes];
   int8_t depth[kMaxNodes];
   alignas(16) int flag[3][2][4];   // [group][tile parity][lane quarter]: chunks where a weight passes kTop
@@ -94,7 +95,7 @@ struct KvSmall {
 // D: head dim.  NG groups of softmax warps, of up to CC 16-column chunks each.  MOD: capped scores or a distance bias.
 template <int D, int NG, int CC, bool MOD>
 struct Kv {
-  static constexpr int NQ = NG * CC * 16 == 144 && MOD && D == 256 ? 128 : NG * CC * 16;   // query columns
+  static constexpr int NQ = NG * CC * 16;                 // query columns
   static constexpr int kWarps = NG * 4, kThreads = (kWarps + 4) * 32;
   using Small = KvSmall<NQ, MOD, NQ == 144 && D == 256>;
   static constexpr int MH = D / 128;                      // 128-dim blocks
@@ -315,6 +316,7 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     for (int i = 0; i < kNumBars; ++i)
       mbar_init(smem_u32(&sm->bar[i]), i == B_PF || (i >= B_SE && i < B_SE + NS) ? (uint32_t)kWarps : i >= B_G ? 4u : 1u);
     sm->abort = 0;
+    sm->q_amax[0] = sm->q_amax[1] = 0u;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   int per, extra;   // units per CTA; >= 0: every segment has CTAs of its own, its draft tile counting 1 + extra units
@@ -738,19 +740,21 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     auto sync_all = [] { asm volatile("bar.sync 7, %0;" ::"n"(kWarps * 32) : "memory"); };        // the softmax warps
     auto sync_group = [&] { asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory"); };     // the group's four
     Ring s_ring, sc_ring;
-    int it = 0;
+    int it = 0, np = 0;
 #pragma unroll 1
-    for (int u = u_begin; u < u_end;) {
+    for (int u = u_begin; u < u_end; ++np) {
       const Piece pc = piece_at(u);
       u += pc.span;
       const int q0 = bd.q_indptr[pc.b], n_nodes = bd.q_indptr[pc.b + 1] - q0;
       const int hpc = min(p.hpc, p.group - pc.c * p.hpc);
       const int head0 = pc.g * p.group + pc.c * p.hpc;
       const int rows = hpc * n_nodes, nc = (rows + 15) / 16;
-      const int mine = nc / NG + (group < nc % NG ? 1 : 0);                       // 16-column chunks of this group
-      const int c_first = group * (nc / NG) + min(group, nc % NG);
+      // 16-column chunks of this group.  It always computes CC of them (straight code); what lies past the columns in use
+      // is never multiplied, and its references below every score keep it out of the way.
+      const int mine = min(CC, max(0, nc - group * CC)), c_first = group * CC;
       const int col0 = c_first * 16;
       const bool has_draft = pc.first == 0;
+      float fac;      // of a raw product, with its token's K scale: the base-2 score
       // ---------------------------------------------------------- staging: Q, the tree, the draft block
       // (the previous piece's products have all finished: its last O_DONE was waited for)
       if (tid < n_nodes) {
@@ -758,91 +762,100 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         sm->par[tid] = (int8_t)(up < -1 || up >= kMaxNodes ? -2 : up);
       }
       {
-        // Rows by warp, U at a time with the next U's loads under way.  The code runs once per piece: it is kept short,
-        // since its first run waits for its own instructions.
-        constexpr int LPR = D / 8, RPW = 32 / LPR;      // lanes per row, rows per warp and load
-        constexpr int U = 3, kStep = kWarps * RPW * U;
-        const int sub = lane / LPR, ch = lane % LPR;    // 8-value chunk of the row
-        const int n_draft = has_draft ? n_nodes : 0;
-        const int n_q = nc * 16, n_stage = n_q + 2 * n_draft;
+        // Rows by warp; a warp's query rows all at once, then, in the draft CTA, the block's K and V rows.  The code runs
+        // once per piece: it is kept short, since its first run waits for its own instructions.
+        constexpr int LPR = D / 8, RPW = 32 / LPR;                     // lanes per row, rows per warp and load
+        constexpr int U = (NQ + kWarps * RPW - 1) / (kWarps * RPW);    // a warp's query rows, RPW at a time
+        const int sub = lane / LPR, ch = lane % LPR;                   // 8-value chunk of the row
+        const int n_q = nc * 16;
         const float inv_hpc = 1.0f / (float)hpc;
+        auto row_amax = [&](uint4& x, bool& wild) {        // a row with a NaN or an infinity counts as zeros
+          uint32_t a = amax_bits(x);
+          if (RPW == 1) {
+            a = __reduce_max_sync(0xffffffffu, a);
+          } else {
+#pragma unroll
+            for (int d = LPR / 2; d >= 1; d >>= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, d));
+          }
+          wild = a >= 0x7f80u;
+          if (wild) x = make_uint4(0, 0, 0, 0);
+          return wild ? 0u : a;
+        };
+        const uint32_t ch_off = (uint32_t)((ch & 1) << 3), ch_chunk = (uint32_t)(ch >> 1) & 7u;
+        auto swizzled = [&](int r) { return (((ch_chunk ^ (uint32_t)r) & 7u) << 4) + ch_off; };
+        uint4 x[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+          const int r = (i * kWarps + warp) * RPW + sub;
+          const int node = __float2int_rz(((float)r + 0.5f) * inv_hpc);   // r / hpc, exact for r < 2^20
+          x[i] = make_uint4(0, 0, 0, 0);
+          if (r < rows)
+            x[i] = __ldg(reinterpret_cast<const uint4*>(p.q + (long long)(q0 + node) * p.q_stride +
+                                                        (head0 + r - node * hpc) * D) + ch);
+        }
         if (has_draft) {
           // the ring slots of the draft tile, once their previous contents have been multiplied
           spin(B_KE + it % KS, it / KS + 1);
           spin(B_VE + 2 * it % VS, 2 * it / VS + 1);
           spin(B_VE + (2 * it + 1) % VS, (2 * it + 1) / VS + 1);
-          const int n_zero = ((n_nodes + 31) & ~31) - n_nodes;       // V rows up to the 32-token step: zeros
+          uint8_t* const k_hi = sK + it % KS * K::kTileBytes;
+          uint8_t* const v_hi = sV + 2 * it % VS * K::kHalf;
+          uint8_t* const v_lo = sV + (2 * it + 1) % VS * K::kHalf;
+          // rows 0 .. n - 1: K, n .. 2 n - 1: V; then zeros up to V's 32-token step
+          const int v_end = n_nodes + ((n_nodes + 31) & ~31);
 #pragma unroll 1
-          for (int e = tid; e < n_zero * (D / 16) * 2; e += kWarps * 32) {
-            const int c16 = (e >> 1) % (D / 16), r = n_nodes + (e >> 1) / (D / 16);
-            *reinterpret_cast<uint4*>(sV + (2 * it + (e & 1)) % VS * K::kHalf + (r >> 3) * K::kGroupBytes +
-                                      (c16 >> 3) * 1024 + (r & 7) * 128 + (((c16 & 7) ^ (r & 7)) << 4)) =
-                make_uint4(0, 0, 0, 0);
+          for (int base = warp * RPW; base < v_end; base += kWarps * RPW) {
+            const int r = base + sub;
+            const bool is_v = r >= n_nodes;
+            const int n = is_v ? r - n_nodes : r;
+            uint4 y = make_uint4(0, 0, 0, 0);
+            if (n < n_nodes)
+              y = __ldg(reinterpret_cast<const uint4*>((is_v ? p.v_new + (long long)(q0 + n) * p.v_stride
+                                                             : p.k_new + (long long)(q0 + n) * p.k_stride) + pc.g * D) + ch);
+            bool wild;
+            const int e = exp_of(row_amax(y, wild));
+            uint2 hi, lo;
+            split8(y, exp2i(-e), hi, lo);
+            if (r < v_end) {
+              const uint32_t off = (uint32_t)((n >> 3) * K::kGroupBytes + (ch >> 4) * 1024 + (n & 7) * 128) + swizzled(n);
+              *reinterpret_cast<uint2*>((is_v ? v_hi : k_hi) + off) = hi;
+              *reinterpret_cast<uint2*>((is_v ? v_lo : k_hi + 8 * K::kGroupBytes) + off) = lo;
+              if (ch == 0 && n < n_nodes) (is_v ? sm->row_v : sm->row_k)[n] = wild ? __int_as_float(0x7fc00000) : exp2i(e);
+            }
           }
         }
-        uint8_t* const k_hi = sK + it % KS * K::kTileBytes;
-        uint8_t* const v_hi = sV + 2 * it % VS * K::kHalf;
-        const int v_lo = (int)(sV + (2 * it + 1) % VS * K::kHalf - v_hi);
-        const uint32_t ch_off = (uint32_t)((ch & 1) << 3), ch_chunk = (uint32_t)(ch >> 1) & 7u;
-        auto load = [&](int r) {
-          const __nv_bfloat16* src = nullptr;
+        uint32_t most = 0, wilds = 0;
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+          bool wild;
+          most = max(most, row_amax(x[i], wild));
+          wilds |= wild ? 1u << i : 0u;
+        }
+        most = __reduce_max_sync(0xffffffffu, most);
+        if (lane == 0) atomicMax(&sm->q_amax[np & 1], most);
+        sync_all();
+        const int e_q = exp_of(sm->q_amax[np & 1]);
+        const float inv = exp2i(-e_q);
+        fac = exp2i(e_q) * p.scale * (MOD && p.softcap > 0.f ? 2.f * kLog2e / p.softcap : kLog2e);
+        if (tid == 0) sm->q_amax[(np + 1) & 1] = 0u;
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+          const int r = (i * kWarps + warp) * RPW + sub;
+          uint2 hi, lo;
+          split8(x[i], inv, hi, lo);
+          if ((wilds >> i) & 1u) hi = make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);     // NaN codes: the column's scores are NaN
           if (r < n_q) {
-            const int node = __float2int_rz(((float)r + 0.5f) * inv_hpc);   // r / hpc, exact for r < 2^20
-            if (r < rows) src = p.q + (long long)(q0 + node) * p.q_stride + (head0 + r - node * hpc) * D;
-          } else if (r < n_stage) {
-            const bool is_v = r >= n_q + n_draft;
-            const long long t = q0 + r - n_q - (is_v ? n_draft : 0);
-            src = (is_v ? p.v_new + t * p.v_stride : p.k_new + t * p.k_stride) + pc.g * D;
-          }
-          return src != nullptr ? __ldg(reinterpret_cast<const uint4*>(src) + ch) : make_uint4(0, 0, 0, 0);
-        };
-        uint4 next[U];
-#pragma unroll
-        for (int i = 0; i < U; ++i) next[i] = load(warp * RPW + sub + i * kWarps * RPW);
-#pragma unroll 1
-        for (int base = warp * RPW; base < n_stage; base += kStep) {
-          uint4 x[U];
-#pragma unroll
-          for (int i = 0; i < U; ++i) {
-            x[i] = next[i];
-            next[i] = load(base + kStep + sub + i * kWarps * RPW);
-          }
-#pragma unroll
-          for (int i = 0; i < U; ++i) {
-            const int r = base + i * kWarps * RPW + sub;
-            uint32_t a = amax_bits(x[i]);
-            if (RPW == 1) {
-              a = __reduce_max_sync(0xffffffffu, a);
-            } else {
-#pragma unroll
-              for (int d = LPR / 2; d >= 1; d >>= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, d));
-            }
-            const bool wild = a >= 0x7f80u;             // a NaN or an infinity: zeros, and a NaN scale
-            if (wild) { x[i] = make_uint4(0, 0, 0, 0); a = 0; }
-            const int e = exp_of(a);
-            uint2 hi, lo;
-            split8(x[i], exp2i(-e), hi, lo);
-            const float s = wild ? __int_as_float(0x7fc00000) : exp2i(e);
-            const bool is_q = r < n_q, is_v = r >= n_q + n_draft;
-            const int t = is_q ? r : r - n_q - (is_v ? n_draft : 0);
-            uint8_t* at = (is_q ? sQ + (ch >> 4) * NQ * 128 + t * 128
-                                : (is_v ? v_hi : k_hi) + (t >> 3) * K::kGroupBytes + (ch >> 4) * 1024 + (t & 7) * 128) +
-                          (((ch_chunk ^ t) & 7u) << 4) + ch_off;     // swizzled
-            const int lo_off = is_q ? K::kQTerm : is_v ? v_lo : 8 * K::kGroupBytes;
-            if (r < n_stage) {
-              *reinterpret_cast<uint2*>(at) = hi;
-              *reinterpret_cast<uint2*>(at + lo_off) = lo;
-              if (ch == 0) (is_q ? sm->f : is_v ? sm->row_v : sm->row_k)[t] = s;
-            }
+            uint8_t* at = sQ + (ch >> 4) * NQ * 128 + r * 128 + swizzled(r);
+            *reinterpret_cast<uint2*>(at) = hi;
+            *reinterpret_cast<uint2*>(at + K::kQTerm) = lo;
           }
         }
       }
       fence_async_smem();
       sync_all();
 #pragma unroll 1
-      for (int q = tid; q < nc * 16; q += kWarps * 32) {
-        sm->f[q] *= p.scale * (MOD && p.softcap > 0.f ? 2.f * kLog2e / p.softcap : kLog2e);
-        sm->m[q] = 0.f;     // no reference yet
+      for (int q = tid; q < NQ; q += kWarps * 32) {
+        sm->m[q] = q < nc * 16 ? 0.f : -1e30f;     // no reference yet; columns past those in use: below everything
         if (MOD) sm->slope[q] = p.slopes != nullptr && q < rows ? p.slopes[head0 + q % hpc] * kLog2e : 0.f;
       }
       // the tree: root paths and depths
@@ -869,7 +882,7 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
       sync_all();
       if (MOD) {
 #pragma unroll 1
-        for (int q = tid; q < nc * 16; q += kWarps * 32) sm->dep[q] = q < rows ? (float)sm->depth[q / hpc] : 0.f;
+        for (int q = tid; q < NQ; q += kWarps * 32) sm->dep[q] = q < rows ? (float)sm->depth[q / hpc] : 0.f;
         sync_all();
       }
       if (tid == 0) {
@@ -932,8 +945,7 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         {
           const uint32_t s_addr = tmem + lane_addr + s_ring.at * NQ + col0;
 #pragma unroll
-          for (int c = 0; c < CC; ++c)
-            if (c < mine) tmem_ld16(s_addr + c * 16, a[c]);
+          for (int c = 0; c < CC; ++c) tmem_ld16(s_addr + c * 16, a[c]);
           tmem_wait_ld();
         }
         tc_fence_before();
@@ -944,42 +956,40 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         uint32_t missed = 0;
         const float limit = 8.807354922f - lv;       // log2(kTop)
         const float rel = draft ? (row < n_nodes ? (float)sm->depth[row] : 0.f) : (float)(t0 + row - pc.L);
+        const float kf = ks * fac;
 #pragma unroll
         for (int c = 0; c < CC; ++c) {
-          if (c < mine) {
-            const int q = col0 + c * 16;
-            float top = -INFINITY;      // of this chunk
+          const int q = col0 + c * 16;
+          float top = -INFINITY;      // of this chunk
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const float4 f = *reinterpret_cast<const float4*>(&sm->f[q + 4 * k]);
-              const float4 m = *reinterpret_cast<const float4*>(&sm->m[q + 4 * k]);
-              float* v = &a[c][4 * k];
-              const float2 kk = make_float2(ks, ks), f0 = mul2(make_float2(f.x, f.y), kk), f1 = mul2(make_float2(f.z, f.w), kk);
-              float2 d0, d1;
-              if (MOD) {
-                float s[4] = {v[0] * f0.x, v[1] * f0.y, v[2] * f1.x, v[3] * f1.y};
-                if (p.softcap > 0.f) {
-                  // c tanh(x / c) = c - 2 c / (1 + 2^(2 log2e x / c)); f holds the factor of the exponent
-                  const float cl = p.softcap * kLog2e;
+          for (int k = 0; k < 4; ++k) {
+            const float4 m = *reinterpret_cast<const float4*>(&sm->m[q + 4 * k]);
+            float* v = &a[c][4 * k];
+            float2 d0, d1;
+            if (MOD) {
+              float s[4] = {v[0] * kf, v[1] * kf, v[2] * kf, v[3] * kf};
+              if (p.softcap > 0.f) {
+                // c tanh(x / c) = c - 2 c / (1 + 2^(2 log2e x / c)); fac holds the factor of the exponent
+                const float cl = p.softcap * kLog2e;
 #pragma unroll
-                  for (int e = 0; e < 4; ++e) s[e] = fmaf(-2.f * cl, fast_rcp(1.f + fast_exp2(s[e])), cl);
-                }
-                const float4 sl = *reinterpret_cast<const float4*>(&sm->slope[q + 4 * k]);
-                const float4 dp = *reinterpret_cast<const float4*>(&sm->dep[q + 4 * k]);
-                d0 = make_float2(fmaf(sl.x, rel - dp.x, s[0]) + m.x, fmaf(sl.y, rel - dp.y, s[1]) + m.y);
-                d1 = make_float2(fmaf(sl.z, rel - dp.z, s[2]) + m.z, fmaf(sl.w, rel - dp.w, s[3]) + m.w);
-              } else {
-                d0 = fma2(make_float2(v[0], v[1]), f0, make_float2(m.x, m.y));
-                d1 = fma2(make_float2(v[2], v[3]), f1, make_float2(m.z, m.w));
+                for (int e = 0; e < 4; ++e) s[e] = fmaf(-2.f * cl, fast_rcp(1.f + fast_exp2(s[e])), cl);
               }
-              v[0] = d0.x; v[1] = d0.y; v[2] = d1.x; v[3] = d1.y;
-              top = fmaxf(fmaxf(top, fmaxf(d0.x, d0.y)), fmaxf(d1.x, d1.y));
+              const float4 sl = *reinterpret_cast<const float4*>(&sm->slope[q + 4 * k]);
+              const float4 dp = *reinterpret_cast<const float4*>(&sm->dep[q + 4 * k]);
+              d0 = make_float2(fmaf(sl.x, rel - dp.x, s[0]) + m.x, fmaf(sl.y, rel - dp.y, s[1]) + m.y);
+              d1 = make_float2(fmaf(sl.z, rel - dp.z, s[2]) + m.z, fmaf(sl.w, rel - dp.w, s[3]) + m.w);
+            } else {
+              d0 = fma2(make_float2(v[0], v[1]), make_float2(kf, kf), make_float2(m.x, m.y));
+              d1 = fma2(make_float2(v[2], v[3]), make_float2(kf, kf), make_float2(m.z, m.w));
             }
-            missed |= top > limit ? 1u << c : 0u;
+            v[0] = d0.x; v[1] = d0.y; v[2] = d1.x; v[3] = d1.y;
+            top = fmaxf(fmaxf(top, fmaxf(d0.x, d0.y)), fmaxf(d1.x, d1.y));
           }
+          missed |= top > limit ? 1u << c : 0u;
         }
         if (__any_sync(0xffffffffu, missed != 0u)) missed = __reduce_or_sync(0xffffffffu, missed);
         const uint32_t all = (1u << mine) - 1u;
+        missed &= all;
         if (masked) {
           // Which columns see this row: one bit each.  Masked exponents are -inf whatever the product was.
           constexpr int VW = (CC * 16 + 31) / 32;
@@ -1024,9 +1034,14 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
           mbar_arrive(bar(B_G + group));
         }
         if (plain) {
+          if (missed == 0u) {
 #pragma unroll
-          for (int c = 0; c < CC; ++c)
-            if (c < mine && !((missed >> c) & 1u)) weigh(c, 1.f);
+            for (int c = 0; c < CC; ++c) weigh(c, 1.f);
+          } else {
+#pragma unroll
+            for (int c = 0; c < CC; ++c)
+              if (!((missed >> c) & 1u)) weigh(c, 1.f);
+          }
         }
         settled = settled || draft || !band;
         spin(B_G + group, it);
@@ -1091,11 +1106,9 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         }
 #pragma unroll
         for (int c = 0; c < CC; ++c) {
-          if (c < mine) {
-            uint8_t* at = sP + (c_first + c) * kTile * 16 + row * 16;
-            *reinterpret_cast<uint4*>(at) = make_uint4(hi[c][0], hi[c][1], hi[c][2], hi[c][3]);
-            *reinterpret_cast<uint4*>(at + K::kPTerm) = make_uint4(lo[c][0], lo[c][1], lo[c][2], lo[c][3]);
-          }
+          uint8_t* at = sP + (c_first + c) * kTile * 16 + row * 16;
+          *reinterpret_cast<uint4*>(at) = make_uint4(hi[c][0], hi[c][1], hi[c][2], hi[c][3]);
+          *reinterpret_cast<uint4*>(at + K::kPTerm) = make_uint4(lo[c][0], lo[c][1], lo[c][2], lo[c][3]);
         }
         tc_fence_before();
         fence_async_smem();
@@ -1108,7 +1121,7 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
       sync_group();      // the last tile's readers of red[] are done
 #pragma unroll
       for (int c = 0; c < CC; ++c) {
-        if (c < mine) {
+        {
           float v[16];
 #pragma unroll
           for (int e = 0; e < 8; ++e) { v[2 * e] = sum[c][e].x; v[2 * e + 1] = sum[c][e].y; }
@@ -1125,8 +1138,8 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         if (quarter * 32 + lane < mine * 16) {
           const float l = sm->red[0][q] + sm->red[1][q] + sm->red[2][q] + sm->red[3][q];
           sm->alpha[q] = l == 0.f ? 0.f : 1.f / l;
-          // the column's output row; the score factors are not needed any more
-          int* out_row = reinterpret_cast<int*>(sm->f);
+          // the column's output row, in place of its sums
+          int* out_row = reinterpret_cast<int*>(sm->red[0]);
           out_row[q] = -1;
           if (q < rows) {
             const int node = q / hpc, at = (q0 + node) * p.hq + head0 + q - node * hpc;
@@ -1150,7 +1163,7 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         for (int k = 0; k < 8; ++k) {
           const int qe = col0 + c * 16 + 2 * k;
           const float2 inv = *reinterpret_cast<const float2*>(&sm->alpha[qe]);
-          const int2 at = *reinterpret_cast<const int2*>(&sm->f[qe]);
+          const int2 at = *reinterpret_cast<const int2*>(&sm->red[0][qe]);
           const int r = odd ? at.y : at.x;
 #pragma unroll
           for (int mb = 0; mb < MH; ++mb) {
