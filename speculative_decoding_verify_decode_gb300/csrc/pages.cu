@@ -48,6 +48,11 @@ __device__ __forceinline__ int find_seq(const int* start, int batch, int e) {
   return lo;
 }
 
+// Page j of sequence b after the call, without the page table having been written.
+__device__ __forceinline__ int page_of(const PagesParams& p, const int* held, const int* first_new, int count, int b, int j) {
+  return j < held[b] ? p.page_table[(size_t)b * p.max_pages + j] : p.free_list[count - 1 - (first_new[b] + j - held[b])];
+}
+
 template <bool PATH>
 __global__ void __launch_bounds__(PATH ? kPathThreads : kPagesThreads)
 pages_extend_kernel(const PagesParams p, const BatchDesc bd) {
@@ -119,44 +124,62 @@ pages_extend_kernel(const PagesParams p, const BatchDesc bd) {
       p.page_table[(size_t)b * p.max_pages + s_held[b] + (e - s_page[b])] = p.free_list[count - 1 - e];
     }
   }
-  // The slot map, four rows (one 16-byte store) per thread and step; behind the last row: -1.
+  // The slot map: a warp takes 512 consecutive rows at a time, a lane four quads of rows (one 16-byte store each, lanes
+  // side by side) whose page lookups are all in flight together; behind the last row: -1.  The warp searches its first
+  // row's sequence once, lanes walk on from there.
   const int n_rows = ok ? s_row[B] : 0;
   bool bad_page = false;
-  const int quads = (int)(((long long)p.max_rows + 3) / 4);
-  for (int qd = first; qd < quads; qd += step) {
-    const int r0 = qd * 4;
-    int slot[4], src[4];
-    int b = r0 < n_rows ? find_seq(s_row, B, r0) : 0;
-    int last = -1, page = -1;   // the page-table entry looked up last: rows of a quad mostly share it
+  constexpr int U = 4;
+  const int lane = t & 31;
+  for (long long w0 = (long long)(first - lane) * (4 * U); w0 < p.max_rows; w0 += (long long)step * (4 * U)) {
+    int b0 = w0 < n_rows ? find_seq(s_row, B, (int)w0) : 0;
+    int seq[U], pos[U], page[U];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int r = r0 + k;
-      slot[k] = src[k] = -1;
+    for (int u = 0; u < U; ++u) {
+      const long long r = w0 + 128 * u + 4 * lane;
+      seq[u] = -1;
       if (r < n_rows) {
-        while (r >= s_row[b + 1]) { ++b; last = -1; }   // ends: r < s_row[B]
-        const int i = r - s_row[b], pos = s_ctx[b] + i, j = pos / kPage;
-        if (j != last) {
-          page = j < s_held[b] ? p.page_table[(size_t)b * p.max_pages + j]
-                               : p.free_list[count - 1 - (s_page[b] + j - s_held[b])];
-          last = j;
-        }
-        const bool in = page >= 0 && page < p.num_pool_pages;
-        bad_page |= !in;
-        slot[k] = in ? page * kPage + pos % kPage : -1;
-        src[k] = PATH ? bd.q_indptr[b] + p.path[(size_t)b * p.max_path + i] : r;
+        while ((int)r >= s_row[b0 + 1]) ++b0;      // ends: r < s_row[B]
+        seq[u] = b0;
+        pos[u] = s_ctx[b0] + (int)r - s_row[b0];
+        page[u] = page_of(p, s_held, s_page, count, b0, pos[u] / kPage);
       }
     }
-    const int m = min(4, p.max_rows - r0);
-    if (m == 4 && p.vec) {
-      *reinterpret_cast<int4*>(p.slots + r0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
-      if (p.rows != nullptr) *reinterpret_cast<int4*>(p.rows + r0) = make_int4(src[0], src[1], src[2], src[3]);
-    } else {
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (k < m) {
-          p.slots[r0 + k] = slot[k];
-          if (p.rows != nullptr) p.rows[r0 + k] = src[k];
+    for (int u = 0; u < U; ++u) {
+      const long long r0 = w0 + 128 * u + 4 * lane;
+      int slot[4], src[4];
+      int b = seq[u], j = b >= 0 ? pos[u] / kPage : 0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const long long r = r0 + k;
+        slot[k] = src[k] = -1;
+        if (r < n_rows) {
+          int at = b;
+          while ((int)r >= s_row[at + 1]) ++at;
+          const int i = (int)r - s_row[at], x = s_ctx[at] + i;
+          if (at != b || x / kPage != j) {         // the quad ends a page or a sequence
+            b = at;
+            j = x / kPage;
+            page[u] = page_of(p, s_held, s_page, count, b, j);
+          }
+          const bool in = page[u] >= 0 && page[u] < p.num_pool_pages;
+          bad_page |= !in;
+          slot[k] = in ? page[u] * kPage + x % kPage : -1;
+          src[k] = PATH ? bd.q_indptr[at] + p.path[(size_t)at * p.max_path + i] : (int)r;
         }
+      }
+      if (r0 + 4 <= p.max_rows && p.vec) {
+        *reinterpret_cast<int4*>(p.slots + r0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+        if (p.rows != nullptr) *reinterpret_cast<int4*>(p.rows + r0) = make_int4(src[0], src[1], src[2], src[3]);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (r0 + k < p.max_rows) {
+            p.slots[r0 + k] = slot[k];
+            if (p.rows != nullptr) p.rows[r0 + k] = src[k];
+          }
+      }
     }
   }
   if (bad_page) report(p.dev_status, SD_DEV_BAD_PAGE);
@@ -206,7 +229,7 @@ __global__ void __launch_bounds__(kPagesThreads) pages_release_kernel(const Page
 
 int blocks_for(long long elements, int per_block) {
   const long long n = (elements + per_block - 1) / per_block;
-  return (int)(n < 1 ? 1 : n > 2 * kSMs ? 2 * kSMs : n);
+  return (int)(n < 1 ? 1 : n > 8 * kSMs ? 8 * kSMs : n);   // one wave at most
 }
 
 }  // namespace
@@ -215,12 +238,12 @@ cudaError_t launch_pages_extend(const PagesParams& p, const BatchDesc& bd, cudaS
   if (p.path != nullptr)
     pages_extend_kernel<true><<<1, kPathThreads, 0, st>>>(p, bd);
   else
-    pages_extend_kernel<false><<<blocks_for(p.max_rows, 8 * kPagesThreads), kPagesThreads, 0, st>>>(p, bd);
+    pages_extend_kernel<false><<<blocks_for(p.max_rows, 16 * kPagesThreads), kPagesThreads, 0, st>>>(p, bd);
   return cudaGetLastError();
 }
 
 cudaError_t launch_pages_release(const PagesParams& p, cudaStream_t st) {
-  pages_release_kernel<<<blocks_for((long long)p.batch * p.max_pages, 16 * kPagesThreads), kPagesThreads, 0, st>>>(p);
+  pages_release_kernel<<<blocks_for((long long)p.batch * p.max_pages, 2 * kPagesThreads), kPagesThreads, 0, st>>>(p);
   return cudaGetLastError();
 }
 

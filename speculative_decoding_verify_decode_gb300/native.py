@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from array import array
 
 import numpy as np
 import torch
@@ -120,7 +121,7 @@ def load() -> ctypes.CDLL:
     lib.sd_pages_release.restype = i32
     lib.sd_pages_release.argtypes = [i32, i32, i32] + [vp] * 8 + [vp]
     lib.sd_kv8_append.restype = i32
-    lib.sd_kv8_append.argtypes = [i32] * 5 + [pp] * 6 + [i64, i32, vp, vp, i32, vp, vp]
+    lib.sd_kv8_append.argtypes = [i32] * 5 + [vp] * 6 + [i64, i32, vp, vp, i32, vp, vp]
     lib.sd_kv8_attn_workspace_size.restype = sz
     lib.sd_kv8_attn_workspace_size.argtypes = [shp]
     lib.sd_kv8_attn.restype = i32
@@ -171,6 +172,11 @@ class Shape:
         self.c = SdShape(len(self.indptr) - 1, ctypes.cast(self.indptr, ctypes.POINTER(ctypes.c_int)),
                          int(num_q_heads), int(num_kv_heads), int(head_dim), 16, int(max_pages_per_seq),
                          int(num_pool_pages), int(num_splits), int(window), int(bool(ctx_stable)))
+        n, c = int(self.indptr[len(self.indptr) - 1]), self.c
+        # shapes of sd_kv8_attn's tensors: q and out, k_new and v_new, codes, scales, page table, per sequence, per node
+        self.dims = ((n, c.num_q_heads, c.head_dim), (n, c.num_kv_heads, c.head_dim),
+                     (c.num_pool_pages, c.num_kv_heads, 16, c.head_dim), (c.num_pool_pages, c.num_kv_heads),
+                     (c.batch, c.max_pages_per_seq), (c.batch,), (n,))
 
     def with_ctx_stable(self, ctx_stable: bool = True) -> "Shape":
         """The same shape with the context-stable launch flag set (see sd_shape.ctx_stable)."""
@@ -364,63 +370,102 @@ def sd_gdn_commit(shape: GdnShape, state_layers, tree_cache_layers, accept_len, 
 
 
 # ---------------------------------------------------------------- the 8-bit block-scaled cache (include/sd_kv8.h)
+#
+# These calls check types, shapes, layouts and devices here.  A call is a few microseconds of Python beside a few of
+# GPU time at the smallest sizes, so the checks are plain comparisons and what they refuse is explained elsewhere.
 
-def _tensor(t, what: str, dtype, shape, device) -> int:
-    """Address of a dense tensor of this type and shape (None in the shape: any size) on `device`."""
-    if t.dtype is not dtype or t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
-        raise ValueError(f"{what}: {dtype} {shape} expected, got {t.dtype} {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{what} is on {t.device}, the other tensors on {device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{what} must be contiguous")
-    return t.data_ptr()
-
-
-def _optional(t, what: str, dtype, shape, device) -> int | None:
-    return None if t is None else _tensor(t, what, dtype, shape, device)
+def _refuse(t, what: str, dtype, shape, index: int):
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{what}: a tensor is needed, got {type(t).__name__}")
+    if t.dtype is not dtype or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what}: {dtype} {tuple(shape)} expected, got {t.dtype} {tuple(t.shape)}")
+    if t.get_device() != index:
+        raise ValueError(f"{what} is on {t.device}, other tensors are not")
+    raise ValueError(f"{what} must be contiguous" if t.dim() != 3 else f"{what}: the heads of a row must be contiguous")
 
 
-def _rows(t, what: str, heads: int, dim: int, device) -> tuple[int, int]:
+def _tensor(t, what: str, dtype, shape, index: int) -> int:
+    """Address of a dense tensor of this type and shape on device `index`."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _refuse(t, what, dtype, shape, index)
+
+
+def _rows(t, what: str, shape, index: int) -> tuple[int, int]:
     """Address and row stride (0: dense) of bf16 [rows, heads, dim]; the rows may lie apart, a row is dense."""
-    if t.dtype is not torch.bfloat16 or t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
-        raise ValueError(f"{what}: torch.bfloat16 [rows, {heads}, {dim}] expected, got {t.dtype} {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{what} is on {t.device}, the other tensors on {device}")
-    if t.is_contiguous():
-        return t.data_ptr(), 0
-    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim):
-        raise ValueError(f"{what}: the heads of a row must be contiguous")
-    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else 0
+    if t.dtype is torch.bfloat16 and t.shape == shape and t.get_device() == index:
+        if t.is_contiguous():
+            return t.data_ptr(), 0
+        if t.stride(2) == 1 and (shape[1] == 1 or t.stride(1) == shape[2]):
+            return t.data_ptr(), t.stride(0) if shape[0] > 1 else 0
+    _refuse(t, what, torch.bfloat16, shape, index)
 
 
-def _on(device, stream, call) -> int:
-    """call(stream handle) with `device` current; the default stream is the device's current one."""
-    if device.type != "cuda":
-        raise ValueError("the tensors must be on a CUDA device")
-    if torch.cuda.current_device() == device.index:
-        return call(_stream(stream))
-    with torch.cuda.device(device):
-        return call(_stream(stream))
+_array_types = {}
 
 
-def _layer_ptrs(x, what: str, dtype, shape, device):
-    """Device addresses of per-layer tensors: a list of them, or one tensor with a leading layer dimension."""
+def _array(ctype, values):
+    """A ctypes array; its type is made once per length (making one takes longer than a call)."""
+    key = (ctype, len(values))
+    kind = _array_types.get(key)
+    if kind is None:
+        kind = _array_types[key] = ctype * key[1]
+    return kind(*values)
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _run(call, what: str, args, index: int, stream) -> None:
+    """call(*args, stream) with device `index` current; the default stream is the device's current one."""
+    if index < 0:
+        raise ValueError(f"{what}: the tensors must be on a CUDA device")
+    if stream is not None:
+        stream = stream if isinstance(stream, int) else stream.cuda_stream
+    elif _raw_stream is not None:
+        stream = _raw_stream(index)
+    else:
+        stream = torch.cuda.current_stream(index).cuda_stream
+    if torch.cuda.current_device() == index:
+        status = call(*args, stream)
+    else:
+        with torch.cuda.device(index):
+            status = call(*args, stream)
+    if status != SD_OK:
+        raise SdError(status, what)
+
+
+def _put_layers(ptrs, x, n: int, what: str, dtype, shape, nbytes: int, index: int) -> None:
+    """Append the device addresses of n per-layer tensors (a list of them, or one tensor with a leading layer dimension)."""
     if isinstance(x, torch.Tensor):
-        base = _tensor(x, what, dtype, (None,) + shape, device)
-        step = x.stride(0) * x.element_size()
-        return (ctypes.c_void_p * x.shape[0])(*range(base, base + step * x.shape[0], step)) if step else None
-    return (ctypes.c_void_p * len(x))(*[_tensor(t, what, dtype, shape, device) for t in x])
+        base = _tensor(x, what, dtype, (n, *shape), index)
+        ptrs.extend([base + nbytes * i for i in range(n)])
+    elif len(x) == n:
+        ptrs.extend([_tensor(t, what, dtype, shape, index) for t in x])
+    else:
+        raise ValueError(f"{what}: {n} layers expected, got {len(x)}")
 
 
-def _layer_rows(x, what: str, heads: int, dim: int, device):
-    """Addresses, common row stride and row count of per-layer [rows, heads, dim] tensors (a list or one tensor)."""
-    got = [_rows(t, what, heads, dim, device) for t in x]
-    if any(s != got[0][1] for _, s in got) or any(t.shape[0] != x[0].shape[0] for t in x):
-        raise ValueError(f"{what}: the layers differ in rows or row stride")
-    return (ctypes.c_void_p * len(got))(*[a for a, _ in got]), got[0][1], int(x[0].shape[0])
+def _put_rows(ptrs, x, n: int, what: str, heads: int, dim: int, index: int) -> tuple[int, int]:
+    """The same for per-layer bf16 [rows, heads, dim]; returns the layers' common row stride and row count."""
+    if isinstance(x, torch.Tensor) and x.dim() == 4 and x.is_contiguous():
+        rows = x.shape[1]
+        _put_layers(ptrs, x, n, what, torch.bfloat16, (rows, heads, dim), 2 * rows * heads * dim, index)
+        return 0, rows
+    if len(x) != n:
+        raise ValueError(f"{what}: {n} layers expected, got {len(x)}")
+    rows = x[0].shape[0] if x[0].dim() else 0
+    got = [_rows(t, what, (rows, heads, dim), index) for t in x]
+    if any(s != got[0][1] for _, s in got):
+        raise ValueError(f"{what}: the layers differ in row stride")
+    ptrs.extend([a for a, _ in got])
+    return got[0][1], rows
 
 
-_I32, _F32 = torch.int32, torch.float32
+_I32, _F32, _U8 = torch.int32, torch.float32, torch.uint8
 
 
 def sd_pages_extend(ctx_lens, add_lens, page_table, held, new_held, free_list, free_count, new_free_count, slots,
@@ -428,36 +473,51 @@ def sd_pages_extend(ctx_lens, add_lens, page_table, held, new_held, free_list, f
                     stream=None) -> None:
     """Pages and slot map for the ``add_lens`` tokens that join every sequence; with ``path`` (and the host
     ``q_indptr``) the accepted nodes of sd_accept, whose ``accept_len`` is ``add_lens``."""
-    dev = page_table.device
-    table = _tensor(page_table, "page_table", _I32, (None, None), dev)
-    batch, max_pages = page_table.shape
-    each = lambda t, what, n=batch: _optional(t, what, _I32, (n,), dev)
-    if held is None or new_held is None or ctx_lens is None or add_lens is None:
-        raise ValueError("ctx_lens, add_lens, held and new_held are needed")
-    ind = None if q_indptr is None else _indptr(q_indptr)
-    if ind is not None and len(ind) != batch + 1:
-        raise ValueError("q_indptr has one entry more than the page table has rows")
-    path_at = _optional(path, "path", _I32, (batch, None), dev)
-    args = (batch, max_pages, free_list.shape[0], each(ctx_lens, "ctx_lens"), each(add_lens, "add_lens"), ind, path_at,
-            0 if path is None else path.shape[1], table, each(held, "held"), each(new_held, "new_held"),
-            each(free_list, "free_list", None), each(free_count, "free_count", 1),
-            each(new_free_count, "new_free_count", 1), slots.shape[0], each(slots, "slots", None),
-            each(rows, "rows", slots.shape[0]), each(row_indptr, "row_indptr", batch + 1),
-            each(new_ctx_lens, "new_ctx_lens"), each(dev_status, "dev_status", 1))
-    _check(_on(dev, stream, lambda s: load().sd_pages_extend(*args, s)), "sd_pages_extend")
+    dev = page_table.get_device()
+    if page_table.dim() != 2 or slots.dim() != 1 or free_list.dim() != 1:
+        raise ValueError("page_table is [batch, pages], slots and free_list are one-dimensional")
+    table_shape = page_table.shape
+    batch, max_pages = table_shape
+    each, one, max_rows, pool = (batch,), (1,), slots.shape[0], free_list.shape[0]
+    ind, path_at, max_path = None, None, 0
+    if q_indptr is not None or path is not None:
+        if q_indptr is not None:
+            ind = _array(ctypes.c_int, q_indptr if isinstance(q_indptr, list) else np.asarray(q_indptr).tolist())
+        if ind is not None and len(ind) != batch + 1:
+            raise ValueError("q_indptr has one entry more than the page table has rows")
+        if path is not None:
+            max_path = path.shape[-1] if path.dim() else 0
+            path_at = _tensor(path, "path", _I32, (batch, max_path), dev)
+    args = (batch, max_pages, pool, _tensor(ctx_lens, "ctx_lens", _I32, each, dev),
+            _tensor(add_lens, "add_lens", _I32, each, dev), ind, path_at, max_path,
+            _tensor(page_table, "page_table", _I32, table_shape, dev), _tensor(held, "held", _I32, each, dev),
+            _tensor(new_held, "new_held", _I32, each, dev), _tensor(free_list, "free_list", _I32, (pool,), dev),
+            _tensor(free_count, "free_count", _I32, one, dev),
+            _tensor(new_free_count, "new_free_count", _I32, one, dev), max_rows,
+            _tensor(slots, "slots", _I32, (max_rows,), dev),
+            None if rows is None else _tensor(rows, "rows", _I32, (max_rows,), dev),
+            None if row_indptr is None else _tensor(row_indptr, "row_indptr", _I32, (batch + 1,), dev),
+            None if new_ctx_lens is None else _tensor(new_ctx_lens, "new_ctx_lens", _I32, each, dev),
+            None if dev_status is None else _tensor(dev_status, "dev_status", _I32, one, dev))
+    _run(load().sd_pages_extend, "sd_pages_extend", args, dev, stream)
 
 
 def sd_pages_release(keep_lens, page_table, held, new_held, free_list, free_count, new_free_count, dev_status=None,
                      stream=None) -> None:
     """Pages behind the first ``keep_lens`` tokens of every sequence back on the free list."""
-    dev = page_table.device
-    table = _tensor(page_table, "page_table", _I32, (None, None), dev)
-    batch, max_pages = page_table.shape
-    each = lambda t, what, n=batch: _tensor(t, what, _I32, (n,), dev)
-    args = (batch, max_pages, free_list.shape[0], each(keep_lens, "keep_lens"), table, each(held, "held"),
-            each(new_held, "new_held"), each(free_list, "free_list", None), each(free_count, "free_count", 1),
-            each(new_free_count, "new_free_count", 1), _optional(dev_status, "dev_status", _I32, (1,), dev))
-    _check(_on(dev, stream, lambda s: load().sd_pages_release(*args, s)), "sd_pages_release")
+    dev = page_table.get_device()
+    if page_table.dim() != 2 or free_list.dim() != 1:
+        raise ValueError("page_table is [batch, pages], free_list is one-dimensional")
+    table_shape = page_table.shape
+    batch, max_pages = table_shape
+    each, one, pool = (batch,), (1,), free_list.shape[0]
+    args = (batch, max_pages, pool, _tensor(keep_lens, "keep_lens", _I32, each, dev),
+            _tensor(page_table, "page_table", _I32, table_shape, dev), _tensor(held, "held", _I32, each, dev),
+            _tensor(new_held, "new_held", _I32, each, dev), _tensor(free_list, "free_list", _I32, (pool,), dev),
+            _tensor(free_count, "free_count", _I32, one, dev),
+            _tensor(new_free_count, "new_free_count", _I32, one, dev),
+            None if dev_status is None else _tensor(dev_status, "dev_status", _I32, one, dev))
+    _run(load().sd_pages_release, "sd_pages_release", args, dev, stream)
 
 
 def sd_kv8_append(k_cache_layers, v_cache_layers, k_scale_layers, v_scale_layers, k_new_layers, v_new_layers, slots,
@@ -466,23 +526,34 @@ def sd_kv8_append(k_cache_layers, v_cache_layers, k_scale_layers, v_scale_layers
 
     Per layer (lists, or tensors with a leading layer dimension): codes uint8 [pool, heads, 16, dim], scales fp32
     [pool, heads], new rows bf16 [rows, heads, dim] (rows may lie apart)."""
-    dev = slots.device
-    n = len(k_cache_layers)
-    if n == 0 or any(len(x) != n for x in (v_cache_layers, k_scale_layers, v_scale_layers, k_new_layers, v_new_layers)):
-        raise ValueError("per-layer lists are empty or differ in length")
-    pool, heads, page, dim = k_cache_layers[0].shape
-    codes = [_layer_ptrs(x, w, torch.uint8, (pool, heads, page, dim), dev)
-             for x, w in ((k_cache_layers, "k_cache"), (v_cache_layers, "v_cache"))]
-    scales = [_layer_ptrs(x, w, _F32, (pool, heads), dev)
-              for x, w in ((k_scale_layers, "k_scales"), (v_scale_layers, "v_scales"))]
-    (k_new, stride, src), (v_new, v_stride, v_src) = (
-        _layer_rows(x, w, heads, dim, dev) for x, w in ((k_new_layers, "k_new"), (v_new_layers, "v_new")))
-    if stride != v_stride or src != v_src:
+    dev, first = slots.get_device(), k_cache_layers
+    if not isinstance(first, torch.Tensor):
+        if not first:
+            raise ValueError("no layers")
+        n, cache = len(first), tuple(first[0].shape)
+    else:
+        n, *cache = first.shape if first.dim() else (0,)
+        cache = tuple(cache)
+    if len(cache) != 4 or slots.dim() != 1:
+        raise ValueError("a layer's cache is [pool, heads, 16, dim], slots is one-dimensional")
+    pool, heads, page, dim = cache
+    max_rows = slots.shape[0]
+    block, codes = (pool, heads), pool * heads * page * dim
+    ptrs = array("Q")      # the six arrays of n addresses, one behind the other
+    _put_layers(ptrs, first, n, "k_cache", _U8, cache, codes, dev)
+    _put_layers(ptrs, v_cache_layers, n, "v_cache", _U8, cache, codes, dev)
+    _put_layers(ptrs, k_scale_layers, n, "k_scales", _F32, block, 4 * pool * heads, dev)
+    _put_layers(ptrs, v_scale_layers, n, "v_scales", _F32, block, 4 * pool * heads, dev)
+    stride, src = _put_rows(ptrs, k_new_layers, n, "k_new", heads, dim, dev)
+    if (stride, src) != _put_rows(ptrs, v_new_layers, n, "v_new", heads, dim, dev):
         raise ValueError("k_new and v_new differ in rows or row stride")
-    args = (n, heads, dim, page, pool, *codes, *scales, k_new, v_new, stride, src,
-            _tensor(slots, "slots", _I32, (None,), dev), _optional(rows, "rows", _I32, (slots.shape[0],), dev),
-            slots.shape[0], _optional(dev_status, "dev_status", _I32, (1,), dev))
-    _check(_on(dev, stream, lambda s: load().sd_kv8_append(*args, s)), "sd_kv8_append")
+    at, step = ptrs.buffer_info()[0], 8 * n
+    args = (n, heads, dim, page, pool, at, at + step, at + 2 * step, at + 3 * step, at + 4 * step, at + 5 * step, stride,
+            src,
+            _tensor(slots, "slots", _I32, (max_rows,), dev),
+            None if rows is None else _tensor(rows, "rows", _I32, (max_rows,), dev), max_rows,
+            None if dev_status is None else _tensor(dev_status, "dev_status", _I32, (1,), dev))
+    _run(load().sd_kv8_append, "sd_kv8_append", args, dev, stream)
 
 
 def sd_kv8_attn_workspace_size(shape: Shape) -> int:
@@ -494,25 +565,24 @@ def sd_kv8_attn(shape: Shape, q, k_cache, v_cache, k_scales, v_scales, k_new, v_
                 stream=None) -> None:
     """sd_verify_attn over the block-scaled cache; ``softcap`` and ``slopes`` (fp32 [query heads]) as in sd_kv8_opts.
     q, k_new and v_new may have rows that lie apart (slices of a fused projection)."""
-    c, dev = shape.c, q.device
-    hq, hkv, dim, n, pool = c.num_q_heads, c.num_kv_heads, c.head_dim, shape.indptr[-1], c.num_pool_pages
-    for t, what in ((q, "q"), (k_new, "k_new"), (v_new, "v_new")):
-        if t.shape[0] != n:
-            raise ValueError(f"{what}: {n} rows expected, got {t.shape[0]}")
-    (q_at, qs), (k_at, ks), (v_at, vs) = (_rows(q, "q", hq, dim, dev), _rows(k_new, "k_new", hkv, dim, dev),
-                                          _rows(v_new, "v_new", hkv, dim, dev))
-    opts = SdKv8Opts(scale, softcap, _optional(slopes, "slopes", _F32, (hq,), dev), qs, ks, vs)
-    cache, block = (pool, hkv, c.page_size, dim), (pool, hkv)
-    ws_bytes = 0
+    dev = q.get_device()
+    q_shape, kv_shape, cache, block, table, batch, n = shape.dims
+    q_at, qs = _rows(q, "q", q_shape, dev)
+    k_at, ks = _rows(k_new, "k_new", kv_shape, dev)
+    v_at, vs = _rows(v_new, "v_new", kv_shape, dev)
+    opts = None
+    if scale or softcap or qs or ks or vs or slopes is not None:
+        opts = ctypes.byref(SdKv8Opts(scale, softcap, None if slopes is None else
+                                      _tensor(slopes, "slopes", _F32, (q_shape[1],), dev), qs, ks, vs))
+    ws_at, ws_bytes = None, 0
     if workspace is not None:
-        if workspace.device != dev or not workspace.is_contiguous():
-            raise ValueError("workspace must be contiguous and on the tensors' device")
         ws_bytes = workspace.numel() * workspace.element_size()
-    args = (shape.ref, ctypes.byref(opts), q_at, _tensor(k_cache, "k_cache", torch.uint8, cache, dev),
-            _tensor(v_cache, "v_cache", torch.uint8, cache, dev), _tensor(k_scales, "k_scales", _F32, block, dev),
+        ws_at = _tensor(workspace, "workspace", workspace.dtype, workspace.shape, dev)
+    args = (shape.ref, opts, q_at, _tensor(k_cache, "k_cache", _U8, cache, dev),
+            _tensor(v_cache, "v_cache", _U8, cache, dev), _tensor(k_scales, "k_scales", _F32, block, dev),
             _tensor(v_scales, "v_scales", _F32, block, dev), k_at, v_at,
-            _tensor(page_table, "page_table", _I32, (c.batch, c.max_pages_per_seq), dev),
-            _tensor(ctx_lens, "ctx_lens", _I32, (c.batch,), dev), _tensor(parents, "parents", _I32, (n,), dev),
-            _tensor(out, "out", torch.bfloat16, (n, hq, dim), dev), _optional(lse, "lse", _F32, (n, hq), dev),
-            _ptr(workspace), ws_bytes, _optional(dev_status, "dev_status", _I32, (1,), dev))
-    _check(_on(dev, stream, lambda s: load().sd_kv8_attn(*args, s)), "sd_kv8_attn")
+            _tensor(page_table, "page_table", _I32, table, dev), _tensor(ctx_lens, "ctx_lens", _I32, batch, dev),
+            _tensor(parents, "parents", _I32, n, dev), _tensor(out, "out", torch.bfloat16, q_shape, dev),
+            None if lse is None else _tensor(lse, "lse", _F32, q_shape[:2], dev), ws_at, ws_bytes,
+            None if dev_status is None else _tensor(dev_status, "dev_status", _I32, (1,), dev))
+    _run(load().sd_kv8_attn, "sd_kv8_attn", args, dev, stream)
