@@ -54,7 +54,7 @@ __device__ __forceinline__ int page_of(const PagesParams& p, const int* held, co
 }
 
 template <bool PATH>
-__global__ void __launch_bounds__(PATH ? kPathThreads : kPagesThreads)
+__global__ void __launch_bounds__(PATH ? kPathThreads : kPagesThreads, PATH ? 1 : 6)
 pages_extend_kernel(const PagesParams p, const BatchDesc bd) {
   __shared__ int s_row[kMaxBatch + 1], s_page[kMaxBatch + 1];   // first row / first new page of each sequence
   __shared__ int s_ctx[kMaxBatch], s_held[kMaxBatch];
@@ -127,55 +127,71 @@ pages_extend_kernel(const PagesParams p, const BatchDesc bd) {
   // The slot map: a warp takes 512 consecutive rows at a time, a lane four quads of rows (one 16-byte store each, lanes
   // side by side) whose page lookups are all in flight together; behind the last row: -1.  The warp searches its first
   // row's sequence once, lanes walk on from there.
-  const int n_rows = ok ? s_row[B] : 0;
+  const unsigned n_rows = ok ? (unsigned)s_row[B] : 0u, max_rows = (unsigned)p.max_rows;
   bool bad_page = false;
-  constexpr int U = 4;
-  const int lane = t & 31;
-  for (long long w0 = (long long)(first - lane) * (4 * U); w0 < p.max_rows; w0 += (long long)step * (4 * U)) {
-    int b0 = w0 < n_rows ? find_seq(s_row, B, (int)w0) : 0;
-    int seq[U], pos[U], page[U];
+  constexpr unsigned U = 4;
+  const unsigned lane = t & 31;
+  auto slot_of = [&](int page, unsigned pos) {
+    const bool in = (unsigned)page < (unsigned)p.num_pool_pages;
+    bad_page |= !in;
+    return in ? page * kPage + (int)(pos % kPage) : -1;
+  };
+  // first * 16 rows is below 2^31 for every warp with work; the step keeps within 2^32 of it
+  for (unsigned w0 = ((unsigned)first - lane) * (4 * U); w0 < max_rows; w0 += (unsigned)step * (4 * U)) {
+    const int b0 = w0 < n_rows ? find_seq(s_row, B, (int)w0) : 0;
+    int seq[U], page[U], page2[U];
+    unsigned pos[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const long long r = w0 + 128 * u + 4 * lane;
+    for (unsigned u = 0; u < U; ++u) {
+      const unsigned r = w0 + 128 * u + 4 * lane;
       seq[u] = -1;
+      pos[u] = 0;
+      page[u] = page2[u] = -1;
       if (r < n_rows) {
-        while ((int)r >= s_row[b0 + 1]) ++b0;      // ends: r < s_row[B]
-        seq[u] = b0;
-        pos[u] = s_ctx[b0] + (int)r - s_row[b0];
-        page[u] = page_of(p, s_held, s_page, count, b0, pos[u] / kPage);
+        const int b = (int)r < s_row[b0 + 1] ? b0 : find_seq(s_row, B, (int)r);
+        seq[u] = b;
+        pos[u] = (unsigned)(s_ctx[b] + (int)r - s_row[b]);
+        page[u] = page_of(p, s_held, s_page, count, b, (int)(pos[u] / kPage));
+        // the page that the quad's last row lands on, if it is another and the sequence's
+        if (pos[u] % kPage > kPage - 4 && (int)r + 3 < s_row[b + 1])
+          page2[u] = page_of(p, s_held, s_page, count, b, (int)(pos[u] / kPage) + 1);
       }
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const long long r0 = w0 + 128 * u + 4 * lane;
-      int slot[4], src[4];
-      int b = seq[u], j = b >= 0 ? pos[u] / kPage : 0;
+    for (unsigned u = 0; u < U; ++u) {
+      const unsigned r0 = w0 + 128 * u + 4 * lane;
+      if (r0 >= max_rows) break;
+      int slot[4] = {-1, -1, -1, -1}, src[4] = {-1, -1, -1, -1};
+      const int b = seq[u];
+      if (b >= 0 && (int)r0 + 3 < s_row[b + 1]) {      // four rows of one sequence, on one page or two
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const long long r = r0 + k;
-        slot[k] = src[k] = -1;
-        if (r < n_rows) {
-          int at = b;
-          while ((int)r >= s_row[at + 1]) ++at;
-          const int i = (int)r - s_row[at], x = s_ctx[at] + i;
-          if (at != b || x / kPage != j) {         // the quad ends a page or a sequence
-            b = at;
-            j = x / kPage;
-            page[u] = page_of(p, s_held, s_page, count, b, j);
+        for (unsigned k = 0; k < 4; ++k) {
+          slot[k] = slot_of(pos[u] % kPage + k < kPage ? page[u] : page2[u], pos[u] + k);
+          src[k] = PATH ? bd.q_indptr[b] + p.path[(size_t)b * p.max_path + ((int)(r0 + k) - s_row[b])] : (int)(r0 + k);
+        }
+      } else if (b >= 0) {                             // a sequence, or all rows, end in the quad
+        int at = b;
+#pragma unroll 1
+        for (unsigned k = 0; k < 4 && r0 + k < n_rows; ++k) {
+          const int r = (int)(r0 + k);
+          while (r >= s_row[at + 1]) ++at;             // ends: r < s_row[B]
+          const unsigned x = (unsigned)(s_ctx[at] + r - s_row[at]);
+          const int s = slot_of(page_of(p, s_held, s_page, count, at, (int)(x / kPage)), x);
+          const int from = PATH ? bd.q_indptr[at] + p.path[(size_t)at * p.max_path + (r - s_row[at])] : r;
+#pragma unroll
+          for (unsigned e = 0; e < 4; ++e) {
+            slot[e] = e == k ? s : slot[e];
+            src[e] = e == k ? from : src[e];
           }
-          const bool in = page[u] >= 0 && page[u] < p.num_pool_pages;
-          bad_page |= !in;
-          slot[k] = in ? page[u] * kPage + x % kPage : -1;
-          src[k] = PATH ? bd.q_indptr[at] + p.path[(size_t)at * p.max_path + i] : (int)r;
         }
       }
-      if (r0 + 4 <= p.max_rows && p.vec) {
+      if (max_rows - r0 >= 4 && p.vec) {
         *reinterpret_cast<int4*>(p.slots + r0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
         if (p.rows != nullptr) *reinterpret_cast<int4*>(p.rows + r0) = make_int4(src[0], src[1], src[2], src[3]);
       } else {
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (r0 + k < p.max_rows) {
+        for (unsigned k = 0; k < 4; ++k)
+          if (k < max_rows - r0) {
             p.slots[r0 + k] = slot[k];
             if (p.rows != nullptr) p.rows[r0 + k] = src[k];
           }
@@ -229,7 +245,7 @@ __global__ void __launch_bounds__(kPagesThreads) pages_release_kernel(const Page
 
 int blocks_for(long long elements, int per_block) {
   const long long n = (elements + per_block - 1) / per_block;
-  return (int)(n < 1 ? 1 : n > 8 * kSMs ? 8 * kSMs : n);   // one wave at most
+  return (int)(n < 1 ? 1 : n > 6 * kSMs ? 6 * kSMs : n);   // one wave at most
 }
 
 }  // namespace
