@@ -23,7 +23,7 @@
 namespace sdv {
 namespace {
 
-constexpr int kAppendThreads = 256;
+constexpr int kAppendThreads = 128;
 constexpr int kMinExp = SD_KV8_MIN_SCALE_EXP, kMaxExp = SD_KV8_MAX_SCALE_EXP;
 
 __device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }   // -126 <= e <= 127
@@ -58,7 +58,7 @@ __device__ __forceinline__ uint32_t requantise4(uint32_t c, float ratio) {
 // D: head_dim.  A CTA looks at `window` rows of the slot map; each row that
 // begins a page there gives 2 * heads warp tasks.
 template <int D>
-__global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(const Kv8AppendParams p, const int window) {
+__global__ void __launch_bounds__(kAppendThreads, 6) kv8_append_kernel(const Kv8AppendParams p, const int window) {
   constexpr int kLanes = D / 8;            // lanes per row (8 values each)
   constexpr int kRowsAtOnce = 32 / kLanes; // rows a warp touches per step
   constexpr int kSteps = kPage / kRowsAtOnce;
@@ -84,7 +84,7 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(const Kv8App
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int combos = 2 * p.heads;
   const int col = lane % kLanes, sub = lane / kLanes;
-  for (int task = warp; task < s_n * combos; task += kAppendThreads / 32) {
+  for (int task = blockIdx.z * (kAppendThreads / 32) + warp; task < s_n * combos; task += gridDim.z * (kAppendThreads / 32)) {
     const int r0 = s_lead[task / combos], combo = task % combos;
     const int head = combo >> 1;
     const bool is_v = combo & 1;
@@ -176,7 +176,9 @@ cudaError_t launch_kv8_append(const Kv8AppendParams& p, cudaStream_t st) {
   // Rows per CTA: a row of its own while that fills the machine about twice over at most (single tokens of
   // a batch, an accepted path); for prompts sixteen, of which one begins a page.
   const int window = (long long)p.max_rows * p.num_layers <= 4 * kSMs ? 1 : kPage;
-  const dim3 grid((p.max_rows + window - 1) / window, p.num_layers);
+  // enough CTAs per window for one page's tasks, a warp each
+  const int share = (2 * p.heads + kAppendThreads / 32 - 1) / (kAppendThreads / 32);
+  const dim3 grid((p.max_rows + window - 1) / window, p.num_layers, share);
   if (p.dim == 256)
     kv8_append_kernel<256><<<grid, kAppendThreads, 0, st>>>(p, window);
   else
