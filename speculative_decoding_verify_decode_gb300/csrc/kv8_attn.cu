@@ -148,7 +148,7 @@ struct Layout {
 };
 Layout layout_of(const Kv8Plan& pl, int hkv, int dim, const BatchDesc& bd, int sms) {
   // a piece and a segment name a partial; along the line of units their numbers rise together
-  const size_t slots = (size_t)sms + (size_t)bd.batch * hkv * pl.hparts;
+  const size_t slots = (size_t)sms * pl.ctas + (size_t)bd.batch * hkv * pl.hparts;
   Layout l;
   l.o = align_up((kMaxBatch + 3) * sizeof(int));
   l.lse = l.o + align_up(slots * pl.nq * dim * sizeof(__nv_bfloat16));
@@ -158,9 +158,13 @@ Layout layout_of(const Kv8Plan& pl, int hkv, int dim, const BatchDesc& bd, int s
 
 }  // namespace
 
-// Query columns of a CTA: as many heads of a KV group as fit, so that the cache is read as few times as can be.
-Kv8Plan kv8_plan(int group, int max_nodes, int dim, bool mod) {
-  // capped or biased scores over 256 dims: the wider columns' slopes and depths find no room beside the operands
+// Query columns of a CTA: as many heads of a KV group as fit, so that the cache is read as few times as can be (capped
+// or biased scores over 256 dims stop at 96: the wider columns' slopes find no room beside the operands).  Up to 16
+// columns, i.e. single tokens, two CTAs share an SM (64 sequences, 1 to 32768 tokens, 128 dims: 389 us against 456 for
+// one).  17 to 32 columns do so when there are segments enough to fill both (64 sequences of 8 nodes, 128 dims: 208 us
+// against 228; 8 sequences: 39 against 44), and otherwise take one CTA of three softmax groups, whose single tile is
+// shorter (one sequence of 8 nodes over 8192 tokens: 17.5 us against 20.3).
+Kv8Plan kv8_plan(int group, int max_nodes, int dim, bool mod, int kv_rows) {
   const int most = mod && dim == 256 ? 96 : 144;
   Kv8Plan pl;
   pl.hparts = 1;
@@ -168,26 +172,29 @@ Kv8Plan kv8_plan(int group, int max_nodes, int dim, bool mod) {
   pl.hpc = (group + pl.hparts - 1) / pl.hparts;
   pl.hparts = (group + pl.hpc - 1) / pl.hpc;
   const int cols = pl.hpc * max_nodes;
-  pl.nq = cols <= 16 ? 16 : cols <= 48 ? 48 : cols <= 96 ? 96 : 144;
+  const bool two = cols <= 16 || (cols <= 32 && kv_rows * pl.hparts >= 64);
+  pl.nq = two ? (cols <= 16 ? 16 : 32) : cols <= 48 ? 48 : cols <= 96 ? 96 : 144;
+  pl.ctas = two ? 2 : 1;
   return pl;
 }
 
 size_t kv8_attn_workspace(int hq, int hkv, int dim, const BatchDesc& bd) {
   // the query does not know whether scores will be capped or biased
   const int sms = sm_count();
-  const size_t a = layout_of(kv8_plan(hq / hkv, bd.max_nodes, dim, false), hkv, dim, bd, sms).total;
-  const size_t b = layout_of(kv8_plan(hq / hkv, bd.max_nodes, dim, true), hkv, dim, bd, sms).total;
+  const size_t a = layout_of(kv8_plan(hq / hkv, bd.max_nodes, dim, false, bd.batch * hkv), hkv, dim, bd, sms).total;
+  const size_t b = layout_of(kv8_plan(hq / hkv, bd.max_nodes, dim, true, bd.batch * hkv), hkv, dim, bd, sms).total;
   return a > b ? a : b;
 }
 
 cudaError_t launch_kv8_attn(Kv8AttnParams p, const BatchDesc& bd, cudaStream_t st) {
   const bool mod = p.softcap > 0.f || p.slopes != nullptr;
-  const Kv8Plan pl = kv8_plan(p.group, bd.max_nodes, p.dim, mod);
+  const Kv8Plan pl = kv8_plan(p.group, bd.max_nodes, p.dim, mod, bd.batch * p.hkv);
   p.hpc = pl.hpc;
   p.hparts = pl.hparts;
   p.nq = pl.nq;
-  p.grid = sm_count();
-  const Layout l = layout_of(pl, p.hkv, p.dim, bd, p.grid);
+  const int sms = sm_count();
+  p.grid = sms * pl.ctas;
+  const Layout l = layout_of(pl, p.hkv, p.dim, bd, sms);
   char* ws = static_cast<char*>(p.workspace);
   p.cum = reinterpret_cast<int*>(ws);
   p.o_part = reinterpret_cast<__nv_bfloat16*>(ws + l.o);

@@ -9,9 +9,9 @@
 // so a V scale goes into the weight and a K scale into the score, each one
 // multiplication per score, constant along a token row, and the tensor core
 // never sees anything but codes.  m is the running maximum of s + log2 c_t
-// less kHead: the weights e c_t stay at or below 2^kHead however uneven the
-// blocks are, and m moves (with O and l rescaled) only when a weight passes
-// kTop, the largest e4m3 value.
+// less a few bits: the weights e c_t stay near 1 however uneven the blocks are,
+// and m moves (with O and l rescaled) only when a weight passes kTop, the
+// largest e4m3 value.
 //
 // The 8-bit operands.  K and V are exact as they lie.  A bf16 query is two
 // e4m3 terms (a power-of-two scale for all the CTA's queries, then the rounded
@@ -61,12 +61,14 @@ namespace sdv {
 namespace {
 
 constexpr int kTile = kTileTokens;
-constexpr float kHead = 5.0f;          // the largest weight sits at 2^5 when m is exact
 constexpr float kTop = 448.0f;         // weights beyond it move m
+// Where the largest weight so far sits after m moved: at 2^3 when m is set by a column's first tile, whose maximum is
+// likely to be passed by some nats further on, at 2^5 when it was passed by so much that m had to move.  Higher keeps
+// more of the small weights' bits, lower lets the maximum grow further before the next move (a move costs a tile 2 us).
+constexpr float kHeadFirst = 3.0f, kHeadNext = 5.0f;
 constexpr float kDown = 0x1p-8f;       // weights are formed times 2^-8 (see split4)
 constexpr float kScaleLo = 0x1p-100f, kScaleHi = 0x1p100f;
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kSmemBytes = 232448;     // 227 KB of dynamic shared memory per CTA
 constexpr int kScaleStages = 6;
 
 // TIGHT: 144 columns of 256 dims leave 7 KB beside the operands and seven 16 KB half tiles.
@@ -75,8 +77,7 @@ struct KvSmall {
   static constexpr int kBars = TIGHT ? 24 : 40;
   float m[NQ];             // the column's reference, negated: -m
   float alpha[NQ];         // rescale factor of the current tile; 1 / l in the epilogue
-  float slope[MOD ? NQ : 4];   // distance bias (base 2) and depth of the column's node
-  float dep[MOD ? NQ : 4];
+  float slope[MOD ? NQ : 4];   // distance bias of the column, base 2
   float red[4][NQ];        // per lane quarter: column maxima of a tile; column sums in the epilogue
   float scale[kScaleStages][16];   // K scales, then V scales, of a tile's eight pages
   float row_k[kMaxNodes], row_v[kMaxNodes];   // scales of the draft block's rows
@@ -98,6 +99,9 @@ struct Kv {
   static constexpr int NQ = NG * CC * 16;                 // query columns
   static constexpr int kWarps = NG * 4, kThreads = (kWarps + 4) * 32;
   using Small = KvSmall<NQ, MOD, NQ == 144 && D == 256>;
+  // One group: a tile is a chain of short steps (scores, weights, products), and a second CTA on the SM fills its waits.
+  static constexpr int kCtas = NG == 1 ? 2 : 1;
+  static constexpr int kSmemBytes = kCtas == 2 ? 115712 : 232448;   // dynamic shared memory a CTA can have
   static constexpr int MH = D / 128;                      // 128-dim blocks
   static constexpr int NS = (2 + MH) * NQ <= 512 ? 2 : 1; // S buffers in tensor memory
   static constexpr int kCols = (NS + MH) * NQ;
@@ -110,10 +114,10 @@ struct Kv {
   static constexpr int kPTerm = NQ * kTile, kPBytes = 2 * kPTerm;
   static constexpr int kLeft = (kSmemBytes - kQBytes - kPBytes - (int)sizeof(Small)) / kHalf;
   static constexpr int kUnits = kLeft > 16 ? 16 : kLeft;  // half tiles of ring
-  static constexpr int KS = kUnits / 4 < 2 ? 2 : kUnits / 4;   // K tiles
+  static constexpr int KS = kUnits < 6 ? 1 : kUnits < 8 ? 2 : kUnits / 4;   // K tiles
   static constexpr int VS = kUnits - 2 * KS;                   // V half tiles
   static constexpr size_t kSmem = (size_t)kQBytes + kPBytes + KS * kTileBytes + VS * kHalf + sizeof(Small);
-  static_assert(VS >= 3, "the V ring holds more than a tile");
+  static_assert(VS >= 2, "the V ring holds a tile");
   static_assert(KS + NS <= kScaleStages, "scale stages");
   static_assert(kSmem <= (size_t)kSmemBytes, "shared memory over 227 KB");
 };
@@ -280,7 +284,7 @@ struct Piece {
 };
 
 template <int D, int NG, int CC, bool MOD>
-__global__ void __launch_bounds__((NG + 1) * 128, 1)
+__global__ void __launch_bounds__((NG + 1) * 128, NG == 1 ? 2 : 1)
 kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                 const Kv8AttnParams p, const BatchDesc bd) {
   using K = Kv<D, NG, CC, MOD>;
@@ -448,7 +452,7 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
 
   // The softmax warps of the wider tiles need more registers than an even share: 3 x 144 + 80 is what the block was
   // launched with (4 x 128 per warp).
-  constexpr bool kShare = CC >= 2;
+  constexpr bool kShare = NG > 1 && CC >= 2;
   if (warp >= kWarps) {
     if (kShare) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
     if (warp <= kWarpV) {
@@ -467,7 +471,9 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         const int* row = p.page_table + (size_t)pc.b * p.max_pages;
         int left = pc.tiles;
         if (pc.first == 0) {
-          // the draft tile is staged by the softmax warps: its slots, and its scale stage, pass by in their turn
+          // The draft tile is staged by the softmax warps: its slots, and its scale stage, pass by in their turn.  In
+          // their turn means waiting for what they held before: a producer that went past a slot without that could
+          // be two rounds ahead of it, which a barrier's parity cannot tell from none.
           if (is_k) {
             ok = __all_sync(0xffffffffu, wait_empty(B_KE, ring));
             if (!ok) break;
@@ -475,8 +481,12 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             sc_ring.next(SC);
             ring.next(KS);
           } else {
-            ring.next(VS);
-            ring.next(VS);
+#pragma unroll 1
+            for (int h = 0; h < 2 && ok; ++h) {
+              ok = __all_sync(0xffffffffu, wait_empty(B_VE, ring));
+              ring.next(VS);
+            }
+            if (!ok) break;
           }
           --left;
         }
@@ -880,11 +890,6 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         if (has_draft && sm->row_v[tid] != sm->row_v[tid]) sm->row_k[tid] = sm->row_v[tid];   // NaN: to the scores
       }
       sync_all();
-      if (MOD) {
-#pragma unroll 1
-        for (int q = tid; q < NQ; q += kWarps * 32) sm->dep[q] = q < rows ? (float)sm->depth[q / hpc] : 0.f;
-        sync_all();
-      }
       if (tid == 0) {
         mbar_arrive(bar(B_Q));
         if (has_draft) {
@@ -900,6 +905,27 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
 #pragma unroll
         for (int e = 0; e < 8; ++e) sum[c][e] = make_float2(0.f, 0.f);
       const int lo_root = p.window > 0 ? pc.L - p.window + 1 : 0;
+      // The scales of this thread's token row in the coming tile: the score factor, log2 of the V scale, and the V scale
+      // on the weights.
+      float kf, lv, vd;
+      auto set_scales = [&](float ks, float vs) {
+        kf = ks * fac;
+        lv = fast_log2(vs);
+        vd = vs * kDown;
+      };
+      auto next_scales = [&] {
+        set_scales(sm->scale[sc_ring.at][row >> 4], sm->scale[sc_ring.at][8 + (row >> 4)]);
+        sc_ring.next(SC);
+      };
+      if (has_draft) {
+        const float rv = row < n_nodes ? sm->row_v[row] : 1.f;
+        set_scales(row < n_nodes ? sm->row_k[row] : 1.f, rv != rv ? 1.f : rv);
+        sc_ring.next(SC);
+      } else {
+        wait_full(B_SC, sc_ring);
+        __syncwarp();
+        next_scales();
+      }
 
       // Until a tile that every column sees something of has passed, columns may have no reference.
       bool settled = false;
@@ -910,33 +936,22 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         const int valid = draft ? n_nodes : min(kTile, pc.L - t0);
         const bool band = !draft && p.window > 0 && t0 < lo_root + kMaxNodes;
         const bool masked = draft || valid < kTile || band;
-        float ks = 1.f, vs = 1.f;
-        if (draft) {
-          if (row < n_nodes) { ks = sm->row_k[row]; vs = sm->row_v[row]; if (vs != vs) vs = 1.f; }
-        } else {
-          wait_full(B_SC, sc_ring);
-          __syncwarp();
-          ks = sm->scale[sc_ring.at][row >> 4];
-          vs = sm->scale[sc_ring.at][8 + (row >> 4)];
-          if (band && t0 + row >= lo_root && t0 + row < min(pc.L, lo_root + kMaxNodes)) {
-            // a token that a window may hide from some nodes: its NaN codes of V become NaN scores
-            const int pg = p.page_table[(size_t)pc.b * p.max_pages + (t0 + row) / kPage];
-            if (pg >= 0 && pg < p.num_pool_pages) {
-              const uint4* src = reinterpret_cast<const uint4*>(
-                  p.v_cache + (((size_t)pg * p.hkv + pc.g) * kPage + (t0 + row) % kPage) * D);
-              uint32_t nan = 0;
+        if (band && t0 + row >= lo_root && t0 + row < min(pc.L, lo_root + kMaxNodes)) {
+          // a token that a window may hide from some nodes: its NaN codes of V become NaN scores
+          const int pg = p.page_table[(size_t)pc.b * p.max_pages + (t0 + row) / kPage];
+          if (pg >= 0 && pg < p.num_pool_pages) {
+            const uint4* src = reinterpret_cast<const uint4*>(
+                p.v_cache + (((size_t)pg * p.hkv + pc.g) * kPage + (t0 + row) % kPage) * D);
+            uint32_t nan = 0;
 #pragma unroll 1
-              for (int e = 0; e < D / 16; ++e) {
-                const uint4 v = __ldg(src + e);
-                nan |= __vcmpeq4(v.x & 0x7f7f7f7fu, 0x7f7f7f7fu) | __vcmpeq4(v.y & 0x7f7f7f7fu, 0x7f7f7f7fu) |
-                       __vcmpeq4(v.z & 0x7f7f7f7fu, 0x7f7f7f7fu) | __vcmpeq4(v.w & 0x7f7f7f7fu, 0x7f7f7f7fu);
-              }
-              if (nan != 0u) ks = __int_as_float(0x7fc00000);
+            for (int e = 0; e < D / 16; ++e) {
+              const uint4 v = __ldg(src + e);
+              nan |= __vcmpeq4(v.x & 0x7f7f7f7fu, 0x7f7f7f7fu) | __vcmpeq4(v.y & 0x7f7f7f7fu, 0x7f7f7f7fu) |
+                     __vcmpeq4(v.z & 0x7f7f7f7fu, 0x7f7f7f7fu) | __vcmpeq4(v.w & 0x7f7f7f7fu, 0x7f7f7f7fu);
             }
+            if (nan != 0u) kf = __int_as_float(0x7fc00000);
           }
         }
-        sc_ring.next(SC);
-        const float lv = fast_log2(vs), vd = vs * kDown;
         // ---- the scores of this token row, and S is free for the tile after the next
         wait_full(B_SF, s_ring);
         __syncwarp();
@@ -955,8 +970,22 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         // ---- exponents against the references as they stand (base 2), and the chunks where a weight would pass kTop
         uint32_t missed = 0;
         const float limit = 8.807354922f - lv;       // log2(kTop)
+        // the bias' distance is counted from the root: a node's depth shifts all its scores alike (see the log-sum-exp)
         const float rel = draft ? (row < n_nodes ? (float)sm->depth[row] : 0.f) : (float)(t0 + row - pc.L);
-        const float kf = ks * fac;
+        if (MOD) {
+#pragma unroll
+          for (int c = 0; c < CC; ++c)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) a[c][e] *= kf;
+          if (p.softcap > 0.f) {
+            // c tanh(x / c) = c - 2 c / (1 + 2^(2 log2e x / c)); fac holds the factor of the exponent
+            const float cl = p.softcap * kLog2e;
+#pragma unroll
+            for (int c = 0; c < CC; ++c)
+#pragma unroll
+              for (int e = 0; e < 16; ++e) a[c][e] = fmaf(-2.f * cl, fast_rcp(1.f + fast_exp2(a[c][e])), cl);
+          }
+        }
 #pragma unroll
         for (int c = 0; c < CC; ++c) {
           const int q = col0 + c * 16;
@@ -966,18 +995,11 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             const float4 m = *reinterpret_cast<const float4*>(&sm->m[q + 4 * k]);
             float* v = &a[c][4 * k];
             float2 d0, d1;
-            if (MOD) {
-              float s[4] = {v[0] * kf, v[1] * kf, v[2] * kf, v[3] * kf};
-              if (p.softcap > 0.f) {
-                // c tanh(x / c) = c - 2 c / (1 + 2^(2 log2e x / c)); fac holds the factor of the exponent
-                const float cl = p.softcap * kLog2e;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) s[e] = fmaf(-2.f * cl, fast_rcp(1.f + fast_exp2(s[e])), cl);
-              }
+            if (MOD) {       // v holds the capped score
               const float4 sl = *reinterpret_cast<const float4*>(&sm->slope[q + 4 * k]);
-              const float4 dp = *reinterpret_cast<const float4*>(&sm->dep[q + 4 * k]);
-              d0 = make_float2(fmaf(sl.x, rel - dp.x, s[0]) + m.x, fmaf(sl.y, rel - dp.y, s[1]) + m.y);
-              d1 = make_float2(fmaf(sl.z, rel - dp.z, s[2]) + m.z, fmaf(sl.w, rel - dp.w, s[3]) + m.w);
+              const float2 rr = make_float2(rel, rel);
+              d0 = add2(fma2(make_float2(sl.x, sl.y), rr, make_float2(v[0], v[1])), make_float2(m.x, m.y));
+              d1 = add2(fma2(make_float2(sl.z, sl.w), rr, make_float2(v[2], v[3])), make_float2(m.z, m.w));
             } else {
               d0 = fma2(make_float2(v[0], v[1]), make_float2(kf, kf), make_float2(m.x, m.y));
               d1 = fma2(make_float2(v[2], v[3]), make_float2(kf, kf), make_float2(m.z, m.w));
@@ -1061,7 +1083,8 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
           const int mine_col = quarter * 32 + lane, q = col0 + mine_col;
           if (mine_col < mine * 16 && ((todo >> (mine_col >> 4)) & 1u)) {
             const float old = -sm->m[q];
-            const float mt = old + fmaxf(fmaxf(sm->red[0][q], sm->red[1][q]), fmaxf(sm->red[2][q], sm->red[3][q])) - kHead;
+            const float mt = old + fmaxf(fmaxf(sm->red[0][q], sm->red[1][q]), fmaxf(sm->red[2][q], sm->red[3][q])) -
+                             (old == 0.f ? kHeadFirst : kHeadNext);
             float now = mt == -INFINITY ? old : old == 0.f ? mt : fmaxf(old, mt);
             if (now == 0.f && mt != -INFINITY) now = 1e-30f;
             sm->alpha[q] = old == 0.f ? 1.f : fast_exp2(old - now);
@@ -1083,6 +1106,12 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
               weigh(c, (missed >> c) & 1u ? 1.f : 0.f);     // 0: this tile's weights are in the sum
             }
           }
+        }
+        // the coming tile's scales while the previous tile's PV runs, if they are there
+        bool ahead = i + 1 >= pc.tiles;
+        if (NG > 1 && !ahead) {
+          ahead = __all_sync(0xffffffffu, mbar_test(bar(B_SC + sc_ring.at), sc_ring.round));
+          if (ahead) next_scales();
         }
         // P and O belong to the previous tile's PV until it has finished
         if (it > 0) spin(B_OD, it - 1);
@@ -1114,6 +1143,11 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(B_PF));
+        if (!ahead) {
+          wait_full(B_SC, sc_ring);
+          __syncwarp();
+          next_scales();
+        }
       }
 
       // ---------------------------------------------------------- results
@@ -1144,7 +1178,8 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
           if (q < rows) {
             const int node = q / hpc, at = (q0 + node) * p.hq + head0 + q - node * hpc;
             out_row[q] = pc.whole ? at : q;
-            const float lse2 = l == 0.f ? -INFINITY : fast_log2(l) - sm->m[q];
+            float lse2 = l == 0.f ? -INFINITY : fast_log2(l) - sm->m[q];
+            if (MOD) lse2 -= sm->slope[q] * (float)sm->depth[node];
             if (!pc.whole) p.lse_part[slot * NQ + q] = lse2;
             else if (p.lse != nullptr) p.lse[at] = lse2 * kLn2;
           }

@@ -13,8 +13,9 @@ namespace sdv {
 struct Kv8Plan {
   int hpc, hparts;   // query heads of a KV group per CTA, and CTA parts per group
   int nq;            // query columns of the kernel instance
+  int ctas;          // of it per SM
 };
-Kv8Plan kv8_plan(int group, int max_nodes, int dim, bool mod);
+Kv8Plan kv8_plan(int group, int max_nodes, int dim, bool mod, int kv_rows);   // kv_rows: sequences x KV heads
 
 cudaError_t launch_kv8_256(const CUtensorMap&, const CUtensorMap&, const Kv8AttnParams&, const BatchDesc&, cudaStream_t);
 cudaError_t launch_kv8_128(const CUtensorMap&, const CUtensorMap&, const Kv8AttnParams&, const BatchDesc&, cudaStream_t);
@@ -42,6 +43,7 @@ cudaError_t launch_kv8_kind(const CUtensorMap& mk, const CUtensorMap& mv, const 
                             cudaStream_t st) {
   switch (p.nq) {
     case 16: return launch_kv8_cols<1, 1>(mk, mv, p, bd, st);
+    case 32: return launch_kv8_cols<1, 2>(mk, mv, p, bd, st);
     case 48: return launch_kv8_cols<3, 1>(mk, mv, p, bd, st);
     case 96: return launch_kv8_cols<3, 2>(mk, mv, p, bd, st);
 #if !(SDV_KV8_MOD && SDV_KV8_DIM == 256)   // see kv8_plan

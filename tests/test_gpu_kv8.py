@@ -165,6 +165,10 @@ CASES = {
     "ragged": ([chain(1), chain(5), tree(3, 22), chain(9), tree(4, 63)], [0, 1, 17, 700, 2049]),
     "ragged_narrow": ([chain(2), tree(5, 30), chain(1), chain(3)], [33, 1500, 0, 640], NARROW),
     "decode_batch": ([chain(1)] * 40, [(37 * i * i) % 700 for i in range(40)], NARROW),
+    "decode_batch_wide": ([chain(1)] * 64, [(53 * i) % 900 for i in range(64)]),
+    "chain5_batch_wide": ([chain(5)] * 40, [(71 * i) % 1300 for i in range(40)]),
+    "chain8_batch_narrow": ([chain(8)] * 50, [(67 * i) % 1100 for i in range(50)], NARROW),
+    "tree15_batch": ([tree(5, 14)] * 40, [(59 * i) % 700 for i in range(40)]),
     "group1": ([tree(7, 11)], [401], (3, 3, 128)),
     "group16": ([tree(8, 6), chain(1)], [401, 90], (16, 1, 256)),
     "group5_narrow": ([tree(9, 20)], [1111], (10, 2, 128)),
