@@ -227,7 +227,7 @@ struct Kv8AttnParams {
   // filled in by the launch: the plan and the workspace's parts
   int hpc, hparts, nq, grid;
   int* cum;                  // [kMaxBatch + 3] first unit of each sequence, then the plan (written for the merge)
-  __nv_bfloat16* o_part;     // [piece + segment][nq][dim] partial outputs
+  float* o_part;             // [piece + segment][nq][dim] partial outputs
   float* lse_part;           // [piece + segment][nq] base-2 log-sum-exps
 };
 constexpr int kMaxKvHeads = 64, kMaxGroup = 16;   // of the block-scaled cache's calls

@@ -79,15 +79,15 @@ __global__ void __launch_bounds__(kMergeThreads) kv8_merge_kernel(const Kv8AttnP
   for (int e = 0; e < E; ++e) acc[e] = 0.f;
   for (int base = warp; base < n; base += kMergeWarps * kBatch) {
     float w[kBatch];
-    uint32_t o[kBatch][E / 2];
+    float o[kBatch][E];
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
       const int i = base + k * kMergeWarps;
       const size_t at = (slot0 + min(i, n - 1)) * p.nq + col;
       w[k] = i < n ? p.lse_part[at] : -INFINITY;
-      const uint32_t* src = reinterpret_cast<const uint32_t*>(p.o_part + at * D + lane * E);
 #pragma unroll
-      for (int e = 0; e < E / 2; ++e) o[k][e] = src[e];
+      for (int e = 0; e < E; e += 4)
+        *reinterpret_cast<float4*>(&o[k][e]) = *reinterpret_cast<const float4*>(p.o_part + at * D + lane * E + e);
     }
     float bm = mx;
 #pragma unroll
@@ -103,13 +103,12 @@ __global__ void __launch_bounds__(kMergeThreads) kv8_merge_kernel(const Kv8AttnP
       const float f = fast_exp2(w[k] - mx);
       den += f;
 #pragma unroll
-      for (int e = 0; e < E / 2; ++e) {
-        const float2 v = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&o[k][e]));
-        acc[2 * e] += f * v.x;
-        acc[2 * e + 1] += f * v.y;
-      }
+      for (int e = 0; e < E; ++e) acc[e] += f * o[k][e];
     }
   }
+  // Every load is under way or done: the next kernel's blocks may come as this one's leave (at the start of the block
+  // they took the SMs of a large merge: 512 rows of 16 partials 209 -> 224 us for the whole call).
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   __shared__ float s_m[kMergeWarps], s_d[kMergeWarps], s_acc[kMergeWarps][D];
   if (lane == 0) { s_m[warp] = mx; s_d[warp] = den; }
 #pragma unroll
@@ -151,7 +150,7 @@ Layout layout_of(const Kv8Plan& pl, int hkv, int dim, const BatchDesc& bd, int s
   const size_t slots = (size_t)sms * pl.ctas + (size_t)bd.batch * hkv * pl.hparts;
   Layout l;
   l.o = align_up((kMaxBatch + 3) * sizeof(int));
-  l.lse = l.o + align_up(slots * pl.nq * dim * sizeof(__nv_bfloat16));
+  l.lse = l.o + align_up(slots * pl.nq * dim * sizeof(float));
   l.total = l.lse + align_up(slots * pl.nq * sizeof(float));
   return l;
 }
@@ -197,7 +196,7 @@ cudaError_t launch_kv8_attn(Kv8AttnParams p, const BatchDesc& bd, cudaStream_t s
   const Layout l = layout_of(pl, p.hkv, p.dim, bd, sms);
   char* ws = static_cast<char*>(p.workspace);
   p.cum = reinterpret_cast<int*>(ws);
-  p.o_part = reinterpret_cast<__nv_bfloat16*>(ws + l.o);
+  p.o_part = reinterpret_cast<float*>(ws + l.o);
   p.lse_part = reinterpret_cast<float*>(ws + l.lse);
   CUtensorMap mk, mv;
   if (!page_map(&mk, p.k_cache, p) || !page_map(&mv, p.v_cache, p)) return cudaErrorInvalidValue;
@@ -205,17 +204,8 @@ cudaError_t launch_kv8_attn(Kv8AttnParams p, const BatchDesc& bd, cudaStream_t s
                                : (mod ? launch_kv8_128_mod(mk, mv, p, bd, st) : launch_kv8_128(mk, mv, p, bd, st));
   if (e != cudaSuccess) return e;
   const dim3 grid(bd.total_nodes, p.hq);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(kMergeThreads);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return p.dim == 256 ? cudaLaunchKernelEx(&cfg, kv8_merge_kernel<256>, p, bd)
-                      : cudaLaunchKernelEx(&cfg, kv8_merge_kernel<128>, p, bd);
+  return p.dim == 256 ? launch_pdl(kv8_merge_kernel<256>, grid, dim3(kMergeThreads), 0, st, p, bd)
+                      : launch_pdl(kv8_merge_kernel<128>, grid, dim3(kMergeThreads), 0, st, p, bd);
 }
 
 }  // namespace sdv

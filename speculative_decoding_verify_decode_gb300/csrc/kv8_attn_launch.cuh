@@ -35,8 +35,7 @@ cudaError_t launch_kv8_cols(const CUtensorMap& mk, const CUtensorMap& mv, const 
   auto kernel = kv8_attn_kernel<SDV_KV8_DIM, NG, CC, SDV_KV8_MOD != 0>;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)K::kSmem);
   if (e != cudaSuccess) return e;
-  kernel<<<p.grid, K::kThreads, K::kSmem, st>>>(mk, mv, p, bd);
-  return cudaGetLastError();
+  return launch_pdl(kernel, dim3(p.grid), dim3(K::kThreads), K::kSmem, st, mk, mv, p, bd);
 }
 
 cudaError_t launch_kv8_kind(const CUtensorMap& mk, const CUtensorMap& mv, const Kv8AttnParams& p, const BatchDesc& bd,

@@ -2,8 +2,8 @@
 
 Tolerance of the attention, per output element, derived from its roundings (half steps relative to the value):
   2^-8 |ref|          the bf16 output
-  2^-8 A              each split's partial output in bf16; A = sum of p |v| / sum of p bounds any convex mix
-  2^-7 A              the softmax weights as an e4m3 value (2^-4) and an e5m2 rest (2^-3 of at most 2^-4)
+  2^-7 A              the softmax weights as an e4m3 value (2^-4) and an e5m2 rest (2^-3 of at most 2^-4);
+                      A = sum of p |v| / sum of p bounds any convex mix
   2 ds A              an absolute error ds of the scores changes a weight by at most e^ds - 1, in sum and in share
   2^-17 max|v_new|    the draft values as two e4m3 terms: a row is scaled so that its amax is 224..448, and what the
                       two terms leave is at most half of e4m3's smallest step 2^-9, so 2^-10 / 224 of amax < 2^-17
@@ -136,7 +136,7 @@ class Case:
         at = ~np.isnan(lse)
         got, got_lse, ds = np64(self.out[:-1]), np64(self.lse), self.score_error()
         assert ds < 0.25, ds
-        bound = 2.0 ** -8 * np.abs(ref) + (2.0 ** -8 + 2.0 ** -7 + 2 * np.expm1(ds)) * spread + \
+        bound = 2.0 ** -8 * np.abs(ref) + (2.0 ** -7 + 2 * np.expm1(ds)) * spread + \
             2.0 ** -17 * float(self.vn.abs().max()) + 1e-30
         over = (np.abs(got - ref) / bound)[at]
         assert np.isfinite(got[at]).all() and over.max() <= 1.0, (over.max(), ds)
@@ -631,7 +631,7 @@ def test_prompt_then_verify_steps(graph):
                                            np64(kn[layer]), np64(vn[layer]), table, ctx, indptr, parents, softcap=20.0)
             got = np64(step.out[layer])
             ds = 2.0 ** -16 * float(q.abs().max()) * 256 * 4 * 2.0 ** it / 16       # |k|_1 <= 256 values of up to 4 * 2^it
-            assert np.all(np.abs(got - ref) <= 2.0 ** -8 * np.abs(ref) + (2.0 ** -8 + 2.0 ** -7 + 2 * np.expm1(ds)) * spread +
+            assert np.all(np.abs(got - ref) <= 2.0 ** -8 * np.abs(ref) + (2.0 ** -7 + 2 * np.expm1(ds)) * spread +
                           2.0 ** -17 * float(vn.abs().max()))
         table, held, free, sl, rows, _, ctx = kv8.pages_extend(ctx, alen, table, held, free, total, indptr, paths)
         assert list(step.slots.cpu().numpy()) == sl and list(step.rows.cpu().numpy()) == rows
