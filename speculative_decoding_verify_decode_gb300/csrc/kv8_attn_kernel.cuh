@@ -35,9 +35,10 @@
 // for at most an eighth more units per CTA, it does (a second piece costs a CTA
 // another staging and epilogue); else the line is cut where it falls, and no CTA
 // idles on a ragged batch.  A segment in several pieces leaves fp32 partial
-// outputs and log-sum-exps for the merge (bf16 ones take 0 to 1 us less of a call,
-// and a typical error of 0.0025 of the outputs instead of 0.0019); one in a single
-// piece is written directly.  Context tiles go from the last to the first: a bias that falls with
+// outputs and log-sum-exps for the merge (bf16 ones are off by 2^-9 each: a typical
+// error of 0.0025 of the outputs instead of 0.0019, and 0 to 1 us less for a call;
+// f16 ones with a scale per column and quarter of the dims cost their maxima what
+// they save); one in a single piece is written directly.  Context tiles go from the last to the first: a bias that falls with
 // distance then has its largest scores first, and m moves once.
 //
 // Per tile (tokens are the MMA's M; NQ columns):
@@ -274,6 +275,19 @@ __device__ __forceinline__ int exp_of(uint32_t bits) {
 }
 __device__ __forceinline__ float exp2i(int e) { return __int_as_float((e + 127) << 23); }
 
+// What a segment's draft tile counts for beyond one unit, where CTAs have `even` units each: staging the block, its masks
+// and the moves of fresh references take some 5 us, a tile of 144 columns 2.2 us and one of 96 or fewer 1.2 to 1.6; in
+// pieces of few units one more would cost the whole.  Against 2 from 12 units and 1 from 5 on: a 24-node tree over 32768
+// tokens 37.5 -> 36.2 us, 8 sequences of 8 nodes 38.1 -> 36.4 (128 dims), 16 nodes over 32768 31.0 -> 28.9.
+template <int NQ>
+__device__ __forceinline__ int extra_units(int even) {
+  return even >= 12 && NQ < 144 ? 3 : even >= 6 ? 2 : even >= 4 ? 1 : 0;
+}
+
+// A bit per column of a softmax group.
+template <int CC> struct BitsOf { using type = uint32_t; };
+template <> struct BitsOf<3> { using type = unsigned long long; };
+
 // One CTA's share of one segment.
 struct Piece {
   int b, g, c;         // sequence, KV head, head part
@@ -338,7 +352,7 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
       units = 1 + (L - window_base(L, p.window, kTile) + kTile - 1) / kTile;
     }
     const int even = (__reduce_add_sync(0xffffffffu, units) * parts + (int)gridDim.x - 1) / (int)gridDim.x;
-    const int more = even >= 12 ? 2 : even >= 5 ? 1 : 0;
+    const int more = extra_units<NQ>(even);
     per = even;
     extra = -1;
 #pragma unroll 1
@@ -374,7 +388,7 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
       for (int b = lane; b < bd.batch; b += 32) sum += sm->cum[b];
       sum = __reduce_add_sync(0xffffffffu, sum);
       const int even = (sum * parts + (int)gridDim.x - 1) / (int)gridDim.x;
-      const int more = even >= 12 ? 2 : even >= 5 ? 1 : 0;
+      const int more = extra_units<NQ>(even);
       const int size = even + warp * max(1, even / 56);
       int need = 0;
 #pragma unroll 1
@@ -1050,27 +1064,28 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         missed &= all;
         if (masked) {
           // Which columns see this row: one bit each.  Masked exponents are -inf whatever the product was.
-          constexpr int VW = (CC * 16 + 31) / 32;
-          uint32_t vis[VW];
-#pragma unroll
-          for (int w = 0; w < VW; ++w) vis[w] = row < valid && !draft && !band ? 0xffffffffu : 0u;
+          using Bits = typename BitsOf<CC>::type;
+          Bits vis = row < valid && !draft && !band ? ~(Bits)0 : 0;
           if (row < valid && (draft || band)) {
-            // node by node: a node's columns see this row, or none of them does
+            // node by node, from the one of the group's first column: its columns see this row, or none of them does
+            const int own = draft ? sm->depth[row] : 0;
+            int n = col0 / hpc, at = n * hpc - col0;       // the node's first column, less the group's
+            const Bits full = ((Bits)1 << hpc) - 1;
+            Bits bits = full >> -at;
 #pragma unroll 1
-            for (int n = 0; n < n_nodes; ++n) {
+            for (; at < CC * 16 && n < n_nodes; ++n) {
               const int dn = sm->depth[n];
-              const bool see = draft ? ((sm->anc[n] >> row) & 1ull) && (p.window <= 0 || dn - sm->depth[row] < p.window)
+              const bool see = draft ? ((sm->anc[n] >> row) & 1ull) != 0ull && (p.window <= 0 || dn - own < p.window)
                                      : t0 + row >= lo_root + dn;
-              if (see) {
-#pragma unroll
-                for (int w = 0; w < VW; ++w) vis[w] |= bit_range(n * hpc - col0 - w * 32, hpc);
-              }
+              vis |= see ? bits : (Bits)0;
+              at += hpc;
+              bits = full << (at & (8 * (int)sizeof(Bits) - 1));
             }
           }
 #pragma unroll
           for (int c = 0; c < CC; ++c)
 #pragma unroll
-            for (int e = 0; e < 16; ++e) a[c][e] = (vis[c / 2] >> ((c & 1) * 16 + e)) & 1u ? a[c][e] : -INFINITY;
+            for (int e = 0; e < 16; ++e) a[c][e] = ((uint32_t)(vis >> (CC > 2 ? c / 2 * 32 : 0)) >> ((c & 1) * 16 + e)) & 1u ? a[c][e] : -INFINITY;
         }
         // ---- the weights, on the assumption that no warp of the group has to move a reference; what they need to know
         // of each other is under way meanwhile.  (The barrier also keeps red[] of this tile behind the last one's readers.)
@@ -1245,12 +1260,13 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             }
           }
         } else {
+          // the columns' rows follow each other in the partial
+          float* dst = p.o_part + (slot * NQ + col0 + c * 16) * D + row;
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
-            const int r = at[k];
 #pragma unroll
             for (int mb = 0; mb < MH; ++mb)
-              if (r >= 0) p.o_part[(slot * NQ + r) * D + mb * 128 + row] = v[mb][k] * inv[k];
+              if (col0 + c * 16 + k < rows) dst[k * D + mb * 128] = v[mb][k] * inv[k];
           }
         }
       }
