@@ -1022,19 +1022,22 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         const float limit = 8.807354922f - lv;       // log2(kTop)
         // the bias' distance is counted from the root: a node's depth shifts all its scores alike (see the log-sum-exp)
         const float rel = draft ? (row < n_nodes ? (float)sm->depth[row] : 0.f) : (float)(t0 + row - pc.L);
-        if (MOD) {
+        float kv = kf;
+        if (MOD && p.softcap > 0.f) {
+          // c tanh(x / c) = c - 2 c / (1 + 2^(2 log2e x / c)); fac holds the factor of the exponent
+          const float cl = p.softcap * kLog2e;
 #pragma unroll
-          for (int c = 0; c < CC; ++c)
+          for (int c = 0; c < CC; ++c) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) a[c][e] *= kf;
-          if (p.softcap > 0.f) {
-            // c tanh(x / c) = c - 2 c / (1 + 2^(2 log2e x / c)); fac holds the factor of the exponent
-            const float cl = p.softcap * kLog2e;
-#pragma unroll
-            for (int c = 0; c < CC; ++c)
-#pragma unroll
-              for (int e = 0; e < 16; ++e) a[c][e] = fmaf(-2.f * cl, fast_rcp(1.f + fast_exp2(a[c][e])), cl);
+            for (int e = 0; e < 16; e += 2) {
+              const float2 y = mul2(make_float2(a[c][e], a[c][e + 1]), make_float2(kf, kf));
+              const float2 d = add2(make_float2(fast_exp2(y.x), fast_exp2(y.y)), make_float2(1.f, 1.f));
+              const float2 s = fma2(make_float2(fast_rcp(d.x), fast_rcp(d.y)), make_float2(-2.f * cl, -2.f * cl), make_float2(cl, cl));
+              a[c][e] = s.x;
+              a[c][e + 1] = s.y;
+            }
           }
+          kv = 1.f;
         }
 #pragma unroll
         for (int c = 0; c < CC; ++c) {
@@ -1044,16 +1047,14 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
           for (int k = 0; k < 4; ++k) {
             const float4 m = *reinterpret_cast<const float4*>(&sm->m[q + 4 * k]);
             float* v = &a[c][4 * k];
-            float2 d0, d1;
-            if (MOD) {       // v holds the capped score
+            float2 m0 = make_float2(m.x, m.y), m1 = make_float2(m.z, m.w);
+            if (MOD) {
               const float4 sl = *reinterpret_cast<const float4*>(&sm->slope[q + 4 * k]);
-              const float2 rr = make_float2(rel, rel);
-              d0 = add2(fma2(make_float2(sl.x, sl.y), rr, make_float2(v[0], v[1])), make_float2(m.x, m.y));
-              d1 = add2(fma2(make_float2(sl.z, sl.w), rr, make_float2(v[2], v[3])), make_float2(m.z, m.w));
-            } else {
-              d0 = fma2(make_float2(v[0], v[1]), make_float2(kf, kf), make_float2(m.x, m.y));
-              d1 = fma2(make_float2(v[2], v[3]), make_float2(kf, kf), make_float2(m.z, m.w));
+              m0 = fma2(make_float2(sl.x, sl.y), make_float2(rel, rel), m0);
+              m1 = fma2(make_float2(sl.z, sl.w), make_float2(rel, rel), m1);
             }
+            const float2 d0 = fma2(make_float2(v[0], v[1]), make_float2(kv, kv), m0);
+            const float2 d1 = fma2(make_float2(v[2], v[3]), make_float2(kv, kv), m1);
             v[0] = d0.x; v[1] = d0.y; v[2] = d1.x; v[3] = d1.y;
             top = fmaxf(fmaxf(top, fmaxf(d0.x, d0.y)), fmaxf(d1.x, d1.y));
           }
