@@ -500,11 +500,11 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
   auto wait_full = [&](int first, const Ring& r) { return wait(first + r.at, (int)r.round); };
   auto wait_empty = [&](int first, const Ring& r) { return wait(first + r.at, (int)r.round ^ 1); };
 
-  // The softmax warps of the wider tiles need more registers than an even share: 3 x 144 + 80 is what the block was
+  // The softmax warps of the wider tiles need more registers than an even share: 3 x 152 + 56 is what the block was
   // launched with (4 x 128 per warp).
   constexpr bool kShare = NG > 1 && CC >= 2;
   if (warp >= kWarps) {
-    if (kShare) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    if (kShare) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (warp <= kWarpV) {
       // ---------------------------------------------------------- producers
       // Page ids come a group of four tiles at a time (lane l: page l % 8 of the group's tile l / 8), two groups ahead of
@@ -793,7 +793,7 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     }
   } else {
     // ------------------------------------------------------------ softmax warps
-    if (kShare) asm volatile("setmaxnreg.inc.sync.aligned.u32 144;");
+    if (kShare) asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
     const int group = warp >> 2, quarter = warp & 3;
     const int row = quarter * 32 + lane;                       // token row of S; dim (mod 128) of O^T
     const uint32_t lane_addr = (uint32_t)(quarter * 32) << 16;
@@ -977,6 +977,25 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         next_scales();
       }
 
+      // The scores of this token row, drawn at the end of the turn before; S is then free for the tile after the next.
+      float a[CC][16];
+      auto draw = [&] {
+        __syncwarp();
+        tc_fence_after();
+        const uint32_t s_addr = tmem + lane_addr + s_ring.at * NQ + col0;
+#pragma unroll
+        for (int c = 0; c < CC; ++c) tmem_ld16(s_addr + c * 16, a[c]);
+        tmem_wait_ld();
+      };
+      auto drawn = [&] {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(B_SE + s_ring.at));
+        s_ring.next(NS);
+      };
+      wait_full(B_SF, s_ring);
+      draw();
+      drawn();
       // Until a tile that every column sees something of has passed, columns may have no reference.
       bool settled = false;
 #pragma unroll 1
@@ -1002,21 +1021,6 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             if (nan != 0u) kf = __int_as_float(0x7fc00000);
           }
         }
-        // ---- the scores of this token row, and S is free for the tile after the next
-        wait_full(B_SF, s_ring);
-        __syncwarp();
-        tc_fence_after();
-        float a[CC][16];
-        {
-          const uint32_t s_addr = tmem + lane_addr + s_ring.at * NQ + col0;
-#pragma unroll
-          for (int c = 0; c < CC; ++c) tmem_ld16(s_addr + c * 16, a[c]);
-          tmem_wait_ld();
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(B_SE + s_ring.at));
-        s_ring.next(NS);
         // ---- exponents against the references as they stand (base 2), and the chunks where a weight would pass kTop
         uint32_t missed = 0;
         const float limit = 8.807354922f - lv;       // log2(kTop)
@@ -1108,7 +1112,7 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
           mbar_arrive(bar(B_G + group));
         }
         if (plain) {
-          if (missed == 0u) {
+          if (MOD && missed == 0u) {
 #pragma unroll
             for (int c = 0; c < CC; ++c) weigh(c, 1.f);
           } else {
@@ -1160,7 +1164,8 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
           }
         }
         // the coming tile's scales while the previous tile's PV runs, if they are there
-        bool ahead = i + 1 >= pc.tiles;
+        const bool last = i + 1 >= pc.tiles;
+        bool ahead = last;
         if (NG > 1 && !ahead) {
           ahead = __all_sync(0xffffffffu, mbar_test(bar(B_SC + sc_ring.at), sc_ring.round));
           if (ahead) next_scales();
@@ -1200,6 +1205,11 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
           __syncwarp();
           next_scales();
         }
+        // (Past the last tile S holds old scores, which nobody uses: drawn all the same, a condition here costs the wide
+        // tiles registers that they do not have, and 87 us become 99.)
+        if (!last) wait_full(B_SF, s_ring);
+        draw();
+        if (!last) drawn();
       }
 
       // ---------------------------------------------------------- results
