@@ -188,12 +188,19 @@ size_t sd_kv8_attn_workspace_size(const sd_shape* shape);
  *   workspace   >= sd_kv8_attn_workspace_size(shape) bytes.  Its contents need not be kept between calls; two calls
  *               that may run at the same time need one each.
  *
- * Numerics: scores, softmax statistics and sums are fp32.  A page id out of
- * range sets SD_DEV_BAD_PAGE and its tokens count as zeros; a scale out of
- * range sets SD_DEV_BAD_SCALE and is clamped.  Codes at masked positions
- * (behind L_b, before a window, on other branches) never reach an output,
- * whatever they hold.  A NaN or an infinity in a q row makes that row's
- * output NaN, one in a k_new row the outputs of the nodes that see it.
+ * Numerics: scores, softmax statistics, sums and the partial outputs of split
+ * sequences are fp32.  The products take 8-bit operands: the cache's codes as
+ * they lie; a query as two e4m3 terms (off by at most 2^-17 of the largest
+ * query amax among the columns that share a CTA); a draft key or value as two
+ * e4m3 terms (2^-17 of its row's amax); a softmax weight as an e4m3 term and an
+ * e5m2 rest (2^-7 of the weight at most; the sum of weights is not rounded).
+ * Outputs are typically within 0.002 of their size, against 0.0017 for the
+ * rounding to bf16 alone.  A page id out of range sets SD_DEV_BAD_PAGE and its
+ * tokens count as zeros; a scale out of range sets SD_DEV_BAD_SCALE and is
+ * clamped.  Codes at masked positions (behind L_b, before a window, on other
+ * branches) never reach an output, whatever they hold.  A NaN or an infinity in
+ * a q row makes that row's output NaN, one in a k_new or v_new row the outputs
+ * of the nodes that see it.
  */
 sd_status sd_kv8_attn(const sd_shape* shape, const sd_kv8_opts* opts, const void* q, const void* k_cache,
                       const void* v_cache, const float* k_scales, const float* v_scales, const void* k_new,

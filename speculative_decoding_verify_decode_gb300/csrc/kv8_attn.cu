@@ -159,10 +159,12 @@ Layout layout_of(const Kv8Plan& pl, int hkv, int dim, const BatchDesc& bd, int s
 
 // Query columns of a CTA: as many heads of a KV group as fit, so that the cache is read as few times as can be (capped
 // or biased scores over 256 dims stop at 96: the wider columns' slopes find no room beside the operands).  Up to 16
-// columns, i.e. single tokens, two CTAs share an SM (64 sequences, 1 to 32768 tokens, 128 dims: 389 us against 456 for
-// one).  17 to 32 columns do so when there are segments enough to fill both (64 sequences of 8 nodes, 128 dims: 208 us
-// against 228; 8 sequences: 39 against 44), and otherwise take one CTA of three softmax groups, whose single tile is
-// shorter (one sequence of 8 nodes over 8192 tokens: 17.5 us against 20.3).
+// columns, i.e. single tokens, two CTAs of one softmax group share an SM (64 sequences, 1 to 32768 tokens, 128 dims:
+// 388 us against 581 for one CTA of three groups; one sequence of 512 tokens 11.3 against 11.7).  So do 17 to 32 columns
+// of 128 dims where there are segments enough to fill both (64 sequences of 8 nodes: 205 us against 224; 8 sequences: 36.5
+// against 43.7); a few segments take one CTA of three groups, whose single tile is shorter (one sequence of 8 nodes over
+// 8192 tokens: 15.5 us against 17.4), and so do 256 dims, where half an SM's shared memory holds one K tile (64 sequences
+// of 5 nodes: 146 us against 149).
 Kv8Plan kv8_plan(int group, int max_nodes, int dim, bool mod, int kv_rows) {
   const int most = mod && dim == 256 ? 96 : 144;
   Kv8Plan pl;
@@ -171,7 +173,7 @@ Kv8Plan kv8_plan(int group, int max_nodes, int dim, bool mod, int kv_rows) {
   pl.hpc = (group + pl.hparts - 1) / pl.hparts;
   pl.hparts = (group + pl.hpc - 1) / pl.hpc;
   const int cols = pl.hpc * max_nodes;
-  const bool two = cols <= 16 || (cols <= 32 && kv_rows * pl.hparts >= 64);
+  const bool two = cols <= 16 || (cols <= 32 && dim == 128 && kv_rows * pl.hparts >= 64);
   pl.nq = two ? (cols <= 16 ? 16 : 32) : cols <= 48 ? 48 : cols <= 96 ? 96 : 144;
   pl.ctas = two ? 2 : 1;
   return pl;

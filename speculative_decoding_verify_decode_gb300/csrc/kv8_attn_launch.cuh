@@ -42,10 +42,12 @@ cudaError_t launch_kv8_kind(const CUtensorMap& mk, const CUtensorMap& mv, const 
                             cudaStream_t st) {
   switch (p.nq) {
     case 16: return launch_kv8_cols<1, 1>(mk, mv, p, bd, st);
+#if SDV_KV8_DIM == 128                     // see kv8_plan
     case 32: return launch_kv8_cols<1, 2>(mk, mv, p, bd, st);
+#endif
     case 48: return launch_kv8_cols<3, 1>(mk, mv, p, bd, st);
     case 96: return launch_kv8_cols<3, 2>(mk, mv, p, bd, st);
-#if !(SDV_KV8_MOD && SDV_KV8_DIM == 256)   // see kv8_plan
+#if !(SDV_KV8_MOD && SDV_KV8_DIM == 256)
     case 144: return launch_kv8_cols<3, 3>(mk, mv, p, bd, st);
 #endif
     default: return cudaErrorInvalidValue;
