@@ -132,6 +132,12 @@ class Kv8Cache:
         self._new = ints(batch), ints(batch), ints(1)
         self.dev_status = ints(1)
 
+    def _on(self, stream):
+        """The context of a stream: a torch stream, a raw handle, or None for the current one."""
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream, self.device) if stream else torch.cuda.default_stream(self.device)
+        return torch.cuda.stream(stream)
+
     def _settle(self, ctx: bool):
         new_ctx, new_held, new_count = self._new
         if ctx:
@@ -142,7 +148,7 @@ class Kv8Cache:
     def extend(self, add_lens, k_new, v_new, slots, rows=None, q_indptr=None, path=None, stream=None):
         """``add_lens`` tokens join every sequence: their pages, then their rows of every layer's ``k_new`` and
         ``v_new`` into the cache.  ``slots`` (and ``rows`` with a path) are int32 scratch with room for all rows."""
-        with torch.cuda.stream(stream):
+        with self._on(stream):
             new_ctx, new_held, new_count = self._new
             native.sd_pages_extend(self.ctx_lens, add_lens, self.page_table, self.held, new_held, self.free_list,
                                    self.free_count, new_count, slots, rows=rows, new_ctx_lens=new_ctx,
@@ -153,12 +159,14 @@ class Kv8Cache:
 
     def release(self, keep_lens, stream=None):
         """Every sequence keeps its first ``keep_lens`` tokens at most; the pages behind them become free."""
-        with torch.cuda.stream(stream):
+        with self._on(stream):
             _, new_held, new_count = self._new
             native.sd_pages_release(keep_lens, self.page_table, self.held, new_held, self.free_list, self.free_count,
                                     new_count, self.dev_status)
             self._settle(ctx=False)
-            torch.minimum(self.ctx_lens, keep_lens, out=self.ctx_lens)
+            # a negative length refuses the whole call: then the contexts stay too
+            keep = torch.where((keep_lens >= 0).all(), keep_lens, self.ctx_lens)
+            torch.minimum(self.ctx_lens, keep, out=self.ctx_lens)
 
 
 class Kv8Step:

@@ -647,3 +647,23 @@ def test_prompt_then_verify_steps(graph):
     assert list(cache.held.cpu().numpy()) == held and int(cache.free_count) == len(free)
     assert list(cache.free_list.cpu().numpy()[:len(free)]) == free
     assert list(cache.ctx_lens.cpu().numpy()) == [100, 0, ctx[2]]
+
+
+@pytest.mark.parametrize("raw", [False, True], ids=["torch_stream", "handle"])
+def test_a_refused_release_leaves_the_cache_as_it_was(raw):
+    cache, rng = Kv8Cache(2, 8, 16, 1), np.random.default_rng(5)
+    x = bf16(rng, 70, 4, 256).cuda()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    stream = side.cuda_stream if raw else side
+    slots = torch.empty(70, dtype=torch.int32, device="cuda")
+    cache.extend(cu([50, 20], torch.int32), [x], [x], slots, stream=stream)
+    side.synchronize()
+    assert cache.ctx_lens.tolist() == [50, 20] and cache.held.tolist() == [4, 2] and int(cache.dev_status) == 0
+    cache.release(cu([10, -1], torch.int32), stream=stream)
+    side.synchronize()
+    assert int(cache.dev_status) == native.SD_DEV_BAD_CTX
+    assert cache.ctx_lens.tolist() == [50, 20] and cache.held.tolist() == [4, 2] and int(cache.free_count) == 10
+    cache.release(cu([10, 100], torch.int32), stream=0 if raw else None)
+    torch.cuda.synchronize()
+    assert cache.ctx_lens.tolist() == [10, 20] and cache.held.tolist() == [1, 2] and int(cache.free_count) == 13
