@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(kAppendThreads, 6) kv8_append_kernel(const Kv8
 cudaError_t launch_kv8_append(const Kv8AppendParams& p, cudaStream_t st) {
   if (p.max_rows == 0) return cudaSuccess;
   // Rows per CTA: a row of its own while that fills the machine about twice over at most (single tokens of a batch, an
-  // accepted path: 8 tokens in 16 layers 3.7 us, against 5.5 by sixteens); for prompts sixteen, of which one begins a page
+  // accepted path: 6 tokens in 16 layers 3.7 us, against 5.5 by sixteens); for prompts sixteen, of which one begins a page
   // (8191 tokens 11.0 us, against 20.3 by single rows).  11.0 us are 4.6 TB/s of the pass's 50 MB.
   const int window = (long long)p.max_rows * p.num_layers <= 4 * kSMs ? 1 : kPage;
   // enough CTAs per window for one page's tasks, a warp each, four to a CTA (eight: 11.4 us and 3.9 for the same two)

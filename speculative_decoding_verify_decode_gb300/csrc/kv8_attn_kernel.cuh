@@ -277,7 +277,7 @@ __device__ __forceinline__ float exp2i(int e) { return __int_as_float((e + 127) 
 
 // What a segment's draft tile counts for beyond one unit, where CTAs have `even` units each: staging the block, its masks
 // and the moves of fresh references take some 5 us, a tile of 144 columns 2.2 us and one of 96 or fewer 1.2 to 1.6; in
-// pieces of few units one more would cost the whole.  Against 2 from 12 units and 1 from 5 on: a 24-node tree over 32768
+// pieces of few units one more would cost the whole.  Against 2 from 12 units and 1 from 5 on: a tree of 23 over 32768
 // tokens 37.5 -> 36.2 us, 8 sequences of 8 nodes 38.1 -> 36.4 (128 dims), 16 nodes over 32768 31.0 -> 28.9.
 template <int NQ>
 __device__ __forceinline__ int extra_units(int even) {
