@@ -15,6 +15,12 @@ namespace {
 sd_status cuda_status(cudaError_t e) { return e == cudaSuccess ? SD_OK : SD_ERR_CUDA; }
 bool aligned(const void* p, unsigned bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
 
+// int32 and fp32 arrays start on 4 bytes.
+template <typename... T>
+bool words(const T*... p) {
+  return ((reinterpret_cast<uintptr_t>(p) | ... | uintptr_t{0}) & 3u) == 0;
+}
+
 sd_status check_pages(int batch, int max_pages, int pool) {
   if (batch < 1 || max_pages < 1 || pool < 1) return SD_ERR_INVALID_ARG;
   if (batch > kMaxBatch || (long long)max_pages * kPage > (1LL << 30) || (long long)pool * kPage > INT_MAX)
@@ -65,6 +71,9 @@ sd_status sd_pages_extend(int batch, int max_pages_per_seq, int num_pool_pages, 
   if (!ctx_lens || !add_lens || !page_table || !held || !new_held || !free_list || !free_count || !new_free_count ||
       max_rows < 0 || (max_rows > 0 && !slots))
     return SD_ERR_INVALID_ARG;
+  if (!words(ctx_lens, add_lens, path, page_table, held, new_held, free_list, free_count, new_free_count, slots, rows,
+             row_indptr, new_ctx_lens, dev_status))
+    return SD_ERR_INVALID_ARG;
   if ((q_indptr_h == nullptr) != (path == nullptr) || (path != nullptr && max_path < 1)) return SD_ERR_INVALID_ARG;
   const int* in[] = {ctx_lens, add_lens, held, free_count, free_list};
   const int* out[] = {new_held, new_free_count, slots, rows, row_indptr, new_ctx_lens};
@@ -109,7 +118,13 @@ sd_status sd_pages_release(int batch, int max_pages_per_seq, int num_pool_pages,
   if (st != SD_OK) return st;
   if (!keep_lens || !page_table || !held || !new_held || !free_list || !free_count || !new_free_count)
     return SD_ERR_INVALID_ARG;
-  if (new_held == held || new_held == keep_lens || new_free_count == free_count) return SD_ERR_INVALID_ARG;
+  if (!words(keep_lens, page_table, held, new_held, free_list, free_count, new_free_count, dev_status))
+    return SD_ERR_INVALID_ARG;
+  const int* in[] = {keep_lens, held, free_count, page_table};
+  const int* out[] = {new_held, new_free_count, free_list};
+  for (const int* o : out)
+    for (const int* i : in)
+      if (o == i) return SD_ERR_INVALID_ARG;
   PagesParams p;
   std::memset(&p, 0, sizeof(p));
   p.ctx_lens = keep_lens;
@@ -140,6 +155,7 @@ sd_status sd_kv8_append(int num_layers, int num_kv_heads, int head_dim, int page
   if (!k_cache_layers || !v_cache_layers || !k_scale_layers || !v_scale_layers || !k_new_layers || !v_new_layers ||
       (max_rows > 0 && !slots))
     return SD_ERR_INVALID_ARG;
+  if (!words(slots, rows, dev_status)) return SD_ERR_INVALID_ARG;
   Kv8AppendParams p;
   std::memset(&p, 0, sizeof(p));
   if (!stride_ok(new_stride, (long long)num_kv_heads * head_dim, &p.new_stride)) return SD_ERR_INVALID_ARG;
@@ -186,6 +202,7 @@ sd_status sd_kv8_attn(const sd_shape* shape, const sd_kv8_opts* opts, const void
   if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(k_new, 16) ||
       !aligned(v_new, 16) || !aligned(out, 16) || !aligned(workspace, 16) || out == q)
     return SD_ERR_INVALID_ARG;
+  if (!words(k_scales, v_scales, page_table, ctx_lens, parents, lse, dev_status)) return SD_ERR_INVALID_ARG;
   Kv8AttnParams p;
   std::memset(&p, 0, sizeof(p));
   const long long q_row = (long long)shape->num_q_heads * shape->head_dim;

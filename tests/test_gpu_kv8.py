@@ -168,6 +168,9 @@ CASES = {
     "decode_batch_wide": ([chain(1)] * 64, [(53 * i) % 900 for i in range(64)]),
     "chain5_batch_wide": ([chain(5)] * 40, [(71 * i) % 1300 for i in range(40)]),
     "chain8_batch_narrow": ([chain(8)] * 50, [(67 * i) % 1100 for i in range(50)], NARROW),
+    "batch_of_32": ([chain(1 + i % 3) for i in range(32)], [(83 * i) % 500 for i in range(32)], NARROW),
+    "batch_of_33": ([chain(1 + i % 3) for i in range(33)], [(83 * i) % 500 for i in range(33)], NARROW),
+    "batch_of_256": ([chain(1)] * 256, [(29 * i) % 300 for i in range(256)], (4, 2, 128)),
     "tree15_batch": ([tree(5, 14)] * 40, [(59 * i) % 700 for i in range(40)]),
     "group1": ([tree(7, 11)], [401], (3, 3, 128)),
     "group16": ([tree(8, 6), chain(1)], [401, 90], (16, 1, 256)),

@@ -36,6 +36,7 @@ def _extend(lib, batch=2, max_pages=8, pool=64, ctx=FAKE, add=FAKE + 64, indptr=
     (dict(indptr=[1, 3, 5], path=FAKE + 600, max_path=4), BAD), (dict(indptr=[0, 3, 68], path=FAKE + 600, max_path=4), UNSUP),
     (dict(new_held=FAKE + 192), BAD), (dict(new_count=FAKE + 384), BAD), (dict(new_ctx=FAKE), BAD),   # aliases
     (dict(new_held=FAKE), BAD), (dict(rows=FAKE + 64), BAD),
+    (dict(ctx=FAKE + 2), BAD), (dict(table=FAKE + 129), BAD), (dict(slots=FAKE + 514), BAD), (dict(rows=FAKE + 701), BAD),
 ])
 def test_pages_extend(lib, kw, status):
     assert _extend(lib, **kw) == status
@@ -50,6 +51,7 @@ def _release(lib, batch=2, max_pages=8, pool=64, keep=FAKE, table=FAKE + 64, hel
     (dict(batch=0), BAD), (dict(batch=257), UNSUP), (dict(pool=0), BAD), (dict(keep=None), BAD), (dict(table=None), BAD),
     (dict(held=None), BAD), (dict(new_held=None), BAD), (dict(free=None), BAD), (dict(count=None), BAD),
     (dict(new_count=None), BAD), (dict(new_held=FAKE + 128), BAD), (dict(new_count=FAKE + 320), BAD),
+    (dict(new_count=FAKE + 128), BAD), (dict(free=FAKE + 64), BAD), (dict(held=FAKE + 130), BAD), (dict(free=FAKE + 257), BAD),
 ])
 def test_pages_release(lib, kw, status):
     assert _release(lib, **kw) == status
@@ -69,7 +71,7 @@ def _append(lib, layers=1, heads=4, dim=256, page=16, pool=8, ptr=FAKE, stride=0
     (dict(layers=0), BAD), (dict(layers=65), UNSUP), (dict(heads=0), BAD), (dict(heads=65), UNSUP), (dict(dim=64), UNSUP),
     (dict(dim=0), BAD), (dict(page=32), UNSUP), (dict(pool=0), BAD), (dict(pool=1 << 27), UNSUP), (dict(ptr=None), BAD),
     (dict(ptr=FAKE + 4), BAD), (dict(stride=1023), BAD), (dict(stride=1028), BAD), (dict(stride=-8), BAD),
-    (dict(src=-1), BAD), (dict(slots=None), BAD), (dict(max_rows=-1), BAD),
+    (dict(src=-1), BAD), (dict(slots=None), BAD), (dict(slots=FAKE + 2), BAD), (dict(max_rows=-1), BAD),
     *[(dict(missing=i), BAD) for i in range(6)], *[(dict(odd=i), BAD) for i in range(6)],
 ])
 def test_append(lib, kw, status):
@@ -83,12 +85,12 @@ def _shape(indptr=(0, 5), hq=24, hkv=4, dim=256, max_pages=40, pool=40, **kw):
     return s
 
 
-def _attn(lib, shape=None, opts=None, ws=FAKE, ws_bytes=1 << 40, missing=None, odd=None, out=FAKE * 2):
+def _attn(lib, shape=None, opts=None, ws=FAKE, ws_bytes=1 << 40, missing=None, odd=None, off=8, out=FAKE * 2):
     ptr = [FAKE] * 10 + [out]
     if missing is not None:
         ptr[missing] = None
     if odd is not None:
-        ptr[odd] += 8
+        ptr[odd] += off
     shape = shape or _shape()
     return lib.sd_kv8_attn(shape.ref, None if opts is None else ctypes.byref(opts), *ptr, None, ws, ws_bytes, None, None)
 
@@ -107,7 +109,8 @@ def test_attention_shapes(lib, kw, status):
 
 
 @pytest.mark.parametrize("kw", [
-    *[dict(missing=i) for i in range(11)], *[dict(odd=i) for i in (0, 1, 2, 5, 6, 10)], dict(out=FAKE), dict(ws=FAKE + 8),
+    *[dict(missing=i) for i in range(11)], *[dict(odd=i) for i in (0, 1, 2, 5, 6, 10)],
+    *[dict(odd=i, off=2) for i in (3, 4, 7, 8, 9)], dict(out=FAKE), dict(ws=FAKE + 8),
     dict(opts=native.SdKv8Opts(-1.0)), dict(opts=native.SdKv8Opts(float("nan"))), dict(opts=native.SdKv8Opts(0, -2.0)),
     dict(opts=native.SdKv8Opts(0, float("inf"))), dict(opts=native.SdKv8Opts(0, 0, FAKE + 2)),
     dict(opts=native.SdKv8Opts(0, 0, None, 100)), dict(opts=native.SdKv8Opts(0, 0, None, 0, 1020)),
