@@ -442,7 +442,7 @@ def _put_layers(ptrs, x, n: int, what: str, dtype, shape, nbytes: int, index: in
     """Append the device addresses of n per-layer tensors (a list of them, or one tensor with a leading layer dimension)."""
     if isinstance(x, torch.Tensor):
         base = _tensor(x, what, dtype, (n, *shape), index)
-        ptrs.extend([base + nbytes * i for i in range(n)])
+        ptrs.extend(range(base, base + nbytes * n, nbytes) if nbytes else [base] * n)
     elif len(x) == n:
         ptrs.extend([_tensor(t, what, dtype, shape, index) for t in x])
     else:
@@ -532,8 +532,8 @@ def sd_kv8_append(k_cache_layers, v_cache_layers, k_scale_layers, v_scale_layers
             raise ValueError("no layers")
         n, cache = len(first), tuple(first[0].shape)
     else:
-        n, *cache = first.shape if first.dim() else (0,)
-        cache = tuple(cache)
+        shape = first.shape
+        n, cache = (shape[0], shape[1:]) if shape else (0, ())
     if len(cache) != 4 or slots.dim() != 1:
         raise ValueError("a layer's cache is [pool, heads, 16, dim], slots is one-dimensional")
     pool, heads, page, dim = cache
