@@ -193,7 +193,10 @@ size_t sd_kv8_attn_workspace_size(const sd_shape* shape);
  * they lie; a query as two e4m3 terms (off by at most 2^-17 of the largest
  * query amax among the columns that share a CTA); a draft key or value as two
  * e4m3 terms (2^-17 of its row's amax); a softmax weight as an e4m3 term and an
- * e5m2 rest (2^-7 of the weight at most; the sum of weights is not rounded).
+ * e5m2 rest (2^-7 of the weight at most; 2^-3 for weights below 2^-9 of the
+ * largest that its CTA has met in the column, and below 2^-20 of that, 2^-22
+ * over more than 8192 tokens of a CTA, 2^-24 over 32768, a weight no longer
+ * reaches the output; the sum of weights is not rounded).
  * Outputs are typically within 0.002 of their size, against 0.0017 for the
  * rounding to bf16 alone.  A page id out of range sets SD_DEV_BAD_PAGE and its
  * tokens count as zeros; a scale out of range sets SD_DEV_BAD_SCALE and is

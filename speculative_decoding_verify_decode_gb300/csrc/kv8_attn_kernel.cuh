@@ -19,8 +19,8 @@
 // largest query's amax, so a score is off by no more than that query's);
 // both multiply the same K tile into the same accumulator.  A weight is an
 // e4m3 term and an e5m2 rest (2^-4 times 2^-3: at most 2^-7 off, about 2^-9.5
-// in the mean square; e5m2 so that the rest of small weights keeps its
-// exponent range, down to 2^-16).  l sums the unrounded fp32 weights.  Draft
+// in the mean square, while the term is normal; e5m2 so that the rest of small
+// weights keeps its exponent range, down to 2^-16).  l sums the unrounded fp32 weights.  Draft
 // keys and values are bf16 and take two e4m3 terms each, four products.
 //
 // What bounds it.  Bytes: 2 D per token and KV head (codes of K and V), read
@@ -73,9 +73,17 @@ namespace {
 constexpr int kTile = kTileTokens;
 constexpr float kTop = 448.0f;         // weights beyond it move m
 // Where the largest weight so far sits after m moved: at 2^3 when m is set by a column's first tile, whose maximum is
-// likely to be passed by some nats further on, at 2^5 when it was passed by so much that m had to move.  Higher keeps
-// more of the small weights' bits, lower lets the maximum grow further before the next move (a move costs a tile 2 us).
+// likely to be passed by some nats further on, at 2^5 when it was passed by so much that m had to move (a move costs a tile
+// 2 us).  Lower means fewer moves, and coarser small weights: where the largest is 2^h, weights below 2^(-6 - h) of it keep
+// an e5m2 value's bits and those below 2^(-17 - h) nothing.  h grows with the piece, so that what is lost of its n tokens,
+// n 2^(-17 - h), stays below 2^-7 of the largest weight up to 131072 of them.  At 2^1 and 2^2 a tree of 23 over 131072 tokens took 79.7 us
+// instead of 85.6, for limits four times as high.  (Tiles go from the last to the first and every piece has references of
+// its own, so a peak at the front of a context hides none of it.)
 constexpr float kHeadFirst = 3.0f, kHeadNext = 5.0f;
+__device__ __forceinline__ float head_of(int tiles, bool first) {
+  const float least = tiles > 256 ? 7.0f : tiles > 64 ? 5.0f : 3.0f;
+  return fmaxf(least, first ? kHeadFirst : kHeadNext);
+}
 constexpr float kDown = 0x1p-8f;       // weights are formed times 2^-8 (see split4)
 constexpr float kScaleLo = 0x1p-100f, kScaleHi = 0x1p100f;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -1151,7 +1159,7 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
           if (mine_col < mine * 16 && ((todo >> (mine_col >> 4)) & 1u)) {
             const float old = -sm->m[q];
             const float mt = old + fmaxf(fmaxf(sm->red[0][q], sm->red[1][q]), fmaxf(sm->red[2][q], sm->red[3][q])) -
-                             (old == 0.f ? kHeadFirst : kHeadNext);
+                             head_of(pc.tiles, old == 0.f);
             float now = mt == -INFINITY ? old : old == 0.f ? mt : fmaxf(old, mt);
             if (now == 0.f && mt != -INFINITY) now = 1e-30f;
             sm->alpha[q] = old == 0.f ? 1.f : fast_exp2(old - now);

@@ -254,6 +254,24 @@ def test_flat_background_below_a_peak():
         c.check()
 
 
+def test_flat_background_behind_a_peak_in_long_pieces():
+    """Sixty-four sequences on one context, some 200 tiles a CTA, their own token 14 nats above 16384 equal ones:
+    the background is 0.0136 of the peak, and an output without it is off by more than the bound of 2^-7 + 2^-8."""
+    c = Case([chain(1)], [16384], (8, 8, 128), seed=4)
+    c.codes["k"][:] = 0x08                                            # 2^-6 each
+    c.codes["v"][:] = 0x38                                            # 1 each
+    c.scales["k"][:] = c.scales["v"][:] = 1.0
+    c.q[:], c.kn[:], c.vn[:] = 0.5, 14.0 / (0.5 * 128 ** 0.5) + 2.0 ** -6, -1.0
+    ds = c.score_error()                                              # the same for every sequence
+    c.score_error = lambda: ds
+    c.q, c.kn, c.vn = (x.expand(64, -1, -1).contiguous() for x in (c.q, c.kn, c.vn))
+    c.indptr, c.parents = np.arange(65), np.full(64, -1, np.int32)
+    c.ctx, c.table = np.full(64, 16384, np.int32), np.tile(c.table, (64, 1))
+    c.upload()
+    c.call()
+    c.check(only={(r, h) for r in (0, 17, 63) for h in (0, 5)})
+
+
 def test_block_scales_at_their_ends():
     """All-zero V blocks with the smallest scale, tiny and huge scales beside ordinary ones."""
     c = Case([tree(5, 9)], [700], seed=6)
