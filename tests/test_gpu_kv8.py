@@ -259,8 +259,8 @@ def test_flat_background_behind_a_peak_in_long_pieces():
     the background is 0.0136 of the peak, and an output without it is off by more than the bound of 2^-7 + 2^-8."""
     c = Case([chain(1)], [16384], (8, 8, 128), seed=4)
     c.codes["k"][:] = 0x08                                            # 2^-6 each
-    c.codes["v"][:] = 0x38                                            # 1 each
-    c.scales["k"][:] = c.scales["v"][:] = 1.0
+    c.codes["v"][:], c.scales["v"][:] = 0x78, 2.0 ** -8               # 1 each, as an append scales it (and the peak)
+    c.scales["k"][:] = 1.0
     c.q[:], c.kn[:], c.vn[:] = 0.5, 14.0 / (0.5 * 128 ** 0.5) + 2.0 ** -6, -1.0
     ds = c.score_error()                                              # the same for every sequence
     c.score_error = lambda: ds
