@@ -73,12 +73,12 @@ namespace {
 constexpr int kTile = kTileTokens;
 constexpr float kTop = 448.0f;         // weights beyond it move m
 // Where the largest weight so far sits after m moved: at 2^3 when m is set by a column's first tile, whose maximum is
-// likely to be passed by some nats further on, at 2^5 when it was passed by so much that m had to move (a move costs a tile
-// 2 us).  Lower means fewer moves, and coarser small weights: where the largest is 2^h, weights below 2^(-6 - h) of it keep
-// an e5m2 value's bits and those below 2^(-17 - h) nothing.  h grows with the piece, so that what is lost of its n tokens,
-// n 2^(-17 - h), stays below 2^-7 of the largest weight up to 131072 of them.  At 2^1 and 2^2 a tree of 23 over 131072 tokens took 79.7 us
-// instead of 85.6, for limits four times as high.  (Tiles go from the last to the first and every piece has references of
-// its own, so a peak at the front of a context hides none of it.)
+// likely to be passed by some nats further on, at 2^5 when it was passed by so much that m had to move (a move costs a
+// tile 2 us).  Lower means fewer moves, and coarser small weights: where the largest is 2^h, weights below 2^(-6 - h)
+// of it keep an e5m2 value's bits and those below 2^(-17 - h) nothing.  h grows with the piece, so that what is lost of
+// its n tokens, n 2^(-17 - h), stays below 2^-7 of the largest weight up to 131072 of them.  At 2^1 and 2^2 a tree of
+// 23 over 131072 tokens took 79.7 us instead of 85.6, for limits four times as high.  (Tiles go from the last to the
+// first and every piece has references of its own, so a peak at the front of a context hides none of it.)
 constexpr float kHeadFirst = 3.0f, kHeadNext = 5.0f;
 __device__ __forceinline__ float head_of(int tiles, bool first) {
   const float least = tiles > 256 ? 7.0f : tiles > 64 ? 5.0f : 3.0f;

@@ -190,7 +190,7 @@ def test_attention_matches_oracle(name):
 
 MODS = {
     "window1": dict(window=1), "window7": dict(window=7), "window100": dict(window=100), "window129": dict(window=129),
-    "window700": dict(window=700), "window5000": dict(window=5000), "softcap": dict(softcap=30.0),
+    "window700": dict(window=700), "window5000": dict(window=5000), "window_largest": dict(window=2 ** 31 - 1), "softcap": dict(softcap=30.0),
     "tight_softcap": dict(softcap=0.5), "bias": dict(slopes=True), "bias_and_cap": dict(softcap=5.0, slopes=True),
     "all": dict(softcap=5.0, slopes=True, window=333), "scale": dict(scale=0.3),
 }
