@@ -395,12 +395,17 @@ def _tensor(t, what: str, dtype, shape, index: int) -> int:
 
 
 def _rows(t, what: str, shape, index: int) -> tuple[int, int]:
-    """Address and row stride (0: dense) of bf16 [rows, heads, dim]; the rows may lie apart, a row is dense."""
+    """Address and row stride (0: dense) of bf16 [rows, heads, dim]; the rows may lie apart, a row is dense.  Rows that
+    share memory (a tensor expanded along them has stride 0, which the C ABI takes for dense) are refused."""
     if t.dtype is torch.bfloat16 and t.shape == shape and t.get_device() == index:
         if t.is_contiguous():
             return t.data_ptr(), 0
         if t.stride(2) == 1 and (shape[1] == 1 or t.stride(1) == shape[2]):
-            return t.data_ptr(), t.stride(0) if shape[0] > 1 else 0
+            if shape[0] <= 1:
+                return t.data_ptr(), 0
+            if t.stride(0) < shape[1] * shape[2]:
+                raise ValueError(f"{what}: the rows overlap (row stride {t.stride(0)}, a row has {shape[1] * shape[2]} values)")
+            return t.data_ptr(), t.stride(0)
     _refuse(t, what, torch.bfloat16, shape, index)
 
 
@@ -525,7 +530,7 @@ def sd_kv8_append(k_cache_layers, v_cache_layers, k_scale_layers, v_scale_layers
     """bf16 rows quantised into the caches of every layer at the slots of a slot map (sd_pages_extend).
 
     Per layer (lists, or tensors with a leading layer dimension): codes uint8 [pool, heads, 16, dim], scales fp32
-    [pool, heads], new rows bf16 [rows, heads, dim] (rows may lie apart)."""
+    [pool, heads], new rows bf16 [rows, heads, dim] (rows may lie apart, not overlap)."""
     dev, first = slots.get_device(), k_cache_layers
     if not isinstance(first, torch.Tensor):
         if not first:
@@ -564,7 +569,7 @@ def sd_kv8_attn(shape: Shape, q, k_cache, v_cache, k_scales, v_scales, k_new, v_
                 out, lse=None, scale: float = 0.0, softcap: float = 0.0, slopes=None, workspace=None, dev_status=None,
                 stream=None) -> None:
     """sd_verify_attn over the block-scaled cache; ``softcap`` and ``slopes`` (fp32 [query heads]) as in sd_kv8_opts.
-    q, k_new and v_new may have rows that lie apart (slices of a fused projection)."""
+    q, k_new and v_new may have rows that lie apart (slices of a fused projection), not rows that overlap."""
     dev = q.get_device()
     q_shape, kv_shape, cache, block, table, batch, n = shape.dims
     q_at, qs = _rows(q, "q", q_shape, dev)

@@ -186,3 +186,38 @@ def test_structs_and_constants_match_the_header():
                                               text=True).stdout.split()]
     assert got == [ctypes.sizeof(native.SdKv8Opts)] + [getattr(native.SdKv8Opts, n).offset for n in names] + \
         [getattr(native, b) for b in bits]
+
+
+def test_binding_refuses_rows_that_overlap():
+    """Rows expanded from one have stride 0, which means dense to the library: it would read behind the tensor."""
+    codes, scales = torch.zeros(8, 4, 16, 256, dtype=torch.uint8), torch.zeros(8, 4)
+    one = lambda heads, layers=(): torch.zeros(*layers, 1, heads, 256, dtype=torch.bfloat16)
+    new, broad = torch.zeros(6, 4, 256, dtype=torch.bfloat16), one(4).expand(6, 4, 256)
+    rows = torch.zeros(6, dtype=torch.int32)
+    shifted = torch.zeros(8 * 512, dtype=torch.bfloat16).as_strided((6, 4, 256), (512, 256, 1))   # half a row apart
+    for k, v in [([broad], [broad]), ([broad], [new]), ([new], [broad]), ([shifted], [shifted]),
+                 (one(4, (1,)).expand(1, 6, 4, 256),) * 2]:
+        with pytest.raises(ValueError, match="rows overlap"):
+            native.sd_kv8_append([codes], [codes], [scales], [scales], k, v, rows)
+    two = one(4, (2,)).expand(2, 6, 4, 256)
+    with pytest.raises(ValueError, match="rows overlap"):
+        native.sd_kv8_append([codes] * 2, [codes] * 2, [scales] * 2, [scales] * 2, two, two, rows)
+    s = _shape((0, 6), pool=8, max_pages=3)
+    i32 = lambda *n: torch.zeros(*n, dtype=torch.int32)
+    q = torch.zeros(6, 24, 256, dtype=torch.bfloat16)
+    ok = [s, q, codes, codes, scales, scales, new, new, i32(1, 3), i32(1), i32(6), torch.empty_like(q)]
+    for at, t in [(1, one(24).expand(6, 24, 256)), (6, broad), (7, broad), (7, shifted)]:
+        args = list(ok)
+        args[at] = t
+        with pytest.raises(ValueError, match="rows overlap"):
+            native.sd_kv8_attn(*args)
+    # one head a row, and one row, have no such stride to check
+    narrow = _shape((0, 6), hq=1, hkv=1, pool=8, max_pages=3)
+    args = [narrow, one(1).expand(6, 1, 256), codes[:, :1].contiguous(), codes[:, :1].contiguous(), scales[:, :1].contiguous(),
+            scales[:, :1].contiguous(), new[:, 0:1].contiguous(), new[:, 0:1].contiguous(), i32(1, 3), i32(1), i32(6),
+            torch.empty(6, 1, 256, dtype=torch.bfloat16)]
+    with pytest.raises(ValueError, match="rows overlap"):
+        native.sd_kv8_attn(*args)
+    args[1] = torch.zeros(6, 3, 256, dtype=torch.bfloat16)[:, 1:2]                  # rows that lie apart pass
+    with pytest.raises(ValueError, match="CUDA"):
+        native.sd_kv8_attn(*args)
