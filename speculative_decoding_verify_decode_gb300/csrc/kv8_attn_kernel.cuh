@@ -351,7 +351,8 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
   if (tid == 0) {
 #pragma unroll 1
     for (int i = 0; i < kNumBars; ++i)
-      mbar_init(smem_u32(&sm->bar[i]), i == B_PF || (i >= B_SE && i < B_SE + NS) ? (uint32_t)kWarps : i >= B_G ? 4u : 1u);
+      mbar_init(smem_u32(&sm->bar[i]), i == B_PF || (i >= B_SE && i < B_SE + NS) ? (uint32_t)kWarps : i >= B_G ? 4u :
+                                           i < B_KE || (i >= B_VF && i < B_VE) ? 2u : 1u);
     sm->abort = 0;
     sm->q_amax[0] = sm->q_amax[1] = 0u;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -540,17 +541,25 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         if (pc.first == 0) {
           // The draft tile is staged by the softmax warps: its slots, and its scale stage, pass by in their turn.  In
           // their turn means waiting for what they held before: a producer that went past a slot without that could
-          // be two rounds ahead of it, which a barrier's parity cannot tell from none.
+          // be two rounds ahead of it, which a barrier's parity cannot tell from none.  Nor may it fall two rounds
+          // behind: a slot is full once it has its contents and its producer has come by (two arrivals a round), so
+          // that no product of a draft tile begins before both producers have passed it.
           if (is_k) {
             ok = __all_sync(0xffffffffu, wait_empty(B_KE, ring));
             if (!ok) break;
-            if (elect_one()) mbar_arrive(bar(B_SC + sc_ring.at));
+            if (elect_one()) {
+              mbar_arrive(bar(B_SC + sc_ring.at));
+              mbar_arrive(bar(B_KF + ring.at));
+            }
+            __syncwarp();
             sc_ring.next(SC);
             ring.next(KS);
           } else {
 #pragma unroll 1
             for (int h = 0; h < 2 && ok; ++h) {
               ok = __all_sync(0xffffffffu, wait_empty(B_VE, ring));
+              if (ok && elect_one()) mbar_arrive(bar(B_VF + ring.at));
+              __syncwarp();
               ring.next(VS);
             }
             if (!ok) break;
@@ -613,6 +622,7 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             for (int j = 0; j < 8; ++j) w[j] = __shfl_sync(0xffffffffu, half_page, sub + j);
             if (elect_one()) {
               mbar_expect_tx(bar(B_KF + ring.at), (uint32_t)__popc(have) * (uint32_t)K::kPageBytes);
+              mbar_arrive(bar(B_KF + ring.at));
 #pragma unroll
               for (int j = 0; j < 8; ++j)
                 if ((have >> j) & 1u) tma_page8(smem_u32(dst) + j * K::kPageBytes, map, w[j], bar(B_KF + ring.at), policy);
@@ -685,6 +695,7 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                   const uint32_t full = bar(B_VF + (hh > h ? other.at : ring.at));
                   const uint32_t mine = (fast >> (4 * hh)) & 0xfu;
                   mbar_expect_tx(full, (uint32_t)__popc(mine) * (uint32_t)K::kPageBytes);
+                  mbar_arrive(full);
 #pragma unroll
                   for (int j = 0; j < 4; ++j)
                     if ((mine >> j) & 1u)

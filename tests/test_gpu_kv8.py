@@ -688,3 +688,21 @@ def test_a_refused_release_leaves_the_cache_as_it_was(raw):
     cache.release(cu([10, 100], torch.int32), stream=0 if raw else None)
     torch.cuda.synchronize()
     assert cache.ctx_lens.tolist() == [10, 20] and cache.held.tolist() == [1, 2] and int(cache.free_count) == 13
+
+
+@pytest.mark.parametrize("heads,nodes", [((24, 4, 256), 1), ((24, 4, 256), 5), ((24, 4, 256), 13), ((24, 4, 256), 23),
+                                         ((16, 16, 128), 9), ((32, 8, 128), 8), ((32, 8, 128), 31)])
+def test_batches_without_context(heads, nodes):
+    """Hundreds of sequences of nothing but a draft block: every CTA works through several pieces that no cache tile
+    separates, with every width of its rings."""
+    batch = 256 if nodes < 20 else 128
+    c = Case([tree(i, nodes - 1) if nodes > 2 else chain(nodes) for i in range(batch)], [0] * batch, heads, seed=nodes).upload()
+    rng, total = np.random.default_rng(nodes), int(c.indptr[-1])
+    c.call()
+    c.check(only={(int(rng.integers(total)), int(rng.integers(c.hq))) for _ in range(200)})
+    want, lse = c.out.clone(), c.lse.clone()
+    for _ in range(10):
+        c.out.fill_(7.0)
+        c.call()
+        assert torch.equal(c.out, want) and torch.equal(c.lse, lse)
+    assert int(c.status) == 0
