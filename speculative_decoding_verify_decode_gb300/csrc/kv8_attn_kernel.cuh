@@ -351,8 +351,7 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
   if (tid == 0) {
 #pragma unroll 1
     for (int i = 0; i < kNumBars; ++i)
-      mbar_init(smem_u32(&sm->bar[i]), i == B_PF || (i >= B_SE && i < B_SE + NS) ? (uint32_t)kWarps : i >= B_G ? 4u :
-                                           i < B_KE || (i >= B_VF && i < B_VE) ? 2u : 1u);
+      mbar_init(smem_u32(&sm->bar[i]), i == B_PF || (i >= B_SE && i < B_SE + NS) ? (uint32_t)kWarps : i >= B_G ? 4u : 1u);
     sm->abort = 0;
     sm->q_amax[0] = sm->q_amax[1] = 0u;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -542,8 +541,8 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
           // The draft tile is staged by the softmax warps: its slots, and its scale stage, pass by in their turn.  In
           // their turn means waiting for what they held before: a producer that went past a slot without that could
           // be two rounds ahead of it, which a barrier's parity cannot tell from none.  Nor may it fall two rounds
-          // behind: a slot is full once it has its contents and its producer has come by (two arrivals a round), so
-          // that no product of a draft tile begins before both producers have passed it.
+          // behind: the producers say that the slots are full as they come by, so that no product of a draft tile begins
+          // before both have passed it (that its contents are there, B_Q and B_PF say).
           if (is_k) {
             ok = __all_sync(0xffffffffu, wait_empty(B_KE, ring));
             if (!ok) break;
@@ -622,7 +621,6 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             for (int j = 0; j < 8; ++j) w[j] = __shfl_sync(0xffffffffu, half_page, sub + j);
             if (elect_one()) {
               mbar_expect_tx(bar(B_KF + ring.at), (uint32_t)__popc(have) * (uint32_t)K::kPageBytes);
-              mbar_arrive(bar(B_KF + ring.at));
 #pragma unroll
               for (int j = 0; j < 8; ++j)
                 if ((have >> j) & 1u) tma_page8(smem_u32(dst) + j * K::kPageBytes, map, w[j], bar(B_KF + ring.at), policy);
@@ -695,7 +693,6 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                   const uint32_t full = bar(B_VF + (hh > h ? other.at : ring.at));
                   const uint32_t mine = (fast >> (4 * hh)) & 0xfu;
                   mbar_expect_tx(full, (uint32_t)__popc(mine) * (uint32_t)K::kPageBytes);
-                  mbar_arrive(full);
 #pragma unroll
                   for (int j = 0; j < 4; ++j)
                     if ((mine >> j) & 1u)
@@ -971,14 +968,7 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         if (has_draft && sm->row_v[tid] != sm->row_v[tid]) sm->row_k[tid] = sm->row_v[tid];   // NaN: to the scores
       }
       sync_all();
-      if (tid == 0) {
-        mbar_arrive(bar(B_Q));
-        if (has_draft) {
-          mbar_arrive(bar(B_KF + it % KS));
-          mbar_arrive(bar(B_VF + 2 * it % VS));
-          mbar_arrive(bar(B_VF + (2 * it + 1) % VS));
-        }
-      }
+      if (tid == 0) mbar_arrive(bar(B_Q));
       if (has_draft && n_nodes > 1) {
         // While the first product runs: the root paths turned round by ballots, a row of the tile a turn.  (Asked node by
         // node in the tile they took 90 ns a node: 89 sequences of up to 62 nodes 475 -> 423 us.)
