@@ -190,8 +190,8 @@ size_t sd_kv8_attn_workspace_size(const sd_shape* shape);
  *
  * Numerics: scores, softmax statistics, sums and the partial outputs of split
  * sequences are fp32.  The products take 8-bit operands: the cache's codes as
- * they lie; a query as two e4m3 terms (off by at most 2^-17 of the largest
- * query amax among the columns that share a CTA); a draft key or value as two
+ * they lie; a query (one node's, of one head) as two e4m3 terms (off by at most
+ * 2^-17 of its own amax); a draft key or value as two
  * e4m3 terms (2^-17 of its row's amax); a softmax weight as an e4m3 term and an
  * e5m2 rest (2^-7 of the weight at most; 2^-3 for weights below 2^-9 of the
  * largest that its CTA has met in the column, and below 2^-20 of that, 2^-22

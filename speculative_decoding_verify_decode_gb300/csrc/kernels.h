@@ -221,6 +221,7 @@ struct Kv8AttnParams {
   int* dev_status;           // nullable
   long long q_stride, k_stride, v_stride;   // elements between rows
   float scale, softcap;      // softcap 0: none
+  float cap_exp;             // 2 / softcap
   int hq, hkv, dim, max_pages, num_pool_pages, window;
   void* workspace;
   int group;                 // query heads per KV head

@@ -232,6 +232,7 @@ sd_status sd_kv8_attn(const sd_shape* shape, const sd_kv8_opts* opts, const void
   p.dev_status = dev_status;
   p.scale = o.scale > 0.f ? o.scale : 1.0f / std::sqrt((float)shape->head_dim);
   p.softcap = o.softcap;
+  p.cap_exp = o.softcap > 0.f ? 2.0f / o.softcap : 0.f;
   p.hq = shape->num_q_heads;
   p.hkv = shape->num_kv_heads;
   p.group = p.hq / p.hkv;

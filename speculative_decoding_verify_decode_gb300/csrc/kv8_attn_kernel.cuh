@@ -14,9 +14,10 @@
 // largest e4m3 value.
 //
 // The 8-bit operands.  K and V are exact as they lie.  A bf16 query is two
-// e4m3 terms (a power-of-two scale for all the CTA's queries, then the rounded
-// value and the rounded rest: 8 significant bits, off by at most 2^-18 of the
-// largest query's amax, so a score is off by no more than that query's);
+// e4m3 terms (a power-of-two scale for each query, which its column's scores
+// take back in fp32, then the rounded value and the rounded rest: off by at
+// most half of e4m3's smallest step, 2^-10 of an amax of 224 to 448, so by less
+// than 2^-17 of the query's own amax);
 // both multiply the same K tile into the same accumulator.  A weight is an
 // e4m3 term and an e5m2 rest (2^-4 times 2^-3: at most 2^-7 off, about 2^-9.5
 // in the mean square, while the term is normal; e5m2 so that the rest of small
@@ -95,7 +96,9 @@ struct KvSmall {
   static constexpr int kBars = TIGHT ? 24 : 40;
   float m[NQ];             // the column's reference, negated: -m
   float alpha[NQ];         // rescale factor of the current tile; 1 / l in the epilogue
+  float qf[NQ];            // power-of-two scale of the column's query
   float slope[MOD ? NQ : 4];   // distance bias of the column, base 2
+  float one[4];            // 1 in place of a query's scale, where the cap has taken it
   float red[4][NQ];        // per lane quarter: column maxima of a tile; column sums in the epilogue
   float scale[kScaleStages][16];   // K scales, then V scales, of a tile's eight pages
   float row_k[kMaxNodes], row_v[kMaxNodes];   // scales of the draft block's rows
@@ -105,7 +108,6 @@ struct KvSmall {
   int cum[kMaxBatch + 1];  // first unit of each sequence
   int scan[8];
   int per, extra;
-  uint32_t q_amax[2];      // bf16 bits of the largest finite query magnitude of this piece, and of the next
   int8_t par[kMaxNodes];
   int8_t depth[kMaxNodes];
   alignas(16) int flag[3][2][4];   // [group][tile parity][lane quarter]: chunks where a weight passes kTop
@@ -290,6 +292,10 @@ __device__ __forceinline__ uint32_t amax_bits(const uint4 x) {
 __device__ __forceinline__ int exp_of(uint32_t bits) {
   return min(100, max(-100, (int)(bits >> 7) - 127 - 8 + ((bits & 0x7fu) > 0x60u ? 1 : 0)));
 }
+// The same for a query, whose scale only its own scores meet: any bf16 amax (2^e and 2^-e are normal numbers).
+__device__ __forceinline__ int query_exp(uint32_t bits) {
+  return max(-126, (int)(bits >> 7) - 127 - 8 + ((bits & 0x7fu) > 0x60u ? 1 : 0));
+}
 __device__ __forceinline__ float exp2i(int e) { return __int_as_float((e + 127) << 23); }
 
 // What a segment's draft tile counts for beyond one unit, where CTAs have `even` units each: staging the block, its masks
@@ -353,7 +359,7 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     for (int i = 0; i < kNumBars; ++i)
       mbar_init(smem_u32(&sm->bar[i]), i == B_PF || (i >= B_SE && i < B_SE + NS) ? (uint32_t)kWarps : i >= B_G ? 4u : 1u);
     sm->abort = 0;
-    sm->q_amax[0] = sm->q_amax[1] = 0u;
+    sm->one[0] = sm->one[1] = sm->one[2] = sm->one[3] = 1.f;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   // Launched as a programmatic dependent: everything above touches no global memory; here the previous kernel's writes
@@ -825,9 +831,9 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     auto sync_all = [] { asm volatile("bar.sync 7, %0;" ::"n"(kWarps * 32) : "memory"); };        // the softmax warps
     auto sync_group = [&] { asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory"); };     // the group's four
     Ring s_ring, sc_ring;
-    int it = 0, np = 0;
+    int it = 0;
 #pragma unroll 1
-    for (int u = u_begin; u < u_end; ++np) {
+    for (int u = u_begin; u < u_end;) {
       const Piece pc = piece_at(u);
       u += pc.span;
       const int q0 = bd.q_indptr[pc.b], n_nodes = bd.q_indptr[pc.b + 1] - q0;
@@ -839,7 +845,6 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
       const int mine = min(CC, max(0, nc - group * CC)), c_first = group * CC;
       const int col0 = c_first * 16;
       const bool has_draft = pc.first == 0;
-      float fac;      // of a raw product, with its token's K scale: the base-2 score
       // ---------------------------------------------------------- staging: Q, the tree, the draft block
       // (the previous piece's products have all finished: its last O_DONE was waited for)
       if (tid < n_nodes) {
@@ -912,30 +917,25 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             }
           }
         }
-        uint32_t most = 0, wilds = 0;
+        int e_q[U];
+        uint32_t wilds = 0;
 #pragma unroll
         for (int i = 0; i < U; ++i) {
           bool wild;
-          most = max(most, row_amax(x[i], wild));
+          e_q[i] = query_exp(row_amax(x[i], wild));
           wilds |= wild ? 1u << i : 0u;
         }
-        most = __reduce_max_sync(0xffffffffu, most);
-        if (lane == 0) atomicMax(&sm->q_amax[np & 1], most);
-        sync_all();
-        const int e_q = exp_of(sm->q_amax[np & 1]);
-        const float inv = exp2i(-e_q);
-        fac = exp2i(e_q) * p.scale * (MOD && p.softcap > 0.f ? 2.f * kLog2e / p.softcap : kLog2e);
-        if (tid == 0) sm->q_amax[(np + 1) & 1] = 0u;
 #pragma unroll
         for (int i = 0; i < U; ++i) {
           const int r = (i * kWarps + warp) * RPW + sub;
           uint2 hi, lo;
-          split8(x[i], inv, hi, lo);
+          split8(x[i], exp2i(-e_q[i]), hi, lo);
           if ((wilds >> i) & 1u) hi = make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);     // NaN codes: the column's scores are NaN
           if (r < n_q) {
             uint8_t* at = sQ + (ch >> 4) * NQ * 128 + r * 128 + swizzled(r);
             *reinterpret_cast<uint2*>(at) = hi;
             *reinterpret_cast<uint2*>(at + K::kQTerm) = lo;
+            if (ch == 0) sm->qf[r] = exp2i(e_q[i]);
           }
         }
       }
@@ -944,6 +944,7 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
 #pragma unroll 1
       for (int q = tid; q < NQ; q += kWarps * 32) {
         sm->m[q] = q < nc * 16 ? 0.f : -1e30f;     // no reference yet; columns past those in use: below everything
+        if (q >= nc * 16) sm->qf[q] = 1.f;
         if (MOD) sm->slope[q] = p.slopes != nullptr && q < rows ? p.slopes[head0 + q % hpc] * kLog2e : 0.f;
       }
       // the tree: root paths and depths
@@ -995,6 +996,7 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
       const int lo_root = p.window > 0 ? pc.L - p.window + 1 : 0;
       // The scales of this thread's token row in the coming tile: the score factor, log2 of the V scale, and the V scale
       // on the weights.
+      const float fac = p.scale * kLog2e;
       float kf, lv, vd;
       auto set_scales = [&](float ks, float vs) {
         kf = ks * fac;
@@ -1064,15 +1066,22 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         const float limit = 8.807354922f - lv;       // log2(kTop)
         // the bias' distance is counted from the root: a node's depth shifts all its scores alike (see the log-sum-exp)
         const float rel = draft ? (row < n_nodes ? (float)sm->depth[row] : 0.f) : (float)(t0 + row - pc.L);
+        // A product becomes a score by its token's factor, then its column's (in this order nothing overflows that the
+        // score itself does not).
+        auto scored = [](float x, float y, float token, float qx, float qy) {
+          return mul2(mul2(make_float2(x, y), make_float2(token, token)), make_float2(qx, qy));
+        };
         float kv = kf;
-        if (MOD && p.softcap > 0.f) {
-          // c tanh(x / c) = c - 2 c / (1 + 2^(2 log2e x / c)); fac holds the factor of the exponent
-          const float cl = p.softcap * kLog2e;
+        const bool cap = MOD && p.softcap > 0.f;
+        if (cap) {
+          // c tanh(x / c) = c - 2 c / (1 + 2^(2 log2e x / c))
+          const float cl = p.softcap * kLog2e, to_exp = p.cap_exp;
 #pragma unroll
           for (int c = 0; c < CC; ++c) {
 #pragma unroll
             for (int e = 0; e < 16; e += 2) {
-              const float2 y = mul2(make_float2(a[c][e], a[c][e + 1]), make_float2(kf, kf));
+              const float2 qf = *reinterpret_cast<const float2*>(&sm->qf[col0 + c * 16 + e]);
+              const float2 y = mul2(scored(a[c][e], a[c][e + 1], kf, qf.x, qf.y), make_float2(to_exp, to_exp));
               const float2 d = add2(make_float2(fast_exp2(y.x), fast_exp2(y.y)), make_float2(1.f, 1.f));
               const float2 s = fma2(make_float2(fast_rcp(d.x), fast_rcp(d.y)), make_float2(-2.f * cl, -2.f * cl), make_float2(cl, cl));
               a[c][e] = s.x;
@@ -1095,8 +1104,9 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
               m0 = fma2(make_float2(sl.x, sl.y), make_float2(rel, rel), m0);
               m1 = fma2(make_float2(sl.z, sl.w), make_float2(rel, rel), m1);
             }
-            const float2 d0 = fma2(make_float2(v[0], v[1]), make_float2(kv, kv), m0);
-            const float2 d1 = fma2(make_float2(v[2], v[3]), make_float2(kv, kv), m1);
+            const float4 qf = *reinterpret_cast<const float4*>(cap ? sm->one : &sm->qf[q + 4 * k]);
+            const float2 d0 = fma2(mul2(make_float2(v[0], v[1]), make_float2(kv, kv)), make_float2(qf.x, qf.y), m0);
+            const float2 d1 = fma2(mul2(make_float2(v[2], v[3]), make_float2(kv, kv)), make_float2(qf.z, qf.w), m1);
             v[0] = d0.x; v[1] = d0.y; v[2] = d1.x; v[3] = d1.y;
             top = fmaxf(fmaxf(top, fmaxf(d0.x, d0.y)), fmaxf(d1.x, d1.y));
           }

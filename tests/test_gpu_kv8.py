@@ -706,3 +706,42 @@ def test_batches_without_context(heads, nodes):
         c.call()
         assert torch.equal(c.out, want) and torch.equal(c.lse, lse)
     assert int(c.status) == 0
+
+
+@pytest.mark.parametrize("heads,mods", [((24, 4, 256), {}), ((32, 8, 128), {}), ((12, 4, 128), dict(softcap=30.0, slopes=True)),
+                                        ((24, 4, 256), dict(slopes=True))], ids=["d256", "d128", "capped_bias", "bias"])
+@pytest.mark.parametrize("power", [-20, 12, 20, 100])
+def test_large_queries_leave_the_others_alone(heads, mods, power):
+    """One node and one head of every group 2^12 to 2^100 times the rest (or the rest that much larger than them):
+    every ordinary row keeps the bound of its own query, whose error is 2^-17 of its own amax."""
+    mods = dict(mods)
+    if mods.get("slopes"):
+        mods["slopes"] = 2.0 ** (-8.0 * np.arange(1, heads[0] + 1) / heads[0])
+    c = Case([tree(3, 12), chain(6)], [700, 90], heads, seed=19, **mods)
+    group = heads[0] // heads[1]
+    apart = np.zeros((int(c.indptr[-1]), heads[0]), bool)
+    apart[[2, 14]] = True
+    apart[:, 1::group] = True
+    c.q[torch.from_numpy(apart)] *= 2.0 ** power
+    c.upload()
+    c.call()
+    torch.cuda.synchronize()
+    assert int(c.status) == 0
+    ref, lse, spread = c.ref()
+    got, got_lse = np64(c.out[:-1]), np64(c.lse)
+    k1 = kinf = 0.0
+    for b, n in enumerate(c.ctx):
+        k = np.abs(kv8.dequantise(c.codes["k"][c.table[b, :-(-int(n) // PAGE)]], c.scales["k"][c.table[b, :-(-int(n) // PAGE)]]))
+        k1, kinf = max(k1, np.nanmax(k.sum(-1))), max(kinf, np.nanmax(k))
+    kn, q = np.abs(np64(c.kn)), np.abs(np64(c.q))
+    k1, kinf = max(k1, kn.sum(-1).max()), max(kinf, kn.max())
+    bias = 0.0 if c.slopes is None else 2.0 ** -23 * float(np.abs(c.slopes).max()) * (float(c.ctx.max()) + 64)
+    ds = (2.0 ** -17 * (q.max(-1) * k1 + kn.max() * q.sum(-1)) + 2.0 ** -20 * q.sum(-1) * kinf) * c.dim ** -0.5 + bias   # a row's
+    small = ds < 0.25
+    assert np.array_equal(small, ~apart) if power > 0 else small.all()
+    bound = 2.0 ** -8 * np.abs(ref) + (2.0 ** -7 + 2 * np.expm1(np.where(small, ds, 0))[..., None]) * spread + \
+        2.0 ** -17 * float(c.vn.abs().max())
+    over = (np.abs(got - ref) / bound)[small]
+    assert over.max() <= 1.0, over.max()
+    assert np.all(np.abs(got_lse - lse)[small] <= (ds + 2.0 ** -20 * (np.abs(lse) + 1))[small])
+    assert np.isfinite(got).all() and np.isfinite(got_lse).all()
