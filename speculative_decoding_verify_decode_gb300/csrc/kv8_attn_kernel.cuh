@@ -9,9 +9,10 @@
 // so a V scale goes into the weight and a K scale into the score, each one
 // multiplication per score, constant along a token row, and the tensor core
 // never sees anything but codes.  m is the running maximum of s + log2 c_t
-// less a few bits: the weights e c_t stay near 1 however uneven the blocks are,
-// and m moves (with O and l rescaled) only when a weight passes kTop, the
-// largest e4m3 value.
+// less a few bits: the largest weight e c_t stays near 1 however uneven the
+// blocks are (a token of the same e in a block of far smaller scale has a small
+// weight), and m moves (with O and l rescaled) only when a weight passes kTop,
+// the largest e4m3 value.
 //
 // The 8-bit operands.  K and V are exact as they lie.  A bf16 query is two
 // e4m3 terms (a power-of-two scale for each query, which its column's scores
@@ -76,8 +77,9 @@ constexpr float kTop = 448.0f;         // weights beyond it move m
 // Where the largest weight so far sits after m moved: at 2^3 when m is set by a column's first tile, whose maximum is
 // likely to be passed by some nats further on, at 2^5 when it was passed by so much that m had to move (a move costs a
 // tile 2 us).  Lower means fewer moves, and coarser small weights: where the largest is 2^h, weights below 2^(-6 - h)
-// of it keep an e5m2 value's bits and those below 2^(-17 - h) nothing.  h grows with the piece, so that what is lost of
-// its n tokens, n 2^(-17 - h), stays below 2^-7 of the largest weight up to 131072 of them.  At 2^1 and 2^2 a tree of
+// of it keep an e5m2 value's bits, right in the mean of many alike (see split4), and those below 2^(-17 - h) nothing.  h
+// grows with the piece, so that what is lost of its n tokens, n 2^(-17 - h), stays below 2^-7 of the largest weight up
+// to 131072 of them.  At 2^1 and 2^2 a tree of
 // 23 over 131072 tokens took 79.7 us instead of 85.6, for limits four times as high.  (Tiles go from the last to the
 // first and every piece has references of its own, so a peak at the front of a context hides none of it.)
 constexpr float kHeadFirst = 3.0f, kHeadNext = 5.0f;
@@ -219,8 +221,17 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
 // has e4m3's exponent bias in f16, subnormals included, so the code is the rounded top byte below the sign; e5m2
 // is the top byte of f16.  Both round half away (off by at most half a step, like any nearest rounding; a tie
 // costs a weight nothing that its rest does not give back).  A NaN weight loses itself here and is carried by the
-// column's sum.
-__device__ __forceinline__ void split4(float2 w0, float2 w1, uint32_t& hi, uint32_t& lo) {
+// column's sum.  Weights below 2^-6 have few bits left in the rest, and a long context has many alike, which a nearest
+// rounding puts off by the same 2^-3 at most (8064 tokens 9.6 nats below a peak: 5.7 times 2^-7 of the output).  Their
+// rests round up from a border of the token row's own instead, `spread` (see spread_of): off by a step of the rest each,
+// but not in the mean of a tile's rows (0.4 times 2^-7; 0.97 where what falls below 2^-17 is counted in).
+__device__ __forceinline__ uint32_t spread_of(int row) {
+  // a 256th for each row, even over any 2^k aligned ones: the row's bits turned round.  What is added before a rest's low
+  // byte is cut, against the 0x80 of a nearest rounding.
+  const uint32_t add = (__brev((uint32_t)row) >> 25) * 2u + 1u;
+  return (add ^ 0x80u) * 0x00010001u;
+}
+__device__ __forceinline__ void split4(float2 w0, float2 w1, uint32_t spread, uint32_t& hi, uint32_t& lo) {
   const __half2 a = __floats2half2_rn(w0.x, w0.y), b = __floats2half2_rn(w1.x, w1.y);
   const uint32_t ta = *reinterpret_cast<const uint32_t*>(&a) + 0x00400040u;
   const uint32_t tb = *reinterpret_cast<const uint32_t*>(&b) + 0x00400040u;
@@ -229,8 +240,10 @@ __device__ __forceinline__ void split4(float2 w0, float2 w1, uint32_t& hi, uint3
   const __half2 up = __halves2half2(__ushort_as_half(0x5c00), __ushort_as_half(0x5c00));   // 2^8
   const __half2 ra = __hmul2(__hsub2(a, *reinterpret_cast<const __half2*>(&ha)), up);
   const __half2 rb = __hmul2(__hsub2(b, *reinterpret_cast<const __half2*>(&hb)), up);
-  lo = __byte_perm(*reinterpret_cast<const uint32_t*>(&ra) + 0x00800080u,
-                   *reinterpret_cast<const uint32_t*>(&rb) + 0x00800080u, 0x7531);
+  const __half2 least = __halves2half2(__ushort_as_half(0x0400), __ushort_as_half(0x0400));   // 2^-14: a weight of 2^-6
+  const uint32_t add_a = (__hlt2_mask(a, least) & spread) ^ 0x00800080u;
+  const uint32_t add_b = (__hlt2_mask(b, least) & spread) ^ 0x00800080u;
+  lo = __byte_perm(*reinterpret_cast<const uint32_t*>(&ra) + add_a, *reinterpret_cast<const uint32_t*>(&rb) + add_b, 0x7531);
 }
 __device__ __forceinline__ float fast_rcp(float x) {
   float y;
@@ -828,6 +841,7 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     const int group = warp >> 2, quarter = warp & 3;
     const int row = quarter * 32 + lane;                       // token row of S; dim (mod 128) of O^T
     const uint32_t lane_addr = (uint32_t)(quarter * 32) << 16;
+    const uint32_t spread = spread_of(row);
     auto sync_all = [] { asm volatile("bar.sync 7, %0;" ::"n"(kWarps * 32) : "memory"); };        // the softmax warps
     auto sync_group = [&] { asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory"); };     // the group's four
     Ring s_ring, sc_ring;
@@ -1156,7 +1170,7 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             const float2 e1 = make_float2(fast_exp2(a[c][4 * k + 2]), fast_exp2(a[c][4 * k + 3]));
             sum[c][2 * k] = fma2(e0, make_float2(add, add), sum[c][2 * k]);
             sum[c][2 * k + 1] = fma2(e1, make_float2(add, add), sum[c][2 * k + 1]);
-            split4(mul2(e0, make_float2(vd, vd)), mul2(e1, make_float2(vd, vd)), hi[c][k], lo[c][k]);
+            split4(mul2(e0, make_float2(vd, vd)), mul2(e1, make_float2(vd, vd)), spread, hi[c][k], lo[c][k]);
           }
         };
         const bool plain = settled && !masked;

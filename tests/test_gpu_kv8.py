@@ -745,3 +745,48 @@ def test_large_queries_leave_the_others_alone(heads, mods, power):
     assert over.max() <= 1.0, over.max()
     assert np.all(np.abs(got_lse - lse)[small] <= (ds + 2.0 ** -20 * (np.abs(lse) + 1))[small])
     assert np.isfinite(got).all() and np.isfinite(got_lse).all()
+
+
+@pytest.mark.parametrize("tiles", [63, 64, 255, 256, 1024])
+def test_flat_backgrounds_at_every_depth(tiles):
+    """One CTA a sequence and KV head, its own token 3 to 18 nats above tens of thousands of equal ones: weights of every
+    size down to those that no longer reach the output, all alike, so that their roundings must not all go one way."""
+    batch = 152
+    c = Case([chain(1)], [128 * tiles], (2, 2, 128), seed=4)
+    c.codes["k"][:] = 0x08                                            # 2^-6 each
+    c.codes["v"][:], c.scales["v"][:] = 0x78, 2.0 ** -8               # 1 each, as an append scales it (and the peak)
+    c.scales["k"][:] = 1.0
+    c.q[:], c.vn[:] = 0.5, -1.0
+    ds = c.score_error() + 2.0 ** -17 * 18.0 * 2                      # of the largest key: 2^-17 of q and of k in the score
+    c.score_error = lambda: ds
+    gap = torch.linspace(3.0, 18.0, batch)
+    kn = (gap / (0.5 * 128 ** 0.5) + 2.0 ** -6)[:, None, None]
+    c.q, c.vn = (x.expand(batch, -1, -1).contiguous() for x in (c.q, c.vn))
+    c.kn = kn.expand(batch, 2, 128).bfloat16().contiguous()
+    c.indptr, c.parents = np.arange(batch + 1), np.full(batch, -1, np.int32)
+    c.ctx, c.table = np.full(batch, 128 * tiles, np.int32), np.tile(c.table, (batch, 1))
+    c.upload()
+    c.call()
+    c.check(only={(r, r % 2) for r in range(0, batch, 2 if tiles < 200 else 7 if tiles < 1000 else 19)})
+
+
+@pytest.mark.parametrize("apart", [8, 12, 15])
+def test_value_scales_far_apart(apart):
+    """Equal softmax weights on blocks whose V scales are 2^8 to 2^15 apart, the large ones zero in half of the dims: what
+    the small blocks put there is off by 2^-7 of its size, or by a quarter where their weights are small."""
+    c = Case([chain(2)], [640], (4, 1, 256), seed=21, spread=0.0)
+    c.q[:] = 0.0
+    small = c.table[0, ::2]
+    c.scales["v"][small] *= 2.0 ** -apart
+    c.vn *= 2.0 ** -apart
+    large = c.table[0, 1:40:2]
+    c.codes["v"][large, :, :, 128:] = 0
+    c.upload()
+    c.call()
+    torch.cuda.synchronize()
+    ref, _, spread = c.ref()
+    got = np64(c.out[:-1])
+    rel = np.where(np.arange(256) < 128, 2.0 ** -7, 2.0 ** -7 if apart <= 8 else 0.25)
+    bound = 2.0 ** -8 * np.abs(ref) + rel * spread + 2.0 ** -17 * float(c.vn.abs().max())
+    over = (np.abs(got - ref) / bound).max()
+    assert int(c.status) == 0 and over <= 1.0, over
