@@ -47,6 +47,7 @@ extern "C" {
 
 #define SD_KV8_MIN_SCALE_EXP (-100)
 #define SD_KV8_MAX_SCALE_EXP 100
+#define SD_KV8_MAX_SOFTCAP 4096.0f
 
 /*
  * sd_pages_extend — page-table entries and the slot map for the tokens that
@@ -154,7 +155,8 @@ sd_status sd_kv8_append(int num_layers, int num_kv_heads, int head_dim, int page
 /* How sd_kv8_attn turns a dot product into a score; NULL = {0, 0, NULL, 0, 0, 0}. */
 typedef struct sd_kv8_opts {
   float scale;            /* multiplies q.k; 0 = 1 / sqrt(head_dim); else positive and finite */
-  float softcap;          /* c > 0: score = c * tanh(score / c) (applied before the bias); 0 = none */
+  float softcap;          /* c > 0: score = c * tanh(score / c) (applied before the bias); 0 = none.  At most
+                             SD_KV8_MAX_SOFTCAP, else SD_ERR_UNSUPPORTED: the capped score is off by some c * 2^-22 */
   const float* slopes;    /* device fp32 [num_q_heads] or NULL: score += slopes[h] * (key position - query position),
                              a bias that falls with distance for positive slopes */
   long long q_stride;     /* elements between rows of q: 0 (dense) or a multiple of 8, >= num_q_heads * head_dim */

@@ -214,6 +214,7 @@ sd_status sd_kv8_attn(const sd_shape* shape, const sd_kv8_opts* opts, const void
       !aligned(o.slopes, 4) || !stride_ok(o.q_stride, q_row, &p.q_stride) ||
       !stride_ok(o.k_stride, kv_row, &p.k_stride) || !stride_ok(o.v_stride, kv_row, &p.v_stride))
     return SD_ERR_INVALID_ARG;
+  if (o.softcap > SD_KV8_MAX_SOFTCAP) return SD_ERR_UNSUPPORTED;
   const size_t need = kv8_attn_workspace(shape->num_q_heads, shape->num_kv_heads, shape->head_dim, bd);
   if (need > 0 && (workspace == nullptr || ws_bytes < need)) return SD_ERR_WORKSPACE;
   p.q = static_cast<const __nv_bfloat16*>(q);
@@ -231,8 +232,9 @@ sd_status sd_kv8_attn(const sd_shape* shape, const sd_kv8_opts* opts, const void
   p.lse = lse;
   p.dev_status = dev_status;
   p.scale = o.scale > 0.f ? o.scale : 1.0f / std::sqrt((float)shape->head_dim);
-  p.softcap = o.softcap;
-  p.cap_exp = o.softcap > 0.f ? 2.0f / o.softcap : 0.f;
+  // a smaller cap leaves scores of 2^-20 at most either way, and the factors of the capped form out of range
+  p.softcap = o.softcap > 0.f ? std::fmax(o.softcap, 0x1p-20f) : 0.f;
+  p.cap_exp = o.softcap > 0.f ? 2.0f / p.softcap : 0.f;
   p.hq = shape->num_q_heads;
   p.hkv = shape->num_kv_heads;
   p.group = p.hq / p.hkv;

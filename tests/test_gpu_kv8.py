@@ -790,3 +790,26 @@ def test_value_scales_far_apart(apart):
     bound = 2.0 ** -8 * np.abs(ref) + rel * spread + 2.0 ** -17 * float(c.vn.abs().max())
     over = (np.abs(got - ref) / bound).max()
     assert int(c.status) == 0 and over <= 1.0, over
+
+
+@pytest.mark.parametrize("heads", [(24, 4, 256), (12, 4, 128)], ids=["d256", "d128"])
+@pytest.mark.parametrize("cap", [1e-38, 1e-3, 64.0, 1e3, 4096.0])
+def test_every_size_of_score_cap(heads, cap):
+    """A cap far above every score changes nothing, a tiny one makes all scores alike: within the bound of any call."""
+    slopes = 2.0 ** (-8.0 * np.arange(1, heads[0] + 1) / heads[0]) if cap == 1e3 else None
+    c = Case([tree(11, 17), chain(9), chain(1)], [1300, 90, 641], heads, seed=5, softcap=cap, slopes=slopes).upload()
+    c.call()
+    c.check()
+
+
+@pytest.mark.parametrize("cap", [40.0, 1000.0])
+def test_scores_that_reach_the_cap(cap):
+    """Scores from far below to the cap itself."""
+    c = Case([tree(2, 12)], [1500], seed=3, softcap=cap)
+    c.q[:] = 1.0
+    c.codes["k"][:] = np.where(c.codes["k"] == 0x7F, 0x7F, 0x38)          # 1.0 each: a score of 16 times the scale
+    for j, page in enumerate(c.table[0]):
+        c.scales["k"][page] = cap / 16 * (j + 1) / 47
+    c.upload()
+    c.call()
+    c.check()

@@ -221,3 +221,10 @@ def test_binding_refuses_rows_that_overlap():
     args[1] = torch.zeros(6, 3, 256, dtype=torch.bfloat16)[:, 1:2]                  # rows that lie apart pass
     with pytest.raises(ValueError, match="CUDA"):
         native.sd_kv8_attn(*args)
+
+
+def test_score_caps_beyond_what_the_formula_keeps(lib):
+    """c - 2 c / (1 + exp(2 x / c)) loses c 2^-22 of a score: 1 % of the weights at 1e5, everything at 1e7."""
+    for cap in (4096.001, 1e5, 1e7, 1e30, 3.4e38):
+        assert _attn(lib, opts=native.SdKv8Opts(0, cap)) == UNSUP
+    assert _attn(lib, opts=native.SdKv8Opts(0, 4096.0), ws=None, ws_bytes=0) == WS       # passes the checks before it
