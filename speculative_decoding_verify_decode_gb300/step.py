@@ -114,7 +114,8 @@ class Kv8Cache:
     """A pool of 8-bit block-scaled K/V pages for every layer, its page tables, and the free list, all on the GPU.
 
     ``extend`` takes pages for joining tokens and appends their K/V, ``release`` gives pages back; both only
-    launch kernels, so a step that contains them can be captured into a CUDA graph and replayed.
+    launch kernels, so a step that contains them can be captured into a CUDA graph and replayed.  The calls of one
+    cache follow each other: they share its state and scratch, so on two streams an event has to order them.
     """
 
     def __init__(self, batch: int, max_pages_per_seq: int, num_pool_pages: int, num_layers: int,
@@ -130,7 +131,7 @@ class Kv8Cache:
         self.free_list = torch.arange(num_pool_pages - 1, -1, -1, dtype=torch.int32, device=dev)
         self.free_count.fill_(num_pool_pages)
         self._new = ints(batch), ints(batch), ints(1)
-        self.dev_status = ints(1)
+        self.dev_status, self._said = ints(1), ints(1)
 
     def _on(self, stream):
         """The context of a stream: a torch stream, a raw handle, or None for the current one."""
@@ -158,15 +159,18 @@ class Kv8Cache:
             self._settle(ctx=True)
 
     def release(self, keep_lens, stream=None):
-        """Every sequence keeps its first ``keep_lens`` tokens at most; the pages behind them become free."""
+        """Every sequence keeps its first ``keep_lens`` tokens at most; the pages behind them become free.  A call that
+        is refused (see sd_pages_release) leaves everything as it was."""
         with self._on(stream):
             _, new_held, new_count = self._new
+            said = self._said.zero_()
             native.sd_pages_release(keep_lens, self.page_table, self.held, new_held, self.free_list, self.free_count,
-                                    new_count, self.dev_status)
+                                    new_count, said)
+            # refused: a status, and no page moved (a page whose id is out of range is reported, and moves)
+            refused = (said != 0) & (new_count == self.free_count)
             self._settle(ctx=False)
-            # a negative length refuses the whole call: then the contexts stay too
-            keep = torch.where((keep_lens >= 0).all(), keep_lens, self.ctx_lens)
-            torch.minimum(self.ctx_lens, keep, out=self.ctx_lens)
+            torch.minimum(self.ctx_lens, torch.where(refused, self.ctx_lens, keep_lens), out=self.ctx_lens)
+            self.dev_status |= said
 
 
 class Kv8Step:

@@ -813,3 +813,40 @@ def test_scores_that_reach_the_cap(cap):
     c.upload()
     c.call()
     c.check()
+
+
+def test_a_release_refused_for_any_reason_leaves_the_cache_as_it_was():
+    """Negative lengths, a held count out of range, a free list without room; a page id out of range is pushed all the same."""
+    def cache():
+        c = Kv8Cache(2, 8, 16, 1)
+        x = bf16(np.random.default_rng(6), 70, 4, 256).cuda()
+        c.extend(cu([50, 20], torch.int32), [x], [x], torch.empty(70, dtype=torch.int32, device="cuda"))
+        torch.cuda.synchronize()
+        assert c.ctx_lens.tolist() == [50, 20] and c.held.tolist() == [4, 2] and int(c.free_count) == 10
+        return c
+    def negative(c): c.keep = [10, -1]
+    def held(c): c.held[1] = 9
+    def below(c): c.held[1] = -1
+    def room(c): c.free_count.fill_(16)
+    def count(c): c.free_count.fill_(-1)
+    for plant, bit in [(negative, native.SD_DEV_BAD_CTX), (held, native.SD_DEV_BAD_CTX), (below, native.SD_DEV_BAD_CTX),
+                       (room, native.SD_DEV_BAD_PAGE), (count, native.SD_DEV_BAD_PAGE)]:
+        c = cache()
+        c.keep = [10, 100]
+        plant(c)
+        state = [x.clone() for x in (c.ctx_lens, c.held, c.free_count, c.free_list, c.page_table)]
+        c.release(cu(c.keep, torch.int32))
+        torch.cuda.synchronize()
+        assert int(c.dev_status) == bit, plant
+        for x, y in zip((c.ctx_lens, c.held, c.free_count, c.free_list, c.page_table), state):
+            assert torch.equal(x, y), plant
+    c = cache()
+    c.page_table[0, 2] = 10 ** 6
+    c.release(cu([10, 18], torch.int32))
+    torch.cuda.synchronize()
+    assert int(c.dev_status) == native.SD_DEV_BAD_PAGE
+    assert c.ctx_lens.tolist() == [10, 18] and c.held.tolist() == [1, 2] and int(c.free_count) == 13
+    c.release(cu([10, 17], torch.int32))                    # no page moves, and the old status does not stand in the way
+    assert c.ctx_lens.tolist() == [10, 17] and int(c.dev_status) == native.SD_DEV_BAD_PAGE
+    c.release(cu([0, 0], torch.int32))
+    assert c.ctx_lens.tolist() == [0, 0] and int(c.free_count) == 16
