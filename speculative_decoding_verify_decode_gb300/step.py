@@ -120,10 +120,11 @@ class Kv8Cache:
 
     def __init__(self, batch: int, max_pages_per_seq: int, num_pool_pages: int, num_layers: int,
                  num_kv_heads: int = 4, head_dim: int = 256, device="cuda"):
-        dev = self.device = torch.device(device)
+        dev = torch.device(device)
         self.num_pool_pages = int(num_pool_pages)
         codes = (num_layers, num_pool_pages, num_kv_heads, 16, head_dim)
         self.k, self.v = (torch.zeros(codes, dtype=torch.uint8, device=dev) for _ in "kv")
+        dev = self.device = self.k.device       # "cuda" is the device that is current now
         self.k_scales, self.v_scales = (torch.ones(codes[:3], dtype=torch.float32, device=dev) for _ in "kv")
         ints = lambda *s: torch.zeros(s, dtype=torch.int32, device=dev)
         self.page_table = torch.full((batch, max_pages_per_seq), -1, dtype=torch.int32, device=dev)
@@ -202,12 +203,14 @@ class Kv8Step:
 
     def run(self, q, k_new, v_new, parents, draft_tokens, logits, stream=None):
         """q, k_new and v_new are per-layer lists (or tensors with a leading layer dimension)."""
-        for layer in range(len(q)):
-            self.attention(layer, q[layer], k_new[layer], v_new[layer], parents, stream)
-        native.sd_accept(self.q_indptr, self.vocab, logits, parents, draft_tokens, self.accept_len, self.path,
-                         self.out_tokens, self.target_tokens, self.max_path, self.acc_ws, self.cache.dev_status,
-                         stream)
-        self.cache.extend(self.accept_len, k_new, v_new, self.slots, self.rows, self.q_indptr, self.path, stream)
+        # sd_accept takes the current device's stream; the other calls go by their tensors
+        with torch.cuda.device(self.cache.device):
+            for layer in range(len(q)):
+                self.attention(layer, q[layer], k_new[layer], v_new[layer], parents, stream)
+            native.sd_accept(self.q_indptr, self.vocab, logits, parents, draft_tokens, self.accept_len, self.path,
+                             self.out_tokens, self.target_tokens, self.max_path, self.acc_ws, self.cache.dev_status,
+                             stream)
+            self.cache.extend(self.accept_len, k_new, v_new, self.slots, self.rows, self.q_indptr, self.path, stream)
 
 
 def device_inputs(w, device="cuda"):

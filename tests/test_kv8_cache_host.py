@@ -5,7 +5,7 @@ import torch
 
 import oracle.kv8_oracle as kv8
 from speculative_decoding_verify_decode_gb300 import native
-from speculative_decoding_verify_decode_gb300.step import Kv8Cache
+from speculative_decoding_verify_decode_gb300.step import Kv8Cache, Kv8Step
 
 
 def _release(keep, table, held, new_held, free_list, count, new_count, status=None, stream=None):
@@ -46,3 +46,31 @@ def test_release_moves_contexts_only_when_pages_may_move(monkeypatch, plant, kee
     if want is None:
         assert torch.equal(c.held, before[0]) and torch.equal(c.free_count, before[1])
         assert int(c.dev_status) & ~native.SD_DEV_BAD_ACCEPT
+
+
+def test_a_step_runs_on_its_caches_device(monkeypatch):
+    """sd_accept goes by the current device, so a step makes its cache's device current."""
+    now, calls = [None], []
+
+    class Current:
+        def __init__(self, device):
+            self.device = device
+
+        def __enter__(self):
+            self.before, now[0] = now[0], self.device
+
+        def __exit__(self, *_):
+            now[0] = self.before
+
+    c = Kv8Cache(2, 8, 16, 2, num_kv_heads=1, head_dim=128, device="cpu")
+    monkeypatch.setattr(native, "sd_kv8_attn_workspace_size", lambda shape: 64)
+    monkeypatch.setattr(native, "sd_accept_workspace_size", lambda indptr, vocab: 64)
+    for name in ("sd_kv8_attn", "sd_accept", "sd_pages_extend", "sd_kv8_append"):
+        monkeypatch.setattr(native, name, lambda *a, name=name, **kw: calls.append((name, now[0])))
+    step = Kv8Step(c, [0, 3, 4], 50, num_q_heads=2)
+    monkeypatch.setattr(torch.cuda, "device", Current)
+    one = lambda heads: torch.zeros(2, 4, heads, 128, dtype=torch.bfloat16)
+    ints = torch.zeros(4, dtype=torch.int32)
+    step.run(one(2), one(1), one(1), ints, ints, torch.zeros(4, 50))
+    assert calls == [(n, c.k.device) for n in ("sd_kv8_attn", "sd_kv8_attn", "sd_accept", "sd_pages_extend", "sd_kv8_append")]
+    assert c.device == c.k.device and now == [None]
