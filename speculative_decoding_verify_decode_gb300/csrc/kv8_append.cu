@@ -88,15 +88,15 @@ __global__ void __launch_bounds__(kAppendThreads, 6) kv8_append_kernel(const Kv8
     const int r0 = s_lead[task / combos], combo = task % combos;
     const int head = combo >> 1;
     const bool is_v = combo & 1;
-    // the group: the following rows on the same page, which must rise by one
+    // the group: the following rows on the same page, which must rise by one (a seventeenth cannot)
     const int slot0 = p.slots[r0], page = slot0 / kPage, first = slot0 % kPage;
     int slot = -1, src = -1;
-    if (lane < kPage && r0 + lane < p.max_rows) {
+    if (lane <= kPage && r0 + lane < p.max_rows) {
       slot = p.slots[r0 + lane];
       src = p.rows != nullptr ? p.rows[r0 + lane] : r0 + lane;
     }
-    const bool same = lane < kPage && slot >= 0 && slot / kPage == page;
-    const int n = __ffs(~__ballot_sync(0xffffffffu, same)) - 1;   // 1..16
+    const bool same = lane <= kPage && slot >= 0 && slot / kPage == page;
+    const int n = __ffs(~__ballot_sync(0xffffffffu, same)) - 1;   // 1..17
     const bool wrong = lane < n && (slot != slot0 + lane || src < 0 || src >= p.num_src_rows);
     if (__any_sync(0xffffffffu, wrong)) {
       if (lane == 0 && layer == 0) report(p.dev_status, SD_DEV_BAD_SLOT);

@@ -850,3 +850,18 @@ def test_a_release_refused_for_any_reason_leaves_the_cache_as_it_was():
     assert c.ctx_lens.tolist() == [10, 17] and int(c.dev_status) == native.SD_DEV_BAD_PAGE
     c.release(cu([0, 0], torch.int32))
     assert c.ctx_lens.tolist() == [0, 0] and int(c.free_count) == 16
+
+
+@pytest.mark.parametrize("extra", [[3], [15], [0, 1, 2]])
+@pytest.mark.parametrize("rows", [20, 900])
+def test_append_reports_rows_behind_a_full_page(rows, extra):
+    """Sixteen rows fill a page; more on the same page break the order, and are not dropped in silence."""
+    slots = list(range(32, 48)) + [32 + i for i in extra] + [64]
+    slots += [-1] * (rows - len(slots))
+    k = torch.full((6, 4, PAGE, 256), 9, dtype=torch.uint8, device="cuda")
+    s = torch.full((6, 4), 0.5, device="cuda")
+    x = torch.ones(rows, 4, 256, dtype=torch.bfloat16, device="cuda")
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    native.sd_kv8_append([k], [k.clone()], [s], [s.clone()], [x], [x], cu(slots, torch.int32), None, st)
+    torch.cuda.synchronize()
+    assert int(st) == native.SD_DEV_BAD_SLOT and torch.all(k[2] == 9) and torch.all(k[4, :, 0] != 9)
