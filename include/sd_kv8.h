@@ -194,16 +194,17 @@ size_t sd_kv8_attn_workspace_size(const sd_shape* shape);
  * sequences are fp32.  The products take 8-bit operands: the cache's codes as
  * they lie; a query (one node's, of one head) as two e4m3 terms (off by at most
  * 2^-17 of its own amax); a draft key or value as two e4m3 terms (2^-17 of its
- * row's amax); a softmax weight times its token's V scale as an e4m3 term and an
- * e5m2 rest.  That product is off by at most 2^-7 of itself; below 2^-9 of the
- * largest such product that its CTA has met in the column by up to a quarter of
- * itself, up or down by the token's place in its 128-token tile, so that many
- * alike are right in the mean; and below 2^-20 (2^-22 over more than 8192
- * tokens of a CTA, 2^-24 over 32768) it no longer reaches the output.  So where
- * tokens share the weight but their blocks' V scales lie further apart than
- * 2^9, the values of the small blocks lose bits, and beyond 2^20 they are lost,
- * in dims that the large blocks leave at zero too.  The sum of weights is not
- * rounded.
+ * row's amax where that is above 448 * 2^-100; magnitudes beyond 448 * 2^100
+ * saturate, as they would in the cache); a softmax weight times its token's V
+ * scale as an e4m3 term and an e5m2 rest.  That product is off by at most 2^-7
+ * of itself; below 2^-9 of the largest such product that its CTA has met in the
+ * column by up to a quarter of itself, up or down by the token's place in its
+ * 128-token tile, so that many alike are right in the mean; and below 2^-20
+ * (2^-22 over more than 8192 tokens of a CTA, 2^-24 over 32768) it no longer
+ * reaches the output.  So where tokens share the weight but their blocks' V
+ * scales lie further apart than 2^9, the values of the small blocks lose bits,
+ * and beyond 2^20 they are lost, in dims that the large blocks leave at zero
+ * too.  The sum of weights is not rounded.
  * Outputs are typically within 0.002 of their size, against 0.0017 for the
  * rounding to bf16 alone.  A page id out of range sets SD_DEV_BAD_PAGE and its
  * tokens count as zeros; a scale out of range sets SD_DEV_BAD_SCALE and is

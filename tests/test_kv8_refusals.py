@@ -228,3 +228,16 @@ def test_score_caps_beyond_what_the_formula_keeps(lib):
     for cap in (4096.001, 1e5, 1e7, 1e30, 3.4e38):
         assert _attn(lib, opts=native.SdKv8Opts(0, cap)) == UNSUP
     assert _attn(lib, opts=native.SdKv8Opts(0, 4096.0), ws=None, ws_bytes=0) == WS       # passes the checks before it
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(indptr=(0, 1)), dict(indptr=(0, 23)), dict(indptr=(0, 64)), dict(indptr=(0, 20, 84)),
+                                dict(indptr=tuple(range(0, 257 * 64, 64))), dict(hq=32, hkv=8, dim=128),
+                                dict(indptr=(0, 31), hq=32, hkv=8, dim=128), dict(hq=64, hkv=64, dim=128), dict(hq=16, hkv=1)])
+def test_every_valid_shape_needs_a_workspace(lib, kw):
+    """Never 0, and a byte less is refused, for plain, capped and biased scores (their plans differ beyond 96 columns)."""
+    s = _shape(**kw)
+    need = native.sd_kv8_attn_workspace_size(s)
+    assert need > 1024
+    for opts in (None, native.SdKv8Opts(0, 30.0), native.SdKv8Opts(0, 0, FAKE)):
+        assert _attn(lib, s, opts=opts, ws=None, ws_bytes=0) == WS
+        assert _attn(lib, s, opts=opts, ws_bytes=need - 1) == WS
