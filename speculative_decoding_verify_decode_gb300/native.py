@@ -172,7 +172,7 @@ class Shape:
         self.c = SdShape(len(self.indptr) - 1, ctypes.cast(self.indptr, ctypes.POINTER(ctypes.c_int)),
                          int(num_q_heads), int(num_kv_heads), int(head_dim), 16, int(max_pages_per_seq),
                          int(num_pool_pages), int(num_splits), int(window), int(bool(ctx_stable)))
-        n, c = int(self.indptr[len(self.indptr) - 1]), self.c
+        n, c = int(self.indptr[-1]) if len(self.indptr) else 0, self.c
         # shapes of sd_kv8_attn's tensors: q and out, k_new and v_new, codes, scales, page table, per sequence, per node
         self.dims = ((n, c.num_q_heads, c.head_dim), (n, c.num_kv_heads, c.head_dim),
                      (c.num_pool_pages, c.num_kv_heads, 16, c.head_dim), (c.num_pool_pages, c.num_kv_heads),

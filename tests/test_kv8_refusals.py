@@ -241,3 +241,10 @@ def test_every_valid_shape_needs_a_workspace(lib, kw):
     for opts in (None, native.SdKv8Opts(0, 30.0), native.SdKv8Opts(0, 0, FAKE)):
         assert _attn(lib, s, opts=opts, ws=None, ws_bytes=0) == WS
         assert _attn(lib, s, opts=opts, ws_bytes=need - 1) == WS
+
+
+def test_an_empty_q_indptr_is_refused_by_the_library(lib):
+    """The shape object carries any q_indptr; what is wrong with it the library says."""
+    s = native.Shape([], 4, 8)
+    assert native.sd_kv8_attn_workspace_size(s) == 0 and native.sd_verify_attn_workspace_size(s) == 0
+    assert _attn(lib, s) == BAD
