@@ -86,8 +86,9 @@ extern "C" {
  *   free_count, new_free_count   int32 [1]
  *   slots                    int32 [max_rows]; rows int32 [max_rows] or NULL; row_indptr int32 [B+1] or NULL
  *   new_ctx_lens             int32 [B] or NULL: ctx + add
- * No output may alias an input (nor new_ctx_lens the ctx_lens); the page
- * table is updated in place.  Pages shared between sequences are not tracked.
+ * No output may alias an input (nor new_ctx_lens the ctx_lens) or another
+ * output, dev_status among them; the page table is updated in place.  Pages
+ * shared between sequences are not tracked.
  */
 sd_status sd_pages_extend(int batch, int max_pages_per_seq, int num_pool_pages, const int* ctx_lens,
                           const int* add_lens, const int* q_indptr_h, const int* path, int max_path,
@@ -108,8 +109,8 @@ sd_status sd_pages_extend(int batch, int max_pages_per_seq, int num_pool_pages, 
  * max_pages_per_seq] (SD_DEV_BAD_CTX), or more pages than free_list has room
  * for (SD_DEV_BAD_PAGE), changes nothing and repeats the old values.  A
  * released id out of [0, num_pool_pages) sets SD_DEV_BAD_PAGE and is pushed as
- * it is.  No output may alias an input; free_list is updated in place behind
- * entry *free_count - 1.
+ * it is.  No output may alias an input or another output; free_list is updated
+ * in place behind entry *free_count - 1.
  */
 sd_status sd_pages_release(int batch, int max_pages_per_seq, int num_pool_pages, const int* keep_lens,
                            const int* page_table, const int* held, int* new_held, int* free_list,

@@ -21,6 +21,19 @@ bool words(const T*... p) {
   return ((reinterpret_cast<uintptr_t>(p) | ... | uintptr_t{0}) & 3u) == 0;
 }
 
+// Whether one of the arrays that a call writes is one that it reads, or written twice (nulls are no arrays).
+template <int W, int R>
+bool aliased(const int* const (&written)[W], const int* const (&read)[R]) {
+  for (int i = 0; i < W; ++i) {
+    if (written[i] == nullptr) continue;
+    for (int j = 0; j < i; ++j)
+      if (written[j] == written[i]) return true;
+    for (const int* r : read)
+      if (r == written[i]) return true;
+  }
+  return false;
+}
+
 sd_status check_pages(int batch, int max_pages, int pool) {
   if (batch < 1 || max_pages < 1 || pool < 1) return SD_ERR_INVALID_ARG;
   if (batch > kMaxBatch || (long long)max_pages * kPage > (1LL << 30) || (long long)pool * kPage > INT_MAX)
@@ -75,11 +88,9 @@ sd_status sd_pages_extend(int batch, int max_pages_per_seq, int num_pool_pages, 
              row_indptr, new_ctx_lens, dev_status))
     return SD_ERR_INVALID_ARG;
   if ((q_indptr_h == nullptr) != (path == nullptr) || (path != nullptr && max_path < 1)) return SD_ERR_INVALID_ARG;
-  const int* in[] = {ctx_lens, add_lens, held, free_count, free_list};
-  const int* out[] = {new_held, new_free_count, slots, rows, row_indptr, new_ctx_lens};
-  for (const int* o : out)
-    for (const int* i : in)
-      if (o != nullptr && o == i) return SD_ERR_INVALID_ARG;
+  if (aliased({page_table, new_held, new_free_count, slots, rows, row_indptr, new_ctx_lens, dev_status},
+              {ctx_lens, add_lens, held, free_count, free_list, path}))
+    return SD_ERR_INVALID_ARG;
   BatchDesc bd;
   std::memset(&bd, 0, sizeof(bd));
   if (q_indptr_h != nullptr) {
@@ -120,11 +131,8 @@ sd_status sd_pages_release(int batch, int max_pages_per_seq, int num_pool_pages,
     return SD_ERR_INVALID_ARG;
   if (!words(keep_lens, page_table, held, new_held, free_list, free_count, new_free_count, dev_status))
     return SD_ERR_INVALID_ARG;
-  const int* in[] = {keep_lens, held, free_count, page_table};
-  const int* out[] = {new_held, new_free_count, free_list};
-  for (const int* o : out)
-    for (const int* i : in)
-      if (o == i) return SD_ERR_INVALID_ARG;
+  if (aliased({new_held, new_free_count, free_list, dev_status}, {keep_lens, held, free_count, page_table}))
+    return SD_ERR_INVALID_ARG;
   PagesParams p;
   std::memset(&p, 0, sizeof(p));
   p.ctx_lens = keep_lens;

@@ -248,3 +248,15 @@ def test_an_empty_q_indptr_is_refused_by_the_library(lib):
     s = native.Shape([], 4, 8)
     assert native.sd_kv8_attn_workspace_size(s) == 0 and native.sd_verify_attn_workspace_size(s) == 0
     assert _attn(lib, s) == BAD
+
+
+@pytest.mark.parametrize("kw", [dict(rows=FAKE + 512), dict(row_indptr=FAKE + 512), dict(new_held=FAKE + 128), dict(table=FAKE),
+                                dict(new_ctx=FAKE + 256), dict(new_ctx=FAKE + 448), dict(table=FAKE + 320),
+                                dict(indptr=[0, 3, 5], path=FAKE + 512, max_path=4), dict(rows=FAKE + 900, row_indptr=FAKE + 900)])
+def test_pages_extend_refuses_arrays_that_are_written_twice(lib, kw):
+    assert _extend(lib, **kw) == BAD
+
+
+@pytest.mark.parametrize("kw", [dict(new_count=FAKE + 192), dict(new_held=FAKE + 256), dict(free=FAKE + 320)])
+def test_pages_release_refuses_arrays_that_are_written_twice(lib, kw):
+    assert _release(lib, **kw) == BAD
