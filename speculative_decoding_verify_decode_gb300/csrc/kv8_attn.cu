@@ -160,11 +160,11 @@ Layout layout_of(const Kv8Plan& pl, int hkv, int dim, const BatchDesc& bd, int s
 // Query columns of a CTA: as many heads of a KV group as fit, so that the cache is read as few times as can be (capped
 // or biased scores over 256 dims stop at 96: the wider columns' slopes find no room beside the operands).  Up to 16
 // columns, i.e. single tokens, two CTAs of one softmax group share an SM (64 sequences, 1 to 32768 tokens, 128 dims:
-// 388 us against 581 for one CTA of three groups; one sequence of 512 tokens 11.3 against 11.7).  So do 17 to 32 columns
-// of 128 dims where there are segments enough to fill both (64 sequences of 8 nodes: 205 us against 224; 8 sequences: 36.5
-// against 43.7); a few segments take one CTA of three groups, whose single tile is shorter (one sequence of 8 nodes over
-// 8192 tokens: 15.5 us against 17.4), and so do 256 dims, where half an SM's shared memory holds one K tile (64 sequences
-// of 5 nodes: 146 us against 149).
+// 394 us against 614 for one CTA of three groups; one sequence of 512 tokens 10.9 against 11.3).  So do 17 to 32 columns
+// of 128 dims where there are segments enough to fill both (64 sequences of 8 nodes: 213 us against 226; 8 sequences: 37.8
+// against 45.5); a few segments take one CTA of three groups, whose single tile is shorter (one sequence of 8 nodes over
+// 8192 tokens: 15.1 us against 16.9), and so do 256 dims, where half an SM's shared memory holds one K tile (64 sequences
+// of 5 nodes: 147 us against 155).
 Kv8Plan kv8_plan(int group, int max_nodes, int dim, bool mod, int kv_rows) {
   const int most = mod && dim == 256 ? 96 : 144;
   Kv8Plan pl;

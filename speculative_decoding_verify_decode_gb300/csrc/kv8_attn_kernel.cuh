@@ -50,14 +50,16 @@
 // columns per group; thread = token row), which also stage Q and the draft block
 // and write the results; then one warp each that loads K and the block scales,
 // loads V, issues QK, issues PV.
-// Measured (one GB300).  A tile costs an SM, 256 dims: 1.41 us up to 48 columns
-// (HBM: 7 TB/s of reads over 152 SMs), 1.81 at 96, 2.50 at 144, where its bytes
+// Measured (one GB300).  A tile costs an SM, 256 dims: 1.42 us up to 48 columns
+// (HBM: 7 TB/s of reads over 152 SMs), 2.04 at 96, 2.53 at 144, where its bytes
 // would take 1.4, its products 1.25 (75 cycles each) and the softmax warps issue in
-// 40 % of their slots; 128 dims: 0.75 at 16, 1.06 at 48, 1.52 at 96, 1.98 at 144.
-// A call costs 9 us beyond its tiles at 16 columns, 10 to 12 up to 48 and 13 to 19
+// 43 % of their slots; 128 dims: 0.75 at 16, 1.12 at 48, 1.65 at 96, 2.09 at 144.
+// A call costs 9 us beyond its tiles at 16 columns, 11 to 12 up to 48 and 14 to 22
 // beyond (plan 1.5, staging 3 to 6, the first references 2, results 1 to 4, the
-// merge 3 to 5).  64 sequences of 1 to 32768 tokens, single tokens, 128 dims: 390 us,
-// 6.4 TB/s; a tree of 23 over 131072 tokens, 256 dims: 85 us, 3.2 TB/s.
+// merge 3 to 5).  64 sequences of 1 to 32768 tokens, single tokens, 128 dims: 393 us,
+// 6.4 TB/s; a tree of 23 over 131072 tokens, 256 dims: 89 us, 3.0 TB/s.  Of that, the
+// queries' own scales (one multiplication a score) are 1.5 us and the small weights'
+// rounding (see split4) 2.
 // Every wait on a barrier is bounded; on expiry the kernel reports
 // SD_DEV_TIMEOUT and runs out.
 #pragma once
@@ -79,9 +81,9 @@ constexpr float kTop = 448.0f;         // weights beyond it move m
 // tile 2 us).  Lower means fewer moves, and coarser small weights: where the largest is 2^h, weights below 2^(-6 - h)
 // of it keep an e5m2 value's bits, right in the mean of many alike (see split4), and those below 2^(-17 - h) nothing.  h
 // grows with the piece, so that what is lost of its n tokens, n 2^(-17 - h), stays below 2^-7 of the largest weight up
-// to 131072 of them.  At 2^1 and 2^2 a tree of
-// 23 over 131072 tokens took 79.7 us instead of 85.6, for limits four times as high.  (Tiles go from the last to the
-// first and every piece has references of its own, so a peak at the front of a context hides none of it.)
+// to 131072 of them.  At 2^1 and 2^2 a tree of 23 over 131072 tokens takes 83.6 us instead of 88.9, for limits four times
+// as high.  (Tiles go from the last to the first and every piece has references of its own, so a peak at the front of a
+// context hides none of it.)
 constexpr float kHeadFirst = 3.0f, kHeadNext = 5.0f;
 __device__ __forceinline__ float head_of(int tiles, bool first) {
   const float least = tiles > 256 ? 7.0f : tiles > 64 ? 5.0f : 3.0f;
@@ -312,9 +314,9 @@ __device__ __forceinline__ int query_exp(uint32_t bits) {
 __device__ __forceinline__ float exp2i(int e) { return __int_as_float((e + 127) << 23); }
 
 // What a segment's draft tile counts for beyond one unit, where CTAs have `even` units each: staging the block, its masks
-// and the moves of fresh references take some 5 us, a tile of 144 columns 2.2 us and one of 96 or fewer 1.2 to 1.6; in
+// and the moves of fresh references take some 5 us, a tile of 144 columns 2.3 us and one of 96 or fewer 1.2 to 1.8; in
 // pieces of few units one more would cost the whole.  Against 2 from 12 units and 1 from 5 on: a tree of 23 over 32768
-// tokens 37.5 -> 36.2 us, 8 sequences of 8 nodes 38.1 -> 36.4 (128 dims), 16 nodes over 32768 31.0 -> 28.9.
+// tokens 39.3 -> 37.8 us, 8 sequences of 8 nodes 38.5 -> 37.8 (128 dims), 16 nodes over 32768 31.7 -> 29.8.
 template <int NQ>
 __device__ __forceinline__ int extra_units(int even) {
   return even >= 12 && NQ < 144 ? 3 : even >= 6 ? 2 : even >= 4 ? 1 : 0;
@@ -919,7 +921,7 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             bool wild = false;
             int e = 0;
             uint2 hi = make_uint2(0, 0), lo = hi;
-            if (base < 2 * n_nodes) {      // zero rows are stored as they are (512-token decode 11.6 -> 11.2 us)
+            if (base < 2 * n_nodes) {      // zero rows are stored as they are (512-token decode 11.6 -> 10.9 us)
               e = exp_of(row_amax(y, wild));
               split8(y, exp2i(-e), hi, lo);
             }
@@ -1276,7 +1278,7 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
           next_scales();
         }
         // (Past the last tile S holds old scores, which nobody uses: drawn all the same, a condition here costs the wide
-        // tiles registers that they do not have, and 87 us become 99.)
+        // tiles registers that they do not have, and 89 us become 91.)
         if (!last) wait_full(B_SF, s_ring);
         draw();
         if (!last) drawn();
