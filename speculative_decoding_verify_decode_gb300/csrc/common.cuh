@@ -10,7 +10,10 @@
 #include <cuda_bf16.h>
 
 #include "../../include/sd_verify.h"
+#include "../../include/sd_kv4.h"
 #include "../../include/sd_kv8.h"
+#include "../../include/sd_logprobs.h"
+#include "../../include/sd_rope.h"
 
 namespace sdv {
 

@@ -235,4 +235,80 @@ constexpr int kMaxKvHeads = 64, kMaxGroup = 16;   // of the block-scaled cache's
 size_t kv8_attn_workspace(int hq, int hkv, int dim, const BatchDesc& bd);
 cudaError_t launch_kv8_attn(Kv8AttnParams p, const BatchDesc& bd, cudaStream_t st);
 
+// Rotation of q and k rows, k and v appended to the paged bf16 cache.
+struct RopeParams {
+  const float* table;        // [table_len][rot_dim]: cosines, sines
+  const int* positions;
+  const int* slots;          // nullable (no append)
+  const __nv_bfloat16 *q, *k, *v;
+  __nv_bfloat16 *q_out, *k_out, *k_cache, *v_cache;   // k_out and the caches nullable
+  int* dev_status;           // nullable
+  long long q_stride, k_stride, v_stride, q_out_stride, k_out_stride;
+  int num_rows, hq, hkv, dim, rot_dim, interleaved, table_len, num_pool_pages;
+};
+cudaError_t launch_rope_append(const RopeParams& p, cudaStream_t st);
+
+// Quantising append into the 4-bit cache, and rows back out of it.
+struct Kv4RowsParams {
+  uint8_t* cache[kMaxLayers];
+  __nv_bfloat16* k_rows[kMaxLayers];   // append: the new rows; read: the output
+  __nv_bfloat16* v_rows[kMaxLayers];
+  const int* slots;
+  const int* rows;           // append: nullable
+  int* dev_status;           // nullable
+  long long stride;          // elements between rows of k_rows and v_rows
+  int num_layers, heads, num_pool_pages, num_src_rows, max_rows;
+};
+cudaError_t launch_kv4_append(const Kv4RowsParams& p, int dim, cudaStream_t st);
+cudaError_t launch_kv4_read(const Kv4RowsParams& p, int dim, cudaStream_t st);
+
+// Verify attention over the 4-bit cache (one layer).
+struct Kv4AttnParams {
+  const __nv_bfloat16* q;
+  const uint8_t* cache;      // [num_pool_pages][hkv][2][9 * dim]
+  const __nv_bfloat16* k_new;
+  const __nv_bfloat16* v_new;
+  const int* page_table;
+  const int* ctx_lens;
+  const int* parents;
+  const float* slopes;       // [hq], nullable
+  __nv_bfloat16* out;
+  float* lse;                // nullable
+  int* dev_status;           // nullable
+  long long q_stride, k_stride, v_stride;   // elements between rows
+  float scale, softcap;      // softcap 0: none
+  float cap_exp;             // 2 / softcap
+  int hq, hkv, dim, max_pages, num_pool_pages, window;
+  void* workspace;
+  int group;                 // query heads per KV head
+  // filled in by the launch: the plan and the workspace's parts
+  int hpc, hparts, nq, grid;
+  int* cum;                  // [kMaxBatch + 3] first unit of each sequence, then the plan (written for the merge)
+  float* o_part;             // [piece + segment][nq][dim] partial outputs
+  float* lse_part;           // [piece + segment][nq] base-2 log-sum-exps
+};
+size_t kv4_attn_workspace(int hq, int hkv, int dim, const BatchDesc& bd);
+cudaError_t launch_kv4_attn(Kv4AttnParams p, const BatchDesc& bd, cudaStream_t st);
+
+// Log probabilities of given tokens, entropy and top alternatives.
+struct LogprobsParams {
+  const void* logits;
+  long long row_stride;
+  const int* tokens;         // [num_rows][given]
+  float* logprobs;
+  int* top_ids;              // [num_rows][top]
+  float* top_logprobs;
+  float* entropy;            // nullable
+  float* lse;                // nullable
+  int* dev_status;           // nullable
+  float inv_t;
+  int num_rows, vocab, dtype, given, top;
+  // filled in by the launch
+  int piece, pieces;         // logits of a piece, pieces of a row
+  float4* stats;             // [num_rows][pieces] maximum, sum, weighted sum, not-finite flag
+  unsigned long long* keys;  // [num_rows][pieces][top]
+};
+size_t logprobs_workspace(int num_rows, int vocab, int top);
+cudaError_t launch_logprobs(LogprobsParams p, void* workspace, cudaStream_t st);
+
 }  // namespace sdv
