@@ -305,7 +305,7 @@ struct LogprobsParams {
   int num_rows, vocab, dtype, given, top;
   // filled in by the launch
   int piece, pieces;         // logits of a piece, pieces of a row
-  float4* stats;             // [num_rows][pieces] maximum, sum, weighted sum, not-finite flag
+  float4* stats;             // [num_rows][pieces] maximum, how often (NaN: a NaN or +infinity was met), sum and weighted sum beside it
   unsigned long long* keys;  // [num_rows][pieces][top]
 };
 size_t logprobs_workspace(int num_rows, int vocab, int top);

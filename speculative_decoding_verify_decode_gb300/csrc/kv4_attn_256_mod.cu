@@ -1,0 +1,12 @@
+// Instances of the 4-bit cache's attention: head dim 256, capped or biased scores.
+#define SDV_KV4_DIM 256
+#define SDV_KV4_MOD 1
+#include "kv4_attn_launch.cuh"
+
+namespace sdv {
+
+cudaError_t launch_kv4_256_mod(const Kv4AttnParams& p, const BatchDesc& bd, cudaStream_t st) {
+  return launch_kv4_kind(p, bd, st);
+}
+
+}  // namespace sdv

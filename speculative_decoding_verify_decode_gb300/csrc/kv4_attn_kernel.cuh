@@ -1,0 +1,1160 @@
+// Verify attention over the 4-bit cache (include/sd_kv4.h: sd_kv4_attn):
+// codes widened in registers into tensor memory, tcgen05 products from there.
+//
+// The mathematics.  A query column is one (draft node, query head) pair of a
+// KV head; a key is a context token with k, v = (c - 8) s, or a draft node.  With
+// s = cap(scale q.k) + bias in base 2 and a running reference m of the column,
+//   e = 2^(s - m),   l += e,   O += bf16(e) v,   out = O / l.
+// (c - 8) s is exactly a bf16 value, so the products are those of a bf16 cache
+// that holds what the codes stand for.  m is the first tile's maximum, and moves
+// (with O and l rescaled) only when a weight passes 2^kRise: fp32 sums and bf16
+// weights are as exact at 2^16 as at 1.
+//
+// Where the widened operand goes.  A tile's 128 tokens x D dims (or D dims x 128
+// tokens of V^T) are the MMA's A operand, which may lie in tensor memory with a row
+// per lane: a thread takes its row's codes out of shared memory (16 bytes are 32
+// values), makes pairs of bf16 with three instructions each, and stores them to its own lane.
+// Nothing widened passes through shared memory, where the same tile would be
+// written and read at four times its size.  The cache's records are laid out for it: K's
+// words go along a token's dims, V's along a dim's tokens, so neither is transposed.
+//
+// What bounds it.  Bytes: 9 D / 8 a token and KV head, read once per CTA column part.
+// Beside that, per 128-token tile of 256 dims: 32 products of M = 128, N = NQ, K = 16
+// (2304 cycles at 144 columns), and the widening, some 900 warp instructions
+// on each of the four schedulers, against 1570 cycles of HBM time.
+//
+// Work split, line of units, pieces and merge: as in kv8_attn_kernel.cuh.
+//
+// Per tile (tokens are the MMA's M; NQ columns):
+//   S[128 tok][NQ]     = K_tile . Q^T          A from tensor memory, Q K-major in shared memory
+//   O^T[D][NQ]        += V_tile^T . P^T        M = 128 dims a product, P MN-major in shared memory
+// Warps: NG groups of four softmax warps (lane quarter = warp % 4, CC chunks of 16 columns a
+// group; thread = token row), four that widen K, four that widen V, then one each that loads K,
+// loads V, issues QK, issues PV.  The softmax reads S twice, first for the columns whose
+// reference must move, then for the weights: its sums are all it holds
+// (48 registers at CC = 3), and masked or capped scores go back to S in between.
+// Every wait on a barrier is bounded; on expiry the kernel reports
+// SD_DEV_TIMEOUT and runs out.
+#pragma once
+
+#include <cstddef>
+
+#include "kernels.h"
+#include "kv4_format.cuh"
+#include "tc_ptx.cuh"
+
+namespace sdv {
+namespace {
+
+constexpr int kTile = kTileTokens;
+constexpr float kRise = 16.0f;         // log2 of the weight beyond which a reference moves
+constexpr float kLog2e = 1.4426950408889634f;
+
+template <int NQ, bool MOD>
+struct Kv4Small {
+  static constexpr int kBars = 64;
+  float m[NQ];             // the column's reference, negated: -m
+  float alpha[NQ];         // rescale factor of the current tile; 1 / l in the epilogue
+  float slope[MOD ? NQ : 4];   // distance bias of the column, base 2
+  float red[4][NQ];        // per lane quarter: column maxima of a tile; column sums in the epilogue
+  alignas(16) uint2 vs[4][2][32];              // per V warp: scales of token pairs, and -24 times them
+  unsigned long long anc[kMaxNodes];          // bit r: node r is on the node's root path; in the draft CTA then turned
+                                              // round, bit n: node n sees the row
+  uint64_t bar[kBars];
+  int cum[kMaxBatch + 1];  // first unit of each sequence
+  int scan[8];
+  int per, extra;
+  int8_t par[kMaxNodes];
+  int8_t depth[kMaxNodes];
+  int8_t wild[kMaxNodes];  // the node's key or value holds a NaN or an infinity
+  alignas(16) int flag[3][2][4];   // [group][tile parity][lane quarter]: chunks where a weight passes 2^kRise
+  uint32_t tmem;
+  int abort;
+};
+
+// D: head dim.  NG groups of softmax warps, of up to CC 16-column chunks each.  MOD: capped scores or a distance bias.
+template <int D, int NG, int CC, bool MOD>
+struct Kv4 {
+  static constexpr int NQ = NG * CC * 16;                 // query columns
+  static constexpr int kWarps = NG * 4, kThreads = (kWarps + 12) * 32;
+  using Small = Kv4Small<NQ, MOD>;
+  static constexpr int kCtas = NQ == 16 ? 2 : 1;
+  static constexpr int kSmemBytes = kCtas == 2 ? 115712 : 232448;   // dynamic shared memory a CTA can have
+  static constexpr int MH = D / 128;                      // 128-dim blocks
+  static constexpr int NS = NQ <= 96 ? 2 : 1;             // S buffers in tensor memory
+  // Widened operands: slots of SW elements a lane, two to a column.
+  static constexpr int SW = NQ == 144 ? 32 : 64;
+  static constexpr int kSlotCols = SW / 2;
+  static constexpr int kColO = NS * NQ, kColA = kColO + MH * NQ;
+  static constexpr int kTmemMost = kCtas == 2 ? 256 : 512;
+  static constexpr int kSlotsLeft = (kTmemMost - kColA) / kSlotCols;
+  static constexpr int KA = kSlotsLeft / 2 > 4 ? 4 : kSlotsLeft / 2;
+  static constexpr int VA = kSlotsLeft - KA > 4 ? 4 : kSlotsLeft - KA;
+  static constexpr int kCols = kColA + (KA + VA) * kSlotCols;
+  static constexpr int kTmem = kCols <= 64 ? 64 : kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
+  static constexpr int kRecord = kv4_record(D), kTileBytes = 8 * kRecord;   // a page's K or V; a tile's
+  static constexpr int kQBytes = NQ * D * 2;
+  static constexpr int kPBytes = NQ * kTile * 2;
+  static constexpr int kLeft = (kSmemBytes - kQBytes - 2 * kPBytes - (int)sizeof(Small)) / kTileBytes;
+  static constexpr int kUnits = kLeft > 16 ? 16 : kLeft;
+  static constexpr int KS = kUnits / 2, VS = kUnits - KS;
+  static constexpr size_t kSmem = (size_t)kQBytes + 2 * kPBytes + (KS + VS) * kTileBytes + sizeof(Small);
+  static_assert(KS >= 2 && VS >= 2, "rings of two tiles at least");
+  static_assert(KA >= 2 && VA >= 2 && kCols <= kTmemMost, "tensor memory");
+  static_assert(kSmem <= (size_t)kSmemBytes, "shared memory over 227 KB");
+};
+
+// ------------------------------------------------------------ small pieces
+
+// A bounded wait: false, with the CTA's abort flag set, if the phase never completes.  The kernel's end reports the flag.
+__device__ __forceinline__ bool wait4(uint32_t bar, uint32_t parity, volatile int* abort) {
+  long long t0 = 0;
+#pragma unroll 1
+  while (!mbar_try(bar, parity)) {
+    const long long now = clock64();
+    if (t0 == 0) t0 = now;
+    if (now - t0 > kWaitCycles || *abort) {
+      *abort = 1;
+      return false;
+    }
+  }
+  return true;
+}
+// One lane of a converged warp (the tensor core's and TMA's instructions take uniform operands).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(ok));
+  return ok != 0;
+}
+__device__ __forceinline__ uint64_t noswz_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+  return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) |
+         ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46);
+}
+// kind::f16, A in tensor memory (128 lanes, two K elements a column), B in shared memory.
+__device__ __forceinline__ void umma_ta(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{ .reg .pred p; setp.ne.b32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }"
+      ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc));
+}
+// A record of one page (a multiple of 16 bytes), read with the evict-first policy.
+__device__ __forceinline__ void bulk_record(uint32_t dst, const uint8_t* src, uint32_t bytes, uint32_t bar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;"
+      ::"r"(dst), "l"(src), "r"(bytes), "r"(bar), "l"(policy)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+      ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
+        "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)));
+  return *reinterpret_cast<float2*>(&r);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)));
+  return *reinterpret_cast<float2*>(&r);
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(r)
+      : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)), "l"(*reinterpret_cast<uint64_t*>(&c)));
+  return *reinterpret_cast<float2*>(&r);
+}
+__device__ __forceinline__ float fast_rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// Maxima of 16 values over the warp's lanes: lane L ends with that of value L % 16.
+__device__ __forceinline__ float warp_max16(const float (&v)[16], int lane) {
+  float r = 0.f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    float x;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(x) : "f"(v[i]));
+    r = (lane & 15) == i ? x : r;
+  }
+  return r;
+}
+// Sums of 16 values over the warp's lanes: lane L ends with that of value L % 16.
+__device__ __forceinline__ float warp_sum16(float (&v)[16], int lane) {
+#pragma unroll
+  for (int half = 8; half >= 1; half >>= 1) {
+    const bool up = (lane & half) != 0;
+#pragma unroll
+    for (int i = 0; i < half; ++i) {
+      const float send = up ? v[i] : v[i + half], keep = up ? v[i + half] : v[i];
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, send, half);
+    }
+  }
+  return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 16);
+}
+__device__ __forceinline__ bool wild8(const uint4 x) {   // a NaN or an infinity among eight bf16 values
+  const uint32_t e = 0x7f807f80u;
+  return (__vcmpeq2(x.x & e, e) | __vcmpeq2(x.y & e, e) | __vcmpeq2(x.z & e, e) | __vcmpeq2(x.w & e, e)) != 0u;
+}
+
+// What a segment's draft tile counts for beyond one unit, where CTAs have `even` units each: staging and the first
+// references take as long as a few tiles; in pieces of few units one more would cost the whole.
+template <int NQ>
+__device__ __forceinline__ int extra_units(int even) {
+  return even >= 12 && NQ < 144 ? 3 : even >= 6 ? 2 : even >= 4 ? 1 : 0;
+}
+
+// A bit per column of a softmax group.
+template <int CC> struct BitsOf { using type = uint32_t; };
+template <> struct BitsOf<3> { using type = unsigned long long; };
+
+// One CTA's share of one segment.
+struct Piece {
+  int b, g, c;         // sequence, KV head, head part
+  int seg;
+  int L, base, nt;     // context length; first position the context tiles cover, and how many there are
+  int first, tiles;    // first tile of the segment (0: the draft block, i: the i-th context tile from the end), how many
+  int span;            // units of the line that the piece takes
+  bool whole;          // the segment lies in this piece alone
+  __device__ __forceinline__ int t0(int i) const { return base + (nt - i) * kTile; }   // position of context tile i
+};
+
+template <int D, int NG, int CC, bool MOD>
+__global__ void __launch_bounds__((NG + 3) * 128, NG * CC == 1 ? 2 : 1)
+kv4_attn_kernel(const Kv4AttnParams p, const BatchDesc bd) {
+  using K = Kv4<D, NG, CC, MOD>;
+  constexpr int NQ = K::NQ, MH = K::MH, NS = K::NS, KS = K::KS, VS = K::VS, KA = K::KA, VA = K::VA, SW = K::SW;
+  constexpr int kWarps = K::kWarps, kAllThreads = K::kThreads;      // softmax warps; all threads
+  constexpr int kWarpWideK = kWarps, kWarpWideV = kWarps + 4, kWarpK = kWarps + 8, kWarpV = kWarps + 9,
+                kWarpQK = kWarps + 10;
+  using Sm = typename K::Small;
+  constexpr int B_KF = 0, B_KE = B_KF + KS, B_VF = B_KE + KS, B_VE = B_VF + VS, B_AKF = B_VE + VS, B_AKE = B_AKF + KA,
+                B_AVF = B_AKE + KA, B_AVE = B_AVF + VA, B_SF = B_AVE + VA, B_SE = B_SF + NS, B_PF = B_SE + NS,
+                B_OD = B_PF + 2, B_Q = B_OD + 2, B_G = B_Q + 1;
+  constexpr int kNumBars = B_G + NG;
+  static_assert(kNumBars <= Sm::kBars, "barriers");
+  extern __shared__ __align__(1024) uint8_t smem4[];
+  uint8_t* sQ = smem4;
+  uint8_t* sP = sQ + K::kQBytes;                 // two buffers
+  uint8_t* sK = sP + 2 * K::kPBytes;
+  uint8_t* sV = sK + KS * K::kTileBytes;
+  Sm* sm = reinterpret_cast<Sm*>(sV + VS * K::kTileBytes);
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+  if (smem_u32(smem4) & 1023u) {   // not expected; refuse rather than mis-swizzle
+    if (tid == 0) report_dep(p.dev_status, SD_DEV_TIMEOUT);
+    return;
+  }
+
+  // ---------------------------------------------------------------- the line of units
+  const int parts = p.hkv * p.hparts;   // segments per sequence
+  auto ctx_of = [&](int b) {
+    const int L = p.ctx_lens[b];
+    return L < 0 ? 0 : min(L, p.max_pages * kPage);
+  };
+  if (tid == 0) {
+#pragma unroll 1
+    for (int i = 0; i < kNumBars; ++i) {
+      const bool by_four = (i >= B_KE && i < B_VF) || (i >= B_VE && i < B_AKE) || (i >= B_AVF && i < B_AVE) || i >= B_G;
+      const bool by_softmax = (i >= B_SE && i < B_SE + NS) || i == B_PF || i == B_PF + 1;
+      mbar_init(smem_u32(&sm->bar[i]), by_softmax ? (uint32_t)kWarps : by_four ? 4u : 1u);
+    }
+    sm->abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  // Launched as a programmatic dependent: everything above touches no global memory; here the previous kernel's writes
+  // become visible.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (bd.batch <= 32) {
+    int per, extra;
+    // a sequence per lane, every warp for itself
+    int units = 0;
+    if (lane < bd.batch) {
+      const int raw = p.ctx_lens[lane], L = ctx_of(lane);
+      if (blockIdx.x == 0 && warp == 0 && raw != L) report(p.dev_status, SD_DEV_BAD_CTX);
+      units = 1 + (L - window_base(L, p.window, kTile) + kTile - 1) / kTile;
+    }
+    const int even = (__reduce_add_sync(0xffffffffu, units) * parts + (int)gridDim.x - 1) / (int)gridDim.x;
+    const int more = extra_units<NQ>(even);
+    per = even;
+    extra = -1;
+#pragma unroll 1
+    for (int w = 0; w < 8 && extra < 0; ++w) {
+      const int size = even + w * max(1, even / 56);
+      const int need = __reduce_add_sync(0xffffffffu, units > 0 ? (units + more + size - 1) / size : 0) * parts;
+      if (need <= (int)gridDim.x) { per = size; extra = more; }
+    }
+    int incl = (extra >= 0 ? (units + (units > 0 ? extra : 0) + per - 1) / per * per : units) * parts;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int up = __shfl_up_sync(0xffffffffu, incl, d);
+      if (lane >= d) incl += up;
+    }
+    if (warp == 0) {
+      if (lane == 0) { sm->cum[0] = 0; sm->per = per; sm->extra = extra; }
+      if (lane < bd.batch) sm->cum[lane + 1] = incl;
+    }
+  } else {
+    int per, extra;
+    int units = 0;
+    if (tid < bd.batch) {
+      const int raw = p.ctx_lens[tid], L = ctx_of(tid);
+      if (blockIdx.x == 0 && raw != L) report(p.dev_status, SD_DEV_BAD_CTX);
+      units = 1 + (L - window_base(L, p.window, kTile) + kTile - 1) / kTile;
+      sm->cum[tid] = units;
+    }
+    __syncthreads();
+    // Eight warps try eight piece sizes, from the even share up.
+    if (warp < 8) {
+      int sum = 0;
+#pragma unroll 1
+      for (int b = lane; b < bd.batch; b += 32) sum += sm->cum[b];
+      sum = __reduce_add_sync(0xffffffffu, sum);
+      const int even = (sum * parts + (int)gridDim.x - 1) / (int)gridDim.x;
+      const int more = extra_units<NQ>(even);
+      const int size = even + warp * max(1, even / 56);
+      int need = 0;
+#pragma unroll 1
+      for (int b = lane; b < bd.batch; b += 32) need += (sm->cum[b] + more + size - 1) / size;
+      need = __reduce_add_sync(0xffffffffu, need) * parts;
+      if (lane == 0) sm->scan[warp] = need <= (int)gridDim.x ? size : 0;
+      if (tid == 0) { sm->flag[0][0][0] = even; sm->flag[0][0][1] = more; }
+    }
+    __syncthreads();
+    per = 0;
+#pragma unroll
+    for (int w = 7; w >= 0; --w) per = sm->scan[w] > 0 ? sm->scan[w] : per;
+    extra = per > 0 ? sm->flag[0][0][1] : -1;
+    if (per == 0) per = sm->flag[0][0][0];
+    __syncthreads();
+    int incl = (extra >= 0 ? (units + (units > 0 ? extra : 0) + per - 1) / per * per : units) * parts;
+    if (warp < 8) {
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int up = __shfl_up_sync(0xffffffffu, incl, d);
+        if (lane >= d) incl += up;
+      }
+      if (lane == 31) sm->scan[warp] = incl;
+    }
+    __syncthreads();
+    if (warp < 8) {
+#pragma unroll 1
+      for (int w = 0; w < warp; ++w) incl += sm->scan[w];
+      if (tid == 0) { sm->cum[0] = 0; sm->per = per; sm->extra = extra; }
+      if (tid < bd.batch) sm->cum[tid + 1] = incl;
+    }
+  }
+  if (warp == kWarpQK) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sm->tmem)),
+                 "n"(K::kTmem));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  // units per CTA; extra >= 0: every segment has CTAs of its own, its draft tile counting 1 + extra units
+  const int per = sm->per, extra = sm->extra;
+  const int total = sm->cum[bd.batch];
+  const int u_begin = min(total, (int)blockIdx.x * per), u_end = min(total, u_begin + per);
+  if (blockIdx.x == 0) {   // for the merge
+#pragma unroll 1
+    for (int i = tid; i <= bd.batch; i += kAllThreads) p.cum[i] = sm->cum[i];
+    if (tid == 0) { p.cum[kMaxBatch + 1] = per; p.cum[kMaxBatch + 2] = extra; }
+  }
+  // The piece that begins at unit u.
+  auto piece_at = [&](int u) {
+    Piece pc;
+    int lo = 0, hi = bd.batch - 1;
+#pragma unroll 1
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (sm->cum[mid] <= u) lo = mid; else hi = mid - 1;
+    }
+    const int line = (sm->cum[lo + 1] - sm->cum[lo]) / parts;     // units of one of the sequence's segments
+    const int rem = u - sm->cum[lo], s = rem / line, at = rem - s * line;
+    pc.b = lo;
+    pc.g = s / p.hparts;
+    pc.c = s - pc.g * p.hparts;
+    pc.seg = lo * parts + s;
+    pc.L = ctx_of(lo);
+    pc.base = window_base(pc.L, p.window, kTile);
+    pc.nt = (pc.L - pc.base + kTile - 1) / kTile;
+    if (extra >= 0) {
+      pc.first = max(0, at - extra);
+      pc.tiles = min(pc.nt + 1, at + per - extra) - pc.first;
+      pc.span = per;
+    } else {
+      pc.first = at;
+      pc.tiles = pc.span = min(line - at, u_end - u);
+    }
+    pc.whole = pc.tiles == pc.nt + 1;
+    // the same for every lane, and known to be
+    pc.b = __shfl_sync(0xffffffffu, pc.b, 0);
+    pc.g = __shfl_sync(0xffffffffu, pc.g, 0);
+    pc.c = __shfl_sync(0xffffffffu, pc.c, 0);
+    pc.first = __shfl_sync(0xffffffffu, pc.first, 0);
+    pc.tiles = __shfl_sync(0xffffffffu, pc.tiles, 0);
+    pc.L = __shfl_sync(0xffffffffu, pc.L, 0);
+    pc.base = __shfl_sync(0xffffffffu, pc.base, 0);
+    pc.nt = __shfl_sync(0xffffffffu, pc.nt, 0);
+    pc.span = __shfl_sync(0xffffffffu, pc.span, 0);
+    return pc;
+  };
+  const uint32_t bars = smem_u32(&sm->bar[0]);
+  auto bar = [&](int i) { return bars + 8u * (uint32_t)i; };
+  auto wait = [&](int i, int n) { return wait4(bar(i), (uint32_t)n & 1u, &sm->abort); };
+  // The softmax warps do not leave early: after an expired wait no other one waits, and they run through, so that
+  // their named barriers always find all of them.
+  auto spin = [&](int i, int n) {
+    wait(i, n);
+    __syncwarp();
+  };
+  const uint32_t tmem = sm->tmem;
+
+  // Positions in the rings, counted along: an index and the parity of its round.
+  struct Ring {
+    int at = 0;
+    uint32_t round = 0;
+    __device__ __forceinline__ void next(int n) {
+      if (++at == n) { at = 0; round ^= 1u; }
+    }
+  };
+  auto wait_full = [&](int first, const Ring& r) { return wait(first + r.at, (int)r.round); };
+  auto wait_empty = [&](int first, const Ring& r) { return wait(first + r.at, (int)r.round ^ 1); };
+  // A position that some query sees: from the root's oldest visible one on.
+  auto first_seen = [&](int L) { return p.window > 0 ? L - p.window + 1 : 0; };
+
+  // 768 threads are launched with 80 registers each: 3 x 128 x 96 + 2 x 128 x 72 + 128 x 48 is what that makes.
+  constexpr bool kShare = NG == 3;
+  if (warp >= kWarpK) {
+    if (kShare) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+    if (warp <= kWarpV) {
+      // ---------------------------------------------------------- producers
+      // Page ids come a group of four tiles at a time (lane l: page l % 8 of the group's tile l / 8), two groups ahead of
+      // their use: under a full memory system a load takes as long as a tile or two.
+      const bool is_k = warp == kWarpK;
+      const int n_ring = is_k ? KS : VS, b_full = is_k ? B_KF : B_VF, b_empty = is_k ? B_KE : B_VE;
+      uint8_t* const buf = is_k ? sK : sV;
+      const uint64_t policy = l2_evict_first();
+      Ring ring;
+      bool ok = true;
+#pragma unroll 1
+      for (int u = u_begin; u < u_end && ok;) {
+        const Piece pc = piece_at(u);
+        u += pc.span;
+        const int* row = p.page_table + (size_t)pc.b * p.max_pages;
+        const int left = pc.tiles - (pc.first == 0 ? 1 : 0);      // the draft tile does not come from the cache
+        const int t0 = pc.t0(max(pc.first, 1));
+        const uint8_t* src = p.cache + (size_t)(2 * pc.g + (is_k ? 0 : 1)) * K::kRecord;
+        const size_t page_bytes = (size_t)p.hkv * 2 * K::kRecord;
+        auto ids_from = [&](int n) {     // of the piece's context tiles n .. n + 3
+          const int t = t0 - (lane >> 3) * kTile + (lane & 7) * kPage;
+          return n + (lane >> 3) < left && t - n * kTile < pc.L ? row[(t - n * kTile) / kPage] : -1;
+        };
+        int ids_next = ids_from(0), ids_after = ids_from(4), ids = -1;
+        uint32_t good = 0;    // pages of the group that can be loaded
+#pragma unroll 1
+        for (int n = 0; n < left; ++n) {
+          const int sub = (n & 3) * 8;
+          if (sub == 0) {
+            ids = ids_next;
+            ids_next = ids_after;
+            ids_after = ids_from(n + 8);
+            const bool in_pool = (unsigned)ids < (unsigned)p.num_pool_pages;
+            good = __ballot_sync(0xffffffffu, in_pool);
+            if (is_k) {
+              const int at = t0 - (n + (lane >> 3)) * kTile + (lane & 7) * kPage;
+              if (n + (lane >> 3) < left && at < pc.L && at + kPage > first_seen(pc.L) && !in_pool)
+                report(p.dev_status, SD_DEV_BAD_PAGE);
+            }
+          }
+          const uint32_t have = (good >> sub) & 0xffu;
+          const int valid = min(kTile, pc.L - (t0 - n * kTile));
+          const uint32_t need = (1u << ((valid + kPage - 1) / kPage)) - 1u;
+          ok = __all_sync(0xffffffffu, wait_empty(b_empty, ring));
+          if (!ok) break;
+          uint8_t* dst = buf + ring.at * K::kTileBytes;
+          if (need & ~have) {   // ids out of range count as zeros: scales of 0
+#pragma unroll 1
+            for (int e = lane; e < 8 * (K::kRecord / 16); e += 32)
+              if (((need & ~have) >> (e / (K::kRecord / 16))) & 1u) reinterpret_cast<uint4*>(dst)[e] = make_uint4(0, 0, 0, 0);
+            fence_async_smem();   // the slot's next contents come by another path
+            __syncwarp();
+          }
+          int page[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) page[j] = __shfl_sync(0xffffffffu, ids, sub + j);
+          if (elect_one()) {
+            mbar_expect_tx(bar(b_full + ring.at), (uint32_t)__popc(have & need) * (uint32_t)K::kRecord);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              if (((have & need) >> j) & 1u)
+                bulk_record(smem_u32(dst) + j * K::kRecord, src + (size_t)page[j] * page_bytes, K::kRecord,
+                            bar(b_full + ring.at), policy);
+          }
+          __syncwarp();
+          ring.next(n_ring);
+        }
+      }
+      // After an abort no copy may still be landing when the CTA ends: wait, bounded, for both rounds of every slot.
+      if (lane == 0 && *(volatile int*)&sm->abort) {
+#pragma unroll 1
+        for (int s = 0; s < 2 * n_ring; ++s) {
+          const long long begin = clock64();
+          while (!mbar_test(bar(b_full + (s >> 1)), (uint32_t)s & 1u) && clock64() - begin < kWaitCycles / 64) {
+          }
+        }
+      }
+    } else if (warp == kWarpQK) {
+      // ---------------------------------------------------------- QK issuer
+      Ring s_ring, a_ring;
+      int np = 0;
+      bool ok = true;
+      const uint64_t q_desc = sw128_desc(smem_u32(sQ), 16, 1024);
+#pragma unroll 1
+      for (int u = u_begin; u < u_end && ok; ++np) {
+        const Piece pc = piece_at(u);
+        u += pc.span;
+        const int n_nodes = bd.q_indptr[pc.b + 1] - bd.q_indptr[pc.b];
+        const int nq = (min(p.hpc, p.group - pc.c * p.hpc) * n_nodes + 15) & ~15;
+        const uint32_t idesc = f16_idesc(128, nq, 0, 0);
+        ok = __all_sync(0xffffffffu, wait(B_Q, np));
+#pragma unroll 1
+        for (int i = 0; i < pc.tiles && ok; ++i) {
+          ok = __all_sync(0xffffffffu, wait_empty(B_SE, s_ring));
+          const uint32_t d = tmem + s_ring.at * NQ;
+#pragma unroll 1
+          for (int ks = 0; ks < D / SW && ok; ++ks) {
+            ok = __all_sync(0xffffffffu, wait_full(B_AKF, a_ring));
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t a = tmem + K::kColA + a_ring.at * K::kSlotCols;
+            if (elect_one()) {
+#pragma unroll
+              for (int kk = 0; kk < SW / 16; ++kk) {
+                const int k16 = ks * (SW / 16) + kk;
+                umma_ta(d, a + kk * 8, q_desc + (((k16 >> 2) * NQ * 128 + (k16 & 3) * 32) >> 4), idesc, k16 > 0 ? 1u : 0u);
+              }
+              umma_commit(bar(B_AKE + a_ring.at));
+              if (ks == D / SW - 1) umma_commit(bar(B_SF + s_ring.at));
+            }
+            __syncwarp();
+            a_ring.next(KA);
+          }
+          s_ring.next(NS);
+        }
+      }
+    } else {
+      // ---------------------------------------------------------- PV issuer
+      Ring a_ring;
+      int it = 0;
+      bool ok = true;
+      // P: 8-column chunks of 128 token rows x 16 bytes; MN-major without a swizzle
+      const uint64_t p_desc0 = noswz_desc(smem_u32(sP), 128, kTile * 16);
+      const uint64_t p_desc1 = noswz_desc(smem_u32(sP + K::kPBytes), 128, kTile * 16);
+#pragma unroll 1
+      for (int u = u_begin; u < u_end && ok;) {
+        const Piece pc = piece_at(u);
+        u += pc.span;
+        const int n_nodes = bd.q_indptr[pc.b + 1] - bd.q_indptr[pc.b];
+        const int nq = (min(p.hpc, p.group - pc.c * p.hpc) * n_nodes + 15) & ~15;
+        const uint32_t idesc = f16_idesc(128, nq, 0, 1);
+#pragma unroll 1
+        for (int i = 0; i < pc.tiles && ok; ++i, ++it) {
+          const int valid = pc.first + i == 0 ? n_nodes : min(kTile, pc.L - pc.t0(pc.first + i));
+          ok = __all_sync(0xffffffffu, wait(B_PF + (it & 1), it >> 1));
+          const uint64_t p0 = it & 1 ? p_desc1 : p_desc0;
+#pragma unroll 1
+          for (int ts = 0; ts * SW < valid && ok; ++ts) {
+#pragma unroll
+            for (int mb = 0; mb < MH; ++mb) {
+              ok = ok && __all_sync(0xffffffffu, wait_full(B_AVF, a_ring));
+              if (!ok) break;
+              tc_fence_after();
+              const uint32_t a = tmem + K::kColA + KA * K::kSlotCols + a_ring.at * K::kSlotCols;
+              if (elect_one()) {
+#pragma unroll
+                for (int kk = 0; kk < SW / 16; ++kk)
+                  if (ts * SW + kk * 16 < valid)
+                    umma_ta(tmem + K::kColO + mb * NQ, a + kk * 8, p0 + (((ts * SW + kk * 16) * 16) >> 4), idesc,
+                            i > 0 || ts > 0 || kk > 0 ? 1u : 0u);
+                umma_commit(bar(B_AVE + a_ring.at));
+              }
+              __syncwarp();
+              a_ring.next(VA);
+            }
+          }
+          if (ok && elect_one()) umma_commit(bar(B_OD + (it & 1)));
+          __syncwarp();
+        }
+      }
+    }
+  } else if (warp >= kWarpWideK) {
+    // ------------------------------------------------------------ the widening warps
+    if (kShare) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    const bool is_k = warp < kWarpWideV;
+    const int quarter = warp & 3, row = quarter * 32 + lane;
+    const uint32_t a_base = tmem + ((uint32_t)(quarter * 32) << 16) + K::kColA + (is_k ? 0 : KA * K::kSlotCols);
+    Ring ring, a_ring;
+    bool ok = true;
+    // A slot's lanes are stored: to the issuer.
+    auto store16 = [&](int at, const uint32_t (&x)[16]) { tmem_st16u(a_base + a_ring.at * K::kSlotCols + at * 16, x); };
+    auto slot_done = [&] {
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar((is_k ? B_AKF : B_AVF) + a_ring.at));
+      a_ring.next(is_k ? KA : VA);
+    };
+    auto slot_free = [&] {
+      ok = __all_sync(0xffffffffu, wait_empty(is_k ? B_AKE : B_AVE, a_ring));
+      tc_fence_after();
+      return ok;
+    };
+    int vs_at = 0;
+#pragma unroll 1
+    for (int u = u_begin; u < u_end && ok;) {
+      const Piece pc = piece_at(u);
+      u += pc.span;
+      const int q0 = bd.q_indptr[pc.b], n_nodes = bd.q_indptr[pc.b + 1] - q0;
+      const int seen = first_seen(pc.L);
+#pragma unroll 1
+      for (int i = 0; i < pc.tiles && ok; ++i) {
+        if (pc.first + i == 0) {
+          // the draft block, bf16 as it is (what is no number there goes through the scores: zeros here, see `wild`)
+          if (is_k) {
+            const uint4* src = reinterpret_cast<const uint4*>(p.k_new + (long long)(q0 + min(row, n_nodes - 1)) * p.k_stride + pc.g * D);
+#pragma unroll 1
+            for (int ks = 0; ks < D / SW && ok; ++ks) {
+              if (!slot_free()) break;
+#pragma unroll
+              for (int h = 0; h < SW / 32; ++h) {
+                uint32_t x[16];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  uint4 v = make_uint4(0, 0, 0, 0);
+                  if (row < n_nodes) v = __ldg(src + (ks * SW + h * 32) / 8 + e);
+                  x[4 * e] = v.x; x[4 * e + 1] = v.y; x[4 * e + 2] = v.z; x[4 * e + 3] = v.w;
+                }
+                store16(h, x);
+              }
+              slot_done();
+            }
+          } else {
+            const uint16_t* src = reinterpret_cast<const uint16_t*>(p.v_new) + (long long)q0 * p.v_stride + pc.g * D + row;
+#pragma unroll 1
+            for (int ts = 0; ts * SW < n_nodes && ok; ++ts) {
+#pragma unroll 1
+              for (int mb = 0; mb < MH; ++mb) {
+                if (!slot_free()) break;
+#pragma unroll
+                for (int h = 0; h < SW / 32; ++h) {
+                  uint32_t x[16];
+#pragma unroll
+                  for (int e = 0; e < 32; ++e) {
+                    const int n = ts * SW + h * 32 + e;
+                    uint32_t v = 0;
+                    if (n < n_nodes) v = __ldg(src + (long long)n * p.v_stride + mb * 128);
+                    if ((v & 0x7f80u) == 0x7f80u) v = 0;
+                    x[e >> 1] = e & 1 ? x[e >> 1] | v << 16 : v;
+                  }
+                  store16(h, x);
+                }
+                slot_done();
+              }
+              if (!ok) break;
+            }
+          }
+          continue;
+        }
+        const int t0 = pc.t0(pc.first + i), valid = min(kTile, pc.L - t0);
+        ok = __all_sync(0xffffffffu, wait_full(is_k ? B_KF : B_VF, ring));
+        if (!ok) break;
+        if (is_k) {
+          // this thread's token: its scales, then block after block
+          const uint8_t* rec = sK + ring.at * K::kTileBytes + (row >> 4) * K::kRecord;
+          const uint8_t* words = rec + (row & 15) * 16;
+          const uint32_t* sc = reinterpret_cast<const uint32_t*>(rec + kv4_codes(D) + (row & 15) * (D / 16));
+          bool bad = false;
+          uint32_t s2[D / 64];       // two blocks' scales each
+#pragma unroll
+          for (int e = 0; e < D / 64; ++e) s2[e] = kv4_sane(sc[e], bad);
+          if (bad && row < valid && t0 + row >= seen) report(p.dev_status, SD_DEV_BAD_SCALE);
+#pragma unroll
+          for (int ks = 0; ks < D / SW; ++ks) {
+            uint4 w[SW / 32];
+#pragma unroll
+            for (int h = 0; h < SW / 32; ++h) w[h] = *reinterpret_cast<const uint4*>(words + (ks * (SW / 32) + h) * 256);
+            if (ks == D / SW - 1) {
+              __syncwarp();
+              if (lane == 0) mbar_arrive(bar(B_KE + ring.at));
+            }
+            if (!slot_free()) break;
+#pragma unroll
+            for (int h = 0; h < SW / 32; ++h) {
+              const int block = ks * (SW / 32) + h;
+              const __nv_bfloat162 s = kv4_scale2(__byte_perm(s2[block >> 1], 0, block & 1 ? 0x3232 : 0x1010));
+              const __nv_bfloat162 less = kv4_less(s);
+              const uint32_t* ww = reinterpret_cast<const uint32_t*>(&w[h]);
+              uint32_t x[16];
+#pragma unroll
+              for (int e = 0; e < 16; ++e) x[e] = kv4_pair(ww[e >> 2], e & 3, s, less);
+              store16(h, x);
+            }
+            slot_done();
+          }
+        } else {
+          // this thread's dim (of each 128): the scales of its block of 32, token pair by token pair, are the warp's
+          const uint8_t* tile = sV + ring.at * K::kTileBytes;
+#pragma unroll 1
+          for (int ts = 0; ts * SW < valid && ok; ++ts) {
+#pragma unroll
+            for (int mb = 0; mb < MH; ++mb) {
+              const uint8_t* pages = tile + ts * (SW / 16) * K::kRecord;
+              uint2* const vs = sm->vs[quarter][vs_at];
+              vs_at ^= 1;
+              if (SW == 64 || lane < SW / 2) {
+                // tokens that nobody sees count 0 (their records may hold anything)
+                uint32_t s2 = *reinterpret_cast<const uint32_t*>(pages + (lane >> 3) * K::kRecord + kv4_codes(D) +
+                                                                 (mb * 4 + quarter) * 32 + (lane & 7) * 4);
+                const int t = t0 + ts * SW + 2 * lane;
+                if (t >= pc.L || t < seen) s2 &= 0xffff0000u;
+                if (t + 1 >= pc.L || t + 1 < seen) s2 &= 0x0000ffffu;
+                bool bad = false;
+                s2 = kv4_sane(s2, bad);
+                if (bad) report(p.dev_status, SD_DEV_BAD_SCALE);
+                const __nv_bfloat162 less = kv4_less(kv4_scale2(s2));
+                vs[lane] = make_uint2(s2, *reinterpret_cast<const uint32_t*>(&less));
+              }
+              __syncwarp();
+              uint2 w[SW / 16];
+#pragma unroll
+              for (int j = 0; j < SW / 16; ++j)
+                w[j] = *reinterpret_cast<const uint2*>(pages + j * K::kRecord + (mb * 128 + row) * 8);
+              if (!slot_free()) break;
+#pragma unroll
+              for (int h = 0; h < SW / 32; ++h) {
+                uint32_t x[16];
+#pragma unroll
+                for (int e = 0; e < 16; e += 2) {
+                  const uint4 sl = *reinterpret_cast<const uint4*>(&vs[h * 16 + e]);
+                  const uint2 ww = w[h * 2 + (e >> 3)];
+                  const uint32_t word = e & 4 ? ww.y : ww.x;
+                  x[e] = kv4_pair(word, e & 3, kv4_scale2(sl.x), kv4_scale2(sl.y));
+                  x[e + 1] = kv4_pair(word, (e & 3) + 1, kv4_scale2(sl.z), kv4_scale2(sl.w));
+                }
+                store16(h, x);
+              }
+              slot_done();
+            }
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(B_VE + ring.at));
+        }
+        ring.next(is_k ? KS : VS);
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ softmax warps
+    if (kShare) asm volatile("setmaxnreg.inc.sync.aligned.u32 96;");
+    const int group = warp >> 2, quarter = warp & 3;
+    const int row = quarter * 32 + lane;                       // token row of S; dim (mod 128) of O^T
+    const uint32_t lane_addr = (uint32_t)(quarter * 32) << 16;
+    auto sync_all = [] { asm volatile("bar.sync 7, %0;" ::"n"(kWarps * 32) : "memory"); };        // the softmax warps
+    auto sync_group = [&] { asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory"); };     // the group's four
+    Ring s_ring;
+    int it = 0;
+#pragma unroll 1
+    for (int u = u_begin; u < u_end;) {
+      const Piece pc = piece_at(u);
+      u += pc.span;
+      const int q0 = bd.q_indptr[pc.b], n_nodes = bd.q_indptr[pc.b + 1] - q0;
+      const int hpc = min(p.hpc, p.group - pc.c * p.hpc);
+      const int head0 = pc.g * p.group + pc.c * p.hpc;
+      const int rows = hpc * n_nodes, nc = (rows + 15) / 16;
+      const int mine = min(CC, max(0, nc - group * CC)), c_first = group * CC;   // chunks of this group in use
+      const int col0 = c_first * 16;
+      const bool has_draft = pc.first == 0;
+      // ---------------------------------------------------------- staging: Q and the tree
+      // (the previous piece's products have all finished: its last scores and its last O were waited for)
+      if (tid < n_nodes) {
+        const int up = p.parents[q0 + tid];
+        sm->par[tid] = (int8_t)(up < -1 || up >= kMaxNodes ? -2 : up);
+        sm->wild[tid] = 0;
+      }
+      {
+        constexpr int LPR = D / 8, RPW = 32 / LPR;                     // lanes per row, rows per warp and load
+        constexpr int U = (NQ + kWarps * RPW - 1) / (kWarps * RPW);    // a warp's query rows, RPW at a time
+        constexpr int UB = U < 4 ? U : 4;                              // of them in flight
+        const int sub = lane / LPR, ch = lane % LPR;                   // 8-value chunk of the row
+        const int n_q = nc * 16;
+        const float inv_hpc = 1.0f / (float)hpc;
+#pragma unroll 1
+        for (int i0 = 0; i0 < U; i0 += UB) {
+          if ((i0 * kWarps + warp) * RPW >= n_q) break;
+          uint4 x[UB];
+#pragma unroll
+          for (int i = 0; i < UB; ++i) {
+            const int r = ((i0 + i) * kWarps + warp) * RPW + sub;
+            const int node = __float2int_rz(((float)r + 0.5f) * inv_hpc);   // r / hpc, exact for r < 2^20
+            x[i] = make_uint4(0, 0, 0, 0);
+            if (r < rows)
+              x[i] = __ldg(reinterpret_cast<const uint4*>(p.q + (long long)(q0 + node) * p.q_stride +
+                                                          (head0 + r - node * hpc) * D) + ch);
+          }
+#pragma unroll
+          for (int i = 0; i < UB; ++i) {
+            const int r = ((i0 + i) * kWarps + warp) * RPW + sub;
+            // a row with a NaN or an infinity: all NaN, and so its scores
+            const uint32_t bad = __ballot_sync(0xffffffffu, wild8(x[i]));
+            if (RPW == 1 ? bad != 0u : (bad >> (sub * LPR) & ((1ull << LPR) - 1ull)) != 0u)
+              x[i] = make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
+            if (r < n_q)
+              *reinterpret_cast<uint4*>(sQ + (ch >> 3) * NQ * 128 + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = x[i];
+          }
+        }
+        sync_all();
+        if (has_draft) {
+#pragma unroll 1
+          for (int r = warp * RPW + sub; r < 2 * n_nodes; r += kWarps * RPW) {
+            const int n = r >> 1;
+            const uint4 y = __ldg(reinterpret_cast<const uint4*>(
+                (r & 1 ? p.v_new + (long long)(q0 + n) * p.v_stride : p.k_new + (long long)(q0 + n) * p.k_stride) + pc.g * D) + ch);
+            if (wild8(y)) sm->wild[n] = 1;
+          }
+        }
+      }
+      fence_async_smem();
+#pragma unroll 1
+      for (int q = tid; q < NQ; q += kWarps * 32) {
+        sm->m[q] = q < nc * 16 ? 0.f : -1e30f;     // no reference yet; columns past those in use: below everything
+        if (MOD) sm->slope[q] = p.slopes != nullptr && q < rows ? p.slopes[head0 + q % hpc] * kLog2e : 0.f;
+      }
+      // the tree: root paths and depths
+      if (tid < n_nodes) {
+        unsigned long long a = 1ull << tid;
+        int d = 0;
+        bool good = sm->par[tid] >= -1 && (tid > 0 || sm->par[0] == -1);
+#pragma unroll 1
+        for (int v = tid; good && v > 0; ++d) {
+          const int up = sm->par[v];
+          good = up >= 0 && up < v;
+          if (good) a |= 1ull << up;
+          v = up;
+        }
+        if (!good) {
+          report(p.dev_status, SD_DEV_BAD_PARENTS);
+          a = 1ull << tid;
+          d = 0;
+        }
+        sm->anc[tid] = a;
+        sm->depth[tid] = d;
+      }
+      sync_all();
+      if (tid == 0) mbar_arrive(bar(B_Q));
+      if (has_draft && n_nodes > 1) {
+        // While the first product runs: the root paths turned round by ballots, a row of the tile a turn.
+        unsigned long long a0 = 0, a1 = 0;
+        int d0 = 0, d1 = 0;
+        if (lane < n_nodes) { a0 = sm->anc[lane]; d0 = sm->depth[lane]; }
+        if (lane + 32 < n_nodes) { a1 = sm->anc[lane + 32]; d1 = sm->depth[lane + 32]; }
+        sync_all();
+#pragma unroll 1
+        for (int r = warp; r < n_nodes; r += kWarps) {
+          const int far = p.window > 0 && p.window < kMaxNodes ? sm->depth[r] + p.window : INT_MAX;   // the depth that no longer sees it
+          const uint32_t lo = __ballot_sync(0xffffffffu, ((a0 >> r) & 1ull) != 0ull && d0 < far);
+          const uint32_t hi = __ballot_sync(0xffffffffu, ((a1 >> r) & 1ull) != 0ull && d1 < far);
+          if (lane == 0) sm->anc[r] = (unsigned long long)hi << 32 | lo;
+        }
+        sync_all();
+      }
+
+      float2 sum[CC][8];
+#pragma unroll
+      for (int c = 0; c < CC; ++c)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum[c][e] = make_float2(0.f, 0.f);
+      const int lo_root = first_seen(pc.L);
+      const float fac = p.scale * kLog2e;
+      // Until a tile that every column sees something of has passed, columns may have no reference.
+      bool settled = false;
+#pragma unroll 1
+      for (int i = 0; i < pc.tiles; ++i, ++it) {
+        const bool draft = pc.first + i == 0;
+        const int t0 = pc.t0(pc.first + i);
+        const int valid = draft ? n_nodes : min(kTile, pc.L - t0);
+        const bool band = !draft && p.window > 0 && t0 < lo_root + kMaxNodes;
+        const bool masked = draft || valid < kTile || band;
+        // Which columns see this row, one bit each.
+        using Bits = typename BitsOf<CC>::type;
+        Bits vis = ~(Bits)0;
+        if (masked) {
+          vis = row < valid && !draft && !band ? ~(Bits)0 : 0;
+          if (row < valid && (draft || band)) {
+            // node by node, from the one of the group's first column: its columns see this row, or none of them does
+            int n = col0 / hpc, at = n * hpc - col0;       // the node's first column, less the group's
+            const Bits full = ((Bits)1 << hpc) - 1;
+            Bits bits = full >> -at;
+            if (draft) {
+              unsigned long long sees = n < n_nodes ? sm->anc[row] >> n : 0ull;
+#pragma unroll 1
+              for (; at < CC * 16 && sees != 0ull; sees >>= 1) {
+                vis |= sees & 1ull ? bits : (Bits)0;
+                at += hpc;
+                bits = full << (at & (8 * (int)sizeof(Bits) - 1));
+              }
+            } else {
+#pragma unroll 1
+              for (; at < CC * 16 && n < n_nodes; ++n) {
+                vis |= t0 + row >= lo_root + sm->depth[n] ? bits : (Bits)0;
+                at += hpc;
+                bits = full << (at & (8 * (int)sizeof(Bits) - 1));
+              }
+            }
+          }
+        }
+        // the bias' distance is counted from the root: a node's depth shifts all its scores alike (see the log-sum-exp)
+        const float rel = draft ? (row < n_nodes ? (float)sm->depth[row] : 0.f) : (float)(t0 + row - pc.L);
+        const bool nan_row = draft && row < n_nodes && sm->wild[row] != 0;
+        // Scores that are more than a multiple of the product are formed once and put back in its place.
+        const bool formed = MOD || masked;
+        const float mul = formed ? 1.f : fac;
+        wait_full(B_SF, s_ring);
+        __syncwarp();
+        tc_fence_after();
+        const uint32_t s_addr = tmem + lane_addr + s_ring.at * NQ + col0;
+        // ---- first reading: the chunks where a weight would pass 2^kRise
+        uint32_t missed = 0;
+#pragma unroll
+        for (int c = 0; c < CC; ++c) {
+          if (c >= mine) break;
+          float a[16];
+          tmem_ld16(s_addr + c * 16, a);
+          tmem_wait_ld();
+          if (formed) {
+            if (MOD && p.softcap > 0.f) {
+              // c tanh(x / c) = c - 2 c / (1 + 2^(2 log2e x / c))
+              const float cl = p.softcap * kLog2e, ky = fac * p.cap_exp;
+#pragma unroll
+              for (int e = 0; e < 16; e += 2) {
+                const float2 y = mul2(make_float2(a[e], a[e + 1]), make_float2(ky, ky));
+                const float2 d = add2(make_float2(fast_exp2(y.x), fast_exp2(y.y)), make_float2(1.f, 1.f));
+                const float2 s = fma2(make_float2(fast_rcp(d.x), fast_rcp(d.y)), make_float2(-2.f * cl, -2.f * cl), make_float2(cl, cl));
+                a[e] = s.x;
+                a[e + 1] = s.y;
+              }
+            } else {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) a[e] *= fac;
+            }
+            if (MOD) {
+#pragma unroll
+              for (int e = 0; e < 16; e += 2) {
+                const float2 sl = *reinterpret_cast<const float2*>(&sm->slope[col0 + c * 16 + e]);
+                const float2 s = fma2(sl, make_float2(rel, rel), make_float2(a[e], a[e + 1]));
+                a[e] = s.x;
+                a[e + 1] = s.y;
+              }
+            }
+            if (masked) {
+              const uint32_t bits = (uint32_t)(vis >> (c * 16));
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                const float s = nan_row ? __int_as_float(0x7fc00000) : a[e];
+                a[e] = (bits >> e) & 1u ? s : -INFINITY;
+              }
+            }
+            tmem_st16(s_addr + c * 16, a);
+          }
+          float top = -INFINITY;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float4 m = *reinterpret_cast<const float4*>(&sm->m[col0 + c * 16 + 4 * k]);
+            const float2 d0 = fma2(make_float2(a[4 * k], a[4 * k + 1]), make_float2(mul, mul), make_float2(m.x, m.y));
+            const float2 d1 = fma2(make_float2(a[4 * k + 2], a[4 * k + 3]), make_float2(mul, mul), make_float2(m.z, m.w));
+            top = fmaxf(fmaxf(top, fmaxf(d0.x, d0.y)), fmaxf(d1.x, d1.y));
+          }
+          missed |= top > kRise ? 1u << c : 0u;
+        }
+        if (formed) tmem_wait_st();
+        const uint32_t all = (1u << mine) - 1u;
+        if (__any_sync(0xffffffffu, missed != 0u)) missed = __reduce_or_sync(0xffffffffu, missed);
+        if (!settled) missed = all;
+        if (lane == 0) {
+          sm->flag[group][it & 1][quarter] = (int)missed;
+          mbar_arrive(bar(B_G + group));
+        }
+        settled = settled || draft || !band;
+        spin(B_G + group, it);
+        const int4 fl = *reinterpret_cast<const int4*>(sm->flag[group][it & 1]);
+        const uint32_t todo = (uint32_t)(fl.x | fl.y | fl.z | fl.w);     // chunks whose references move
+        if (todo != 0u) {
+          // The exact maxima of these chunks' columns and new references (unset ones are 0, set ones never are).
+#pragma unroll
+          for (int c = 0; c < CC; ++c) {
+            if ((todo >> c) & 1u) {
+              float a[16];
+              tmem_ld16(s_addr + c * 16, a);
+              tmem_wait_ld();
+              const float mx = warp_max16(a, lane) * mul;
+              if (lane < 16) sm->red[quarter][col0 + c * 16 + lane] = mx;
+            }
+          }
+          sync_group();
+          const int mine_col = quarter * 32 + lane, q = col0 + mine_col;
+          if (mine_col < mine * 16 && ((todo >> (mine_col >> 4)) & 1u)) {
+            const float old = -sm->m[q];
+            const float mt = fmaxf(fmaxf(sm->red[0][q], sm->red[1][q]), fmaxf(sm->red[2][q], sm->red[3][q]));
+            float now = mt == -INFINITY ? old : old == 0.f ? mt : fmaxf(old, mt);
+            if (now == 0.f && mt != -INFINITY) now = 1e-30f;
+            sm->alpha[q] = old == 0.f ? 1.f : fast_exp2(old - now);
+            sm->m[q] = -now;
+          }
+          sync_group();
+          // O belongs to the previous tile's PV until it has finished
+          if (i > 0) spin(B_OD + ((it - 1) & 1), (it - 1) >> 1);
+          tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < CC; ++c) {
+            if (i == 0 || !((todo >> c) & 1u)) continue;
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              sum[c][e] = mul2(sum[c][e], *reinterpret_cast<const float2*>(&sm->alpha[col0 + c * 16 + 2 * e]));
+#pragma unroll 1
+            for (int mb = 0; mb < MH; ++mb) {
+              float v[16];
+              const uint32_t ad = tmem + lane_addr + K::kColO + mb * NQ + col0 + c * 16;
+              tmem_ld16(ad, v);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) v[e] *= sm->alpha[col0 + c * 16 + e];
+              tmem_st16(ad, v);
+            }
+          }
+          tmem_wait_st();
+        }
+        // ---- second reading: the weights, into the buffer that the PV before the last has left
+        if (it >= 2) spin(B_OD + (it & 1), (it >> 1) - 1);
+        uint8_t* const p_row = sP + (it & 1) * K::kPBytes + row * 16;
+#pragma unroll
+        for (int c = 0; c < CC; ++c) {
+          if (c >= mine) break;
+          float a[16];
+          tmem_ld16(s_addr + c * 16, a);
+          tmem_wait_ld();
+          uint32_t w[8];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float4 m = *reinterpret_cast<const float4*>(&sm->m[col0 + c * 16 + 4 * k]);
+            const float2 d0 = fma2(make_float2(a[4 * k], a[4 * k + 1]), make_float2(mul, mul), make_float2(m.x, m.y));
+            const float2 d1 = fma2(make_float2(a[4 * k + 2], a[4 * k + 3]), make_float2(mul, mul), make_float2(m.z, m.w));
+            const float2 e0 = make_float2(fast_exp2(d0.x), fast_exp2(d0.y));
+            const float2 e1 = make_float2(fast_exp2(d1.x), fast_exp2(d1.y));
+            sum[c][2 * k] = add2(sum[c][2 * k], e0);
+            sum[c][2 * k + 1] = add2(sum[c][2 * k + 1], e1);
+            const __nv_bfloat162 h0 = __floats2bfloat162_rn(e0.x, e0.y), h1 = __floats2bfloat162_rn(e1.x, e1.y);
+            w[2 * k] = *reinterpret_cast<const uint32_t*>(&h0);
+            w[2 * k + 1] = *reinterpret_cast<const uint32_t*>(&h1);
+          }
+          uint8_t* at = p_row + (c_first + c) * 2 * kTile * 16;
+          *reinterpret_cast<uint4*>(at) = make_uint4(w[0], w[1], w[2], w[3]);
+          *reinterpret_cast<uint4*>(at + kTile * 16) = make_uint4(w[4], w[5], w[6], w[7]);
+        }
+        tc_fence_before();
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(bar(B_SE + s_ring.at));
+          mbar_arrive(bar(B_PF + (it & 1)));
+        }
+        s_ring.next(NS);
+      }
+
+      // ---------------------------------------------------------- results
+      // Column sums over the tile's 128 token rows: the lanes, then the quarters.
+      sync_group();      // the last tile's readers of red[] are done
+#pragma unroll
+      for (int c = 0; c < CC; ++c) {
+        float v[16];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) { v[2 * e] = sum[c][e].x; v[2 * e + 1] = sum[c][e].y; }
+        const float s = warp_sum16(v, lane);
+        if (lane < 16) sm->red[quarter][col0 + c * 16 + lane] = s;
+      }
+      sync_group();
+      spin(B_OD + ((it - 1) & 1), (it - 1) >> 1);
+      tc_fence_after();
+      const size_t slot = (size_t)blockIdx.x + pc.seg;      // rises by at least one along the pieces: unique
+      {
+        const int q = col0 + quarter * 32 + lane;
+        if (quarter * 32 + lane < mine * 16) {
+          const float l = sm->red[0][q] + sm->red[1][q] + sm->red[2][q] + sm->red[3][q];
+          sm->alpha[q] = l == 0.f ? 0.f : 1.f / l;
+          // the column's output row, in place of its sums
+          int* out_row = reinterpret_cast<int*>(sm->red[0]);
+          out_row[q] = -1;
+          if (q < rows) {
+            const int node = q / hpc, at = (q0 + node) * p.hq + head0 + q - node * hpc;
+            out_row[q] = pc.whole ? at : q;
+            float lse2 = l == 0.f ? -INFINITY : fast_log2(l) - sm->m[q];
+            if (MOD) lse2 -= sm->slope[q] * (float)sm->depth[node];
+            if (!pc.whole) p.lse_part[slot * NQ + q] = lse2;
+            else if (p.lse != nullptr) p.lse[at] = lse2 * kLn2;
+          }
+        }
+      }
+      sync_group();
+#pragma unroll 1
+      for (int c = 0; c < mine; ++c) {
+        float v[MH][16];
+#pragma unroll
+        for (int mb = 0; mb < MH; ++mb) tmem_ld16(tmem + lane_addr + K::kColO + mb * NQ + col0 + c * 16, v[mb]);
+        tmem_wait_ld();
+        const float* inv = sm->alpha + col0 + c * 16;
+        const int* at = reinterpret_cast<const int*>(sm->red[0]) + col0 + c * 16;
+        if (pc.whole) {
+          const bool odd = lane & 1;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int r = at[2 * k + odd];
+#pragma unroll
+            for (int mb = 0; mb < MH; ++mb) {
+              const float ev = v[mb][2 * k] * inv[2 * k], od = v[mb][2 * k + 1] * inv[2 * k + 1];
+              // even lanes keep the even column and take the odd lane's dim of it; odd lanes the reverse
+              const float got = __shfl_xor_sync(0xffffffffu, odd ? ev : od, 1);
+              const __nv_bfloat162 h = __floats2bfloat162_rn(odd ? got : ev, odd ? od : got);
+              if (r >= 0) *reinterpret_cast<__nv_bfloat162*>(p.out + (size_t)r * D + mb * 128 + (row & ~1)) = h;
+            }
+          }
+        } else {
+          // the columns' rows follow each other in the partial
+          float* dst = p.o_part + (slot * NQ + col0 + c * 16) * D + row;
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+#pragma unroll
+            for (int mb = 0; mb < MH; ++mb)
+              if (col0 + c * 16 + k < rows) dst[k * D + mb * 128] = v[mb][k] * inv[k];
+          }
+        }
+      }
+      tc_fence_before();
+      // every warp is done with the columns' arrays and O before the next piece is staged
+      sync_all();
+      tc_fence_after();
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (tid == 0 && sm->abort) report(p.dev_status, SD_DEV_TIMEOUT);
+  if (warp == kWarpQK) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(K::kTmem));
+  }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+}  // namespace
+}  // namespace sdv

@@ -1,4 +1,4 @@
-"""ctypes binding of libsdverify.so (include/sd_verify.h, sd_gdn.h, sd_kv8.h).
+"""ctypes binding of libsdverify.so (include/sd_verify.h, sd_gdn.h, sd_kv8.h, sd_kv4.h, sd_rope.h, sd_logprobs.h).
 
 Argument marshalling only: every function here turns torch tensors into the
 device pointers and host arrays of the C ABI and raises on a non-zero status.
@@ -29,6 +29,8 @@ SD_DEV_TIMEOUT = 64
 SD_DEV_NO_PAGES = 128
 SD_DEV_BAD_SCALE = 256
 SD_DEV_BAD_SLOT = 512
+SD_DEV_NOT_FINITE = 1024
+SD_DEV_BAD_POSITION = 2048
 MAX_NODES = 64
 MAX_BATCH = 256
 MAX_LAYERS = 64
@@ -51,6 +53,12 @@ class SdGdnShape(ctypes.Structure):
 class SdKv8Opts(ctypes.Structure):
     _fields_ = [("scale", ctypes.c_float), ("softcap", ctypes.c_float), ("slopes", ctypes.c_void_p),
                 ("q_stride", ctypes.c_longlong), ("k_stride", ctypes.c_longlong), ("v_stride", ctypes.c_longlong)]
+
+
+class SdRopeShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("num_rows", "num_q_heads", "num_kv_heads", "head_dim", "rot_dim", "interleaved",
+                                            "table_len", "page_size", "num_pool_pages")] + \
+               [(n, ctypes.c_longlong) for n in ("q_stride", "k_stride", "v_stride", "q_out_stride", "k_out_stride")]
 
 
 class SdError(RuntimeError):
@@ -126,6 +134,20 @@ def load() -> ctypes.CDLL:
     lib.sd_kv8_attn_workspace_size.argtypes = [shp]
     lib.sd_kv8_attn.restype = i32
     lib.sd_kv8_attn.argtypes = [shp, ctypes.POINTER(SdKv8Opts)] + [vp] * 12 + [vp, sz, vp, vp]
+    lib.sd_kv4_append.restype = i32
+    lib.sd_kv4_append.argtypes = [i32] * 5 + [vp] * 3 + [i64, i32, vp, vp, i32, vp, vp]
+    lib.sd_kv4_read.restype = i32
+    lib.sd_kv4_read.argtypes = [i32] * 5 + [vp] * 3 + [i64, vp, i32, vp, vp]
+    lib.sd_kv4_attn_workspace_size.restype = sz
+    lib.sd_kv4_attn_workspace_size.argtypes = [shp]
+    lib.sd_kv4_attn.restype = i32
+    lib.sd_kv4_attn.argtypes = [shp, ctypes.POINTER(SdKv8Opts)] + [vp] * 9 + [vp, sz, vp, vp]
+    lib.sd_rope_append.restype = i32
+    lib.sd_rope_append.argtypes = [ctypes.POINTER(SdRopeShape)] + [vp] * 12
+    lib.sd_logprobs_workspace_size.restype = sz
+    lib.sd_logprobs_workspace_size.argtypes = [i32] * 3
+    lib.sd_logprobs.restype = i32
+    lib.sd_logprobs.argtypes = [i32, i32, i32, vp, i64, f32, i32, vp, vp, i32, vp, vp, vp, vp, vp, sz, vp, vp]
     _lib = lib
     return lib
 
@@ -163,7 +185,7 @@ def _indptr(q_indptr) -> ctypes.Array:
 
 
 class Shape:
-    """An sd_shape with its host q_indptr kept alive (head geometries other than 24/4/256: sd_kv8_attn only)."""
+    """An sd_shape with its host q_indptr kept alive (head geometries other than 24/4/256: sd_kv8_attn and sd_kv4_attn)."""
 
     def __init__(self, q_indptr, max_pages_per_seq: int, num_pool_pages: int, num_splits: int = 0,
                  window: int = 0, ctx_stable: bool = False, num_q_heads: int = 24, num_kv_heads: int = 4,
@@ -173,7 +195,7 @@ class Shape:
                          int(num_q_heads), int(num_kv_heads), int(head_dim), 16, int(max_pages_per_seq),
                          int(num_pool_pages), int(num_splits), int(window), int(bool(ctx_stable)))
         n, c = int(self.indptr[-1]) if len(self.indptr) else 0, self.c
-        # shapes of sd_kv8_attn's tensors: q and out, k_new and v_new, codes, scales, page table, per sequence, per node
+        # shapes of the quantised caches' attention: q and out, k_new and v_new, codes, scales, page table, per sequence, per node
         self.dims = ((n, c.num_q_heads, c.head_dim), (n, c.num_kv_heads, c.head_dim),
                      (c.num_pool_pages, c.num_kv_heads, 16, c.head_dim), (c.num_pool_pages, c.num_kv_heads),
                      (c.batch, c.max_pages_per_seq), (c.batch,), (n,))
@@ -591,3 +613,188 @@ def sd_kv8_attn(shape: Shape, q, k_cache, v_cache, k_scales, v_scales, k_new, v_
             None if lse is None else _tensor(lse, "lse", _F32, q_shape[:2], dev), ws_at, ws_bytes,
             None if dev_status is None else _tensor(dev_status, "dev_status", _I32, (1,), dev))
     _run(load().sd_kv8_attn, "sd_kv8_attn", args, dev, stream)
+
+
+# ---------------------------------------------------------------- the 4-bit cache (include/sd_kv4.h)
+
+def kv4_cache_shape(num_pool_pages: int, num_kv_heads: int, head_dim: int) -> tuple[int, int, int, int]:
+    """Shape of one layer's 4-bit cache (uint8)."""
+    return int(num_pool_pages), int(num_kv_heads), 2, 9 * int(head_dim)
+
+
+def _kv4_layers(cache_layers):
+    """(layers, one layer's shape) of a list of caches or a tensor with a leading layer dimension."""
+    if isinstance(cache_layers, torch.Tensor):
+        shape = cache_layers.shape
+        n, cache = (shape[0], tuple(shape[1:])) if shape else (0, ())
+    else:
+        if not cache_layers:
+            raise ValueError("no layers")
+        n, cache = len(cache_layers), tuple(cache_layers[0].shape)
+    if len(cache) != 4 or cache[2] != 2 or cache[3] % 9:
+        raise ValueError("a layer's 4-bit cache is uint8 [pool, heads, 2, 9 * dim]")
+    return n, cache
+
+
+def _kv4_rows(cache_layers, k_layers, v_layers, slots, names):
+    """Checked arguments of sd_kv4_append and sd_kv4_read: sizes, addresses (the array keeps them alive), stride, rows."""
+    dev = slots.get_device()
+    n, cache = _kv4_layers(cache_layers)
+    if slots.dim() != 1:
+        raise ValueError("slots is one-dimensional")
+    pool, heads, dim = cache[0], cache[1], cache[3] // 9
+    ptrs = array("Q")      # the three arrays of n addresses, one behind the other
+    _put_layers(ptrs, cache_layers, n, "cache", _U8, cache, pool * heads * 18 * dim, dev)
+    stride, rows = _put_rows(ptrs, k_layers, n, names[0], heads, dim, dev)
+    if (stride, rows) != _put_rows(ptrs, v_layers, n, names[1], heads, dim, dev):
+        raise ValueError(f"{names[0]} and {names[1]} differ in rows or row stride")
+    at, step = ptrs.buffer_info()[0], 8 * n
+    return ptrs, (n, heads, dim, 16, pool, at, at + step, at + 2 * step, stride), rows, dev
+
+
+def sd_kv4_append(cache_layers, k_new_layers, v_new_layers, slots, rows=None, dev_status=None, stream=None) -> None:
+    """bf16 rows quantised into the 4-bit caches of every layer at the slots of a slot map (sd_pages_extend).
+
+    Per layer (lists, or tensors with a leading layer dimension): cache uint8 [pool, heads, 2, 9 * dim], new rows bf16
+    [rows, heads, dim] (rows may lie apart, not overlap)."""
+    ptrs, head, src, dev = _kv4_rows(cache_layers, k_new_layers, v_new_layers, slots, ("k_new", "v_new"))
+    max_rows = slots.shape[0]
+    args = (*head, src, _tensor(slots, "slots", _I32, (max_rows,), dev),
+            None if rows is None else _tensor(rows, "rows", _I32, (max_rows,), dev), max_rows,
+            None if dev_status is None else _tensor(dev_status, "dev_status", _I32, (1,), dev))
+    _run(load().sd_kv4_append, "sd_kv4_append", args, dev, stream)
+
+
+def sd_kv4_read(cache_layers, slots, k_out_layers, v_out_layers, dev_status=None, stream=None) -> None:
+    """The values at these slots of the 4-bit caches of every layer, as bf16 rows [len(slots), heads, dim] (rows of slot
+    -1 stay as they are)."""
+    ptrs, head, rows, dev = _kv4_rows(cache_layers, k_out_layers, v_out_layers, slots, ("k_out", "v_out"))
+    max_rows = slots.shape[0]
+    if rows != max_rows:
+        raise ValueError(f"k_out has {rows} rows, slots {max_rows}")
+    args = (*head, _tensor(slots, "slots", _I32, (max_rows,), dev), max_rows,
+            None if dev_status is None else _tensor(dev_status, "dev_status", _I32, (1,), dev))
+    _run(load().sd_kv4_read, "sd_kv4_read", args, dev, stream)
+
+
+def sd_kv4_attn_workspace_size(shape: Shape) -> int:
+    return int(load().sd_kv4_attn_workspace_size(shape.ref))
+
+
+def sd_kv4_attn(shape: Shape, q, cache, k_new, v_new, page_table, ctx_lens, parents, out, lse=None, scale: float = 0.0,
+                softcap: float = 0.0, slopes=None, workspace=None, dev_status=None, stream=None) -> None:
+    """sd_verify_attn over the 4-bit cache; ``softcap`` and ``slopes`` (fp32 [query heads]) as in sd_kv8_opts.
+    q, k_new and v_new may have rows that lie apart (slices of a fused projection), not rows that overlap."""
+    dev = q.get_device()
+    q_shape, kv_shape, codes, _, table, batch, n = shape.dims
+    q_at, qs = _rows(q, "q", q_shape, dev)
+    k_at, ks = _rows(k_new, "k_new", kv_shape, dev)
+    v_at, vs = _rows(v_new, "v_new", kv_shape, dev)
+    opts = None
+    if scale or softcap or qs or ks or vs or slopes is not None:
+        opts = ctypes.byref(SdKv8Opts(scale, softcap, None if slopes is None else
+                                      _tensor(slopes, "slopes", _F32, (q_shape[1],), dev), qs, ks, vs))
+    ws_at, ws_bytes = None, 0
+    if workspace is not None:
+        ws_bytes = workspace.numel() * workspace.element_size()
+        ws_at = _tensor(workspace, "workspace", workspace.dtype, workspace.shape, dev)
+    args = (shape.ref, opts, q_at, _tensor(cache, "cache", _U8, (codes[0], codes[1], 2, 9 * codes[3]), dev), k_at, v_at,
+            _tensor(page_table, "page_table", _I32, table, dev), _tensor(ctx_lens, "ctx_lens", _I32, batch, dev),
+            _tensor(parents, "parents", _I32, n, dev), _tensor(out, "out", torch.bfloat16, q_shape, dev),
+            None if lse is None else _tensor(lse, "lse", _F32, q_shape[:2], dev), ws_at, ws_bytes,
+            None if dev_status is None else _tensor(dev_status, "dev_status", _I32, (1,), dev))
+    _run(load().sd_kv4_attn, "sd_kv4_attn", args, dev, stream)
+
+
+# ---------------------------------------------------------------- rotation and append (include/sd_rope.h)
+
+def sd_rope_append(table, positions, q=None, k=None, v=None, q_out=None, k_out=None, k_cache=None, v_cache=None,
+                   slots=None, interleaved: bool = False, dev_status=None, stream=None) -> None:
+    """q and k rows turned to their positions into ``q_out`` and ``k_out`` (which may be q and k), and with ``v``, the
+    bf16 caches [pool, heads, 16, dim] and ``slots`` also appended there.  ``table`` fp32 [positions, rot_dim]:
+    cosines, then sines (step.rope_table).  q, k, v and the outputs may have rows that lie apart."""
+    dev = table.get_device()
+    if table.dim() != 2 or positions.dim() != 1:
+        raise ValueError("table is [positions, rot_dim], positions is one-dimensional")
+    table_len, rot = table.shape
+    rows = positions.shape[0]
+    some = q if q is not None else k
+    if some is None or some.dim() != 3:
+        raise ValueError("q and k are [rows, heads, dim]; one of them is needed")
+    dim = some.shape[2]
+    q_at = k_at = v_at = qo_at = ko_at = kc_at = vc_at = slots_at = None
+    qs = ks = vs = qos = kos = hq = hkv = pool = 0
+    if q is not None:
+        shape = (rows, q.shape[1], dim)
+        hq = shape[1]
+        q_at, qs = _rows(q, "q", shape, dev)
+    if q_out is not None:
+        qo_at, qos = _rows(q_out, "q_out", (rows, hq, dim), dev)
+    if k is not None:
+        if k.dim() != 3:
+            raise ValueError("k is [rows, heads, dim]")
+        shape = (rows, k.shape[1], dim)
+        hkv = shape[1]
+        k_at, ks = _rows(k, "k", shape, dev)
+    if k_out is not None:
+        ko_at, kos = _rows(k_out, "k_out", (rows, hkv, dim), dev)
+    if v is not None:
+        v_at, vs = _rows(v, "v", (rows, hkv, dim), dev)
+    if k_cache is not None:
+        pool = k_cache.shape[0] if k_cache.dim() else 0
+        kc_at = _tensor(k_cache, "k_cache", torch.bfloat16, (pool, hkv, 16, dim), dev)
+    if v_cache is not None:
+        vc_at = _tensor(v_cache, "v_cache", torch.bfloat16, (pool, hkv, 16, dim), dev)
+    if slots is not None:
+        slots_at = _tensor(slots, "slots", _I32, (rows,), dev)
+    shape = SdRopeShape(rows, hq, hkv, dim, rot, 1 if interleaved else 0, table_len, 16, pool, qs, ks, vs, qos, kos)
+    args = (ctypes.byref(shape), _tensor(table, "table", _F32, (table_len, rot), dev),
+            _tensor(positions, "positions", _I32, (rows,), dev), q_at, k_at, v_at, qo_at, ko_at, kc_at, vc_at, slots_at,
+            None if dev_status is None else _tensor(dev_status, "dev_status", _I32, (1,), dev))
+    _run(load().sd_rope_append, "sd_rope_append", args, dev, stream)
+
+
+# ---------------------------------------------------------------- log probabilities (include/sd_logprobs.h)
+
+_LOGITS = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+
+
+def sd_logprobs_workspace_size(num_rows: int, vocab: int, top: int) -> int:
+    return int(load().sd_logprobs_workspace_size(int(num_rows), int(vocab), int(top)))
+
+
+def sd_logprobs(logits, tokens=None, logprobs=None, top_ids=None, top_logprobs=None, entropy=None, lse=None,
+                temperature: float = 1.0, workspace=None, dev_status=None, stream=None) -> None:
+    """Log probabilities of ``tokens`` int32 [rows, given], the largest logits' ids and log probabilities [rows, top],
+    entropy and log-sum-exp [rows] of logits [rows, vocab] (fp32, bf16 or fp16; the rows may lie apart)."""
+    dev = logits.get_device()
+    dtype = _LOGITS.get(logits.dtype)
+    if dtype is None or logits.dim() != 2:
+        raise ValueError("logits are fp32, bf16 or fp16 [rows, vocab]")
+    rows, vocab = logits.shape
+    stride = 0
+    if not logits.is_contiguous():
+        stride = logits.stride(0) if rows > 1 else 0
+        if (vocab > 1 and logits.stride(1) != 1) or (rows > 1 and stride < vocab):
+            raise ValueError("logits: a row must be contiguous, and rows must not overlap")
+    given, top = 0, 0
+    if tokens is not None:
+        given = tokens.shape[-1] if tokens.dim() else 0
+        tokens = _tensor(tokens, "tokens", _I32, (rows, given), dev)
+    if logprobs is not None:
+        logprobs = _tensor(logprobs, "logprobs", _F32, (rows, given), dev)
+    if top_ids is not None:
+        top = top_ids.shape[-1] if top_ids.dim() else 0
+        top_ids = _tensor(top_ids, "top_ids", _I32, (rows, top), dev)
+    if top_logprobs is not None:
+        top_logprobs = _tensor(top_logprobs, "top_logprobs", _F32, (rows, top), dev)
+    ws_at, ws_bytes = None, 0
+    if workspace is not None:
+        ws_bytes = workspace.numel() * workspace.element_size()
+        ws_at = _tensor(workspace, "workspace", workspace.dtype, workspace.shape, dev)
+    args = (rows, vocab, dtype, logits.data_ptr(), stride, temperature, given, tokens or None, logprobs or None, top,
+            top_ids or None, top_logprobs or None,
+            None if entropy is None else _tensor(entropy, "entropy", _F32, (rows,), dev),
+            None if lse is None else _tensor(lse, "lse", _F32, (rows,), dev), ws_at, ws_bytes,
+            None if dev_status is None else _tensor(dev_status, "dev_status", _I32, (1,), dev))
+    _run(load().sd_logprobs, "sd_logprobs", args, dev, stream)
