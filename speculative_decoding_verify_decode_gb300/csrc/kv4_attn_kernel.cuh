@@ -674,31 +674,21 @@ kv4_attn_kernel(const Kv4AttnParams p, const BatchDesc bd) {
         ok = __all_sync(0xffffffffu, wait_full(is_k ? B_KF : B_VF, ring));
         if (!ok) break;
         if (is_k) {
-          // this thread's token: its scales, then block after block
+          // this thread's token, block after block of 32 dims (rolled: the roles' loops share an instruction cache)
           const uint8_t* rec = sK + ring.at * K::kTileBytes + (row >> 4) * K::kRecord;
           const uint8_t* words = rec + (row & 15) * 16;
-          const uint32_t* sc = reinterpret_cast<const uint32_t*>(rec + kv4_codes(D) + (row & 15) * (D / 16));
+          const uint16_t* sc = reinterpret_cast<const uint16_t*>(rec + kv4_codes(D) + (row & 15) * (D / 16));
           bool bad = false;
-          uint32_t s2[D / 64];       // two blocks' scales each
-#pragma unroll
-          for (int e = 0; e < D / 64; ++e) s2[e] = kv4_sane(sc[e], bad);
-          if (bad && row < valid && t0 + row >= seen) report(p.dev_status, SD_DEV_BAD_SCALE);
-#pragma unroll
+#pragma unroll 1
           for (int ks = 0; ks < D / SW; ++ks) {
-            uint4 w[SW / 32];
-#pragma unroll
-            for (int h = 0; h < SW / 32; ++h) w[h] = *reinterpret_cast<const uint4*>(words + (ks * (SW / 32) + h) * 256);
-            if (ks == D / SW - 1) {
-              __syncwarp();
-              if (lane == 0) mbar_arrive(bar(B_KE + ring.at));
-            }
             if (!slot_free()) break;
-#pragma unroll
+#pragma unroll 1
             for (int h = 0; h < SW / 32; ++h) {
-              const int block = ks * (SW / 32) + h;
-              const __nv_bfloat162 s = kv4_scale2(__byte_perm(s2[block >> 1], 0, block & 1 ? 0x3232 : 0x1010));
-              const __nv_bfloat162 less = kv4_less(s);
-              const uint32_t* ww = reinterpret_cast<const uint32_t*>(&w[h]);
+              const uint4 w = *reinterpret_cast<const uint4*>(words);
+              const __nv_bfloat162 s = kv4_scale2(kv4_sane(*sc * 0x10001u, bad)), less = kv4_less(s);
+              words += kPage * 16;
+              ++sc;
+              const uint32_t* ww = reinterpret_cast<const uint32_t*>(&w);
               uint32_t x[16];
 #pragma unroll
               for (int e = 0; e < 16; ++e) x[e] = kv4_pair(ww[e >> 2], e & 3, s, less);
@@ -706,50 +696,49 @@ kv4_attn_kernel(const Kv4AttnParams p, const BatchDesc bd) {
             }
             slot_done();
           }
+          if (bad && row < valid && t0 + row >= seen) report(p.dev_status, SD_DEV_BAD_SCALE);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(B_KE + ring.at));
         } else {
           // this thread's dim (of each 128): the scales of its block of 32, token pair by token pair, are the warp's
           const uint8_t* tile = sV + ring.at * K::kTileBytes;
+          const int slots = (valid + SW - 1) / SW * MH;
 #pragma unroll 1
-          for (int ts = 0; ts * SW < valid && ok; ++ts) {
-#pragma unroll
-            for (int mb = 0; mb < MH; ++mb) {
-              const uint8_t* pages = tile + ts * (SW / 16) * K::kRecord;
-              uint2* const vs = sm->vs[quarter][vs_at];
-              vs_at ^= 1;
-              if (SW == 64 || lane < SW / 2) {
-                // tokens that nobody sees count 0 (their records may hold anything)
-                uint32_t s2 = *reinterpret_cast<const uint32_t*>(pages + (lane >> 3) * K::kRecord + kv4_codes(D) +
-                                                                 (mb * 4 + quarter) * 32 + (lane & 7) * 4);
-                const int t = t0 + ts * SW + 2 * lane;
-                if (t >= pc.L || t < seen) s2 &= 0xffff0000u;
-                if (t + 1 >= pc.L || t + 1 < seen) s2 &= 0x0000ffffu;
-                bool bad = false;
-                s2 = kv4_sane(s2, bad);
-                if (bad) report(p.dev_status, SD_DEV_BAD_SCALE);
-                const __nv_bfloat162 less = kv4_less(kv4_scale2(s2));
-                vs[lane] = make_uint2(s2, *reinterpret_cast<const uint32_t*>(&less));
-              }
-              __syncwarp();
-              uint2 w[SW / 16];
-#pragma unroll
-              for (int j = 0; j < SW / 16; ++j)
-                w[j] = *reinterpret_cast<const uint2*>(pages + j * K::kRecord + (mb * 128 + row) * 8);
-              if (!slot_free()) break;
-#pragma unroll
-              for (int h = 0; h < SW / 32; ++h) {
-                uint32_t x[16];
-#pragma unroll
-                for (int e = 0; e < 16; e += 2) {
-                  const uint4 sl = *reinterpret_cast<const uint4*>(&vs[h * 16 + e]);
-                  const uint2 ww = w[h * 2 + (e >> 3)];
-                  const uint32_t word = e & 4 ? ww.y : ww.x;
-                  x[e] = kv4_pair(word, e & 3, kv4_scale2(sl.x), kv4_scale2(sl.y));
-                  x[e + 1] = kv4_pair(word, (e & 3) + 1, kv4_scale2(sl.z), kv4_scale2(sl.w));
-                }
-                store16(h, x);
-              }
-              slot_done();
+          for (int n = 0; n < slots; ++n) {
+            const int ts = n / MH, mb = n % MH;
+            const uint8_t* pages = tile + ts * (SW / 16) * K::kRecord;
+            uint2* const vs = sm->vs[quarter][vs_at];
+            vs_at ^= 1;
+            if (SW == 64 || lane < SW / 2) {
+              // tokens that nobody sees count 0 (their records may hold anything)
+              uint32_t s2 = *reinterpret_cast<const uint32_t*>(pages + (lane >> 3) * K::kRecord + kv4_codes(D) +
+                                                               (mb * 4 + quarter) * 32 + (lane & 7) * 4);
+              const int t = t0 + ts * SW + 2 * lane;
+              if (t >= pc.L || t < seen) s2 &= 0xffff0000u;
+              if (t + 1 >= pc.L || t + 1 < seen) s2 &= 0x0000ffffu;
+              bool bad = false;
+              s2 = kv4_sane(s2, bad);
+              if (bad) report(p.dev_status, SD_DEV_BAD_SCALE);
+              const __nv_bfloat162 less = kv4_less(kv4_scale2(s2));
+              vs[lane] = make_uint2(s2, *reinterpret_cast<const uint32_t*>(&less));
             }
+            __syncwarp();
+            if (!slot_free()) break;
+            const uint8_t* words = pages + (mb * 128 + row) * 8;
+#pragma unroll 1
+            for (int h = 0; h < SW / 32; ++h, words += 2 * K::kRecord) {
+              const uint2 w0 = *reinterpret_cast<const uint2*>(words), w1 = *reinterpret_cast<const uint2*>(words + K::kRecord);
+              uint32_t x[16];
+#pragma unroll
+              for (int e = 0; e < 16; e += 2) {
+                const uint4 sl = *reinterpret_cast<const uint4*>(&vs[h * 16 + e]);
+                const uint32_t word = e & 8 ? (e & 4 ? w1.y : w1.x) : (e & 4 ? w0.y : w0.x);
+                x[e] = kv4_pair(word, e & 3, kv4_scale2(sl.x), kv4_scale2(sl.y));
+                x[e + 1] = kv4_pair(word, (e & 3) + 1, kv4_scale2(sl.z), kv4_scale2(sl.w));
+              }
+              store16(h, x);
+            }
+            slot_done();
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(B_VE + ring.at));

@@ -25,7 +25,8 @@ __host__ __device__ constexpr int kv4_shift(int e) { return 16 * (e & 1) + 4 * (
 // 16 + c; times s, less 24 s, is (c - 8) s in one exact fused step (24 s has 2 + 5 bits, the result 3 + 5).
 __device__ __forceinline__ uint32_t kv4_pair(uint32_t word, int i, __nv_bfloat162 s, __nv_bfloat162 less) {
   const uint32_t at = i == 0 ? word << 3 : word >> (4 * i - 3);
-  const uint32_t x = (at & 0x00780078u) | 0x41804180u;
+  uint32_t x;   // (at & mask) | 16, as one instruction: the compiler makes two of it, a constant each
+  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(x) : "r"(at), "r"(0x00780078u), "r"(0x41804180u));
   const __nv_bfloat162 y = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x), s, less);
   return *reinterpret_cast<const uint32_t*>(&y);
 }
