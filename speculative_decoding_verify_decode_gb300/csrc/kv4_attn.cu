@@ -8,11 +8,10 @@ namespace sdv {
 namespace {
 
 // Query columns of a CTA: as many heads of a KV group as fit, so that the cache is read and widened as few times as
-// can be.  Up to 16 columns, i.e. single tokens, two CTAs share an SM.
+// can be.
 struct Kv4Plan {
   int hpc, hparts;   // query heads of a KV group per CTA, and CTA parts per group
   int nq;            // query columns of the kernel instance
-  int ctas;          // of it per SM
 };
 Kv4Plan kv4_plan(int group, int max_nodes) {
   Kv4Plan pl;
@@ -22,7 +21,6 @@ Kv4Plan kv4_plan(int group, int max_nodes) {
   pl.hparts = (group + pl.hpc - 1) / pl.hpc;
   const int cols = pl.hpc * max_nodes;
   pl.nq = cols <= 16 ? 16 : cols <= 48 ? 48 : cols <= 96 ? 96 : 144;
-  pl.ctas = pl.nq == 16 ? 2 : 1;
   return pl;
 }
 
@@ -30,7 +28,7 @@ Kv4Plan kv4_plan(int group, int max_nodes) {
 
 size_t kv4_attn_workspace(int hq, int hkv, int dim, const BatchDesc& bd) {
   const Kv4Plan pl = kv4_plan(hq / hkv, bd.max_nodes);
-  return layout_of(pl.nq, pl.ctas, pl.hparts, hkv, dim, bd, sm_count()).total;
+  return layout_of(pl.nq, 1, pl.hparts, hkv, dim, bd, sm_count()).total;
 }
 
 cudaError_t launch_kv4_attn(Kv4AttnParams p, const BatchDesc& bd, cudaStream_t st) {
@@ -40,8 +38,8 @@ cudaError_t launch_kv4_attn(Kv4AttnParams p, const BatchDesc& bd, cudaStream_t s
   p.hparts = pl.hparts;
   p.nq = pl.nq;
   const int sms = sm_count();
-  p.grid = sms * pl.ctas;
-  const Layout l = layout_of(pl.nq, pl.ctas, pl.hparts, p.hkv, p.dim, bd, sms);
+  p.grid = sms;
+  const Layout l = layout_of(pl.nq, 1, pl.hparts, p.hkv, p.dim, bd, sms);
   char* ws = static_cast<char*>(p.workspace);
   p.cum = reinterpret_cast<int*>(ws);
   p.o_part = reinterpret_cast<float*>(ws + l.o);

@@ -46,18 +46,18 @@
 namespace sdv {
 namespace {
 
-constexpr int kTile = kTileTokens;
+constexpr int kTile = kTileTokens;     // tokens of a product's M
 constexpr float kRise = 16.0f;         // log2 of the weight beyond which a reference moves
 constexpr float kLog2e = 1.4426950408889634f;
 
-template <int NQ, bool MOD>
+template <int NQ, int WG, bool MOD>
 struct Kv4Small {
   static constexpr int kBars = 64;
   float m[NQ];             // the column's reference, negated: -m
   float alpha[NQ];         // rescale factor of the current tile; 1 / l in the epilogue
   float slope[MOD ? NQ : 4];   // distance bias of the column, base 2
   float red[4][NQ];        // per lane quarter: column maxima of a tile; column sums in the epilogue
-  alignas(16) uint2 vs[4][2][32];              // per V warp: scales of token pairs, and -24 times them
+  alignas(16) uint2 vs[WG * 4][2][32];        // per V warp: scales of token pairs, and -24 times them
   unsigned long long anc[kMaxNodes];          // bit r: node r is on the node's root path; in the draft CTA then turned
                                               // round, bit n: node n sees the row
   uint64_t bar[kBars];
@@ -76,31 +76,39 @@ struct Kv4Small {
 template <int D, int NG, int CC, bool MOD>
 struct Kv4 {
   static constexpr int NQ = NG * CC * 16;                 // query columns
-  static constexpr int kWarps = NG * 4, kThreads = (kWarps + 12) * 32;
-  using Small = Kv4Small<NQ, MOD>;
-  static constexpr int kCtas = NQ == 16 ? 2 : 1;
-  static constexpr int kSmemBytes = kCtas == 2 ? 115712 : 232448;   // dynamic shared memory a CTA can have
+  // Groups of four warps that widen K, and as many that widen V, tile by tile in turn; each has rings of its own (what is
+  // counted below), so that no barrier has a user that passes some of its phases by.
+  static constexpr int WG = NG == 1 ? 2 : 1;
+  static constexpr int kWarps = NG * 4, kThreads = (kWarps + WG * 8 + 4) * 32;
+  using Small = Kv4Small<NQ, WG, MOD>;
+  static constexpr int kSmemBytes = 232448;               // dynamic shared memory a CTA can have
   static constexpr int MH = D / 128;                      // 128-dim blocks
+  // Tiles that pass the softmax together: what a turn costs beyond them (barriers, the references' check, bookkeeping)
+  // is as much as sixteen columns of a tile or two.
+  static constexpr int T = NQ == 16 ? 4 : NQ == 48 ? 2 : 1;
   static constexpr int NS = NQ <= 96 ? 2 : 1;             // S buffers in tensor memory
   // Widened operands: slots of SW elements a lane, two to a column.
   static constexpr int SW = NQ == 144 ? 32 : 64;
   static constexpr int kSlotCols = SW / 2;
-  static constexpr int kColO = NS * NQ, kColA = kColO + MH * NQ;
-  static constexpr int kTmemMost = kCtas == 2 ? 256 : 512;
-  static constexpr int kSlotsLeft = (kTmemMost - kColA) / kSlotCols;
-  static constexpr int KA = kSlotsLeft / 2 > 4 ? 4 : kSlotsLeft / 2;
-  static constexpr int VA = kSlotsLeft - KA > 4 ? 4 : kSlotsLeft - KA;
-  static constexpr int kCols = kColA + (KA + VA) * kSlotCols;
-  static constexpr int kTmem = kCols <= 64 ? 64 : kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
+  static constexpr int kColO = NS * T * NQ, kColA = kColO + MH * NQ;
+  static constexpr int kSlotsLeft = (512 - kColA) / kSlotCols / WG;
+  static constexpr int KA = kSlotsLeft / 2 > 1 ? 2 : 1, VA = 2;
+  // A tile takes the ring round KU (VU) times: which slot, and which phase of it, is known without counting.
+  static constexpr int KU = D / SW / KA, VU = kTile / SW * MH / VA;
   static constexpr int kRecord = kv4_record(D), kTileBytes = 8 * kRecord;   // a page's K or V; a tile's
   static constexpr int kQBytes = NQ * D * 2;
-  static constexpr int kPBytes = NQ * kTile * 2;
+  static constexpr int kPBytes = NQ * T * kTile * 2;      // [8-column chunk][token][16 bytes]
   static constexpr int kLeft = (kSmemBytes - kQBytes - 2 * kPBytes - (int)sizeof(Small)) / kTileBytes;
-  static constexpr int kUnits = kLeft > 16 ? 16 : kLeft;
-  static constexpr int KS = kUnits / 2, VS = kUnits - KS;
-  static constexpr size_t kSmem = (size_t)kQBytes + 2 * kPBytes + (KS + VS) * kTileBytes + sizeof(Small);
-  static_assert(KS >= 2 && VS >= 2, "rings of two tiles at least");
-  static_assert(KA >= 2 && VA >= 2 && kCols <= kTmemMost, "tensor memory");
+  // A page's K and V lie together: one ring of both where it holds eight tiles, else a ring each (V is needed later than K).
+  static constexpr bool kJoint = kLeft >= 16;
+  static constexpr int kUnits = kLeft > 20 ? 20 : kLeft;
+  static constexpr int KS = kUnits / 2 / WG, VS = kJoint ? KS : kUnits / WG - KS;
+  static constexpr int kPageStride = kJoint ? 2 * kRecord : kRecord, kSlotBytes = 8 * kPageStride;
+  static constexpr size_t kRingBytes = (size_t)(kJoint ? KS : KS + VS) * WG * kSlotBytes;
+  static constexpr size_t kSmem = (size_t)kQBytes + 2 * kPBytes + kRingBytes + sizeof(Small);
+  static_assert(KS * WG >= 2 && VS * WG >= 2, "rings of two tiles at least");
+  static_assert(kColA + WG * (KA + VA) * kSlotCols <= 512, "tensor memory");
+  static_assert(KU * KA * SW == D && VU * VA * SW == kTile * MH && (MH == 1 || MH == VA), "slots of a tile");
   static_assert(kSmem <= (size_t)kSmemBytes, "shared memory over 227 KB");
 };
 
@@ -131,10 +139,17 @@ __device__ __forceinline__ uint64_t noswz_desc(uint32_t saddr, uint32_t lbo, uin
          ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46);
 }
 // kind::f16, A in tensor memory (128 lanes, two K elements a column), B in shared memory.
-__device__ __forceinline__ void umma_ta(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{ .reg .pred p; setp.ne.b32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }"
-      ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc));
+// ACC: 1 adds to D, 2 as `acc` says.
+template <int ACC>
+__device__ __forceinline__ void umma_ta(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc = 1) {
+  if (ACC == 2)
+    asm volatile(
+        "{ .reg .pred p; setp.ne.b32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }"
+        ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc));
+  else
+    asm volatile(
+        "{ .reg .pred p; setp.ne.b32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }"
+        ::"r"(d), "r"(a), "l"(b), "r"(idesc), "n"(ACC));
 }
 // A record of one page (a multiple of 16 bytes), read with the evict-first policy.
 __device__ __forceinline__ void bulk_record(uint32_t dst, const uint8_t* src, uint32_t bytes, uint32_t bar, uint64_t policy) {
@@ -224,16 +239,17 @@ struct Piece {
 };
 
 template <int D, int NG, int CC, bool MOD>
-__global__ void __launch_bounds__((NG + 3) * 128, NG * CC == 1 ? 2 : 1)
+__global__ void __launch_bounds__((NG + (NG == 1 ? 4 : 2) + 1) * 128, 1)
 kv4_attn_kernel(const Kv4AttnParams p, const BatchDesc bd) {
   using K = Kv4<D, NG, CC, MOD>;
-  constexpr int NQ = K::NQ, MH = K::MH, NS = K::NS, KS = K::KS, VS = K::VS, KA = K::KA, VA = K::VA, SW = K::SW;
+  constexpr int NQ = K::NQ, MH = K::MH, NS = K::NS, KS = K::KS, VS = K::VS, KA = K::KA, VA = K::VA, SW = K::SW, WG = K::WG,
+                T = K::T;
   constexpr int kWarps = K::kWarps, kAllThreads = K::kThreads;      // softmax warps; all threads
-  constexpr int kWarpWideK = kWarps, kWarpWideV = kWarps + 4, kWarpK = kWarps + 8, kWarpV = kWarps + 9,
-                kWarpQK = kWarps + 10;
+  constexpr int kWarpWideK = kWarps, kWarpWideV = kWarps + WG * 4, kWarpK = kWarps + WG * 8, kWarpV = kWarpK + 1,
+                kWarpQK = kWarpK + 2;
   using Sm = typename K::Small;
-  constexpr int B_KF = 0, B_KE = B_KF + KS, B_VF = B_KE + KS, B_VE = B_VF + VS, B_AKF = B_VE + VS, B_AKE = B_AKF + KA,
-                B_AVF = B_AKE + KA, B_AVE = B_AVF + VA, B_SF = B_AVE + VA, B_SE = B_SF + NS, B_PF = B_SE + NS,
+  constexpr int B_KF = 0, B_KE = B_KF + KS * WG, B_VF = K::kJoint ? B_KF : B_KE + KS * WG, B_VE = K::kJoint ? B_KE : B_VF + VS * WG,
+                B_AKF = B_VE + VS * WG, B_AKE = B_AKF + KA * WG, B_AVF = B_AKE + KA * WG, B_AVE = B_AVF + VA * WG, B_SF = B_AVE + VA * WG, B_SE = B_SF + NS, B_PF = B_SE + NS,
                 B_OD = B_PF + 2, B_Q = B_OD + 2, B_G = B_Q + 1;
   constexpr int kNumBars = B_G + NG;
   static_assert(kNumBars <= Sm::kBars, "barriers");
@@ -241,8 +257,8 @@ kv4_attn_kernel(const Kv4AttnParams p, const BatchDesc bd) {
   uint8_t* sQ = smem4;
   uint8_t* sP = sQ + K::kQBytes;                 // two buffers
   uint8_t* sK = sP + 2 * K::kPBytes;
-  uint8_t* sV = sK + KS * K::kTileBytes;
-  Sm* sm = reinterpret_cast<Sm*>(sV + VS * K::kTileBytes);
+  uint8_t* sV = K::kJoint ? sK + K::kRecord : sK + KS * WG * K::kSlotBytes;
+  Sm* sm = reinterpret_cast<Sm*>(sK + K::kRingBytes);
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   if (smem_u32(smem4) & 1023u) {   // not expected; refuse rather than mis-swizzle
     if (tid == 0) report_dep(p.dev_status, SD_DEV_TIMEOUT);
@@ -258,9 +274,10 @@ kv4_attn_kernel(const Kv4AttnParams p, const BatchDesc bd) {
   if (tid == 0) {
 #pragma unroll 1
     for (int i = 0; i < kNumBars; ++i) {
-      const bool by_four = (i >= B_KE && i < B_VF) || (i >= B_VE && i < B_AKE) || (i >= B_AVF && i < B_AVE) || i >= B_G;
+      const bool empties = (i >= B_KE && i < B_KE + KS * WG) || (i >= B_VE && i < B_VE + VS * WG);
+      const bool by_four = (i >= B_AKF && i < B_AKE) || (i >= B_AVF && i < B_AVE) || i >= B_G;
       const bool by_softmax = (i >= B_SE && i < B_SE + NS) || i == B_PF || i == B_PF + 1;
-      mbar_init(smem_u32(&sm->bar[i]), by_softmax ? (uint32_t)kWarps : by_four ? 4u : 1u);
+      mbar_init(smem_u32(&sm->bar[i]), by_softmax ? (uint32_t)kWarps : empties ? (K::kJoint ? 8u : 4u) : by_four ? 4u : 1u);
     }
     sm->abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -349,7 +366,7 @@ kv4_attn_kernel(const Kv4AttnParams p, const BatchDesc bd) {
   }
   if (warp == kWarpQK) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sm->tmem)),
-                 "n"(K::kTmem));
+                 "n"(512));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
   tc_fence_before();
@@ -422,37 +439,48 @@ kv4_attn_kernel(const Kv4AttnParams p, const BatchDesc bd) {
       if (++at == n) { at = 0; round ^= 1u; }
     }
   };
+  // A ring for each group of widening warps, `size` barriers apart.
+  struct Rings {
+    Ring of[WG];
+    __device__ __forceinline__ Ring get(int g) const { return WG == 2 && g ? of[WG - 1] : of[0]; }
+    __device__ __forceinline__ void next(int g, int n) {
+      if (WG == 2 && g) of[WG - 1].next(n); else of[0].next(n);
+    }
+  };
   auto wait_full = [&](int first, const Ring& r) { return wait(first + r.at, (int)r.round); };
   auto wait_empty = [&](int first, const Ring& r) { return wait(first + r.at, (int)r.round ^ 1); };
   // A position that some query sees: from the root's oldest visible one on.
   auto first_seen = [&](int L) { return p.window > 0 ? L - p.window + 1 : 0; };
 
-  // 768 threads are launched with 80 registers each: 3 x 128 x 96 + 2 x 128 x 72 + 128 x 48 is what that makes.
-  constexpr bool kShare = NG == 3;
+  // The block is launched with 61440 registers (768 x 80, 640 x 96): the softmax warps take 112 (three groups) or 136 each,
+  // the widening ones 56 or 72, the others 32 or 56.
   if (warp >= kWarpK) {
-    if (kShare) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+    if (NG == 3) asm volatile("setmaxnreg.dec.sync.aligned.u32 32;"); else asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (warp <= kWarpV) {
-      // ---------------------------------------------------------- producers
-      // Page ids come a group of four tiles at a time (lane l: page l % 8 of the group's tile l / 8), two groups ahead of
+      // ---------------------------------------------------------- producers (where the ring is joint, the first alone)
+      // Page ids come a group of four tiles at a time (lane l: page l % 8 of the group's l / 8), two groups ahead of
       // their use: under a full memory system a load takes as long as a tile or two.
       const bool is_k = warp == kWarpK;
+      constexpr uint32_t kBytes = K::kPageStride;     // of a page
       const int n_ring = is_k ? KS : VS, b_full = is_k ? B_KF : B_VF, b_empty = is_k ? B_KE : B_VE;
       uint8_t* const buf = is_k ? sK : sV;
       const uint64_t policy = l2_evict_first();
-      Ring ring;
-      bool ok = true;
+      Rings rings;
+      int turn = 0;      // whose tile it is
+      bool ok = is_k || !K::kJoint;
 #pragma unroll 1
       for (int u = u_begin; u < u_end && ok;) {
         const Piece pc = piece_at(u);
         u += pc.span;
         const int* row = p.page_table + (size_t)pc.b * p.max_pages;
         const int left = pc.tiles - (pc.first == 0 ? 1 : 0);      // the draft tile does not come from the cache
+        if (pc.first == 0) turn = turn + 1 == WG ? 0 : turn + 1;
         const int t0 = pc.t0(max(pc.first, 1));
         const uint8_t* src = p.cache + (size_t)(2 * pc.g + (is_k ? 0 : 1)) * K::kRecord;
         const size_t page_bytes = (size_t)p.hkv * 2 * K::kRecord;
         auto ids_from = [&](int n) {     // of the piece's context tiles n .. n + 3
-          const int t = t0 - (lane >> 3) * kTile + (lane & 7) * kPage;
-          return n + (lane >> 3) < left && t - n * kTile < pc.L ? row[(t - n * kTile) / kPage] : -1;
+          const int t = t0 - (n + (lane >> 3)) * kTile + (lane & 7) * kPage;
+          return n + (lane >> 3) < left && t < pc.L ? row[t / kPage] : -1;
         };
         int ids_next = ids_from(0), ids_after = ids_from(4), ids = -1;
         uint32_t good = 0;    // pages of the group that can be loaded
@@ -471,16 +499,18 @@ kv4_attn_kernel(const Kv4AttnParams p, const BatchDesc bd) {
                 report(p.dev_status, SD_DEV_BAD_PAGE);
             }
           }
-          const uint32_t have = (good >> sub) & 0xffu;
           const int valid = min(kTile, pc.L - (t0 - n * kTile));
           const uint32_t need = (1u << ((valid + kPage - 1) / kPage)) - 1u;
-          ok = __all_sync(0xffffffffu, wait_empty(b_empty, ring));
+          const uint32_t have = (good >> sub) & need;
+          const Ring ring = rings.get(turn);
+          const int at = turn * n_ring + ring.at;
+          ok = __all_sync(0xffffffffu, wait_empty(b_empty + turn * n_ring, ring));
           if (!ok) break;
-          uint8_t* dst = buf + ring.at * K::kTileBytes;
-          if (need & ~have) {   // ids out of range count as zeros: scales of 0
+          uint8_t* dst = buf + at * K::kSlotBytes;
+          if (need != have) {   // ids out of range count as zeros: scales of 0
 #pragma unroll 1
-            for (int e = lane; e < 8 * (K::kRecord / 16); e += 32)
-              if (((need & ~have) >> (e / (K::kRecord / 16))) & 1u) reinterpret_cast<uint4*>(dst)[e] = make_uint4(0, 0, 0, 0);
+            for (int e = lane; e < 8 * (int)(kBytes / 16); e += 32)
+              if (((need & ~have) >> (e / (kBytes / 16))) & 1u) reinterpret_cast<uint4*>(dst)[e] = make_uint4(0, 0, 0, 0);
             fence_async_smem();   // the slot's next contents come by another path
             __syncwarp();
           }
@@ -488,21 +518,26 @@ kv4_attn_kernel(const Kv4AttnParams p, const BatchDesc bd) {
 #pragma unroll
           for (int j = 0; j < 8; ++j) page[j] = __shfl_sync(0xffffffffu, ids, sub + j);
           if (elect_one()) {
-            mbar_expect_tx(bar(b_full + ring.at), (uint32_t)__popc(have & need) * (uint32_t)K::kRecord);
+            const uint32_t full = bar(b_full + at), to = smem_u32(dst);
+            mbar_expect_tx(full, (uint32_t)__popc(have) * kBytes);
+            if (have == 0xffu) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-              if (((have & need) >> j) & 1u)
-                bulk_record(smem_u32(dst) + j * K::kRecord, src + (size_t)page[j] * page_bytes, K::kRecord,
-                            bar(b_full + ring.at), policy);
+              for (int j = 0; j < 8; ++j) bulk_record(to + j * kBytes, src + (size_t)page[j] * page_bytes, kBytes, full, policy);
+            } else {
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                if ((have >> j) & 1u) bulk_record(to + j * kBytes, src + (size_t)page[j] * page_bytes, kBytes, full, policy);
+            }
           }
           __syncwarp();
-          ring.next(n_ring);
+          rings.next(turn, n_ring);
+          turn = turn + 1 == WG ? 0 : turn + 1;
         }
       }
       // After an abort no copy may still be landing when the CTA ends: wait, bounded, for both rounds of every slot.
       if (lane == 0 && *(volatile int*)&sm->abort) {
 #pragma unroll 1
-        for (int s = 0; s < 2 * n_ring; ++s) {
+        for (int s = 0; s < 2 * n_ring * WG; ++s) {
           const long long begin = clock64();
           while (!mbar_test(bar(b_full + (s >> 1)), (uint32_t)s & 1u) && clock64() - begin < kWaitCycles / 64) {
           }
@@ -510,8 +545,9 @@ kv4_attn_kernel(const Kv4AttnParams p, const BatchDesc bd) {
       }
     } else if (warp == kWarpQK) {
       // ---------------------------------------------------------- QK issuer
-      Ring s_ring, a_ring;
-      int np = 0;
+      Ring s_ring;
+      int np = 0, turn = 0;
+      uint32_t phase = 0;            // of a group's slots: a bit each
       bool ok = true;
       const uint64_t q_desc = sw128_desc(smem_u32(sQ), 16, 1024);
 #pragma unroll 1
@@ -522,39 +558,56 @@ kv4_attn_kernel(const Kv4AttnParams p, const BatchDesc bd) {
         const int nq = (min(p.hpc, p.group - pc.c * p.hpc) * n_nodes + 15) & ~15;
         const uint32_t idesc = f16_idesc(128, nq, 0, 0);
         ok = __all_sync(0xffffffffu, wait(B_Q, np));
+        const int end = pc.first + pc.tiles;
 #pragma unroll 1
-        for (int i = 0; i < pc.tiles && ok; ++i) {
+        for (int i = pc.first, n; i < end && ok; i += n) {
+          n = min(T, end - i);
           ok = __all_sync(0xffffffffu, wait_empty(B_SE, s_ring));
-          const uint32_t d = tmem + s_ring.at * NQ;
+          uint32_t d = tmem + s_ring.at * T * NQ;
 #pragma unroll 1
-          for (int ks = 0; ks < D / SW && ok; ++ks) {
-            ok = __all_sync(0xffffffffu, wait_full(B_AKF, a_ring));
-            if (!ok) break;
-            tc_fence_after();
-            const uint32_t a = tmem + K::kColA + a_ring.at * K::kSlotCols;
-            if (elect_one()) {
+          for (int j = 0; j < n && ok; ++j, d += NQ) {
+            const uint32_t a0 = tmem + K::kColA + turn * KA * K::kSlotCols;
+            const uint32_t full = bar(B_AKF + turn * KA), empty = bar(B_AKE + turn * KA);
+            const uint32_t odd = (phase >> turn) & 1u;
+#pragma unroll 1
+            for (int k = 0; k < K::KU; ++k) {
 #pragma unroll
-              for (int kk = 0; kk < SW / 16; ++kk) {
-                const int k16 = ks * (SW / 16) + kk;
-                umma_ta(d, a + kk * 8, q_desc + (((k16 >> 2) * NQ * 128 + (k16 & 3) * 32) >> 4), idesc, k16 > 0 ? 1u : 0u);
+              for (int s = 0; s < KA; ++s) {
+                wait4(full + 8 * s, K::KU % 2 == 0 ? k & 1 : odd ^ (k & 1), &sm->abort);
+                __syncwarp();
+                tc_fence_after();
+                if (elect_one()) {
+                  // a 64-dim block of Q^T is NQ rows of 128 bytes
+                  const int ks = k * KA + s;
+                  const uint64_t b = q_desc + (SW >= 64 ? ks * (SW / 64) * (NQ * 128 >> 4) : (ks >> 1) * (NQ * 128 >> 4) + (ks & 1) * 4);
+#pragma unroll
+                  for (int kk = 0; kk < SW / 16; ++kk) {
+                    if (s > 0 || kk > 0)
+                      umma_ta<1>(d, a0 + s * K::kSlotCols + kk * 8, b + (kk >> 2) * (NQ * 128 >> 4) + (kk & 3) * 2, idesc);
+                    else
+                      umma_ta<2>(d, a0, b, idesc, k > 0 ? 1u : 0u);
+                  }
+                  umma_commit(empty + 8 * s);
+                  if (s == KA - 1 && k == K::KU - 1 && j == n - 1) umma_commit(bar(B_SF + s_ring.at));
+                }
+                __syncwarp();
               }
-              umma_commit(bar(B_AKE + a_ring.at));
-              if (ks == D / SW - 1) umma_commit(bar(B_SF + s_ring.at));
             }
-            __syncwarp();
-            a_ring.next(KA);
+            ok = *(volatile int*)&sm->abort == 0;
+            phase ^= 1u << turn;
+            turn = turn + 1 == WG ? 0 : turn + 1;
           }
           s_ring.next(NS);
         }
       }
     } else {
       // ---------------------------------------------------------- PV issuer
-      Ring a_ring;
-      int it = 0;
+      int it = 0, turn = 0;
+      uint32_t phase = 0;
       bool ok = true;
-      // P: 8-column chunks of 128 token rows x 16 bytes; MN-major without a swizzle
-      const uint64_t p_desc0 = noswz_desc(smem_u32(sP), 128, kTile * 16);
-      const uint64_t p_desc1 = noswz_desc(smem_u32(sP + K::kPBytes), 128, kTile * 16);
+      // P: 8-column chunks of T x 128 token rows x 16 bytes; MN-major without a swizzle
+      const uint64_t p_desc0 = noswz_desc(smem_u32(sP), 128, T * kTile * 16);
+      const uint64_t p_desc1 = noswz_desc(smem_u32(sP + K::kPBytes), 128, T * kTile * 16);
 #pragma unroll 1
       for (int u = u_begin; u < u_end && ok;) {
         const Piece pc = piece_at(u);
@@ -562,30 +615,48 @@ kv4_attn_kernel(const Kv4AttnParams p, const BatchDesc bd) {
         const int n_nodes = bd.q_indptr[pc.b + 1] - bd.q_indptr[pc.b];
         const int nq = (min(p.hpc, p.group - pc.c * p.hpc) * n_nodes + 15) & ~15;
         const uint32_t idesc = f16_idesc(128, nq, 0, 1);
+        const int end = pc.first + pc.tiles;
 #pragma unroll 1
-        for (int i = 0; i < pc.tiles && ok; ++i, ++it) {
-          const int valid = pc.first + i == 0 ? n_nodes : min(kTile, pc.L - pc.t0(pc.first + i));
+        for (int i = pc.first, n; i < end && ok; i += n, ++it) {
+          n = min(T, end - i);
           ok = __all_sync(0xffffffffu, wait(B_PF + (it & 1), it >> 1));
-          const uint64_t p0 = it & 1 ? p_desc1 : p_desc0;
+          uint64_t b = it & 1 ? p_desc1 : p_desc0;
 #pragma unroll 1
-          for (int ts = 0; ts * SW < valid && ok; ++ts) {
+          for (int j = 0; j < n && ok; ++j, b += kTile) {
+            const int valid = i + j == 0 ? n_nodes : min(kTile, pc.L - pc.t0(i + j));
+            const uint32_t fresh = i == pc.first && j == 0 ? 0u : 1u;       // the piece's first products overwrite O
+            const uint32_t a0 = tmem + K::kColA + (KA * WG + turn * VA) * K::kSlotCols;
+            const uint32_t full = bar(B_AVF + turn * VA), empty = bar(B_AVE + turn * VA);
+            const uint32_t odd = (phase >> turn) & 1u;
+#pragma unroll 1
+            for (int k = 0; k < K::VU; ++k) {
 #pragma unroll
-            for (int mb = 0; mb < MH; ++mb) {
-              ok = ok && __all_sync(0xffffffffu, wait_full(B_AVF, a_ring));
-              if (!ok) break;
-              tc_fence_after();
-              const uint32_t a = tmem + K::kColA + KA * K::kSlotCols + a_ring.at * K::kSlotCols;
-              if (elect_one()) {
+              for (int s = 0; s < VA; ++s) {
+                wait4(full + 8 * s, K::VU % 2 == 0 ? k & 1 : odd ^ (k & 1), &sm->abort);
+                __syncwarp();
+                tc_fence_after();
+                // slot k VA + s: 128-dim block mb of SW tokens
+                const int mb = MH == 1 ? 0 : s, ts = MH == 1 ? k * VA + s : k;
+                const uint32_t d = tmem + K::kColO + mb * NQ, a = a0 + s * K::kSlotCols;
+                const int steps = (valid - ts * SW + 15) / 16;      // of 16 tokens that hold any
+                if (elect_one()) {
+                  const uint64_t bb = b + ts * SW;
+                  if (steps >= SW / 16) {
+                    umma_ta<2>(d, a, bb, idesc, ts > 0 ? 1u : fresh);
 #pragma unroll
-                for (int kk = 0; kk < SW / 16; ++kk)
-                  if (ts * SW + kk * 16 < valid)
-                    umma_ta(tmem + K::kColO + mb * NQ, a + kk * 8, p0 + (((ts * SW + kk * 16) * 16) >> 4), idesc,
-                            i > 0 || ts > 0 || kk > 0 ? 1u : 0u);
-                umma_commit(bar(B_AVE + a_ring.at));
+                    for (int kk = 1; kk < SW / 16; ++kk) umma_ta<1>(d, a + kk * 8, bb + kk * 16, idesc);
+                  } else {
+#pragma unroll 1
+                    for (int kk = 0; kk < steps; ++kk) umma_ta<2>(d, a + kk * 8, bb + kk * 16, idesc, ts > 0 || kk > 0 ? 1u : fresh);
+                  }
+                  umma_commit(empty + 8 * s);
+                }
+                __syncwarp();
               }
-              __syncwarp();
-              a_ring.next(VA);
             }
+            ok = *(volatile int*)&sm->abort == 0;
+            phase ^= 1u << turn;
+            turn = turn + 1 == WG ? 0 : turn + 1;
           }
           if (ok && elect_one()) umma_commit(bar(B_OD + (it & 1)));
           __syncwarp();
@@ -594,161 +665,171 @@ kv4_attn_kernel(const Kv4AttnParams p, const BatchDesc bd) {
     }
   } else if (warp >= kWarpWideK) {
     // ------------------------------------------------------------ the widening warps
-    if (kShare) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    // After an expired wait no other one waits, and they run through.
+    if (NG == 3) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;"); else asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     const bool is_k = warp < kWarpWideV;
     const int quarter = warp & 3, row = quarter * 32 + lane;
-    const uint32_t a_base = tmem + ((uint32_t)(quarter * 32) << 16) + K::kColA + (is_k ? 0 : KA * K::kSlotCols);
-    Ring ring, a_ring;
-    bool ok = true;
+    const int group = (warp - (is_k ? kWarpWideK : kWarpWideV)) >> 2;
+    const uint32_t a_base = tmem + ((uint32_t)(quarter * 32) << 16) + K::kColA + (is_k ? group * KA : KA * WG + group * VA) * K::kSlotCols;
+    const uint32_t a_full = bar(is_k ? B_AKF + group * KA : B_AVF + group * VA), a_empty = bar(is_k ? B_AKE + group * KA : B_AVE + group * VA);
+    const int n_ring = is_k ? KS : VS, b_full = (is_k ? B_KF : B_VF) + group * n_ring, b_empty = (is_k ? B_KE : B_VE) + group * n_ring;
+    const uint8_t* const buf = (is_k ? sK : sV) + group * n_ring * K::kSlotBytes;
+    Ring ring;
+    uint32_t odd = 0;             // parity of the group's tiles
+    auto slot_free = [&](int s, uint32_t parity) {
+      wait4(a_empty + 8 * s, parity ^ 1u, &sm->abort);
+      __syncwarp();
+      tc_fence_after();
+    };
     // A slot's lanes are stored: to the issuer.
-    auto store16 = [&](int at, const uint32_t (&x)[16]) { tmem_st16u(a_base + a_ring.at * K::kSlotCols + at * 16, x); };
-    auto slot_done = [&] {
+    auto slot_done = [&](int s) {
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar((is_k ? B_AKF : B_AVF) + a_ring.at));
-      a_ring.next(is_k ? KA : VA);
+      if (lane == 0) mbar_arrive(a_full + 8 * s);
     };
-    auto slot_free = [&] {
-      ok = __all_sync(0xffffffffu, wait_empty(is_k ? B_AKE : B_AVE, a_ring));
-      tc_fence_after();
-      return ok;
-    };
-    int vs_at = 0;
+    int turn = 0;      // whose turn the tile is
 #pragma unroll 1
-    for (int u = u_begin; u < u_end && ok;) {
+    for (int u = u_begin; u < u_end;) {
       const Piece pc = piece_at(u);
       u += pc.span;
       const int q0 = bd.q_indptr[pc.b], n_nodes = bd.q_indptr[pc.b + 1] - q0;
       const int seen = first_seen(pc.L);
 #pragma unroll 1
-      for (int i = 0; i < pc.tiles && ok; ++i) {
-        if (pc.first + i == 0) {
+      for (int i = pc.first; i < pc.first + pc.tiles; ++i) {
+        const bool draft = i == 0, mine = turn == group;
+        turn = turn + 1 == WG ? 0 : turn + 1;
+        if (!mine) continue;
+        if (draft) {
           // the draft block, bf16 as it is (what is no number there goes through the scores: zeros here, see `wild`)
-          if (is_k) {
-            const uint4* src = reinterpret_cast<const uint4*>(p.k_new + (long long)(q0 + min(row, n_nodes - 1)) * p.k_stride + pc.g * D);
 #pragma unroll 1
-            for (int ks = 0; ks < D / SW && ok; ++ks) {
-              if (!slot_free()) break;
-#pragma unroll
+          for (int n = 0; n < (is_k ? K::KU * KA : K::VU * VA); ++n) {
+            const int s = n % (is_k ? KA : VA), k = n / (is_k ? KA : VA);
+            slot_free(s, (is_k ? K::KU : K::VU) % 2 == 0 ? k & 1 : odd ^ (k & 1));
+            if (is_k) {
+              const uint4* src = reinterpret_cast<const uint4*>(p.k_new + (long long)(q0 + min(row, n_nodes - 1)) * p.k_stride + pc.g * D);
+#pragma unroll 1
               for (int h = 0; h < SW / 32; ++h) {
                 uint32_t x[16];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                   uint4 v = make_uint4(0, 0, 0, 0);
-                  if (row < n_nodes) v = __ldg(src + (ks * SW + h * 32) / 8 + e);
+                  if (row < n_nodes) v = __ldg(src + (n * SW + h * 32) / 8 + e);
                   x[4 * e] = v.x; x[4 * e + 1] = v.y; x[4 * e + 2] = v.z; x[4 * e + 3] = v.w;
                 }
-                store16(h, x);
+                tmem_st16u(a_base + s * K::kSlotCols + h * 16, x);
               }
-              slot_done();
-            }
-          } else {
-            const uint16_t* src = reinterpret_cast<const uint16_t*>(p.v_new) + (long long)q0 * p.v_stride + pc.g * D + row;
+            } else {
+              const int ts = n / MH, mb = n % MH;
+              const uint16_t* src = reinterpret_cast<const uint16_t*>(p.v_new) + (long long)q0 * p.v_stride + pc.g * D + mb * 128 + row;
 #pragma unroll 1
-            for (int ts = 0; ts * SW < n_nodes && ok; ++ts) {
-#pragma unroll 1
-              for (int mb = 0; mb < MH; ++mb) {
-                if (!slot_free()) break;
+              for (int h = 0; h < SW / 32 && ts * SW + h * 32 < n_nodes; ++h) {
+                uint32_t x[16];
 #pragma unroll
-                for (int h = 0; h < SW / 32; ++h) {
-                  uint32_t x[16];
-#pragma unroll
-                  for (int e = 0; e < 32; ++e) {
-                    const int n = ts * SW + h * 32 + e;
-                    uint32_t v = 0;
-                    if (n < n_nodes) v = __ldg(src + (long long)n * p.v_stride + mb * 128);
-                    if ((v & 0x7f80u) == 0x7f80u) v = 0;
-                    x[e >> 1] = e & 1 ? x[e >> 1] | v << 16 : v;
-                  }
-                  store16(h, x);
+                for (int e = 0; e < 32; ++e) {
+                  const int r = ts * SW + h * 32 + e;
+                  uint32_t v = 0;
+                  if (r < n_nodes) v = __ldg(src + (long long)r * p.v_stride);
+                  if ((v & 0x7f80u) == 0x7f80u) v = 0;
+                  x[e >> 1] = e & 1 ? x[e >> 1] | v << 16 : v;
                 }
-                slot_done();
+                tmem_st16u(a_base + s * K::kSlotCols + h * 16, x);
               }
-              if (!ok) break;
             }
+            slot_done(s);
           }
+          odd ^= 1u;
           continue;
         }
-        const int t0 = pc.t0(pc.first + i), valid = min(kTile, pc.L - t0);
-        ok = __all_sync(0xffffffffu, wait_full(is_k ? B_KF : B_VF, ring));
-        if (!ok) break;
+        const int t0 = pc.t0(i);
+        wait_full(b_full, ring);
+        __syncwarp();
         if (is_k) {
           // this thread's token, block after block of 32 dims (rolled: the roles' loops share an instruction cache)
-          const uint8_t* rec = sK + ring.at * K::kTileBytes + (row >> 4) * K::kRecord;
+          const uint8_t* rec = buf + ring.at * K::kSlotBytes + (row >> 4) * K::kPageStride;
           const uint8_t* words = rec + (row & 15) * 16;
           const uint16_t* sc = reinterpret_cast<const uint16_t*>(rec + kv4_codes(D) + (row & 15) * (D / 16));
-          bool bad = false;
+          uint32_t most = 0;
 #pragma unroll 1
-          for (int ks = 0; ks < D / SW; ++ks) {
-            if (!slot_free()) break;
+          for (int n = 0; n < K::KU * KA; ++n) {
+            const int s = n % KA, k = n / KA;
+            const uint32_t to = a_base + s * K::kSlotCols;
+            slot_free(s, K::KU % 2 == 0 ? k & 1 : odd ^ (k & 1));
 #pragma unroll 1
             for (int h = 0; h < SW / 32; ++h) {
               const uint4 w = *reinterpret_cast<const uint4*>(words);
-              const __nv_bfloat162 s = kv4_scale2(kv4_sane(*sc * 0x10001u, bad)), less = kv4_less(s);
+              uint32_t s1 = *sc & kKv4ScaleBits;
               words += kPage * 16;
               ++sc;
+              most = max(most, s1 & 0x7fffu);
+              s1 = (s1 & 0x7fffu) >= kKv4BadScale ? 0u : s1;
+              const __nv_bfloat162 sv = kv4_scale2(__byte_perm(s1, 0, 0x1010)), less = kv4_less(sv);
               const uint32_t* ww = reinterpret_cast<const uint32_t*>(&w);
               uint32_t x[16];
 #pragma unroll
-              for (int e = 0; e < 16; ++e) x[e] = kv4_pair(ww[e >> 2], e & 3, s, less);
-              store16(h, x);
+              for (int e = 0; e < 16; ++e) x[e] = kv4_pair(ww[e >> 2], e & 3, sv, less);
+              tmem_st16u(to + h * 16, x);
             }
-            slot_done();
+            slot_done(s);
           }
-          if (bad && row < valid && t0 + row >= seen) report(p.dev_status, SD_DEV_BAD_SCALE);
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(B_KE + ring.at));
+          if (most >= kKv4BadScale && t0 + row < pc.L && t0 + row >= seen) report(p.dev_status, SD_DEV_BAD_SCALE);
         } else {
           // this thread's dim (of each 128): the scales of its block of 32, token pair by token pair, are the warp's
-          const uint8_t* tile = sV + ring.at * K::kTileBytes;
-          const int slots = (valid + SW - 1) / SW * MH;
+          const uint8_t* pages = buf + ring.at * K::kSlotBytes;
+          const bool plain = t0 >= seen && t0 + kTile <= pc.L;
 #pragma unroll 1
-          for (int n = 0; n < slots; ++n) {
-            const int ts = n / MH, mb = n % MH;
-            const uint8_t* pages = tile + ts * (SW / 16) * K::kRecord;
-            uint2* const vs = sm->vs[quarter][vs_at];
-            vs_at ^= 1;
+          for (int n = 0; n < K::VU * VA; ++n) {
+            const int s = n % VA, k = n / VA, mb = n % MH, ts = n / MH;      // 128-dim block mb of SW tokens
+            const uint8_t* at = pages + ts * (SW / 16) * K::kPageStride;
+            uint2* const vs = sm->vs[group * 4 + quarter][s];
             if (SW == 64 || lane < SW / 2) {
-              // tokens that nobody sees count 0 (their records may hold anything)
-              uint32_t s2 = *reinterpret_cast<const uint32_t*>(pages + (lane >> 3) * K::kRecord + kv4_codes(D) +
+              uint32_t s2 = *reinterpret_cast<const uint32_t*>(at + (lane >> 3) * K::kPageStride + kv4_codes(D) +
                                                                (mb * 4 + quarter) * 32 + (lane & 7) * 4);
-              const int t = t0 + ts * SW + 2 * lane;
-              if (t >= pc.L || t < seen) s2 &= 0xffff0000u;
-              if (t + 1 >= pc.L || t + 1 < seen) s2 &= 0x0000ffffu;
-              bool bad = false;
-              s2 = kv4_sane(s2, bad);
-              if (bad) report(p.dev_status, SD_DEV_BAD_SCALE);
+              s2 &= kKv4ScaleBits | kKv4ScaleBits << 16;
+              if (!plain) {
+                // tokens that nobody sees count 0 (their records may hold anything)
+                const int t = t0 + ts * SW + 2 * lane;
+                if (t >= pc.L || t < seen) s2 &= 0xffff0000u;
+                if (t + 1 >= pc.L || t + 1 < seen) s2 &= 0x0000ffffu;
+              }
+              if (__vmaxu2(s2 & 0x7fff7fffu, kKv4BadScale - 1u | (kKv4BadScale - 1u) << 16) !=
+                  (kKv4BadScale - 1u | (kKv4BadScale - 1u) << 16)) {
+                bool bad = false;
+                s2 = kv4_sane(s2, bad);
+                report(p.dev_status, SD_DEV_BAD_SCALE);
+              }
               const __nv_bfloat162 less = kv4_less(kv4_scale2(s2));
               vs[lane] = make_uint2(s2, *reinterpret_cast<const uint32_t*>(&less));
             }
-            __syncwarp();
-            if (!slot_free()) break;
-            const uint8_t* words = pages + (mb * 128 + row) * 8;
+            slot_free(s, K::VU % 2 == 0 ? k & 1 : odd ^ (k & 1));
+            const uint8_t* words = at + (mb * 128 + row) * 8;
+            const uint4* sl_at = reinterpret_cast<const uint4*>(vs);
+            const uint32_t to = a_base + s * K::kSlotCols;
 #pragma unroll 1
-            for (int h = 0; h < SW / 32; ++h, words += 2 * K::kRecord) {
-              const uint2 w0 = *reinterpret_cast<const uint2*>(words), w1 = *reinterpret_cast<const uint2*>(words + K::kRecord);
+            for (int h = 0; h < SW / 32; ++h, words += 2 * K::kPageStride, sl_at += 8) {
+              const uint2 w0 = *reinterpret_cast<const uint2*>(words), w1 = *reinterpret_cast<const uint2*>(words + K::kPageStride);
               uint32_t x[16];
 #pragma unroll
               for (int e = 0; e < 16; e += 2) {
-                const uint4 sl = *reinterpret_cast<const uint4*>(&vs[h * 16 + e]);
+                const uint4 sl = sl_at[e >> 1];
                 const uint32_t word = e & 8 ? (e & 4 ? w1.y : w1.x) : (e & 4 ? w0.y : w0.x);
                 x[e] = kv4_pair(word, e & 3, kv4_scale2(sl.x), kv4_scale2(sl.y));
                 x[e + 1] = kv4_pair(word, (e & 3) + 1, kv4_scale2(sl.z), kv4_scale2(sl.w));
               }
-              store16(h, x);
+              tmem_st16u(to + h * 16, x);
             }
-            slot_done();
+            slot_done(s);
           }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(B_VE + ring.at));
         }
-        ring.next(is_k ? KS : VS);
+        odd ^= 1u;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(b_empty + ring.at));
+        ring.next(n_ring);
       }
     }
   } else {
     // ------------------------------------------------------------ softmax warps
-    if (kShare) asm volatile("setmaxnreg.inc.sync.aligned.u32 96;");
+    if (NG == 3) asm volatile("setmaxnreg.inc.sync.aligned.u32 112;"); else asm volatile("setmaxnreg.inc.sync.aligned.u32 136;");
     const int group = warp >> 2, quarter = warp & 3;
     const int row = quarter * 32 + lane;                       // token row of S; dim (mod 128) of O^T
     const uint32_t lane_addr = (uint32_t)(quarter * 32) << 16;
@@ -870,113 +951,143 @@ kv4_attn_kernel(const Kv4AttnParams p, const BatchDesc bd) {
       const float fac = p.scale * kLog2e;
       // Until a tile that every column sees something of has passed, columns may have no reference.
       bool settled = false;
+      const int end = pc.first + pc.tiles;
 #pragma unroll 1
-      for (int i = 0; i < pc.tiles; ++i, ++it) {
-        const bool draft = pc.first + i == 0;
-        const int t0 = pc.t0(pc.first + i);
-        const int valid = draft ? n_nodes : min(kTile, pc.L - t0);
-        const bool band = !draft && p.window > 0 && t0 < lo_root + kMaxNodes;
-        const bool masked = draft || valid < kTile || band;
-        // Which columns see this row, one bit each.
-        using Bits = typename BitsOf<CC>::type;
-        Bits vis = ~(Bits)0;
-        if (masked) {
-          vis = row < valid && !draft && !band ? ~(Bits)0 : 0;
-          if (row < valid && (draft || band)) {
-            // node by node, from the one of the group's first column: its columns see this row, or none of them does
-            int n = col0 / hpc, at = n * hpc - col0;       // the node's first column, less the group's
-            const Bits full = ((Bits)1 << hpc) - 1;
-            Bits bits = full >> -at;
-            if (draft) {
-              unsigned long long sees = n < n_nodes ? sm->anc[row] >> n : 0ull;
-#pragma unroll 1
-              for (; at < CC * 16 && sees != 0ull; sees >>= 1) {
-                vis |= sees & 1ull ? bits : (Bits)0;
-                at += hpc;
-                bits = full << (at & (8 * (int)sizeof(Bits) - 1));
-              }
-            } else {
-#pragma unroll 1
-              for (; at < CC * 16 && n < n_nodes; ++n) {
-                vis |= t0 + row >= lo_root + sm->depth[n] ? bits : (Bits)0;
-                at += hpc;
-                bits = full << (at & (8 * (int)sizeof(Bits) - 1));
-              }
-            }
-          }
-        }
-        // the bias' distance is counted from the root: a node's depth shifts all its scores alike (see the log-sum-exp)
-        const float rel = draft ? (row < n_nodes ? (float)sm->depth[row] : 0.f) : (float)(t0 + row - pc.L);
-        const bool nan_row = draft && row < n_nodes && sm->wild[row] != 0;
-        // Scores that are more than a multiple of the product are formed once and put back in its place.
+      for (int i = pc.first, subs; i < end; i += subs, ++it) {
+        const bool fresh = i == pc.first;
+        subs = min(T, end - i);
+        const bool band = p.window > 0 && pc.t0(i + subs - 1) < lo_root + kMaxNodes;
+        const bool masked = i <= 1 && (i == 0 || pc.L - pc.t0(1) < kTile) || band;
+        // Scores that are more than a multiple of the product are formed first and put back in its place.
         const bool formed = MOD || masked;
         const float mul = formed ? 1.f : fac;
         wait_full(B_SF, s_ring);
         __syncwarp();
         tc_fence_after();
-        const uint32_t s_addr = tmem + lane_addr + s_ring.at * NQ + col0;
-        // ---- first reading: the chunks where a weight would pass 2^kRise
-        uint32_t missed = 0;
-#pragma unroll
-        for (int c = 0; c < CC; ++c) {
-          if (c >= mine) break;
-          float a[16];
-          tmem_ld16(s_addr + c * 16, a);
-          tmem_wait_ld();
-          if (formed) {
-            if (MOD && p.softcap > 0.f) {
-              // c tanh(x / c) = c - 2 c / (1 + 2^(2 log2e x / c))
-              const float cl = p.softcap * kLog2e, ky = fac * p.cap_exp;
-#pragma unroll
-              for (int e = 0; e < 16; e += 2) {
-                const float2 y = mul2(make_float2(a[e], a[e + 1]), make_float2(ky, ky));
-                const float2 d = add2(make_float2(fast_exp2(y.x), fast_exp2(y.y)), make_float2(1.f, 1.f));
-                const float2 s = fma2(make_float2(fast_rcp(d.x), fast_rcp(d.y)), make_float2(-2.f * cl, -2.f * cl), make_float2(cl, cl));
-                a[e] = s.x;
-                a[e + 1] = s.y;
-              }
-            } else {
-#pragma unroll
-              for (int e = 0; e < 16; ++e) a[e] *= fac;
-            }
-            if (MOD) {
-#pragma unroll
-              for (int e = 0; e < 16; e += 2) {
-                const float2 sl = *reinterpret_cast<const float2*>(&sm->slope[col0 + c * 16 + e]);
-                const float2 s = fma2(sl, make_float2(rel, rel), make_float2(a[e], a[e + 1]));
-                a[e] = s.x;
-                a[e + 1] = s.y;
+        const uint32_t s_addr = tmem + lane_addr + s_ring.at * T * NQ + col0;
+        if (formed) {
+#pragma unroll 1
+          for (int j = 0; j < subs; ++j) {
+            const bool draft = i + j == 0;
+            const int t0 = pc.t0(i + j), valid = draft ? n_nodes : min(kTile, pc.L - t0);
+            // Which columns see this row, one bit each.
+            using Bits = typename BitsOf<CC>::type;
+            Bits vis = row < valid && !draft && !band ? ~(Bits)0 : 0;
+            if (row < valid && (draft || band)) {
+              // node by node, from the one of the group's first column: its columns see this row, or none of them does
+              int n = col0 / hpc, at = n * hpc - col0;       // the node's first column, less the group's
+              const Bits full = ((Bits)1 << hpc) - 1;
+              Bits bits = full >> -at;
+              unsigned long long sees = draft && n < n_nodes ? sm->anc[row] >> n : 0ull;
+#pragma unroll 1
+              for (; at < CC * 16 && n < n_nodes; ++n, sees >>= 1) {
+                vis |= (draft ? (sees & 1ull) != 0ull : t0 + row >= lo_root + sm->depth[n]) ? bits : (Bits)0;
+                at += hpc;
+                bits = full << (at & (8 * (int)sizeof(Bits) - 1));
               }
             }
-            if (masked) {
-              const uint32_t bits = (uint32_t)(vis >> (c * 16));
+            // the bias' distance is counted from the root: a node's depth shifts all its scores alike (see the log-sum-exp)
+            const float rel = draft ? (row < n_nodes ? (float)sm->depth[row] : 0.f) : (float)(t0 + row - pc.L);
+            const bool nan_row = draft && row < n_nodes && sm->wild[row] != 0;
+#pragma unroll 1
+            for (int c = 0; c < mine; ++c) {
+              float a[16];
+              tmem_ld16(s_addr + j * NQ + c * 16, a);
+              tmem_wait_ld();
+              if (MOD && p.softcap > 0.f) {
+                // c tanh(x / c) = c - 2 c / (1 + 2^(2 log2e x / c))
+                const float cl = p.softcap * kLog2e, ky = fac * p.cap_exp;
 #pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                const float s = nan_row ? __int_as_float(0x7fc00000) : a[e];
-                a[e] = (bits >> e) & 1u ? s : -INFINITY;
+                for (int e = 0; e < 16; e += 2) {
+                  const float2 y = mul2(make_float2(a[e], a[e + 1]), make_float2(ky, ky));
+                  const float2 d = add2(make_float2(fast_exp2(y.x), fast_exp2(y.y)), make_float2(1.f, 1.f));
+                  const float2 s = fma2(make_float2(fast_rcp(d.x), fast_rcp(d.y)), make_float2(-2.f * cl, -2.f * cl), make_float2(cl, cl));
+                  a[e] = s.x;
+                  a[e + 1] = s.y;
+                }
+              } else {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) a[e] *= fac;
               }
+              if (MOD) {
+#pragma unroll
+                for (int e = 0; e < 16; e += 2) {
+                  const float2 sl = *reinterpret_cast<const float2*>(&sm->slope[col0 + c * 16 + e]);
+                  const float2 s = fma2(sl, make_float2(rel, rel), make_float2(a[e], a[e + 1]));
+                  a[e] = s.x;
+                  a[e + 1] = s.y;
+                }
+              }
+              if (masked) {
+                const uint32_t bits = (uint32_t)(vis >> (c * 16));
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                  const float s = nan_row ? __int_as_float(0x7fc00000) : a[e];
+                  a[e] = (bits >> e) & 1u ? s : -INFINITY;
+                }
+              }
+              tmem_st16(s_addr + j * NQ + c * 16, a);
             }
-            tmem_st16(s_addr + c * 16, a);
           }
-          float top = -INFINITY;
+          tmem_wait_st();
+        }
+        // ---- the weights, on the assumption that no warp of the group has to move a reference; a chunk where one of this
+        // warp's would pass 2^kRise waits for that
+        uint32_t missed = 0;
+        uint8_t* const p_row = sP + (it & 1) * K::kPBytes + c_first * 2 * T * kTile * 16 + row * 16;
+        auto scored = [&](int c, const float (&a)[16], float (&d)[16]) {     // exponents; their maximum
+          float most = -INFINITY;
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const float4 m = *reinterpret_cast<const float4*>(&sm->m[col0 + c * 16 + 4 * k]);
             const float2 d0 = fma2(make_float2(a[4 * k], a[4 * k + 1]), make_float2(mul, mul), make_float2(m.x, m.y));
             const float2 d1 = fma2(make_float2(a[4 * k + 2], a[4 * k + 3]), make_float2(mul, mul), make_float2(m.z, m.w));
-            top = fmaxf(fmaxf(top, fmaxf(d0.x, d0.y)), fmaxf(d1.x, d1.y));
+            d[4 * k] = d0.x; d[4 * k + 1] = d0.y; d[4 * k + 2] = d1.x; d[4 * k + 3] = d1.y;
+            most = fmaxf(fmaxf(most, fmaxf(d0.x, d0.y)), fmaxf(d1.x, d1.y));
           }
-          missed |= top > kRise ? 1u << c : 0u;
-        }
-        if (formed) tmem_wait_st();
+          return most;
+        };
+        auto weigh = [&](float2 (&total)[8], int j, int c, const float (&d)[16], float add) {
+          uint32_t w[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const float2 e = make_float2(fast_exp2(d[2 * k]), fast_exp2(d[2 * k + 1]));
+            total[k] = fma2(e, make_float2(add, add), total[k]);
+            const __nv_bfloat162 h = __floats2bfloat162_rn(e.x, e.y);
+            w[k] = *reinterpret_cast<const uint32_t*>(&h);
+          }
+          uint8_t* at = p_row + j * kTile * 16 + c * 2 * T * kTile * 16;
+          *reinterpret_cast<uint4*>(at) = make_uint4(w[0], w[1], w[2], w[3]);
+          *reinterpret_cast<uint4*>(at + T * kTile * 16) = make_uint4(w[4], w[5], w[6], w[7]);
+        };
         const uint32_t all = (1u << mine) - 1u;
-        if (__any_sync(0xffffffffu, missed != 0u)) missed = __reduce_or_sync(0xffffffffu, missed);
-        if (!settled) missed = all;
+        // (into the buffer that the PV before the last has left)
+        if (it >= 2) spin(B_OD + (it & 1), (it >> 1) - 1);
+        if (settled) {
+#pragma unroll 1
+          for (int j = 0; j < subs; ++j) {
+#pragma unroll
+            for (int c = 0; c < CC; ++c) {
+              if (c >= mine) break;
+              float a[16], d[16];
+              tmem_ld16(s_addr + j * NQ + c * 16, a);
+              tmem_wait_ld();
+              if (__any_sync(0xffffffffu, scored(c, a, d) > kRise)) missed |= 1u << (j * CC + c);
+              else weigh(sum[c], j, c, d, 1.f);
+            }
+          }
+        } else {
+          missed = 0xffffffffu;
+        }
+        // chunks of any tile
+        uint32_t chunks = missed;
+#pragma unroll
+        for (int j = 1; j < T; ++j) chunks |= missed >> (j * CC);
         if (lane == 0) {
-          sm->flag[group][it & 1][quarter] = (int)missed;
+          sm->flag[group][it & 1][quarter] = (int)(chunks & all);
           mbar_arrive(bar(B_G + group));
         }
-        settled = settled || draft || !band;
+        settled = settled || i == 0 || !band;
         spin(B_G + group, it);
         const int4 fl = *reinterpret_cast<const int4*>(sm->flag[group][it & 1]);
         const uint32_t todo = (uint32_t)(fl.x | fl.y | fl.z | fl.w);     // chunks whose references move
@@ -985,11 +1096,16 @@ kv4_attn_kernel(const Kv4AttnParams p, const BatchDesc bd) {
 #pragma unroll
           for (int c = 0; c < CC; ++c) {
             if ((todo >> c) & 1u) {
-              float a[16];
-              tmem_ld16(s_addr + c * 16, a);
-              tmem_wait_ld();
-              const float mx = warp_max16(a, lane) * mul;
-              if (lane < 16) sm->red[quarter][col0 + c * 16 + lane] = mx;
+              float mx = -INFINITY;
+#pragma unroll 1
+              for (int j = 0; j < subs; ++j) {
+                float a[16];
+                tmem_ld16(s_addr + j * NQ + c * 16, a);
+                tmem_wait_ld();
+                const float x = warp_max16(a, lane);
+                mx = x != x ? x : fmaxf(mx, x);      // a column of NaN stays one
+              }
+              if (lane < 16) sm->red[quarter][col0 + c * 16 + lane] = mx * mul;
             }
           }
           sync_group();
@@ -1004,16 +1120,16 @@ kv4_attn_kernel(const Kv4AttnParams p, const BatchDesc bd) {
           }
           sync_group();
           // O belongs to the previous tile's PV until it has finished
-          if (i > 0) spin(B_OD + ((it - 1) & 1), (it - 1) >> 1);
+          if (!fresh) spin(B_OD + ((it - 1) & 1), (it - 1) >> 1);
           tc_fence_after();
 #pragma unroll
           for (int c = 0; c < CC; ++c) {
-            if (i == 0 || !((todo >> c) & 1u)) continue;
+            if (!((todo >> c) & 1u)) continue;
 #pragma unroll
             for (int e = 0; e < 8; ++e)
               sum[c][e] = mul2(sum[c][e], *reinterpret_cast<const float2*>(&sm->alpha[col0 + c * 16 + 2 * e]));
 #pragma unroll 1
-            for (int mb = 0; mb < MH; ++mb) {
+            for (int mb = 0; mb < (fresh ? 0 : MH); ++mb) {
               float v[16];
               const uint32_t ad = tmem + lane_addr + K::kColO + mb * NQ + col0 + c * 16;
               tmem_ld16(ad, v);
@@ -1024,33 +1140,19 @@ kv4_attn_kernel(const Kv4AttnParams p, const BatchDesc bd) {
             }
           }
           tmem_wait_st();
-        }
-        // ---- second reading: the weights, into the buffer that the PV before the last has left
-        if (it >= 2) spin(B_OD + (it & 1), (it >> 1) - 1);
-        uint8_t* const p_row = sP + (it & 1) * K::kPBytes + row * 16;
+          // the weights of these chunks; sums have them already where this warp did not wait
+#pragma unroll 1
+          for (int j = 0; j < subs; ++j) {
 #pragma unroll
-        for (int c = 0; c < CC; ++c) {
-          if (c >= mine) break;
-          float a[16];
-          tmem_ld16(s_addr + c * 16, a);
-          tmem_wait_ld();
-          uint32_t w[8];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float4 m = *reinterpret_cast<const float4*>(&sm->m[col0 + c * 16 + 4 * k]);
-            const float2 d0 = fma2(make_float2(a[4 * k], a[4 * k + 1]), make_float2(mul, mul), make_float2(m.x, m.y));
-            const float2 d1 = fma2(make_float2(a[4 * k + 2], a[4 * k + 3]), make_float2(mul, mul), make_float2(m.z, m.w));
-            const float2 e0 = make_float2(fast_exp2(d0.x), fast_exp2(d0.y));
-            const float2 e1 = make_float2(fast_exp2(d1.x), fast_exp2(d1.y));
-            sum[c][2 * k] = add2(sum[c][2 * k], e0);
-            sum[c][2 * k + 1] = add2(sum[c][2 * k + 1], e1);
-            const __nv_bfloat162 h0 = __floats2bfloat162_rn(e0.x, e0.y), h1 = __floats2bfloat162_rn(e1.x, e1.y);
-            w[2 * k] = *reinterpret_cast<const uint32_t*>(&h0);
-            w[2 * k + 1] = *reinterpret_cast<const uint32_t*>(&h1);
+            for (int c = 0; c < CC; ++c) {
+              if (!((todo >> c) & 1u)) continue;
+              float a[16], d[16];
+              tmem_ld16(s_addr + j * NQ + c * 16, a);
+              tmem_wait_ld();
+              scored(c, a, d);
+              weigh(sum[c], j, c, d, (missed >> (j * CC + c)) & 1u ? 1.f : 0.f);
+            }
           }
-          uint8_t* at = p_row + (c_first + c) * 2 * kTile * 16;
-          *reinterpret_cast<uint4*>(at) = make_uint4(w[0], w[1], w[2], w[3]);
-          *reinterpret_cast<uint4*>(at + kTile * 16) = make_uint4(w[4], w[5], w[6], w[7]);
         }
         tc_fence_before();
         fence_async_smem();
@@ -1140,7 +1242,7 @@ kv4_attn_kernel(const Kv4AttnParams p, const BatchDesc bd) {
   if (tid == 0 && sm->abort) report(p.dev_status, SD_DEV_TIMEOUT);
   if (warp == kWarpQK) {
     tc_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(K::kTmem));
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(512));
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
