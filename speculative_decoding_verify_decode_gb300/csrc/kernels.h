@@ -287,6 +287,7 @@ struct Kv4AttnParams {
   float* o_part;             // [piece + segment][nq][dim] partial outputs
   float* lse_part;           // [piece + segment][nq] base-2 log-sum-exps
 };
+constexpr int kv4_ctas(int nq, int dim) { return nq == 16 && dim == 256 ? 2 : 1; }   // of the attention, per SM
 size_t kv4_attn_workspace(int hq, int hkv, int dim, const BatchDesc& bd);
 cudaError_t launch_kv4_attn(Kv4AttnParams p, const BatchDesc& bd, cudaStream_t st);
 

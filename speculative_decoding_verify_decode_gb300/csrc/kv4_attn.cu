@@ -12,8 +12,9 @@ namespace {
 struct Kv4Plan {
   int hpc, hparts;   // query heads of a KV group per CTA, and CTA parts per group
   int nq;            // query columns of the kernel instance
+  int ctas;          // of it per SM
 };
-Kv4Plan kv4_plan(int group, int max_nodes) {
+Kv4Plan kv4_plan(int group, int max_nodes, int dim) {
   Kv4Plan pl;
   pl.hparts = 1;
   while ((group + pl.hparts - 1) / pl.hparts * max_nodes > 144) ++pl.hparts;
@@ -21,25 +22,26 @@ Kv4Plan kv4_plan(int group, int max_nodes) {
   pl.hparts = (group + pl.hpc - 1) / pl.hpc;
   const int cols = pl.hpc * max_nodes;
   pl.nq = cols <= 16 ? 16 : cols <= 48 ? 48 : cols <= 96 ? 96 : 144;
+  pl.ctas = kv4_ctas(pl.nq, dim);
   return pl;
 }
 
 }  // namespace
 
 size_t kv4_attn_workspace(int hq, int hkv, int dim, const BatchDesc& bd) {
-  const Kv4Plan pl = kv4_plan(hq / hkv, bd.max_nodes);
-  return layout_of(pl.nq, 1, pl.hparts, hkv, dim, bd, sm_count()).total;
+  const Kv4Plan pl = kv4_plan(hq / hkv, bd.max_nodes, dim);
+  return layout_of(pl.nq, pl.ctas, pl.hparts, hkv, dim, bd, sm_count()).total;
 }
 
 cudaError_t launch_kv4_attn(Kv4AttnParams p, const BatchDesc& bd, cudaStream_t st) {
   const bool mod = p.softcap > 0.f || p.slopes != nullptr;
-  const Kv4Plan pl = kv4_plan(p.group, bd.max_nodes);
+  const Kv4Plan pl = kv4_plan(p.group, bd.max_nodes, p.dim);
   p.hpc = pl.hpc;
   p.hparts = pl.hparts;
   p.nq = pl.nq;
   const int sms = sm_count();
-  p.grid = sms;
-  const Layout l = layout_of(pl.nq, 1, pl.hparts, p.hkv, p.dim, bd, sms);
+  p.grid = sms * pl.ctas;
+  const Layout l = layout_of(pl.nq, pl.ctas, pl.hparts, p.hkv, p.dim, bd, sms);
   char* ws = static_cast<char*>(p.workspace);
   p.cum = reinterpret_cast<int*>(ws);
   p.o_part = reinterpret_cast<float*>(ws + l.o);

@@ -78,20 +78,25 @@ struct Kv4 {
   static constexpr int NQ = NG * CC * 16;                 // query columns
   // Groups of four warps that widen K, and as many that widen V, tile by tile in turn; each has rings of its own (what is
   // counted below), so that no barrier has a user that passes some of its phases by.
-  static constexpr int WG = NG == 1 ? 2 : 1;
+  // Single tokens: half a CTA's columns, and where a tile is large (256 dims) two CTAs, of which one works while the other
+  // goes from piece to piece (64 sequences of 1 to 16384 tokens 236 -> 213 us, one of 512 tokens 12.4 -> 11.4); of 128
+  // dims one CTA with two groups is faster (64 sequences of 1 to 32768 tokens 427 us against 463).
+  static constexpr int kCtas = kv4_ctas(NQ, D);
+  static constexpr int WG = NG == 1 && kCtas == 1 ? 2 : 1;
   static constexpr int kWarps = NG * 4, kThreads = (kWarps + WG * 8 + 4) * 32;
   using Small = Kv4Small<NQ, WG, MOD>;
-  static constexpr int kSmemBytes = 232448;               // dynamic shared memory a CTA can have
+  static constexpr int kSmemBytes = kCtas == 2 ? 115712 : 232448;   // dynamic shared memory a CTA can have
+  static constexpr int kTmem = 512 / kCtas;
   static constexpr int MH = D / 128;                      // 128-dim blocks
   // Tiles that pass the softmax together: what a turn costs beyond them (barriers, the references' check, bookkeeping)
   // is as much as sixteen columns of a tile or two.
-  static constexpr int T = NQ == 16 ? 4 : NQ == 48 ? 2 : 1;
+    static constexpr int T = NQ == 16 && kCtas == 1 ? 4 : NQ <= 48 ? 2 : 1;
   static constexpr int NS = NQ <= 96 ? 2 : 1;             // S buffers in tensor memory
   // Widened operands: slots of SW elements a lane, two to a column.
   static constexpr int SW = NQ == 144 ? 32 : 64;
   static constexpr int kSlotCols = SW / 2;
   static constexpr int kColO = NS * T * NQ, kColA = kColO + MH * NQ;
-  static constexpr int kSlotsLeft = (512 - kColA) / kSlotCols / WG;
+  static constexpr int kSlotsLeft = (kTmem - kColA) / kSlotCols / WG;
   static constexpr int KA = kSlotsLeft / 2 > 1 ? 2 : 1, VA = 2;
   // A tile takes the ring round KU (VU) times: which slot, and which phase of it, is known without counting.
   static constexpr int KU = D / SW / KA, VU = kTile / SW * MH / VA;
@@ -107,7 +112,7 @@ struct Kv4 {
   static constexpr size_t kRingBytes = (size_t)(kJoint ? KS : KS + VS) * WG * kSlotBytes;
   static constexpr size_t kSmem = (size_t)kQBytes + 2 * kPBytes + kRingBytes + sizeof(Small);
   static_assert(KS * WG >= 2 && VS * WG >= 2, "rings of two tiles at least");
-  static_assert(kColA + WG * (KA + VA) * kSlotCols <= 512, "tensor memory");
+  static_assert(kColA + WG * (KA + VA) * kSlotCols <= kTmem, "tensor memory");
   static_assert(KU * KA * SW == D && VU * VA * SW == kTile * MH && (MH == 1 || MH == VA), "slots of a tile");
   static_assert(kSmem <= (size_t)kSmemBytes, "shared memory over 227 KB");
 };
@@ -239,7 +244,7 @@ struct Piece {
 };
 
 template <int D, int NG, int CC, bool MOD>
-__global__ void __launch_bounds__((NG + (NG == 1 ? 4 : 2) + 1) * 128, 1)
+__global__ void __launch_bounds__(Kv4<D, NG, CC, MOD>::kThreads, Kv4<D, NG, CC, MOD>::kCtas)
 kv4_attn_kernel(const Kv4AttnParams p, const BatchDesc bd) {
   using K = Kv4<D, NG, CC, MOD>;
   constexpr int NQ = K::NQ, MH = K::MH, NS = K::NS, KS = K::KS, VS = K::VS, KA = K::KA, VA = K::VA, SW = K::SW, WG = K::WG,
@@ -366,7 +371,7 @@ kv4_attn_kernel(const Kv4AttnParams p, const BatchDesc bd) {
   }
   if (warp == kWarpQK) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sm->tmem)),
-                 "n"(512));
+                 "n"(K::kTmem));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
   tc_fence_before();
@@ -455,7 +460,8 @@ kv4_attn_kernel(const Kv4AttnParams p, const BatchDesc bd) {
   // The block is launched with 61440 registers (768 x 80, 640 x 96): the softmax warps take 112 (three groups) or 136 each,
   // the widening ones 56 or 72, the others 32 or 56.
   if (warp >= kWarpK) {
-    if (NG == 3) asm volatile("setmaxnreg.dec.sync.aligned.u32 32;"); else asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if (K::kCtas == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    else if (NG == 3) asm volatile("setmaxnreg.dec.sync.aligned.u32 32;"); else asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (warp <= kWarpV) {
       // ---------------------------------------------------------- producers (where the ring is joint, the first alone)
       // Page ids come a group of four tiles at a time (lane l: page l % 8 of the group's l / 8), two groups ahead of
@@ -666,6 +672,7 @@ kv4_attn_kernel(const Kv4AttnParams p, const BatchDesc bd) {
   } else if (warp >= kWarpWideK) {
     // ------------------------------------------------------------ the widening warps
     // After an expired wait no other one waits, and they run through.
+    if (K::kCtas == 2) { } else
     if (NG == 3) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;"); else asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     const bool is_k = warp < kWarpWideV;
     const int quarter = warp & 3, row = quarter * 32 + lane;
@@ -829,7 +836,8 @@ kv4_attn_kernel(const Kv4AttnParams p, const BatchDesc bd) {
     }
   } else {
     // ------------------------------------------------------------ softmax warps
-    if (NG == 3) asm volatile("setmaxnreg.inc.sync.aligned.u32 112;"); else asm volatile("setmaxnreg.inc.sync.aligned.u32 136;");
+    if (K::kCtas == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 88;");
+    else if (NG == 3) asm volatile("setmaxnreg.inc.sync.aligned.u32 112;"); else asm volatile("setmaxnreg.inc.sync.aligned.u32 136;");
     const int group = warp >> 2, quarter = warp & 3;
     const int row = quarter * 32 + lane;                       // token row of S; dim (mod 128) of O^T
     const uint32_t lane_addr = (uint32_t)(quarter * 32) << 16;
@@ -1242,7 +1250,7 @@ kv4_attn_kernel(const Kv4AttnParams p, const BatchDesc bd) {
   if (tid == 0 && sm->abort) report(p.dev_status, SD_DEV_TIMEOUT);
   if (warp == kWarpQK) {
     tc_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(512));
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(K::kTmem));
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }

@@ -4,9 +4,9 @@
 // Append.  Per block of 32 dims of a row: m, the value largest in magnitude;
 // s = m / -8 in 5 bits; c = rint(x / s) + 8.  x / s is a quotient of an 8-bit and a
 // 5-bit number, so it is either exactly half way between two integers or at
-// least 2^-13 away from that: the product with the rounded reciprocal, rounded to a
-// multiple of 2^-16, is right in both cases, and no division is needed (its
-// dozen instructions for each of a prompt's values would take longer than their bytes).
+// least 2^-13 away from that: the product with an approximate reciprocal (off by 2^-20 at most), rounded to a
+// multiple of 2^-16, is right in both cases, and no division is needed.  Two values share each step: the maxima are of
+// 16-bit pairs, the roundings of fp32 pairs.
 //
 // One warp owns one (layer, K or V, page, KV head): the page's new rows are
 // in its registers, so bytes are read once, and V's words, which hold eight
@@ -59,22 +59,36 @@ __device__ __forceinline__ uint32_t tamed(uint32_t two, uint32_t mag) {
   }
   return r;
 }
+// Magnitudes beyond 8 times the largest scale become the largest that it reaches.
+__device__ __forceinline__ uint32_t reached(uint32_t two) {
+  const uint32_t top = kKv4BadScale - 8u + (3u << 7);     // 8 * 1.3125 * 2^123
+  return (two & 0x80008000u) | __vminu2(two & 0x7fff7fffu, top | top << 16);
+}
 __device__ __forceinline__ bool wild(const uint4 x) {   // a NaN or an infinity among eight
   const uint32_t e = 0x7f807f80u;
   return (__vcmpeq2(x.x & e, e) | __vcmpeq2(x.y & e, e) | __vcmpeq2(x.z & e, e) | __vcmpeq2(x.w & e, e)) != 0u;
 }
 
-// The code of x as the low bits of a float's: 2^23 + c.  inv: 1 / s, rounded (0 for s = 0: the code is 8).
-__device__ __forceinline__ uint32_t code_bits(float x, float inv) {
-  // 200 + q has multiples of 2^-16; q + 8 is exact, 2^23 + (q + 8) rounds to even
-  const float q = __fadd_rn(__fadd_rn(__fmul_rn(x, inv), 200.f), -192.f);
-  return __float_as_uint(__fadd_rn(fminf(fmaxf(q, 0.f), 15.f), 8388608.f));
+// Codes of a pair of values, one in each half.  inv: 1 / s (0 for s = 0: both codes are 8).  200 + q has multiples of
+// 2^-16, which leaves a tie one; that plus 2^23 - 192 is 2^23 + (q + 8) rounded to even.  |q| <= 8.25, so what there is to
+// keep within 0..15 is 16.
+__device__ __forceinline__ uint32_t codes2(uint32_t two, float inv) {
+  const float2 x = make_float2(__uint_as_float(two << 16), __uint_as_float(two & 0xffff0000u));
+  uint64_t q, c;
+  const float2 k200 = make_float2(200.f, 200.f), k23 = make_float2(8388416.f, 8388416.f), f = make_float2(inv, inv);
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(q) : "l"(*reinterpret_cast<const uint64_t*>(&x)),
+      "l"(*reinterpret_cast<const uint64_t*>(&f)), "l"(*reinterpret_cast<const uint64_t*>(&k200)));
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(c) : "l"(q), "l"(*reinterpret_cast<const uint64_t*>(&k23)));
+  return __vminu2(__byte_perm((uint32_t)c, (uint32_t)(c >> 32), 0x5410), 0x000f000fu);
 }
-constexpr uint32_t kCodeBias = 0x4b000000u;   // 2^23
+__device__ __forceinline__ float fast_rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 
-// (|s| is 2^-103 to 2^124, so 1 / s is a normal number; |x| <= 8.25 |s|, or 24.5 |s| at the largest scale.)
 template <int D>
-__global__ void __launch_bounds__(kRowsThreads, 5) kv4_append_kernel(const Kv4RowsParams p, const int window) {
+__global__ void __launch_bounds__(kRowsThreads, 4) kv4_append_kernel(const Kv4RowsParams p, const int window) {
   constexpr int kLanes = D / 8;            // lanes per row (8 values each)
   constexpr int kRowsAtOnce = 32 / kLanes; // rows a warp touches per step
   constexpr int kSteps = kPage / kRowsAtOnce;
@@ -134,6 +148,12 @@ __global__ void __launch_bounds__(kRowsThreads, 5) kv4_append_kernel(const Kv4Ro
     }
     uint8_t* const rec = p.cache[layer] + (((size_t)page * p.heads + head) * 2 + (is_v ? 1 : 0)) * kv4_record(D);
     uint16_t* const scales = reinterpret_cast<uint16_t*>(rec + kv4_codes(D));
+    uint4 old[4];                          // V: what a page that stays in part holds
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      old[e] = make_uint4(0, 0, 0, 0);
+      if (is_v && n < kPage && sub == 0) old[e] = reinterpret_cast<const uint4*>(rec + col * 64)[e];
+    }
     uint32_t acc[2][8];                    // V: the words of this lane's dims
 #pragma unroll
     for (int h = 0; h < 2; ++h)
@@ -142,40 +162,49 @@ __global__ void __launch_bounds__(kRowsThreads, 5) kv4_append_kernel(const Kv4Ro
 #pragma unroll
     for (int k = 0; k < kSteps; ++k) {
       const int token = k * kRowsAtOnce + sub;
+      // (the same for the whole warp: nobody has a row of this step)
+      if (k * kRowsAtOnce + kRowsAtOnce <= first || k * kRowsAtOnce >= first + n) continue;
       const bool mine = token >= first && token < first + n;
-      uint32_t key = top_key(v[k], (lane & 3) * 8);
-      key = max(key, __shfl_xor_sync(0xffffffffu, key, 1));
-      key = max(key, __shfl_xor_sync(0xffffffffu, key, 2));
-      if (wild(v[k])) {
-        any_wild = true;
-        v[k] = make_uint4(tamed(v[k].x, key >> 6), tamed(v[k].y, key >> 6), tamed(v[k].z, key >> 6), tamed(v[k].w, key >> 6));
+      // The largest of the block's values and of their negatives, as integers, where one of the two is above the other.
+      const uint32_t flip = 0x80008000u;
+      uint32_t up = __vmaxs2(__vmaxs2(v[k].x, v[k].y), __vmaxs2(v[k].z, v[k].w));
+      uint32_t down = __vmaxs2(__vmaxs2(v[k].x ^ flip, v[k].y ^ flip), __vmaxs2(v[k].z ^ flip, v[k].w ^ flip));
+      // low half: of the values, high half: of the negatives
+      uint32_t most = __vmaxs2(__byte_perm(up, down, 0x5410), __byte_perm(up, down, 0x7632));
+      most = __vmaxs2(most, __shfl_xor_sync(0xffffffffu, most, 1));
+      most = __vmaxs2(most, __shfl_xor_sync(0xffffffffu, most, 2));
+      const int hi = (int)(short)(most & 0xffffu), lo = (int)(short)(most >> 16);
+      uint32_t key = hi > lo ? (uint32_t)hi << 6 : (uint32_t)lo << 6 | 1u;
+      // ties of magnitude, what is no number, and magnitudes that the largest scale does not reach
+      if (__any_sync(0xffffffffu, hi == lo || max(hi, lo) >= 0x7e80)) {
+        key = top_key(v[k], (lane & 3) * 8);
+        key = max(key, __shfl_xor_sync(0xffffffffu, key, 1));
+        key = max(key, __shfl_xor_sync(0xffffffffu, key, 2));
+        if (wild(v[k])) {
+          any_wild = true;
+          v[k] = make_uint4(tamed(v[k].x, key >> 6), tamed(v[k].y, key >> 6), tamed(v[k].z, key >> 6), tamed(v[k].w, key >> 6));
+        }
+        v[k] = make_uint4(reached(v[k].x), reached(v[k].y), reached(v[k].z), reached(v[k].w));
       }
       const uint32_t s = scale_of(key);
-      const float inv = s == 0u ? 0.f : __frcp_rn(bf16_value(s));
+      const float inv = s == 0u ? 0.f : fast_rcp(bf16_value(s));
       if (mine && (lane & 3) == 0) {
         const int block = col >> 2;
         scales[is_v ? block * kPage + token : token * kBlocks + block] = (uint16_t)s;
       }
-      const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
-      uint32_t c[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        c[e] = code_bits(__uint_as_float(e & 1 ? w[e >> 1] & 0xffff0000u : w[e >> 1] << 16), inv);
+      const uint32_t c[4] = {codes2(v[k].x, inv), codes2(v[k].y, inv), codes2(v[k].z, inv), codes2(v[k].w, inv)};
       if (!is_v) {
-        // the biases of the eight add up to a constant
-        uint32_t word = 0u, bias = 0u;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          word += c[e] << kv4_shift(e);
-          bias += kCodeBias << kv4_shift(e);
-        }
-        s_k[warp][(col >> 2) * (kPage * 4) + token * 4 + (col & 3)] = word - bias;
+        s_k[warp][(col >> 2) * (kPage * 4) + token * 4 + (col & 3)] = c[0] | c[1] << 4 | c[2] << 8 | c[3] << 12;
       } else {
-        // the tokens of a step lie in one half of the page: its word and shift are constants but for `sub`
+        // a dim's code into the half of its token's parity, four bits on for every two tokens
         const int h = k / (kSteps / 2);
-        const int shift = kRowsAtOnce == 1 ? kv4_shift(k & 7) : kv4_shift(2 * (k & 3)) + 16 * sub;
+        const bool odd = kRowsAtOnce == 1 ? (k & 1) : sub;
+        const int shift = kRowsAtOnce == 1 ? 4 * ((k & 7) >> 1) : 4 * (k & 3);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) acc[h][e] |= mine ? (c[e] & 15u) << shift : 0u;
+        for (int e = 0; e < 4; ++e) {
+          acc[h][2 * e] |= __byte_perm(c[e], 0u, odd ? 0x1044 : 0x4410) << shift;
+          acc[h][2 * e + 1] |= __byte_perm(c[e], 0u, odd ? 0x3244 : 0x4432) << shift;
+        }
       }
     }
     if (any_wild) report(p.dev_status, SD_DEV_NOT_FINITE);
@@ -207,13 +236,9 @@ __global__ void __launch_bounds__(kRowsThreads, 5) kv4_append_kernel(const Kv4Ro
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           uint4 o = make_uint4(acc[0][2 * e], acc[1][2 * e], acc[0][2 * e + 1], acc[1][2 * e + 1]);
-          if (n < kPage) {
-            const uint4 old = at[e];
-            o.x |= old.x & keep[0];
-            o.y |= old.y & keep[1];
-            o.z |= old.z & keep[0];
-            o.w |= old.w & keep[1];
-          }
+          if (n < kPage)
+            o = make_uint4((o.x & ~keep[0]) | (old[e].x & keep[0]), (o.y & ~keep[1]) | (old[e].y & keep[1]),
+                           (o.z & ~keep[0]) | (old[e].z & keep[0]), (o.w & ~keep[1]) | (old[e].w & keep[1]));
           at[e] = o;
         }
       }

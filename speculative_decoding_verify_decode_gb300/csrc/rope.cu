@@ -53,7 +53,7 @@ __device__ __forceinline__ void turn(uint4& a, const float* c, const float* s) {
 }
 
 template <bool INTER>
-__global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads, 4) rope_append_kernel(const RopeParams p) {
   __shared__ __align__(16) float s_table[SD_ROPE_MAX_DIM];
   const int row = blockIdx.x, t = threadIdx.x;
   pdl_wait();
