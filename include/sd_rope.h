@@ -56,7 +56,7 @@ typedef struct sd_rope_shape {
  *   q_out[r] = the turned q[r];  k_out[r] = the turned k[r];
  *   slots[r] >= 0:  k_cache, v_cache at slot slots[r] (page slots[r] / 16,
  *   token slots[r] % 16) = the turned k[r], and v[r] as it is.
- * positions[r] = -1 is padding: nothing of the row is read or written.  A
+ * positions[r] = -1 is padding: nothing is written for the row.  A
  * position outside [-1, table_len) sets SD_DEV_BAD_POSITION and the row is
  * skipped; a slot below -1 or behind the pool sets SD_DEV_BAD_SLOT and the row
  * is not appended.  Rows that name the same slot leave values of either there.

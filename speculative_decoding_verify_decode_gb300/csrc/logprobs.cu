@@ -30,10 +30,14 @@ namespace sdv {
 namespace {
 
 constexpr int kLpThreads = 256, kLpWarps = kLpThreads / 32;
-constexpr int kPer = 16;                        // logits of a thread and tile
-constexpr int kLpTile = kLpThreads * kPer;
-constexpr int kListCut = 256;                   // the list is cut back when it is longer
-constexpr int kListMax = kListCut + kLpTile;
+constexpr int kPer = 16;                        // logits of a thread that are looked at together
+constexpr int kGroup = kLpThreads * kPer;
+constexpr int kListCut = 128;                   // the list is cut back when it is longer
+constexpr int kFew = 2 * kLpThreads;            // keys that are ranked one by one
+constexpr int kListMax = kListCut + kGroup;
+// 64 bytes of a thread are a tile, asked for while the tile before is looked at: 64 KB under way on an SM.
+template <typename T>
+constexpr int kLpTile = kLpThreads * 64 / (int)sizeof(T);
 constexpr float kLog2eLp = 1.4426950408889634f;
 using Key = unsigned long long;
 
@@ -81,87 +85,118 @@ struct LpShared {
   Key bar;
   int n;             // keys in the list
   int count;         // of a search
+  Key few[kFew];     // what a cut looks at
   uint32_t warp_bar[kLpWarps];
+  Key top_of[kLpWarps];
   float m[kLpWarps], c[kLpWarps], s[kLpWarps], w[kLpWarps];
 };
 
-// The `top` largest of the list's keys to its front, in descending order; all threads call it, n uniform.
-__device__ __forceinline__ void cut_list(LpShared& sh, int n, int top) {
+// The j-th largest of o over the warp's lanes (0 where there are fewer).
+__device__ __forceinline__ uint32_t warp_jth(uint32_t o, int j) {
+  uint32_t best = 0u;
+#pragma unroll 1
+  for (int k = 0; k < j; ++k) {
+    best = __reduce_max_sync(0xffffffffu, o);
+    const uint32_t who = __ballot_sync(0xffffffffu, o == best);
+    if ((int)(threadIdx.x & 31) == __ffs(who) - 1) o = 0u;
+  }
+  return best;
+}
+
+// The `top` largest of the list's n keys to its front, in descending order; all threads call it, n uniform.
+// A key's place is the number of larger ones, so the keys are thinned out first: of the threads' largest keys (values
+// alone), the j-th of each of W warps, j = ceil(top / W), and of these the smallest; `top` keys at least are no smaller.
+// (Ranked as they were, the 380 that 38 pieces of a row leave took 8 us.)
+__device__ __noinline__ void cut_list(LpShared& sh, int n, int top) {
   const int t = threadIdx.x;
-  if (n > 2 * kListCut) {
-    // many: the largest bar that leaves at least `top`, bit by bit, then what is not below it
-    Key bar = 0;
+  const Key* from_list = sh.list;
+  if (n > 64) {
+    Key most = 0;
 #pragma unroll 1
-    for (int bit = 63; bit >= 0; --bit) {
-      const Key with = bar | (Key)1 << bit;
-      int mine = 0;
+    for (int i = t; i < n; i += kLpThreads) most = sh.list[i] > most ? sh.list[i] : most;
+    const int full = min(kLpWarps, n >> 5), j = (top + full - 1) / full;     // warps whose threads all have a key
+    const uint32_t jth = warp_jth((uint32_t)(most >> 32), j);
+    if (t == 0) sh.count = 0;
+    if ((t & 31) == 0) sh.warp_bar[t >> 5] = jth;
+    __syncthreads();
+    uint32_t value = sh.warp_bar[0];
 #pragma unroll 1
-      for (int i = t; i < n; i += kLpThreads) mine += sh.list[i] >= with ? 1 : 0;
+    for (int w = 1; w < full; ++w) value = min(value, sh.warp_bar[w]);
+    Key bar = (Key)value << 32;
+    auto take = [&] {
+#pragma unroll 1
+      for (int i = t; i < n; i += kLpThreads) {
+        const Key k = sh.list[i];
+        if (k >= bar) {
+          const int at = atomicAdd(&sh.count, 1);
+          if (at < kFew) sh.few[at] = k;
+        }
+      }
+      __syncthreads();
+    };
+    take();
+    if (sh.count > kFew) {
+      // many alike: the largest bar that leaves `top`, bit by bit (keys are distinct)
+      bar = 0;
+#pragma unroll 1
+      for (int bit = 63; bit >= 0; --bit) {
+        const Key with = bar | (Key)1 << bit;
+        int mine = 0;
+#pragma unroll 1
+        for (int i = t; i < n; i += kLpThreads) mine += sh.list[i] >= with ? 1 : 0;
+        __syncthreads();
+        if (t == 0) sh.count = 0;
+        __syncthreads();
+        mine = __reduce_add_sync(0xffffffffu, mine);
+        if ((t & 31) == 0 && mine != 0) atomicAdd(&sh.count, mine);
+        __syncthreads();
+        if (sh.count >= top) bar = with;
+      }
+      __syncthreads();
       if (t == 0) sh.count = 0;
       __syncthreads();
-      mine = __reduce_add_sync(0xffffffffu, mine);
-      if ((t & 31) == 0 && mine != 0) atomicAdd(&sh.count, mine);
-      __syncthreads();
-      if (sh.count >= top) bar = with;
-      __syncthreads();
+      take();
     }
-    // keys are distinct, so exactly `top` remain; every thread holds its own until all have looked
-    if (t == 0) sh.count = 0;
-    Key held[kListMax / kLpThreads];
-#pragma unroll
-    for (int k = 0; k < kListMax / kLpThreads; ++k) {
-      const int i = t + k * kLpThreads;
-      held[k] = i < n ? sh.list[i] : 0;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < kListMax / kLpThreads; ++k)
-      if (held[k] >= bar && held[k] != 0) sh.list[atomicAdd(&sh.count, 1)] = held[k];
-    __syncthreads();
     n = sh.count;
+    from_list = sh.few;
   }
-  // few: a key's place is the number of larger ones
+  // as many neighbouring threads a key as there are to spare
+  int shift = 0;
+  while (shift < 3 && n << (shift + 1) <= kLpThreads) ++shift;
+  const int parts = 1 << shift, part = t & (parts - 1), step = (n + parts - 1) >> shift;
+  const int begin = part * step, end = min(n, begin + step);
   Key mine[2];
-  int place[2];
+  int larger[2] = {0, 0};
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
-    const int i = t + k * kLpThreads;
-    mine[k] = i < n ? sh.list[i] : 0;
-    place[k] = i < n ? 0 : INT_MAX;
-  }
-  const bool second = n > kLpThreads;
-  if (second) {
+    const int i = (t >> shift) + k * kLpThreads;
+    mine[k] = i < n ? from_list[i] : 0;
+    if (k > 0 && n <= kLpThreads) continue;
 #pragma unroll 4
-    for (int i = 0; i < n; ++i) {
-      const Key k = sh.list[i];
-      place[0] += k > mine[0] && place[0] != INT_MAX ? 1 : 0;
-      place[1] += k > mine[1] && place[1] != INT_MAX ? 1 : 0;
-    }
-  } else if ((t & ~31) < n) {
-#pragma unroll 4
-    for (int i = 0; i < n; ++i) place[0] += sh.list[i] > mine[0] && place[0] != INT_MAX ? 1 : 0;
+    for (int o = begin; o < end; ++o) larger[k] += from_list[o] > mine[k] ? 1 : 0;
+    for (int d = 1; d < parts; d <<= 1) larger[k] += __shfl_xor_sync(0xffffffffu, larger[k], d);
   }
   __syncthreads();
 #pragma unroll
   for (int k = 0; k < 2; ++k)
-    if (place[k] < top) sh.list[place[k]] = mine[k];
+    if (mine[k] != 0 && part == 0 && larger[k] < top) sh.list[larger[k]] = mine[k];
   __syncthreads();
 }
 
-// Sixteen logits of a thread: kVec at a time, kVec * kLpThreads apart.
+// A 16-byte piece as floats.
 template <typename T>
 struct Load;
 template <>
 struct Load<float> {
   static constexpr int kVec = 4;
-  using V = float4;
-  static __device__ __forceinline__ void put(const V& v, float* x) { x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w; }
+  static __device__ __forceinline__ void put(const uint4& v, float* x) {
+    x[0] = __uint_as_float(v.x); x[1] = __uint_as_float(v.y); x[2] = __uint_as_float(v.z); x[3] = __uint_as_float(v.w);
+  }
 };
 template <>
 struct Load<__nv_bfloat16> {
   static constexpr int kVec = 8;
-  using V = uint4;
-  static __device__ __forceinline__ void put(const V& v, float* x) {
+  static __device__ __forceinline__ void put(const uint4& v, float* x) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -173,8 +208,7 @@ struct Load<__nv_bfloat16> {
 template <>
 struct Load<__half> {
   static constexpr int kVec = 8;
-  using V = uint4;
-  static __device__ __forceinline__ void put(const V& v, float* x) {
+  static __device__ __forceinline__ void put(const uint4& v, float* x) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -187,9 +221,18 @@ struct Load<__half> {
 template <typename T>
 __device__ __forceinline__ float value_of(T x) { return static_cast<float>(x); }
 
+// The logit of a row's t-th given token (one a thread); -infinity where it is none.
+static_assert(SD_LOGPROBS_MAX_GIVEN <= kLpThreads, "a thread for each given token");
+template <typename T>
+__device__ __forceinline__ float given_logit(const LogprobsParams& p, int row) {
+  if ((int)threadIdx.x >= p.given) return -INFINITY;
+  const int v = p.tokens[(size_t)row * p.given + threadIdx.x];
+  return v >= 0 && v < p.vocab ? value_of(static_cast<const T*>(p.logits)[(long long)row * p.row_stride + v]) : -INFINITY;
+}
+
 // A row's results from its statistics and (in sh.list, descending) its top keys.
 template <typename T>
-__device__ void finish_row(const LogprobsParams& p, const LpShared& sh, int row, Stats st, bool bad) {
+__device__ void finish_row(const LogprobsParams& p, const LpShared& sh, int row, Stats st, bool bad, float given) {
   const int t = threadIdx.x;
   const bool none = st.c == 0.f;      // nothing but -infinity
   const float log_s = bad ? NAN : none ? -INFINITY : logf(st.c) + log1pf(st.s / st.c);
@@ -200,12 +243,7 @@ __device__ void finish_row(const LogprobsParams& p, const LpShared& sh, int row,
     if (p.lse != nullptr) p.lse[row] = bad ? NAN : none ? -INFINITY : m * p.inv_t + log_s;
     if (p.entropy != nullptr) p.entropy[row] = bad ? NAN : none ? 0.f : log_s - st.w / (st.c + st.s) * kLn2;
   }
-  const T* x = static_cast<const T*>(p.logits) + (long long)row * p.row_stride;
-  for (int i = t; i < p.given; i += kLpThreads) {
-    const size_t at = (size_t)row * p.given + i;
-    const int v = p.tokens[at];
-    p.logprobs[at] = v >= 0 && v < p.vocab ? logprob(value_of(x[v])) : bad ? NAN : -INFINITY;
-  }
+  if (t < p.given) p.logprobs[(size_t)row * p.given + t] = logprob(given);
   for (int i = t; i < p.top; i += kLpThreads) {
     const size_t at = (size_t)row * p.top + i;
     const Key k = sh.list[i];
@@ -243,10 +281,9 @@ __device__ __forceinline__ Stats block_stats(LpShared& sh, Stats st, float f) {
 
 // VEC: the rows start on 16 bytes and so does every 16-byte piece of them.
 template <typename T, bool TOP, bool VEC>
-__global__ void __launch_bounds__(kLpThreads, TOP ? 4 : 6) logprobs_piece_kernel(const LogprobsParams p) {
+__global__ void __launch_bounds__(kLpThreads, TOP ? 4 : 5) logprobs_piece_kernel(const LogprobsParams p) {
   __shared__ LpShared sh;
-  constexpr int kVec = Load<T>::kVec, kLoads = kPer / kVec;
-  using V = typename Load<T>::V;
+  constexpr int kVec = Load<T>::kVec, kTile = kLpTile<T>, kPieces = kPer / kVec, kGroups = kTile / kGroup;
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const int row = blockIdx.x / p.pieces, piece = blockIdx.x - row * p.pieces;
   const T* x = static_cast<const T*>(p.logits) + (long long)row * p.row_stride;
@@ -258,30 +295,37 @@ __global__ void __launch_bounds__(kLpThreads, TOP ? 4 : 6) logprobs_piece_kernel
   st.m = -INFINITY;
   st.c = st.s = st.w = 0.f;
   bool bad = false;
-  // A thread's logits of a tile: vector j at begin + (j * kLpThreads + t) * kVec.
-  V raw[kLoads];
+  // A thread's logits of a tile: 16-byte piece j at begin + (j * kLpThreads + t) * kVec.
+  uint4 raw[4];
   auto fetch = [&](int at) {
 #pragma unroll
-    for (int j = 0; j < kLoads; ++j) {
+    for (int j = 0; j < 4; ++j) {
       const int v = at + (j * kLpThreads + t) * kVec;
       if (VEC && v + kVec <= end) {
-        raw[j] = __ldcs(reinterpret_cast<const V*>(x + v));
+        raw[j] = __ldcs(reinterpret_cast<const uint4*>(x + v));
       } else {
         // what lies past the end counts as tokens that cannot come
         alignas(16) T e[kVec];
 #pragma unroll
         for (int k = 0; k < kVec; ++k) e[k] = v + k < end ? x[v + k] : static_cast<T>(-INFINITY);
-        raw[j] = *reinterpret_cast<const V*>(e);
+        raw[j] = *reinterpret_cast<const uint4*>(e);
       }
     }
   };
   fetch(begin);
 #pragma unroll 1
-  for (int at = begin; at < end; at += kLpTile) {
+  for (int tile = begin; tile < end; tile += kTile) {
+    uint4 held[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) held[j] = raw[j];
+    if (tile + kTile < end) fetch(tile + kTile);
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) {
+    const int at = tile + g * kGroup;
+    if (at >= end) break;
     float y[kPer];
 #pragma unroll
-    for (int j = 0; j < kLoads; ++j) Load<T>::put(raw[j], y + j * kVec);
-    if (at + kLpTile < end) fetch(at + kLpTile);
+    for (int j = 0; j < kPieces; ++j) Load<T>::put(held[g * kPieces + j], y + j * kVec);
     float top = y[0];
 #pragma unroll
     for (int e = 1; e < kPer; ++e) top = max_nan(top, y[e]);
@@ -316,15 +360,8 @@ __global__ void __launch_bounds__(kLpThreads, TOP ? 4 : 6) logprobs_piece_kernel
         // a first bar (32 bits of it): in each warp the j-th largest of the threads' maxima
         uint32_t o = order_of(top);
         if (top != top) o = 0u;
-        const int j = (p.top + kLpWarps - 1) / kLpWarps;
-        uint32_t best = 0u;
-#pragma unroll 1
-        for (int k = 0; k < j; ++k) {
-          best = __reduce_max_sync(0xffffffffu, o);
-          const uint32_t who = __ballot_sync(0xffffffffu, o == best);
-          if (lane == __ffs(who) - 1) o = 0u;
-        }
-        if (lane == 0) sh.warp_bar[warp] = best;
+        const uint32_t jth = warp_jth(o, (p.top + kLpWarps - 1) / kLpWarps);
+        if (lane == 0) sh.warp_bar[warp] = jth;
         __syncthreads();
         uint32_t bar = sh.warp_bar[0];
 #pragma unroll
@@ -334,18 +371,30 @@ __global__ void __launch_bounds__(kLpThreads, TOP ? 4 : 6) logprobs_piece_kernel
       }
       const Key bar = sh.bar;
       const float bar_value = order_value((uint32_t)(bar >> 32));   // (NaN for 0: every comparison below then holds)
+      // this thread's logits that reach the bar, a bit each: few, taken one after the other
+      uint32_t pass = 0;
       bool pushed = false;
-      if (!(top < bar_value)) {
+      if (__any_sync(0xffffffffu, !(top < bar_value))) {
 #pragma unroll
-        for (int e = 0; e < kPer; ++e) {
-          if (!(y[e] < bar_value)) {
-            const int v = at + ((e / kVec) * kLpThreads + t) * kVec + e % kVec;
-            const Key k = key_of(y[e], v);
-            if (v < end && k >= bar && y[e] == y[e]) {
-              sh.list[atomicAdd(&sh.n, 1)] = k;
-              pushed = true;
-            }
+        for (int e = 0; e < kPer; ++e) pass |= y[e] < bar_value ? 0u : 1u << e;
+#pragma unroll 1
+        while (__any_sync(0xffffffffu, pass != 0)) {
+          const int e0 = __ffs(pass) - 1;      // -1: none
+          float value = 0.f;
+#pragma unroll
+          for (int e = 0; e < kPer; ++e) value = e0 == e ? y[e] : value;
+          const int v = at + ((e0 / kVec) * kLpThreads + t) * kVec + e0 % kVec;
+          const Key k = key_of(value, v);
+          const bool ok = pass != 0 && v < end && k >= bar && value == value;
+          const uint32_t who = __ballot_sync(0xffffffffu, ok);
+          if (who != 0u) {
+            int place = 0;
+            if (lane == 0) place = atomicAdd(&sh.n, __popc(who));
+            place = __shfl_sync(0xffffffffu, place, 0) + __popc(who & ((1u << lane) - 1u));
+            if (ok) sh.list[place] = k;
+            pushed = true;
           }
+          pass &= pass - 1u;
         }
       }
       // a tile in which nobody had anything leaves the list as it was
@@ -362,6 +411,7 @@ __global__ void __launch_bounds__(kLpThreads, TOP ? 4 : 6) logprobs_piece_kernel
         }
       }
     }
+    }
   }
   if (TOP) {
     const int n = sh.n;
@@ -373,7 +423,7 @@ __global__ void __launch_bounds__(kLpThreads, TOP ? 4 : 6) logprobs_piece_kernel
   const bool any_bad = __syncthreads_or(bad ? 1 : 0) != 0;
   st = block_stats(sh, st, f);
   if (p.pieces == 1) {
-    finish_row<T>(p, sh, row, st, any_bad);
+    finish_row<T>(p, sh, row, st, any_bad, given_logit<T>(p, row));
   } else {
     if (t == 0) p.stats[blockIdx.x] = make_float4(st.m, any_bad ? NAN : st.c, st.s, st.w);
     if (TOP)
@@ -391,6 +441,7 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_join_kernel(const Logprob
   const int row = blockIdx.x, t = threadIdx.x;
   const float f = p.inv_t * kLog2eLp;
   pdl_wait();
+  const float given = given_logit<T>(p, row);
   Stats st;
   st.m = -INFINITY;
   st.c = st.s = st.w = 0.f;
@@ -403,14 +454,19 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_join_kernel(const Logprob
     st.s = v.z;
     st.w = v.w;
   }
-  if (t == 0) { sh.n = 0; sh.bar = 0; }
+  if (t == 0) sh.n = 0;
   __syncthreads();
   if (p.top > 0) {
     // a piece's last key has `top` keys of its own piece no smaller: the largest of these is a bar
     const Key* keys = p.keys + (size_t)row * p.pieces * p.top;
-    if (t < p.pieces) atomicMax(&sh.bar, keys[(size_t)t * p.top + p.top - 1]);
+    const Key last = t < p.pieces ? keys[(size_t)t * p.top + p.top - 1] : 0;
+    const uint32_t hi = __reduce_max_sync(0xffffffffu, (uint32_t)(last >> 32));
+    const uint32_t lo = __reduce_max_sync(0xffffffffu, (uint32_t)(last >> 32) == hi ? (uint32_t)last : 0u);
+    if ((t & 31) == 0) sh.top_of[t >> 5] = (Key)hi << 32 | lo;
     __syncthreads();
-    const Key bar = sh.bar;
+    Key bar = 0;
+#pragma unroll
+    for (int w = 0; w < kLpWarps; ++w) bar = sh.top_of[w] > bar ? sh.top_of[w] : bar;
     for (int i = t; i < p.pieces * p.top; i += kLpThreads) {
       const Key k = keys[i];
       if (k != 0 && k >= bar) sh.list[atomicAdd(&sh.n, 1)] = k;
@@ -423,17 +479,19 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_join_kernel(const Logprob
     __syncthreads();
     cut_list(sh, n, p.top);
   }
-  finish_row<T>(p, sh, row, st, bad);
+  finish_row<T>(p, sh, row, st, bad, given);
 }
 
-// Pieces of a row: so many that the grid has about four CTAs for each SM, none smaller than a tile.
+// Pieces of a row (of whole 4096-logit groups, whatever the type): one while the rows make three waves of CTAs, else so
+// many that there is about one wave, and none smaller than a group.
 int pieces_of(int rows, int vocab, int* piece) {
-  const int tiles = (vocab + kLpTile - 1) / kLpTile;
-  const int want = rows >= 4 * kSMs ? 1 : (4 * kSMs + rows - 1) / rows;
-  const int n = want < tiles ? (want < kMaxPieces ? want : kMaxPieces) : (tiles < kMaxPieces ? tiles : kMaxPieces);
-  const int per = (tiles + n - 1) / n;
-  *piece = per * kLpTile;
-  return (tiles + per - 1) / per;
+  const int groups = (vocab + kGroup - 1) / kGroup, wave = 4 * kSMs;
+  int n = rows >= 3 * wave ? 1 : rows > wave / 2 ? (2 * wave + rows - 1) / rows : (wave + rows - 1) / rows;
+  n = n < groups ? n : groups;
+  n = n < kMaxPieces ? n : kMaxPieces;
+  const int per = (groups + n - 1) / n;
+  *piece = per * kGroup;
+  return (groups + per - 1) / per;
 }
 
 constexpr size_t align_up(size_t x) { return (x + 255) / 256 * 256; }

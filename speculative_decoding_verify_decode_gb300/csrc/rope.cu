@@ -59,92 +59,83 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_append_kernel(const Rope
   pdl_wait();
   const int pos = p.positions[row];
   int slot = p.slots != nullptr ? p.slots[row] : -1;
+  // Items of a rotated head: `turned` pairs of pieces (or single pieces), then `plain` pieces behind rot_dim; then V's.
+  const int half = p.rot_dim / 2;
+  const int turned = INTER ? p.rot_dim / 8 : p.rot_dim / 16, plain = (p.dim - p.rot_dim) / 8, per_head = turned + plain;
+  const int rotated = (p.hq + p.hkv) * per_head, per_v = p.dim / 8;
+  const int items = rotated + (p.v != nullptr ? p.hkv * per_v : 0);
+  const float inv = 1.0f / (float)per_head, inv_v = 1.0f / (float)per_v;
+  // An item's head (V's behind the others) and first dim; quotients by one multiplication: exact, the halves keep them
+  // away from the borders (i < 2^17).
+  auto place = [&](int i, int& h, int& d, bool& turns) {
+    const bool is_v = i >= rotated;
+    const int j = is_v ? i - rotated : i, per = is_v ? per_v : per_head;
+    h = __float2int_rz(((float)j + 0.5f) * (is_v ? inv_v : inv));
+    const int e = j - h * per;
+    turns = !is_v && e < turned;
+    d = is_v || turns ? e * 8 : p.rot_dim + (e - turned) * 8;
+    if (is_v) h += p.hq + p.hkv;
+  };
+  auto fetch = [&](int i, uint4& a, uint4& b) {
+    if (i >= items) return;
+    int h, d;
+    bool turns;
+    place(i, h, d, turns);
+    const __nv_bfloat16* src = h < p.hq              ? p.q + (long long)row * p.q_stride + h * p.dim
+                               : h < p.hq + p.hkv    ? p.k + (long long)row * p.k_stride + (h - p.hq) * p.dim
+                                                     : p.v + (long long)row * p.v_stride + (h - p.hq - p.hkv) * p.dim;
+    a = *reinterpret_cast<const uint4*>(src + d);
+    if (!INTER && turns) b = *reinterpret_cast<const uint4*>(src + d + half);
+  };
+  auto finish = [&](int i, uint4& a, uint4& b) {
+    if (i >= items) return;
+    int h, d;
+    bool turns;
+    place(i, h, d, turns);
+    if (turns) {
+      if (INTER) turn(a, s_table + d / 2, s_table + d / 2 + half);
+      else turn(a, b, s_table + d, s_table + d + half);
+    }
+    const int mate = !INTER && turns ? half : 0;
+    __nv_bfloat16* out = nullptr;
+    if (h < p.hq) out = p.q_out + (long long)row * p.q_out_stride + h * p.dim + d;
+    else if (h < p.hq + p.hkv && p.k_out != nullptr) out = p.k_out + (long long)row * p.k_out_stride + (h - p.hq) * p.dim + d;
+    if (out != nullptr) {
+      *reinterpret_cast<uint4*>(out) = a;
+      if (mate) *reinterpret_cast<uint4*>(out + mate) = b;
+    }
+    if (h >= p.hq && slot >= 0) {
+      const bool is_v = h >= p.hq + p.hkv;
+      __nv_bfloat16* cache = (is_v ? p.v_cache : p.k_cache) +
+                             (((size_t)(slot / kPage) * p.hkv + (h - p.hq - (is_v ? p.hkv : 0))) * kPage + slot % kPage) * p.dim + d;
+      *reinterpret_cast<uint4*>(cache) = a;
+      if (mate) *reinterpret_cast<uint4*>(cache + mate) = b;
+    }
+  };
+  // the row's own pieces are asked for before its position is known
+  constexpr int U = 3;
+  uint4 a[U], b[U];
+#pragma unroll
+  for (int k = 0; k < U; ++k) fetch(t + k * kRopeThreads, a[k], b[k]);
   if (pos < 0 || pos >= p.table_len) {
     if (pos != -1 && t == 0) report(p.dev_status, SD_DEV_BAD_POSITION);
     return;
   }
   if (slot < -1 || slot / kPage >= p.num_pool_pages) {
-    if (t == 0) report(p.dev_status, SD_DEV_BAD_SLOT);
+    if (t == 0 && p.slots != nullptr) report(p.dev_status, SD_DEV_BAD_SLOT);
     slot = -1;
   }
-  // Items of a rotated head: `turned` pairs of pieces (or single pieces), then `plain` pieces behind rot_dim; then V's.
-  const int half = p.rot_dim / 2;
-  const int turned = INTER ? p.rot_dim / 8 : p.rot_dim / 16, plain = (p.dim - p.rot_dim) / 8, per_head = turned + plain;
-  const int heads = p.hq + p.hkv, rotated = heads * per_head;
-  const int items = rotated + (slot >= 0 ? p.hkv * (p.dim / 8) : 0);
-  const size_t page = slot >= 0 ? (size_t)(slot / kPage) * p.hkv : 0;
-  const int in_page = slot >= 0 ? slot % kPage : 0;
-  const float inv = 1.0f / (float)per_head, inv_v = 8.0f / (float)p.dim;
-
-  struct Item {
-    uint4 a, b;
-    const float* c;              // null: not turned
-    __nv_bfloat16 *out, *cache;  // where the first piece goes (nullable)
-    int mate;                    // dims from the first piece to the second, 0: none
-  };
-  auto fetch = [&](int i) {
-    Item it;
-    it.c = nullptr;
-    it.out = it.cache = nullptr;
-    it.mate = 0;
-    it.a = it.b = make_uint4(0, 0, 0, 0);
-    if (i >= items) return it;
-    const bool is_v = i >= rotated;
-    // quotients by one multiplication: exact, the halves keep them away from the borders (i < 2^17)
-    const int j = is_v ? i - rotated : i;
-    const int per = is_v ? p.dim / 8 : per_head;
-    const int h = __float2int_rz(((float)j + 0.5f) * (is_v ? inv_v : inv)), e = j - h * per;
-    int d;
-    if (is_v) d = e * 8;
-    else if (e < turned) d = e * 8;
-    else d = p.rot_dim + (e - turned) * 8;
-    const __nv_bfloat16* src;
-    if (is_v) {
-      src = p.v + (long long)row * p.v_stride + h * p.dim + d;
-    } else if (h < p.hq) {
-      src = p.q + (long long)row * p.q_stride + h * p.dim + d;
-      it.out = p.q_out + (long long)row * p.q_out_stride + h * p.dim + d;
-    } else {
-      src = p.k + (long long)row * p.k_stride + (h - p.hq) * p.dim + d;
-      if (p.k_out != nullptr) it.out = p.k_out + (long long)row * p.k_out_stride + (h - p.hq) * p.dim + d;
-    }
-    if (slot >= 0 && (is_v || h >= p.hq))
-      it.cache = (is_v ? p.v_cache : p.k_cache) + ((page + (is_v ? h : h - p.hq)) * kPage + in_page) * p.dim + d;
-    it.a = *reinterpret_cast<const uint4*>(src);
-    if (!is_v && e < turned) {
-      it.c = s_table + (INTER ? e * 4 : e * 8);
-      if (!INTER) {
-        it.mate = half;
-        it.b = *reinterpret_cast<const uint4*>(src + half);
-      }
-    }
-    return it;
-  };
-  auto finish = [&](Item& it) {
-    if (it.c != nullptr) {
-      if (INTER) turn(it.a, it.c, it.c + half);
-      else turn(it.a, it.b, it.c, it.c + half);
-    }
-    if (it.out != nullptr) {
-      *reinterpret_cast<uint4*>(it.out) = it.a;
-      if (it.mate) *reinterpret_cast<uint4*>(it.out + it.mate) = it.b;
-    }
-    if (it.cache != nullptr) {
-      *reinterpret_cast<uint4*>(it.cache) = it.a;
-      if (it.mate) *reinterpret_cast<uint4*>(it.cache + it.mate) = it.b;
-    }
-  };
-  Item x = fetch(t), y = fetch(t + kRopeThreads);
   for (int i = t; i < p.rot_dim / 4; i += kRopeThreads)
     reinterpret_cast<float4*>(s_table)[i] = __ldg(reinterpret_cast<const float4*>(p.table + (size_t)pos * p.rot_dim) + i);
   __syncthreads();
-  finish(x);
-  finish(y);
-  for (int i = t + 2 * kRopeThreads; i < items; i += 2 * kRopeThreads) {
-    x = fetch(i);
-    y = fetch(i + kRopeThreads);
-    finish(x);
-    finish(y);
+#pragma unroll 1
+  for (int i = t;;) {
+#pragma unroll
+    for (int k = 0; k < U; ++k) finish(i + k * kRopeThreads, a[k], b[k]);
+    i += U * kRopeThreads;
+    if (i - t >= items) break;
+#pragma unroll
+    for (int k = 0; k < U; ++k) fetch(i + k * kRopeThreads, a[k], b[k]);
   }
 }
 
