@@ -50,14 +50,14 @@ constexpr int kTile = kTileTokens;     // tokens of a product's M
 constexpr float kRise = 16.0f;         // log2 of the weight beyond which a reference moves
 constexpr float kLog2e = 1.4426950408889634f;
 
-template <int NQ, int WG, bool MOD>
+template <int NQ, int WG, int MH, bool MOD>
 struct Kv4Small {
   static constexpr int kBars = 64;
   float m[NQ];             // the column's reference, negated: -m
   float alpha[NQ];         // rescale factor of the current tile; 1 / l in the epilogue
   float slope[MOD ? NQ : 4];   // distance bias of the column, base 2
   float red[4][NQ];        // per lane quarter: column maxima of a tile; column sums in the epilogue
-  alignas(16) uint2 vs[WG * 4][2][32];        // per V warp: scales of token pairs, and -24 times them
+  alignas(16) uint2 vs[WG * 4][MH][64];       // per V warp: scales of a tile's token pairs, and -24 times them
   unsigned long long anc[kMaxNodes];          // bit r: node r is on the node's root path; in the draft CTA then turned
                                               // round, bit n: node n sees the row
   uint64_t bar[kBars];
@@ -84,20 +84,23 @@ struct Kv4 {
   static constexpr int kCtas = kv4_ctas(NQ, D);
   static constexpr int WG = NG == 1 && kCtas == 1 ? 2 : 1;
   static constexpr int kWarps = NG * 4, kThreads = (kWarps + WG * 8 + 4) * 32;
-  using Small = Kv4Small<NQ, WG, MOD>;
   static constexpr int kSmemBytes = kCtas == 2 ? 115712 : 232448;   // dynamic shared memory a CTA can have
   static constexpr int kTmem = 512 / kCtas;
   static constexpr int MH = D / 128;                      // 128-dim blocks
+  using Small = Kv4Small<NQ, WG, MH, MOD>;
   // Tiles that pass the softmax together: what a turn costs beyond them (barriers, the references' check, bookkeeping)
   // is as much as sixteen columns of a tile or two.
     static constexpr int T = NQ == 16 && kCtas == 1 ? 4 : NQ <= 48 ? 2 : 1;
   static constexpr int NS = NQ <= 96 ? 2 : 1;             // S buffers in tensor memory
   // Widened operands: slots of SW elements a lane, two to a column.
-  static constexpr int SW = NQ == 144 ? 32 : 64;
+  #ifndef SW16
+#define SW16 128
+#endif
+  static constexpr int SW = NQ == 144 ? 32 : NQ == 16 ? SW16 : 64;
   static constexpr int kSlotCols = SW / 2;
   static constexpr int kColO = NS * T * NQ, kColA = kColO + MH * NQ;
   static constexpr int kSlotsLeft = (kTmem - kColA) / kSlotCols / WG;
-  static constexpr int KA = kSlotsLeft / 2 > 1 ? 2 : 1, VA = 2;
+  static constexpr int KA = kSlotsLeft / 2 > 1 ? 2 : 1, VA = kSlotsLeft - KA > 1 ? 2 : 1;
   // A tile takes the ring round KU (VU) times: which slot, and which phase of it, is known without counting.
   static constexpr int KU = D / SW / KA, VU = kTile / SW * MH / VA;
   static constexpr int kRecord = kv4_record(D), kTileBytes = 8 * kRecord;   // a page's K or V; a tile's
@@ -113,7 +116,7 @@ struct Kv4 {
   static constexpr size_t kSmem = (size_t)kQBytes + 2 * kPBytes + kRingBytes + sizeof(Small);
   static_assert(KS * WG >= 2 && VS * WG >= 2, "rings of two tiles at least");
   static_assert(kColA + WG * (KA + VA) * kSlotCols <= kTmem, "tensor memory");
-  static_assert(KU * KA * SW == D && VU * VA * SW == kTile * MH && (MH == 1 || MH == VA), "slots of a tile");
+  static_assert(KU * KA * SW == D && VU * VA * SW == kTile * MH, "slots of a tile");
   static_assert(kSmem <= (size_t)kSmemBytes, "shared memory over 227 KB");
 };
 
@@ -642,7 +645,7 @@ kv4_attn_kernel(const Kv4AttnParams p, const BatchDesc bd) {
                 __syncwarp();
                 tc_fence_after();
                 // slot k VA + s: 128-dim block mb of SW tokens
-                const int mb = MH == 1 ? 0 : s, ts = MH == 1 ? k * VA + s : k;
+                const int mb = (k * VA + s) % MH, ts = (k * VA + s) / MH;
                 const uint32_t d = tmem + K::kColO + mb * NQ, a = a0 + s * K::kSlotCols;
                 const int steps = (valid - ts * SW + 15) / 16;      // of 16 tokens that hold any
                 if (elect_one()) {
@@ -755,8 +758,20 @@ kv4_attn_kernel(const Kv4AttnParams p, const BatchDesc bd) {
           // this thread's token, block after block of 32 dims (rolled: the roles' loops share an instruction cache)
           const uint8_t* rec = buf + ring.at * K::kSlotBytes + (row >> 4) * K::kPageStride;
           const uint8_t* words = rec + (row & 15) * 16;
-          const uint16_t* sc = reinterpret_cast<const uint16_t*>(rec + kv4_codes(D) + (row & 15) * (D / 16));
-          uint32_t most = 0;
+          uint16_t* sc = reinterpret_cast<uint16_t*>(const_cast<uint8_t*>(rec) + kv4_codes(D) + (row & 15) * (D / 16));
+          bool odd_scale = false;      // one with bits that do not count, or beyond the largest
+#pragma unroll
+          for (int e = 0; e < D / 64; ++e) {
+            const uint32_t two = reinterpret_cast<const uint32_t*>(sc)[e], most = kKv4BadScale - 1u | (kKv4BadScale - 1u) << 16;
+            odd_scale |= (two & 0x00070007u) != 0u || __vmaxu2(two & 0x7fff7fffu, most) != most;
+          }
+          if (odd_scale) {             // rare: put right in place (nobody else reads this token's)
+            bool bad = false;
+#pragma unroll 1
+            for (int e = 0; e < D / 64; ++e) reinterpret_cast<uint32_t*>(sc)[e] = kv4_sane(reinterpret_cast<uint32_t*>(sc)[e], bad);
+            fence_async_smem();
+            if (bad && t0 + row < pc.L && t0 + row >= seen) report(p.dev_status, SD_DEV_BAD_SCALE);
+          }
 #pragma unroll 1
           for (int n = 0; n < K::KU * KA; ++n) {
             const int s = n % KA, k = n / KA;
@@ -765,12 +780,9 @@ kv4_attn_kernel(const Kv4AttnParams p, const BatchDesc bd) {
 #pragma unroll 1
             for (int h = 0; h < SW / 32; ++h) {
               const uint4 w = *reinterpret_cast<const uint4*>(words);
-              uint32_t s1 = *sc & kKv4ScaleBits;
+              const __nv_bfloat162 sv = kv4_scale2(__byte_perm(*sc, 0, 0x1010)), less = kv4_less(sv);
               words += kPage * 16;
               ++sc;
-              most = max(most, s1 & 0x7fffu);
-              s1 = (s1 & 0x7fffu) >= kKv4BadScale ? 0u : s1;
-              const __nv_bfloat162 sv = kv4_scale2(__byte_perm(s1, 0, 0x1010)), less = kv4_less(sv);
               const uint32_t* ww = reinterpret_cast<const uint32_t*>(&w);
               uint32_t x[16];
 #pragma unroll
@@ -779,38 +791,38 @@ kv4_attn_kernel(const Kv4AttnParams p, const BatchDesc bd) {
             }
             slot_done(s);
           }
-          if (most >= kKv4BadScale && t0 + row < pc.L && t0 + row >= seen) report(p.dev_status, SD_DEV_BAD_SCALE);
         } else {
           // this thread's dim (of each 128): the scales of its block of 32, token pair by token pair, are the warp's
           const uint8_t* pages = buf + ring.at * K::kSlotBytes;
           const bool plain = t0 >= seen && t0 + kTile <= pc.L;
+          uint2* const vs = sm->vs[group * 4 + quarter][0];
+#pragma unroll
+          for (int r = 0; r < 2 * MH; ++r) {
+            const int mb = r >> 1, pair = (r & 1) * 32 + lane;
+            uint32_t s2 = *reinterpret_cast<const uint32_t*>(pages + (pair >> 3) * K::kPageStride + kv4_codes(D) +
+                                                             (mb * 4 + quarter) * 32 + (pair & 7) * 4);
+            s2 &= kKv4ScaleBits | kKv4ScaleBits << 16;
+            if (!plain) {
+              // tokens that nobody sees count 0 (their records may hold anything)
+              const int t = t0 + 2 * pair;
+              if (t >= pc.L || t < seen) s2 &= 0xffff0000u;
+              if (t + 1 >= pc.L || t + 1 < seen) s2 &= 0x0000ffffu;
+            }
+            const uint32_t most = kKv4BadScale - 1u | (kKv4BadScale - 1u) << 16;
+            if (__vmaxu2(s2 & 0x7fff7fffu, most) != most) {
+              bool bad = false;
+              s2 = kv4_sane(s2, bad);
+              report(p.dev_status, SD_DEV_BAD_SCALE);
+            }
+            const __nv_bfloat162 less = kv4_less(kv4_scale2(s2));
+            vs[mb * 64 + pair] = make_uint2(s2, *reinterpret_cast<const uint32_t*>(&less));
+          }
 #pragma unroll 1
           for (int n = 0; n < K::VU * VA; ++n) {
             const int s = n % VA, k = n / VA, mb = n % MH, ts = n / MH;      // 128-dim block mb of SW tokens
-            const uint8_t* at = pages + ts * (SW / 16) * K::kPageStride;
-            uint2* const vs = sm->vs[group * 4 + quarter][s];
-            if (SW == 64 || lane < SW / 2) {
-              uint32_t s2 = *reinterpret_cast<const uint32_t*>(at + (lane >> 3) * K::kPageStride + kv4_codes(D) +
-                                                               (mb * 4 + quarter) * 32 + (lane & 7) * 4);
-              s2 &= kKv4ScaleBits | kKv4ScaleBits << 16;
-              if (!plain) {
-                // tokens that nobody sees count 0 (their records may hold anything)
-                const int t = t0 + ts * SW + 2 * lane;
-                if (t >= pc.L || t < seen) s2 &= 0xffff0000u;
-                if (t + 1 >= pc.L || t + 1 < seen) s2 &= 0x0000ffffu;
-              }
-              if (__vmaxu2(s2 & 0x7fff7fffu, kKv4BadScale - 1u | (kKv4BadScale - 1u) << 16) !=
-                  (kKv4BadScale - 1u | (kKv4BadScale - 1u) << 16)) {
-                bool bad = false;
-                s2 = kv4_sane(s2, bad);
-                report(p.dev_status, SD_DEV_BAD_SCALE);
-              }
-              const __nv_bfloat162 less = kv4_less(kv4_scale2(s2));
-              vs[lane] = make_uint2(s2, *reinterpret_cast<const uint32_t*>(&less));
-            }
             slot_free(s, K::VU % 2 == 0 ? k & 1 : odd ^ (k & 1));
-            const uint8_t* words = at + (mb * 128 + row) * 8;
-            const uint4* sl_at = reinterpret_cast<const uint4*>(vs);
+            const uint8_t* words = pages + ts * (SW / 16) * K::kPageStride + (mb * 128 + row) * 8;
+            const uint4* sl_at = reinterpret_cast<const uint4*>(vs + mb * 64 + ts * (SW / 2));
             const uint32_t to = a_base + s * K::kSlotCols;
 #pragma unroll 1
             for (int h = 0; h < SW / 32; ++h, words += 2 * K::kPageStride, sl_at += 8) {

@@ -32,7 +32,7 @@ namespace {
 constexpr int kLpThreads = 256, kLpWarps = kLpThreads / 32;
 constexpr int kPer = 16;                        // logits of a thread that are looked at together
 constexpr int kGroup = kLpThreads * kPer;
-constexpr int kListCut = 128;                   // the list is cut back when it is longer
+constexpr int kListCut = 64;                    // the list is cut back when it is longer
 constexpr int kFew = 2 * kLpThreads;            // keys that are ranked one by one
 constexpr int kListMax = kListCut + kGroup;
 // 64 bytes of a thread are a tile, asked for while the tile before is looked at: 64 KB under way on an SM.
