@@ -82,7 +82,7 @@ struct Kv4 {
   // goes from piece to piece (64 sequences of 1 to 16384 tokens 236 -> 213 us, one of 512 tokens 12.4 -> 11.4); of 128
   // dims one CTA with two groups is faster (64 sequences of 1 to 32768 tokens 427 us against 463).
   static constexpr int kCtas = kv4_ctas(NQ, D);
-  static constexpr int WG = NG == 1 && kCtas == 1 ? 2 : 1;
+  static constexpr int WG = NQ == 16 && kCtas == 1 ? 2 : 1;
   static constexpr int kWarps = NG * 4, kThreads = (kWarps + WG * 8 + 4) * 32;
   static constexpr int kSmemBytes = kCtas == 2 ? 115712 : 232448;   // dynamic shared memory a CTA can have
   static constexpr int kTmem = 512 / kCtas;
@@ -93,14 +93,11 @@ struct Kv4 {
     static constexpr int T = NQ == 16 && kCtas == 1 ? 4 : NQ <= 48 ? 2 : 1;
   static constexpr int NS = NQ <= 96 ? 2 : 1;             // S buffers in tensor memory
   // Widened operands: slots of SW elements a lane, two to a column.
-  #ifndef SW16
-#define SW16 128
-#endif
-  static constexpr int SW = NQ == 144 ? 32 : NQ == 16 ? SW16 : 64;
+    static constexpr int SW = NQ < 144 ? 128 : D == 128 ? 64 : 32;
   static constexpr int kSlotCols = SW / 2;
   static constexpr int kColO = NS * T * NQ, kColA = kColO + MH * NQ;
   static constexpr int kSlotsLeft = (kTmem - kColA) / kSlotCols / WG;
-  static constexpr int KA = kSlotsLeft / 2 > 1 ? 2 : 1, VA = kSlotsLeft - KA > 1 ? 2 : 1;
+  static constexpr int KA = kSlotsLeft / 2 > 1 && D / SW > 1 ? 2 : 1, VA = kSlotsLeft - KA > 1 && kTile / SW * MH > 1 ? 2 : 1;
   // A tile takes the ring round KU (VU) times: which slot, and which phase of it, is known without counting.
   static constexpr int KU = D / SW / KA, VU = kTile / SW * MH / VA;
   static constexpr int kRecord = kv4_record(D), kTileBytes = 8 * kRecord;   // a page's K or V; a tile's
