@@ -97,7 +97,8 @@ def codes_and_scales(cache):
     k = codes[:, :, 0].reshape(pages, heads, nb, PAGE, 4 * 8).transpose(0, 1, 3, 2, 4).reshape(pages, heads, PAGE, dim)
     v = codes[:, :, 1].reshape(pages, heads, dim, PAGE).transpose(0, 1, 3, 2)
     raw = np.ascontiguousarray(cache[..., 8 * dim:]).view("<u2") & 0xFFF8
-    scales = (raw.astype(np.uint32) << 16).view(np.float32).astype(np.float64)
+    with np.errstate(invalid="ignore"):        # bits that are no number stay none
+        scales = (raw.astype(np.uint32) << 16).view(np.float32).astype(np.float64)
     sk = scales[:, :, 0].reshape(pages, heads, PAGE, nb)
     sv = scales[:, :, 1].reshape(pages, heads, nb, PAGE).transpose(0, 1, 3, 2)
     return (k, sk), (v, sv)

@@ -5,7 +5,7 @@ synchronisation between them, so a step can also be captured into a CUDA
 graph (``VerifyStep.capture``).  This module owns the output buffers and the
 workspaces; the inputs (queries, draft K/V, caches, logits, tree, page
 table) belong to the caller.  ``Kv8Cache`` and ``Kv8Step`` are the same over
-the 8-bit block-scaled cache, with its pages allocated on the GPU.
+the 8-bit block-scaled cache, with its pages allocated on the GPU, ``Kv4Cache`` and ``Kv4Step`` over the 4-bit one.
 """
 from __future__ import annotations
 
@@ -110,22 +110,25 @@ class VerifyStep:
         return g
 
 
-class Kv8Cache:
-    """A pool of 8-bit block-scaled K/V pages for every layer, its page tables, and the free list, all on the GPU.
+def rope_table(length: int, rot_dim: int, theta: float = 1e6, device="cuda") -> torch.Tensor:
+    """Cosines, then sines, of ``length`` positions for sd_rope_append, fp32 [length, rot_dim]; the angles are formed in
+    64 bits (in 32 those of far positions lose their digits)."""
+    dev = torch.device(device)
+    freq = theta ** (-torch.arange(0, rot_dim, 2, dtype=torch.float64, device=dev) / rot_dim)
+    angle = torch.arange(length, dtype=torch.float64, device=dev)[:, None] * freq
+    return torch.cat([angle.cos(), angle.sin()], 1).float().contiguous()
+
+
+class _PagedCache:
+    """Page tables and the free list of a pool of pages, all on the GPU.
 
     ``extend`` takes pages for joining tokens and appends their K/V, ``release`` gives pages back; both only
     launch kernels, so a step that contains them can be captured into a CUDA graph and replayed.  The calls of one
     cache follow each other: they share its state and scratch, so on two streams an event has to order them.
     """
 
-    def __init__(self, batch: int, max_pages_per_seq: int, num_pool_pages: int, num_layers: int,
-                 num_kv_heads: int = 4, head_dim: int = 256, device="cuda"):
-        dev = torch.device(device)
-        self.num_pool_pages = int(num_pool_pages)
-        codes = (num_layers, num_pool_pages, num_kv_heads, 16, head_dim)
-        self.k, self.v = (torch.zeros(codes, dtype=torch.uint8, device=dev) for _ in "kv")
-        dev = self.device = self.k.device       # "cuda" is the device that is current now
-        self.k_scales, self.v_scales = (torch.ones(codes[:3], dtype=torch.float32, device=dev) for _ in "kv")
+    def _init_pages(self, batch: int, max_pages_per_seq: int, num_pool_pages: int):
+        dev, self.num_pool_pages = self.device, int(num_pool_pages)
         ints = lambda *s: torch.zeros(s, dtype=torch.int32, device=dev)
         self.page_table = torch.full((batch, max_pages_per_seq), -1, dtype=torch.int32, device=dev)
         self.ctx_lens, self.held, self.free_count = ints(batch), ints(batch), ints(1)
@@ -155,8 +158,7 @@ class Kv8Cache:
             native.sd_pages_extend(self.ctx_lens, add_lens, self.page_table, self.held, new_held, self.free_list,
                                    self.free_count, new_count, slots, rows=rows, new_ctx_lens=new_ctx,
                                    q_indptr=q_indptr, path=path, dev_status=self.dev_status)
-            native.sd_kv8_append(self.k, self.v, self.k_scales, self.v_scales, k_new, v_new, slots, rows,
-                                 self.dev_status)
+            self._append(k_new, v_new, slots, rows)
             self._settle(ctx=True)
 
     def release(self, keep_lens, stream=None):
@@ -174,6 +176,40 @@ class Kv8Cache:
             self.dev_status |= said
 
 
+class Kv8Cache(_PagedCache):
+    """A pool of 8-bit block-scaled K/V pages for every layer, its page tables, and the free list, all on the GPU."""
+
+    def __init__(self, batch: int, max_pages_per_seq: int, num_pool_pages: int, num_layers: int,
+                 num_kv_heads: int = 4, head_dim: int = 256, device="cuda"):
+        dev = torch.device(device)
+        codes = (num_layers, num_pool_pages, num_kv_heads, 16, head_dim)
+        self.k, self.v = (torch.zeros(codes, dtype=torch.uint8, device=dev) for _ in "kv")
+        self.device = self.k.device       # "cuda" is the device that is current now
+        self.k_scales, self.v_scales = (torch.ones(codes[:3], dtype=torch.float32, device=self.device) for _ in "kv")
+        self._init_pages(batch, max_pages_per_seq, num_pool_pages)
+
+    def _append(self, k_new, v_new, slots, rows):
+        native.sd_kv8_append(self.k, self.v, self.k_scales, self.v_scales, k_new, v_new, slots, rows, self.dev_status)
+
+
+class Kv4Cache(_PagedCache):
+    """The same with 4-bit pages: ``kv`` uint8 [layers, pool, heads, 2, 9 * dim] (include/sd_kv4.h)."""
+
+    def __init__(self, batch: int, max_pages_per_seq: int, num_pool_pages: int, num_layers: int,
+                 num_kv_heads: int = 4, head_dim: int = 256, device="cuda"):
+        shape = native.kv4_cache_shape(num_pool_pages, num_kv_heads, head_dim)
+        self.kv = torch.zeros((num_layers, *shape), dtype=torch.uint8, device=torch.device(device))
+        self.device = self.kv.device      # "cuda" is the device that is current now
+        self._init_pages(batch, max_pages_per_seq, num_pool_pages)
+
+    def _append(self, k_new, v_new, slots, rows):
+        native.sd_kv4_append(self.kv, k_new, v_new, slots, rows, self.dev_status)
+
+    def read(self, slots, k_out, v_out, stream=None):
+        """The values at these slots, every layer's, as bf16 rows (sd_kv4_read)."""
+        native.sd_kv4_read(self.kv, slots, k_out, v_out, self.dev_status, stream)
+
+
 class Kv8Step:
     """One verify step over a Kv8Cache: every layer's attention, accept, the accepted path's pages and append."""
 
@@ -181,19 +217,26 @@ class Kv8Step:
                  softcap: float = 0.0, slopes=None, max_path: int | None = None):
         self.cache, self.vocab, self.softcap, self.slopes = cache, int(vocab), softcap, slopes
         self.q_indptr = np.asarray(q_indptr, dtype=np.int32)
-        layers, pool, heads, _, dim = cache.k.shape
+        layers, pool, heads, dim = self._geometry()
         batch, total, dev = len(self.q_indptr) - 1, int(self.q_indptr[-1]), cache.device
         self.shape = native.Shape(self.q_indptr, cache.page_table.shape[1], pool, window=window,
                                   num_q_heads=num_q_heads, num_kv_heads=heads, head_dim=dim)
         self.max_path = int(max_path or int(np.diff(self.q_indptr).max()))
         byte = lambda n: torch.empty(max(n, 16), dtype=torch.uint8, device=dev)
-        self.attn_ws = byte(native.sd_kv8_attn_workspace_size(self.shape))
+        self.attn_ws = byte(self._workspace_size())
         self.acc_ws = byte(native.sd_accept_workspace_size(self.q_indptr, self.vocab))
         ints = lambda *s: torch.empty(s, dtype=torch.int32, device=dev)
         self.out = torch.empty((layers, total, num_q_heads, dim), dtype=torch.bfloat16, device=dev)
         self.accept_len, self.target_tokens = ints(batch), ints(total)
         self.path, self.out_tokens = ints(batch, self.max_path), ints(batch, self.max_path)
         self.slots, self.rows = ints(total), ints(total)
+
+    def _geometry(self):
+        layers, pool, heads, _, dim = self.cache.k.shape
+        return layers, pool, heads, dim
+
+    def _workspace_size(self):
+        return native.sd_kv8_attn_workspace_size(self.shape)
 
     def attention(self, layer, q, k_new, v_new, parents, stream=None):
         c = self.cache
@@ -211,6 +254,53 @@ class Kv8Step:
                              self.out_tokens, self.target_tokens, self.max_path, self.acc_ws, self.cache.dev_status,
                              stream)
             self.cache.extend(self.accept_len, k_new, v_new, self.slots, self.rows, self.q_indptr, self.path, stream)
+
+
+class Kv4Step(Kv8Step):
+    """One verify step over a Kv4Cache; with ``top`` it also leaves every node's log probabilities: of the target's own
+    choice (``logprobs`` [nodes, 1]; the emitted tokens' are the rows of the accepted path) and of its ``top`` likeliest
+    tokens (``top_ids``, ``top_logprobs``), and the entropy."""
+
+    def __init__(self, cache: Kv4Cache, q_indptr, vocab: int, num_q_heads: int = 24, window: int = 0, softcap: float = 0.0,
+                 slopes=None, max_path: int | None = None, top: int = 0):
+        super().__init__(cache, q_indptr, vocab, num_q_heads, window, softcap, slopes, max_path)
+        self.top, total, dev = int(top), int(self.q_indptr[-1]), cache.device
+        layers, _, heads, dim = self._geometry()
+        self.q_turned, self.k_turned = (torch.empty((layers, total, h, dim), dtype=torch.bfloat16, device=dev)
+                                        for h in (num_q_heads, heads))
+        if self.top:
+            f32 = lambda *s: torch.empty(s, dtype=torch.float32, device=dev)
+            self.logprobs, self.top_logprobs, self.entropy = f32(total, 1), f32(total, self.top), f32(total)
+            self.top_ids = torch.empty((total, self.top), dtype=torch.int32, device=dev)
+            self.lp_ws = torch.empty(max(16, native.sd_logprobs_workspace_size(total, self.vocab, self.top)),
+                                     dtype=torch.uint8, device=dev)
+
+    def _geometry(self):
+        layers, pool, heads, _, width = self.cache.kv.shape
+        return layers, pool, heads, width // 9
+
+    def _workspace_size(self):
+        return native.sd_kv4_attn_workspace_size(self.shape)
+
+    def attention(self, layer, q, k_new, v_new, parents, stream=None):
+        c = self.cache
+        native.sd_kv4_attn(self.shape, q, c.kv[layer], k_new, v_new, c.page_table, c.ctx_lens, parents, self.out[layer],
+                           softcap=self.softcap, slopes=self.slopes, workspace=self.attn_ws, dev_status=c.dev_status,
+                           stream=stream)
+
+    def run(self, q, k_new, v_new, parents, draft_tokens, logits, stream=None, rope=None):
+        """As Kv8Step.run; ``rope`` = (table, positions of the nodes) turns q and k_new first."""
+        status = self.cache.dev_status
+        if rope is not None:
+            table, positions = rope
+            for layer in range(len(q)):
+                native.sd_rope_append(table, positions, q[layer], k_new[layer], q_out=self.q_turned[layer],
+                                      k_out=self.k_turned[layer], dev_status=status, stream=stream)
+            q, k_new = self.q_turned, self.k_turned
+        super().run(q, k_new, v_new, parents, draft_tokens, logits, stream)
+        if self.top:
+            native.sd_logprobs(logits, self.target_tokens[:, None], self.logprobs, self.top_ids, self.top_logprobs,
+                               self.entropy, workspace=self.lp_ws, dev_status=status, stream=stream)
 
 
 def device_inputs(w, device="cuda"):
