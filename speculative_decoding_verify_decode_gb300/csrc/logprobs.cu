@@ -9,17 +9,23 @@
 // is beside 1 (the log-probability of a near-certain token, and the entropy then, are nothing else).
 // m rises in few tiles: the others pay one warp maximum for it.  Base 2 inside: d carries log2 e.
 //
+// Exponents are formed as x f - M, f = log2 e / T, M = m f rounded: one packed fma for two logits (with the difference first,
+// and the type's own maxima, 12 instructions a logit became 8).  They are all off by r = m f - M, the exact
+// remainder of an fma, which is put right in the sums: s by 2^-r, w by 2^-r (w - r s).
+//
 // Top.  A logit and its index make one 64-bit key that orders as they do (value, then
 // the smaller index), so ties need no care and the `top` largest keys are one set.  A
-// CTA keeps them in a list with a bar, the smallest key that can still matter; a tile's
-// keys above the bar join the list, which is cut back to the `top` largest when it has
-// grown.  Before there is a bar one is taken from the tile: in each warp the j-th
-// largest of the threads' maxima with j = ceil(top / warps), the smallest of
-// them over the warps; at least `top` keys are no smaller.  Whatever the data,
-// the list has room for all of a tile (sorted rows are slow, not wrong).
+// warp's 512 neighbouring logits are a segment, of which the stream keeps the maximum alone.  The `top` best segments by
+// (maximum, then the smaller index) hold all of the set: what lies in another one has `top` maxima before it.
+// They are looked through again (most of it comes from L2), for logits that reach a bar that `top` keys reach for certain:
+// the last of those maxima, or the smallest over the warps of the ceil(top / warps)-th largest of the threads' maxima,
+// whichever is more.  (With a list and a bar that followed the stream, and a barrier for each 4096 logits, 2047 rows of
+// 151936 with 20 alternatives took 217 us, now 131.)
 //
-// Bound by HBM for many rows: 6 instructions and one ex2 a logit.  Rows are
-// cut into pieces over CTAs where there are few, and joined by a second launch.
+// Bound by HBM for many rows without alternatives (1824 rows of 151936 bf16 logits 88 us, 0.93 of the copy rate); with 20 of
+// them by what follows a row's stream, which the other three rows of an SM hide in part (115 us).  A fifth row
+// would spill registers (92 -> 153 us).  Rows are cut into pieces over CTAs where there are few, and joined by a second
+// launch.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -32,9 +38,10 @@ namespace {
 constexpr int kLpThreads = 256, kLpWarps = kLpThreads / 32;
 constexpr int kPer = 16;                        // logits of a thread that are looked at together
 constexpr int kGroup = kLpThreads * kPer;
-constexpr int kListCut = 64;                    // the list is cut back when it is longer
+constexpr int kSegment = 32 * kPer;             // logits that a warp looks at together
 constexpr int kFew = 2 * kLpThreads;            // keys that are ranked one by one
-constexpr int kListMax = kListCut + kGroup;
+constexpr int kListMax = 2048;
+constexpr int kMaxGroups = kListMax / kLpWarps; // of a piece: a key for each segment fits the list
 // 64 bytes of a thread are a tile, asked for while the tile before is looked at: 64 KB under way on an SM.
 template <typename T>
 constexpr int kLpTile = kLpThreads * 64 / (int)sizeof(T);
@@ -71,24 +78,20 @@ struct Stats {
     c = 0.f;
     m = to;
   }
-  __device__ __forceinline__ void join(Stats o, float f) {
-    if (o.m > m) rise(o.m, f);
-    if (m > o.m) o.rise(m, f);
-    c += o.c;
-    s += o.s;
-    w += o.w;
-  }
 };
 
 struct LpShared {
   Key list[kListMax];
-  Key bar;
   int n;             // keys in the list
+  int segment[SD_LOGPROBS_MAX_TOP];
   int count;         // of a search
-  Key few[kFew];     // what a cut looks at
-  uint32_t warp_bar[kLpWarps];
-  Key top_of[kLpWarps];
-  float m[kLpWarps], c[kLpWarps], s[kLpWarps], w[kLpWarps];
+  uint32_t warp_bar[kLpWarps], thread_bar[kLpWarps];
+  union {
+    float top_of[kListMax];      // segments' maxima
+    Key few[kFew];               // what a cut looks at
+  };
+  Key last[kLpWarps];
+  float4 stats[kLpWarps];
 };
 
 // The j-th largest of o over the warp's lanes (0 where there are fewer).
@@ -183,7 +186,8 @@ __device__ __noinline__ void cut_list(LpShared& sh, int n, int top) {
   __syncthreads();
 }
 
-// A 16-byte piece as floats.
+// 16-byte pieces: as floats, their maximum (NaN where there is one), and no smaller than a bound (of the type, in each half
+// of a word if it has two).
 template <typename T>
 struct Load;
 template <>
@@ -191,6 +195,14 @@ struct Load<float> {
   static constexpr int kVec = 4;
   static __device__ __forceinline__ void put(const uint4& v, float* x) {
     x[0] = __uint_as_float(v.x); x[1] = __uint_as_float(v.y); x[2] = __uint_as_float(v.z); x[3] = __uint_as_float(v.w);
+  }
+  static __device__ __forceinline__ uint32_t most(uint32_t a, uint32_t b) {
+    return __float_as_uint(max_nan(__uint_as_float(a), __uint_as_float(b)));
+  }
+  static __device__ __forceinline__ float most_of(uint32_t a) { return __uint_as_float(a); }
+  static __device__ __forceinline__ uint32_t bound(float lo) { return __float_as_uint(lo); }
+  static __device__ __forceinline__ uint32_t above(uint32_t a, uint32_t lo) {
+    return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(lo)));
   }
 };
 template <>
@@ -204,30 +216,61 @@ struct Load<__nv_bfloat16> {
       x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
     }
   }
+  static __device__ __forceinline__ uint32_t most(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+  }
+  static __device__ __forceinline__ float most_of(uint32_t a) {
+    return max_nan(__uint_as_float(a << 16), __uint_as_float(a & 0xffff0000u));
+  }
+  static __device__ __forceinline__ uint32_t bound(float lo) {     // rounded down
+    return (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rd(lo)) * 0x10001u;
+  }
+  static __device__ __forceinline__ uint32_t above(uint32_t a, uint32_t lo) {
+    uint32_t r;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(lo));
+    return r;
+  }
 };
 template <>
 struct Load<__half> {
   static constexpr int kVec = 8;
+  static __device__ __forceinline__ float2 pair(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2*>(&w)); }
   static __device__ __forceinline__ void put(const uint4& v, float* x) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+      const float2 f = pair(w[i]);
       x[2 * i] = f.x;
       x[2 * i + 1] = f.y;
     }
+  }
+  static __device__ __forceinline__ uint32_t most(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+  }
+  static __device__ __forceinline__ float most_of(uint32_t a) { return max_nan(pair(a).x, pair(a).y); }
+  static __device__ __forceinline__ uint32_t bound(float lo) { return (uint32_t)__half_as_ushort(__float2half_rd(lo)) * 0x10001u; }
+  static __device__ __forceinline__ uint32_t above(uint32_t a, uint32_t lo) {
+    uint32_t r;
+    asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(lo));
+    return r;
   }
 };
 template <typename T>
 __device__ __forceinline__ float value_of(T x) { return static_cast<float>(x); }
 
-// The logit of a row's t-th given token (one a thread); -infinity where it is none.
+// A row's t-th given token (one a thread; -1: none), and its logit; -infinity where it is none.
 static_assert(SD_LOGPROBS_MAX_GIVEN <= kLpThreads, "a thread for each given token");
+__device__ __forceinline__ int given_token(const LogprobsParams& p, int row) {
+  const int v = (int)threadIdx.x < p.given ? p.tokens[(size_t)row * p.given + threadIdx.x] : -1;
+  return v < p.vocab ? v : -1;
+}
 template <typename T>
-__device__ __forceinline__ float given_logit(const LogprobsParams& p, int row) {
-  if ((int)threadIdx.x >= p.given) return -INFINITY;
-  const int v = p.tokens[(size_t)row * p.given + threadIdx.x];
-  return v >= 0 && v < p.vocab ? value_of(static_cast<const T*>(p.logits)[(long long)row * p.row_stride + v]) : -INFINITY;
+__device__ __forceinline__ T logit_of(const LogprobsParams& p, int row, int token) {
+  return token >= 0 ? static_cast<const T*>(p.logits)[(long long)row * p.row_stride + token] : static_cast<T>(-INFINITY);
 }
 
 // A row's results from its statistics and (in sh.list, descending) its top keys.
@@ -255,167 +298,292 @@ __device__ void finish_row(const LogprobsParams& p, const LpShared& sh, int row,
 // Statistics over the warps, the same for every thread.
 __device__ __forceinline__ Stats block_stats(LpShared& sh, Stats st, float f) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const float m = warp_max(st.m);
+  if (st.m < m) st.rise(m, f);
 #pragma unroll
   for (int d = 16; d >= 1; d >>= 1) {
-    Stats o;
-    o.m = __shfl_xor_sync(0xffffffffu, st.m, d);
-    o.c = __shfl_xor_sync(0xffffffffu, st.c, d);
-    o.s = __shfl_xor_sync(0xffffffffu, st.s, d);
-    o.w = __shfl_xor_sync(0xffffffffu, st.w, d);
-    // the lower lane's first, so that both lanes compute the same
-    Stats a = (lane & d) ? o : st;
-    a.join((lane & d) ? st : o, f);
-    st = a;
+    st.c += __shfl_xor_sync(0xffffffffu, st.c, d);
+    st.s += __shfl_xor_sync(0xffffffffu, st.s, d);
+    st.w += __shfl_xor_sync(0xffffffffu, st.w, d);
   }
-  if (lane == 0) { sh.m[warp] = st.m; sh.c[warp] = st.c; sh.s[warp] = st.s; sh.w[warp] = st.w; }
+  if (lane == 0) sh.stats[warp] = make_float4(m, st.c, st.s, st.w);
   __syncthreads();
-  st.m = sh.m[0]; st.c = sh.c[0]; st.s = sh.s[0]; st.w = sh.w[0];
+  Stats all;
+  all.m = -INFINITY;
+  all.c = all.s = all.w = 0.f;
 #pragma unroll
-  for (int w = 1; w < kLpWarps; ++w) {
-    Stats o;
-    o.m = sh.m[w]; o.c = sh.c[w]; o.s = sh.s[w]; o.w = sh.w[w];
-    st.join(o, f);
+  for (int w = 0; w < kLpWarps; ++w) all.m = fmaxf(all.m, sh.stats[w].x);
+#pragma unroll
+  for (int w = 0; w < kLpWarps; ++w) {
+    const float4 o = sh.stats[w];
+    Stats x;
+    x.m = o.x; x.c = o.y; x.s = o.z; x.w = o.w;
+    if (x.m < all.m) x.rise(all.m, f);
+    all.c += x.c;
+    all.s += x.s;
+    all.w += x.w;
   }
-  return st;
+  return all;
 }
+
+__device__ __forceinline__ float2 lp_fma2(float2 a, float2 b, float2 c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(r)
+      : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)), "l"(*reinterpret_cast<uint64_t*>(&c)));
+  return *reinterpret_cast<float2*>(&r);
+}
+__device__ __forceinline__ float2 lp_add2(float2 a, float2 b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)));
+  return *reinterpret_cast<float2*>(&r);
+}
+
+// The sums of tiles below the maximum, with exponents y f - M (see above), and what goes with that maximum.
+struct Quick {
+  float2 s, w;
+  float less, r;        // -M; m f - M
+  uint32_t lo;          // what counts for nothing counts as this, so that no exponent is infinite
+  float floor;          // the same as a float
+  bool on;
+  __device__ __forceinline__ void clear() { s = w = make_float2(0.f, 0.f); }
+  __device__ __forceinline__ void into(Stats& st) {
+    if (on) {
+      const float all = s.x + s.y, a = fast_exp2(-r);
+      st.s = fmaf(a, all, st.s);
+      st.w = fmaf(a, fmaf(-r, all, w.x + w.y), st.w);
+    }
+    clear();
+  }
+  template <typename T>
+  __device__ __forceinline__ void none() {
+    on = false;
+    lo = Load<T>::bound(-INFINITY);
+    floor = -INFINITY;
+  }
+  // far: 512 / f.  Not for maxima whose product with f is large (r would be), nor where the type has no number far enough
+  // below.
+  template <typename T>
+  __device__ __forceinline__ void follow(float m, float f, float far) {
+    less = -(m * f);
+    r = fmaf(m, f, less);
+    lo = Load<T>::bound(m - far);
+    float y[Load<T>::kVec];
+    Load<T>::put(make_uint4(lo, lo, lo, lo), y);
+    floor = y[0];
+    on = fabsf(less) < 1048576.f && floor > -INFINITY && (m - floor) * f < 1e30f;
+    if (!on) none<T>();
+  }
+};
 
 // VEC: the rows start on 16 bytes and so does every 16-byte piece of them.
 template <typename T, bool TOP, bool VEC>
-__global__ void __launch_bounds__(kLpThreads, TOP ? 4 : 5) logprobs_piece_kernel(const LogprobsParams p) {
+__global__ void __launch_bounds__(kLpThreads, 4) logprobs_piece_kernel(const LogprobsParams p) {
   __shared__ LpShared sh;
   constexpr int kVec = Load<T>::kVec, kTile = kLpTile<T>, kPieces = kPer / kVec, kGroups = kTile / kGroup;
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const int row = blockIdx.x / p.pieces, piece = blockIdx.x - row * p.pieces;
   const T* x = static_cast<const T*>(p.logits) + (long long)row * p.row_stride;
   const int begin = piece * p.piece, end = min(p.vocab, begin + p.piece);
-  const float f = p.inv_t * kLog2eLp;
+  const float f = p.inv_t * kLog2eLp, far = 512.f / f;
   pdl_wait();
-  if (TOP && t == 0) { sh.n = 0; sh.bar = 0; }
   Stats st;
   st.m = -INFINITY;
   st.c = st.s = st.w = 0.f;
+  Quick quick;
+  quick.clear();
+  quick.none<T>();
+  float most = -INFINITY;      // of this thread
   bool bad = false;
-  // A thread's logits of a tile: 16-byte piece j at begin + (j * kLpThreads + t) * kVec.
+  // A 16-byte piece; what lies past the end counts as tokens that cannot come.
+  auto piece_at = [&](int v) {
+    if (VEC && v + kVec <= end) return __ldcs(reinterpret_cast<const uint4*>(x + v));
+    alignas(16) T e[kVec];
+#pragma unroll
+    for (int k = 0; k < kVec; ++k) e[k] = v + k < end ? x[v + k] : static_cast<T>(-INFINITY);
+    return *reinterpret_cast<const uint4*>(e);
+  };
+  // A thread's logits of a tile: of its warp's segment in each group, kPieces pieces; a group's are asked for when those of
+  // the tile before it have become floats.
   uint4 raw[4];
-  auto fetch = [&](int at) {
+  int from = begin + warp * kSegment + lane * kVec;      // of the pieces that are asked for next
+  auto fetch = [&](int g) {
+    if (VEC && from + (g * kGroup + (kPieces - 1) * 32 * kVec + kVec) <= end) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int v = at + (j * kLpThreads + t) * kVec;
-      if (VEC && v + kVec <= end) {
-        raw[j] = __ldcs(reinterpret_cast<const uint4*>(x + v));
-      } else {
-        // what lies past the end counts as tokens that cannot come
-        alignas(16) T e[kVec];
+      for (int j = 0; j < kPieces; ++j)
+        raw[g * kPieces + j] = __ldcs(reinterpret_cast<const uint4*>(x + from) + (g * kGroup / kVec + j * 32));
+    } else {
 #pragma unroll
-        for (int k = 0; k < kVec; ++k) e[k] = v + k < end ? x[v + k] : static_cast<T>(-INFINITY);
-        raw[j] = *reinterpret_cast<const uint4*>(e);
-      }
+      for (int j = 0; j < kPieces; ++j) raw[g * kPieces + j] = piece_at(from + g * kGroup + j * 32 * kVec);
     }
   };
-  fetch(begin);
+  // Where a row is one long stream, the tile after the next is asked for into L2, as the registers hold one (2047 rows of
+  // 151936 144 -> 131 us; four tiles on 132; for rows in three pieces 63 -> 64).
+  auto ahead = [&](int at) {
+    if (VEC && p.pieces == 1 && t == 0 && at < end) {
+      const uint32_t bytes = (uint32_t)min(kTile, end - at) * (uint32_t)sizeof(T) & ~15u;
+      if (bytes > 0u) asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(x + at), "r"(bytes) : "memory");
+    }
+  };
+#pragma unroll
+  for (int g = 0; g < kGroups; ++g) fetch(g);
+  ahead(begin + kTile);
+  const int token = p.pieces == 1 ? given_token(p, row) : -1;      // (its logit: once the stream is over)
 #pragma unroll 1
   for (int tile = begin; tile < end; tile += kTile) {
-    uint4 held[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) held[j] = raw[j];
-    if (tile + kTile < end) fetch(tile + kTile);
+    from += kTile;
+    ahead(tile + 2 * kTile);
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) {
-    const int at = tile + g * kGroup;
-    if (at >= end) break;
-    float y[kPer];
+      const int at = tile + g * kGroup + warp * kSegment;
+      if (at >= end) break;
+      uint32_t big = raw[g * kPieces].x;
 #pragma unroll
-    for (int j = 0; j < kPieces; ++j) Load<T>::put(held[g * kPieces + j], y + j * kVec);
-    float top = y[0];
-#pragma unroll
-    for (int e = 1; e < kPer; ++e) top = max_nan(top, y[e]);
-    bad |= top != top;
-    const float warp_top = warp_max(top);
-    // a logit of -infinity: e^d = 0, and d is kept finite so that the product is 0
-    if (warp_top >= st.m) {
-      if (warp_top > st.m) st.rise(warp_top, f);
-      const float m = st.m == -INFINITY ? 0.f : st.m;
-#pragma unroll
-      for (int e = 0; e < kPer; ++e) {
-        const float d = fmaxf((y[e] - m) * f, -1e30f), a = fast_exp2(d);
-        const bool at_top = y[e] == m;
-        st.c += at_top ? 1.f : 0.f;
-        st.s += at_top ? 0.f : a;
-        st.w = fmaf(a, d, st.w);
+      for (int j = 0; j < kPieces; ++j) {
+        const uint4 v = raw[g * kPieces + j];
+        big = Load<T>::most(Load<T>::most(Load<T>::most(big, v.x), Load<T>::most(v.y, v.z)), v.w);
       }
-      bad |= warp_top == INFINITY;
-    } else {
-      float sum = 0.f, w = 0.f;
-#pragma unroll
-      for (int e = 0; e < kPer; ++e) {
-        const float d = fmaxf((y[e] - st.m) * f, -1e30f), a = fast_exp2(d);
-        sum += a;
-        w = fmaf(a, d, w);
+      const float top = Load<T>::most_of(big);
+      bad |= top != top;
+      const float warp_top = warp_max(top);
+      if (TOP) {
+        most = fmaxf(most, top);
+        if (lane == 0) sh.top_of[(at - begin) / kSegment] = warp_top;
       }
-      st.s += sum;
-      st.w += w;
-    }
-    if (TOP) {
-      if (at == begin) {
-        // a first bar (32 bits of it): in each warp the j-th largest of the threads' maxima
-        uint32_t o = order_of(top);
-        if (top != top) o = 0u;
-        const uint32_t jth = warp_jth(o, (p.top + kLpWarps - 1) / kLpWarps);
-        if (lane == 0) sh.warp_bar[warp] = jth;
-        __syncthreads();
-        uint32_t bar = sh.warp_bar[0];
-#pragma unroll
-        for (int w2 = 1; w2 < kLpWarps; ++w2) bar = min(bar, sh.warp_bar[w2]);
-        if (t == 0) sh.bar = (Key)bar << 32;
-        __syncthreads();
+      if (warp_top > st.m) {
+        quick.into(st);
+        st.rise(warp_top, f);
+        quick.follow<T>(warp_top, f, far);
+        bad |= warp_top == INFINITY;
       }
-      const Key bar = sh.bar;
-      const float bar_value = order_value((uint32_t)(bar >> 32));   // (NaN for 0: every comparison below then holds)
-      // this thread's logits that reach the bar, a bit each: few, taken one after the other
-      uint32_t pass = 0;
-      bool pushed = false;
-      if (__any_sync(0xffffffffu, !(top < bar_value))) {
+      float y[kPer];
 #pragma unroll
-        for (int e = 0; e < kPer; ++e) pass |= y[e] < bar_value ? 0u : 1u << e;
-#pragma unroll 1
-        while (__any_sync(0xffffffffu, pass != 0)) {
-          const int e0 = __ffs(pass) - 1;      // -1: none
-          float value = 0.f;
+      for (int j = 0; j < kPieces; ++j) {
+        const uint4 v = raw[g * kPieces + j];
+        Load<T>::put(make_uint4(Load<T>::above(v.x, quick.lo), Load<T>::above(v.y, quick.lo), Load<T>::above(v.z, quick.lo),
+                                Load<T>::above(v.w, quick.lo)), y + j * kVec);
+      }
+      if (tile + kTile < end) fetch(g);
+      if (warp_top == st.m && warp_top > -INFINITY) {
+        float c = 0.f;
 #pragma unroll
-          for (int e = 0; e < kPer; ++e) value = e0 == e ? y[e] : value;
-          const int v = at + ((e0 / kVec) * kLpThreads + t) * kVec + e0 % kVec;
-          const Key k = key_of(value, v);
-          const bool ok = pass != 0 && v < end && k >= bar && value == value;
-          const uint32_t who = __ballot_sync(0xffffffffu, ok);
-          if (who != 0u) {
-            int place = 0;
-            if (lane == 0) place = atomicAdd(&sh.n, __popc(who));
-            place = __shfl_sync(0xffffffffu, place, 0) + __popc(who & ((1u << lane) - 1u));
-            if (ok) sh.list[place] = k;
-            pushed = true;
-          }
-          pass &= pass - 1u;
+        for (int e = 0; e < kPer; ++e) {
+          const bool at_top = y[e] == st.m;
+          c += at_top ? 1.f : 0.f;
+          y[e] = at_top ? quick.floor : y[e];
         }
+        st.c += c;
       }
-      // a tile in which nobody had anything leaves the list as it was
-      if (__syncthreads_or(pushed ? 1 : 0)) {
-        const int n = sh.n;
-        __syncthreads();
-        if (n > kListCut || (at == begin && n > p.top)) {
-          cut_list(sh, n, p.top);
-          if (t == 0) {
-            sh.n = min(n, p.top);
-            if (n >= p.top) sh.bar = sh.list[p.top - 1];
-          }
-          __syncthreads();
+      if (quick.on) {
+        float2 sum = make_float2(0.f, 0.f), w = sum;
+#pragma unroll
+        for (int e = 0; e < kPer; e += 2) {
+          const float2 d = lp_fma2(make_float2(y[e], y[e + 1]), make_float2(f, f), make_float2(quick.less, quick.less));
+          const float2 a = make_float2(fast_exp2(d.x), fast_exp2(d.y));
+          sum = lp_add2(sum, a);
+          w = lp_fma2(a, d, w);
         }
+        quick.s = lp_add2(quick.s, sum);
+        quick.w = lp_add2(quick.w, w);
+      } else if (st.m > -INFINITY) {
+        // rare; d is kept finite, so that the product is 0 where e^d is
+        float sum = 0.f, w = 0.f;
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) {
+          const float d = fmaxf((y[e] - st.m) * f, -1e30f), a = fast_exp2(d);
+          sum += a;
+          w = fmaf(a, d, w);
+        }
+        st.s += sum;
+        st.w += w;
       }
-    }
     }
   }
+  const T given = logit_of<T>(p, row, token);
+  quick.into(st);
   if (TOP) {
-    const int n = sh.n;
+    const int segments = (end - begin + kSegment - 1) / kSegment;
+    // a bar from the threads' maxima: `top` of them at least are no smaller
+    const uint32_t jth = warp_jth(most != most ? 0u : order_of(most), (p.top + kLpWarps - 1) / kLpWarps);
+    if (lane == 0) sh.thread_bar[warp] = jth;
+    if (t == 0) sh.n = 0;
     __syncthreads();
+    uint32_t bar = sh.thread_bar[0];
+#pragma unroll
+    for (int w = 1; w < kLpWarps; ++w) bar = min(bar, sh.thread_bar[w]);
+    // the segments that reach it: about twice `top`, if not all the same
+    for (int i = t; i < segments; i += kLpThreads) {
+      const uint32_t o = order_of(sh.top_of[i]);
+      if (o >= bar) sh.list[atomicAdd(&sh.n, 1)] = (Key)o << 32 | (uint32_t)~i;
+    }
+    __syncthreads();
+    int taken = sh.n;
+    if (taken > p.top) {
+      cut_list(sh, taken, p.top);
+      taken = p.top;
+      bar = max(bar, (uint32_t)(sh.list[p.top - 1] >> 32));
+    }
+    if (t < taken) sh.segment[t] = (int)~(uint32_t)sh.list[t];
+    if (t == 0) sh.n = 0;
+    __syncthreads();
+    const float reach = order_value(bar);
+#pragma unroll 1
+    for (int i = warp; i < taken; i += kLpWarps) {
+      const int at = begin + sh.segment[i] * kSegment + lane * kVec;
+      uint32_t pass = 0;       // this lane's logits that reach the bar, a bit each
+      float y[kPer];
+#pragma unroll
+      for (int j = 0; j < kPieces; ++j) {
+        const int v = at + j * 32 * kVec;
+        Load<T>::put(piece_at(v), y + j * kVec);
+#pragma unroll
+        for (int k = 0; k < kVec; ++k) pass |= y[j * kVec + k] >= reach ? 1u << (j * kVec + k) : 0u;
+        if (v + kVec > end) pass &= ~(((1u << kVec) - 1u) << j * kVec) | (((1u << max(end - v, 0)) - 1u) << j * kVec);
+      }
+      auto key = [&](int e) {
+        const int v = at + e / kVec * (32 * kVec) + e % kVec;
+        return key_of(value_of(x[v]), v);
+      };
+      int count = __reduce_add_sync(0xffffffffu, __popc(pass));
+      if (count > 64) {
+        // (sorted logits: all of a segment) a bar of its own, from the threads' maxima as above
+        float own = -INFINITY;
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) own = (pass >> e) & 1u ? fmaxf(own, y[e]) : own;
+        own = order_value(warp_jth(pass != 0u ? order_of(own) : order_of(-INFINITY), p.top));
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) pass &= y[e] >= own ? ~0u : ~(1u << e);
+        count = __reduce_add_sync(0xffffffffu, __popc(pass));
+      }
+      if (count <= 64) {
+#pragma unroll 1
+        for (; pass != 0; pass &= pass - 1u) {
+          const Key k = key(__ffs(pass) - 1);
+          sh.list[atomicAdd(&sh.n, 1)] = k;
+        }
+        __syncwarp();
+      } else {
+        // many alike: the segment's best, one by one, as many as there can be in the set
+#pragma unroll 1
+        for (int k = 0; k < p.top && __any_sync(0xffffffffu, pass != 0); ++k) {
+          Key best = 0;
+#pragma unroll 1
+          for (uint32_t left = pass; left != 0; left &= left - 1u) {
+            const Key c = key(__ffs(left) - 1);
+            best = c > best ? c : best;
+          }
+          const uint32_t hi = __reduce_max_sync(0xffffffffu, (uint32_t)(best >> 32));
+          const uint32_t lo = __reduce_max_sync(0xffffffffu, (uint32_t)(best >> 32) == hi ? (uint32_t)best : 0u);
+          if (best == ((Key)hi << 32 | lo)) {
+            sh.list[atomicAdd(&sh.n, 1)] = best;
+            const int off = (int)~lo - at;        // j * 32 kVec + k
+            pass &= ~(1u << (off / (32 * kVec) * kVec + off % (32 * kVec)));
+          }
+        }
+      }
+    }
+    __syncthreads();
+    const int n = sh.n;
     cut_list(sh, n, p.top);
     // a piece with fewer than `top` keys (the last of a row, or one with NaN): the rest sort behind everything
     for (int i = min(n, p.top) + t; i < p.top; i += kLpThreads) sh.list[i] = 0;
@@ -423,7 +591,7 @@ __global__ void __launch_bounds__(kLpThreads, TOP ? 4 : 5) logprobs_piece_kernel
   const bool any_bad = __syncthreads_or(bad ? 1 : 0) != 0;
   st = block_stats(sh, st, f);
   if (p.pieces == 1) {
-    finish_row<T>(p, sh, row, st, any_bad, given_logit<T>(p, row));
+    finish_row<T>(p, sh, row, st, any_bad, value_of(given));
   } else {
     if (t == 0) p.stats[blockIdx.x] = make_float4(st.m, any_bad ? NAN : st.c, st.s, st.w);
     if (TOP)
@@ -432,7 +600,7 @@ __global__ void __launch_bounds__(kLpThreads, TOP ? 4 : 5) logprobs_piece_kernel
 }
 
 // The pieces of a row joined: at most kMaxPieces of them.
-constexpr int kMaxPieces = 128;
+constexpr int kMaxPieces = 64;
 static_assert(kMaxPieces * SD_LOGPROBS_MAX_TOP <= kListMax && kMaxPieces <= kLpThreads, "a row's keys fit the list");
 
 template <typename T>
@@ -441,7 +609,7 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_join_kernel(const Logprob
   const int row = blockIdx.x, t = threadIdx.x;
   const float f = p.inv_t * kLog2eLp;
   pdl_wait();
-  const float given = given_logit<T>(p, row);
+  const float given = value_of(logit_of<T>(p, row, given_token(p, row)));
   Stats st;
   st.m = -INFINITY;
   st.c = st.s = st.w = 0.f;
@@ -462,11 +630,11 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_join_kernel(const Logprob
     const Key last = t < p.pieces ? keys[(size_t)t * p.top + p.top - 1] : 0;
     const uint32_t hi = __reduce_max_sync(0xffffffffu, (uint32_t)(last >> 32));
     const uint32_t lo = __reduce_max_sync(0xffffffffu, (uint32_t)(last >> 32) == hi ? (uint32_t)last : 0u);
-    if ((t & 31) == 0) sh.top_of[t >> 5] = (Key)hi << 32 | lo;
+    if ((t & 31) == 0) sh.last[t >> 5] = (Key)hi << 32 | lo;
     __syncthreads();
     Key bar = 0;
 #pragma unroll
-    for (int w = 0; w < kLpWarps; ++w) bar = sh.top_of[w] > bar ? sh.top_of[w] : bar;
+    for (int w = 0; w < kLpWarps; ++w) bar = sh.last[w] > bar ? sh.last[w] : bar;
     for (int i = t; i < p.pieces * p.top; i += kLpThreads) {
       const Key k = keys[i];
       if (k != 0 && k >= bar) sh.list[atomicAdd(&sh.n, 1)] = k;
@@ -489,6 +657,7 @@ int pieces_of(int rows, int vocab, int* piece) {
   int n = rows >= 3 * wave ? 1 : rows > wave / 2 ? (2 * wave + rows - 1) / rows : (wave + rows - 1) / rows;
   n = n < groups ? n : groups;
   n = n < kMaxPieces ? n : kMaxPieces;
+  if (n * kMaxGroups < groups) n = (groups + kMaxGroups - 1) / kMaxGroups;      // (at most 16)
   const int per = (groups + n - 1) / n;
   *piece = per * kGroup;
   return (groups + per - 1) / per;

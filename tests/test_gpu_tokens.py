@@ -281,3 +281,41 @@ def test_logprobs_are_the_same_bits_every_time_and_in_a_graph():
     g.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(out[k], first[k]) for k in first)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_long_rows_where_the_set_is_hard_to_find(dtype):
+    """Rows that one CTA works through alone: sorted, alike, few values, masked, a late rise."""
+    rows, vocab, top = 1830, 41001, 32
+    gen = torch.Generator().manual_seed(4)
+    x = torch.randn(rows, vocab, generator=gen).mul_(3).to(dtype)
+    ramp = torch.linspace(-20, 20, vocab)
+    some = {0: ramp, 1: -ramp, 2: torch.full((vocab,), 1.5), 3: (torch.arange(vocab) % 3).float(), 4: torch.full((vocab,), -math.inf),
+            5: torch.where(torch.arange(vocab) > vocab - 20, 1.0, -math.inf), 6: torch.cat([torch.zeros(vocab - 5), torch.full((5,), 40.0)]),
+            7: torch.where(torch.arange(vocab) % 512 == 511, 2.0, 0.0), 8: torch.where(torch.arange(vocab) // 512 == 40, 2.0, 0.0),
+            9: torch.full((vocab,), torch.finfo(dtype).min), 10: torch.cat([torch.full((vocab - 40,), torch.finfo(dtype).min), torch.zeros(40)])}
+    for r, v in some.items():
+        x[r] = v.to(dtype)
+        x[rows - 1 - r] = v.to(dtype)
+    x, out, status = run(x, tokens=torch.randint(vocab, (rows, 3), generator=gen), top=top, dtype=dtype)
+    assert status == 0
+    check(x, out, rows=[r for r in some if r != 4] + [rows - 1, rows - 9, 100, 900, 1500])
+    for r in (4, rows - 5):        # nothing but -infinity: exact
+        assert float(out["entropy"][r]) == 0.0 and float(out["lse"][r]) == -math.inf and out["top_ids"][r].tolist() == list(range(top))
+        assert torch.all(out["logprobs"][r] == -math.inf) and torch.all(out["top_logprobs"][r] == -math.inf)
+
+
+@pytest.mark.parametrize("dtype,size,temperature", [(torch.float16, 1.0, 1000.0), (torch.float16, 20.0, 60.0), (torch.float16, 1.0, 100.0),
+                                                    (torch.bfloat16, 1e4, 1e-3), (torch.float32, 3e6, 1.0), (torch.float32, 1.0, 1e30),
+                                                    (torch.float32, 1e30, 1e30), (torch.bfloat16, 1e35, 1e36)])
+@pytest.mark.parametrize("rows", [1, 700])
+def test_scales_of_logits_and_temperatures(rows, dtype, size, temperature):
+    """Where the exponents' shift is large, or the type has nothing far enough below the maximum; masked tokens count nothing."""
+    gen = torch.Generator().manual_seed(9)
+    x = torch.randn(rows, 9001, generator=gen)
+    x[:, 100:4000] = -math.inf
+    x[0, 8000] = 6.0
+    x[rows - 1, 9000] = 7.0
+    x, out, status = run((x * size).to(dtype), tokens=torch.randint(9001, (rows, 4), generator=gen), top=7, temperature=temperature, dtype=dtype)
+    assert status == 0
+    check(x, out, rows=[0, rows - 1, rows // 2], temperature=temperature)
