@@ -8,15 +8,20 @@
 // multiple of 2^-16, is right in both cases, and no division is needed.  Two values share each step: the maxima are of
 // 16-bit pairs, the roundings of fp32 pairs.
 //
-// One warp owns one (layer, K or V, page, KV head): the page's new rows are
+// One warp owns one (layer, K or V, half page, KV head): the half's new rows are
 // in its registers, so bytes are read once, and V's words, which hold eight
 // tokens each, are put together without a second writer.  A lane has eight
 // consecutive dims: four lanes are a block, two shuffles its maximum.  K's words go through
-// shared memory (a row's lie 256 bytes apart), so that both records leave in
-// 16-byte pieces.  Bound by HBM: 2 bytes read and 9/16 written a value.
+// shared memory (a row's lie 256 bytes apart), so that its record leaves in
+// 16-byte pieces; V's codes add up in halves of a word, two dims at a time.  Every warp finds its rows in the slot map for
+// itself.  2 bytes read and 9/16 written a value, and some 15 instructions, which bound it: 8191 rows of 4 heads of 256
+// dims take 16 us where their bytes take 6.4 (whole pages a warp, 128 registers: 17.6); 6 rows of 16 layers take 3.4, of
+// which a launch is 2.
 //
 // Read.  One warp per (layer, K or V, KV head, up to 16 entries of the slot map); V's
-// words of a page are loaded once for the entries that lie on it.
+// words of a page are loaded once for the entries that lie on it.  16383 rows of 4 heads of 256 dims take 17 us, 0.75 of
+// the copy rate; half of the instructions' rate is in use, so neither bound is near.  (V's scales of all entries first:
+// 18.2.)
 #include "kernels.h"
 #include "kv4_format.cuh"
 
@@ -88,83 +93,85 @@ __device__ __forceinline__ float fast_rcp(float x) {
 }
 
 template <int D>
-__global__ void __launch_bounds__(kRowsThreads, 4) kv4_append_kernel(const Kv4RowsParams p, const int window) {
+__global__ void __launch_bounds__(kRowsThreads, 6) kv4_append_kernel(const Kv4RowsParams p, const int window) {
   constexpr int kLanes = D / 8;            // lanes per row (8 values each)
   constexpr int kRowsAtOnce = 32 / kLanes; // rows a warp touches per step
-  constexpr int kSteps = kPage / kRowsAtOnce;
+  constexpr int kHalf = kPage / 2, kSteps = kHalf / kRowsAtOnce;
   constexpr int kBlocks = D / kKv4Block;
-  __shared__ int s_lead[kPage], s_n;
-  __shared__ __align__(16) uint32_t s_k[kRowsWarps][kPage * D / 8];
-  const int layer = blockIdx.y;
-  const int r_base = blockIdx.x * window;
-  if (threadIdx.x < 32) {
-    const int t = threadIdx.x, r = r_base + t;
-    bool lead = false;
-    if (t < window && r < p.max_rows) {
-      const int slot = p.slots[r], prev = r > 0 ? p.slots[r - 1] : -1;
-      if (slot < -1 || slot / kPage >= p.num_pool_pages) {
-        if (layer == 0) report(p.dev_status, SD_DEV_BAD_SLOT);
-      } else if (slot >= 0) {
-        lead = prev < 0 || prev / kPage != slot / kPage;
-      }
-    }
-    const uint32_t m = __ballot_sync(0xffffffffu, lead);
-    if (lead) s_lead[__popc(m & ((1u << t) - 1u))] = r;
-    if (t == 0) s_n = __popc(m);
-  }
-  __syncthreads();
+  __shared__ __align__(16) uint32_t s_k[kRowsWarps][kHalf * D / 8];
+  const int layer = blockIdx.y, r_base = blockIdx.x * window;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int combos = 2 * p.heads;
+  const int combo = blockIdx.z * kRowsWarps + warp;
+  if (combo >= 4 * p.heads) return;
+  const int head = combo >> 2, half = combo & 1;      // tokens 0..7 of the page, or 8..15
+  const bool is_v = combo & 2;
   const int col = lane % kLanes, sub = lane / kLanes;
-#pragma unroll 1
-  for (int task = blockIdx.z * kRowsWarps + warp; task < s_n * combos; task += gridDim.z * kRowsWarps) {
-    const int r0 = s_lead[task / combos], combo = task % combos;
-    const int head = combo >> 1;
-    const bool is_v = combo & 1;
-    // the group: the following rows on the same page, which must rise by one (a seventeenth cannot)
-    const int slot0 = p.slots[r0], page = slot0 / kPage, first = slot0 % kPage;
-    int slot = -1, src = -1;
-    if (lane <= kPage && r0 + lane < p.max_rows) {
-      slot = p.slots[r0 + lane];
-      src = p.rows != nullptr ? p.rows[r0 + lane] : r0 + lane;
+  // The window's entries and the 16 behind it, one a lane: every warp finds its groups for itself, in one latency.
+  int slot = -1, src = -1, prev = -1;
+  if (r_base + lane < p.max_rows) {
+    slot = p.slots[r_base + lane];
+    src = p.rows != nullptr ? p.rows[r_base + lane] : r_base + lane;
+  }
+  if (lane == 0 && r_base > 0) prev = p.slots[r_base - 1];
+  const int up = __shfl_up_sync(0xffffffffu, slot, 1);
+  if (lane > 0) prev = up;
+  bool lead = false;
+  if (lane < window) {
+    if (slot < -1 || slot / kPage >= p.num_pool_pages) {
+      if (layer == 0 && combo == 0) report(p.dev_status, SD_DEV_BAD_SLOT);
+    } else if (slot >= 0) {
+      lead = prev < 0 || prev / kPage != slot / kPage;
     }
-    const bool same = lane <= kPage && slot >= 0 && slot / kPage == page;
-    const int n = __ffs(~__ballot_sync(0xffffffffu, same)) - 1;   // 1..17
-    const bool wrong = lane < n && (slot != slot0 + lane || src < 0 || src >= p.num_src_rows);
+  }
+#pragma unroll 1
+  for (uint32_t leads = __ballot_sync(0xffffffffu, lead); leads != 0u; leads &= leads - 1u) {
+    // the group: the following rows on the same page, which must rise by one (a seventeenth cannot)
+    const int l0 = __ffs(leads) - 1;
+    const int slot0 = __shfl_sync(0xffffffffu, slot, l0), page = slot0 / kPage, first = slot0 % kPage;
+    const bool same = lane >= l0 && slot >= 0 && slot / kPage == page;
+    const int n = __ffs(~(__ballot_sync(0xffffffffu, same) >> l0 & 0x1ffffu)) - 1;   // 1..17
+    const int i_lane = lane - l0;
+    const bool wrong = i_lane >= 0 && i_lane < n && (slot != slot0 + i_lane || src < 0 || src >= p.num_src_rows);
     if (__any_sync(0xffffffffu, wrong)) {
       if (lane == 0 && layer == 0) report(p.dev_status, SD_DEV_BAD_SLOT);
       continue;
     }
+    // the half's tokens that get a row
+    const int lo = max(first, half * kHalf) - half * kHalf, hi = min(first + n, half * kHalf + kHalf) - half * kHalf;
+    if (lo >= hi) continue;
     const __nv_bfloat16* x = (is_v ? p.v_rows[layer] : p.k_rows[layer]) + head * D + col * 8;
-    // A lane's rows by their token in the page: step k is token k * kRowsAtOnce + sub.
+    // A lane's rows by their token in the half: step k is token k * kRowsAtOnce + sub.
     uint4 v[kSteps];
     bool any_wild = false;
 #pragma unroll
     for (int k = 0; k < kSteps; ++k) {
-      const int i = k * kRowsAtOnce + sub - first;
-      const int from = __shfl_sync(0xffffffffu, src, i < 0 || i >= n ? 0 : i);
+      const int token = k * kRowsAtOnce + sub;
+      const bool mine = token >= lo && token < hi;
+      const int from = __shfl_sync(0xffffffffu, src, mine ? l0 + token + half * kHalf - first : l0);
       v[k] = make_uint4(0, 0, 0, 0);
-      if (i >= 0 && i < n) v[k] = __ldg(reinterpret_cast<const uint4*>(x + (long long)from * p.stride));
+      if (mine) v[k] = __ldg(reinterpret_cast<const uint4*>(x + (long long)from * p.stride));
     }
     uint8_t* const rec = p.cache[layer] + (((size_t)page * p.heads + head) * 2 + (is_v ? 1 : 0)) * kv4_record(D);
     uint16_t* const scales = reinterpret_cast<uint16_t*>(rec + kv4_codes(D));
-    uint4 old[4];                          // V: what a page that stays in part holds
+    const bool whole = lo == 0 && hi == kHalf;
+    uint32_t* const words = reinterpret_cast<uint32_t*>(rec) + col * 16 + half;      // V: this lane's dims, two words apart
+    // V: codes of two dims in the halves of a sum, four bits on for every second token; sums of the even and the odd tokens
+    // (over 128 dims the two halves of the warp have one each)
+    constexpr int kSums = 2 / kRowsAtOnce;
+    uint32_t acc[kSums][4], old[8];        // old: what a half page that stays in part holds
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      old[e] = make_uint4(0, 0, 0, 0);
-      if (is_v && n < kPage && sub == 0) old[e] = reinterpret_cast<const uint4*>(rec + col * 64)[e];
+    for (int e = 0; e < 4 * kSums; ++e) acc[e / 4][e % 4] = 0u;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      old[e] = 0u;
+      if (is_v && !whole && sub == 0) old[e] = words[2 * e];
     }
-    uint32_t acc[2][8];                    // V: the words of this lane's dims
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) acc[h][e] = 0u;
 #pragma unroll
     for (int k = 0; k < kSteps; ++k) {
       const int token = k * kRowsAtOnce + sub;
       // (the same for the whole warp: nobody has a row of this step)
-      if (k * kRowsAtOnce + kRowsAtOnce <= first || k * kRowsAtOnce >= first + n) continue;
-      const bool mine = token >= first && token < first + n;
+      if (k * kRowsAtOnce + kRowsAtOnce <= lo || k * kRowsAtOnce >= hi) continue;
+      const bool mine = token >= lo && token < hi;
       // The largest of the block's values and of their negatives, as integers, where one of the two is above the other.
       const uint32_t flip = 0x80008000u;
       uint32_t up = __vmaxs2(__vmaxs2(v[k].x, v[k].y), __vmaxs2(v[k].z, v[k].w));
@@ -173,10 +180,10 @@ __global__ void __launch_bounds__(kRowsThreads, 4) kv4_append_kernel(const Kv4Ro
       uint32_t most = __vmaxs2(__byte_perm(up, down, 0x5410), __byte_perm(up, down, 0x7632));
       most = __vmaxs2(most, __shfl_xor_sync(0xffffffffu, most, 1));
       most = __vmaxs2(most, __shfl_xor_sync(0xffffffffu, most, 2));
-      const int hi = (int)(short)(most & 0xffffu), lo = (int)(short)(most >> 16);
-      uint32_t key = hi > lo ? (uint32_t)hi << 6 : (uint32_t)lo << 6 | 1u;
+      const int pos = (int)(short)(most & 0xffffu), neg = (int)(short)(most >> 16);
+      uint32_t key = pos > neg ? (uint32_t)pos << 6 : (uint32_t)neg << 6 | 1u;
       // ties of magnitude, what is no number, and magnitudes that the largest scale does not reach
-      if (__any_sync(0xffffffffu, hi == lo || max(hi, lo) >= 0x7e80)) {
+      if (__any_sync(0xffffffffu, pos == neg || max(pos, neg) >= 0x7e80)) {
         key = top_key(v[k], (lane & 3) * 8);
         key = max(key, __shfl_xor_sync(0xffffffffu, key, 1));
         key = max(key, __shfl_xor_sync(0xffffffffu, key, 2));
@@ -189,22 +196,15 @@ __global__ void __launch_bounds__(kRowsThreads, 4) kv4_append_kernel(const Kv4Ro
       const uint32_t s = scale_of(key);
       const float inv = s == 0u ? 0.f : fast_rcp(bf16_value(s));
       if (mine && (lane & 3) == 0) {
-        const int block = col >> 2;
-        scales[is_v ? block * kPage + token : token * kBlocks + block] = (uint16_t)s;
+        const int block = col >> 2, in_page = token + half * kHalf;
+        scales[is_v ? block * kPage + in_page : in_page * kBlocks + block] = (uint16_t)s;
       }
       const uint32_t c[4] = {codes2(v[k].x, inv), codes2(v[k].y, inv), codes2(v[k].z, inv), codes2(v[k].w, inv)};
       if (!is_v) {
-        s_k[warp][(col >> 2) * (kPage * 4) + token * 4 + (col & 3)] = c[0] | c[1] << 4 | c[2] << 8 | c[3] << 12;
+        s_k[warp][(col >> 2) * (kHalf * 4) + token * 4 + (col & 3)] = c[0] + (c[1] << 4) + (c[2] << 8) + (c[3] << 12);
       } else {
-        // a dim's code into the half of its token's parity, four bits on for every two tokens
-        const int h = k / (kSteps / 2);
-        const bool odd = kRowsAtOnce == 1 ? (k & 1) : sub;
-        const int shift = kRowsAtOnce == 1 ? 4 * ((k & 7) >> 1) : 4 * (k & 3);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          acc[h][2 * e] |= __byte_perm(c[e], 0u, odd ? 0x1044 : 0x4410) << shift;
-          acc[h][2 * e + 1] |= __byte_perm(c[e], 0u, odd ? 0x3244 : 0x4432) << shift;
-        }
+        for (int e = 0; e < 4; ++e) acc[k % kSums][e] += c[e] << (4 * (k / kSums));
       }
     }
     if (any_wild) report(p.dev_status, SD_DEV_NOT_FINITE);
@@ -212,35 +212,29 @@ __global__ void __launch_bounds__(kRowsThreads, 4) kv4_append_kernel(const Kv4Ro
       __syncwarp();
       // 16-byte pieces: [block][token]
 #pragma unroll
-      for (int k = 0; k < kBlocks * kPage / 32; ++k) {
-        const int e = k * 32 + lane, token = e % kPage;
-        if (token >= first && token < first + n)
-          reinterpret_cast<uint4*>(rec)[e] = reinterpret_cast<const uint4*>(s_k[warp])[e];
+      for (int k = 0; k < kBlocks * kHalf / 32; ++k) {
+        const int e = k * 32 + lane, token = e % kHalf;
+        if (token >= lo && token < hi)
+          reinterpret_cast<uint4*>(rec)[e / kHalf * kPage + half * kHalf + token] = reinterpret_cast<const uint4*>(s_k[warp])[e];
       }
       __syncwarp();
     } else {
-      if (kRowsAtOnce == 2) {              // the other half of the lanes has the other tokens of the same dims
+      uint32_t word[8];
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int e = 0; e < 8; ++e) acc[h][e] |= __shfl_xor_sync(0xffffffffu, acc[h][e], 16);
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t even = acc[0][e], odd = kSums == 2 ? acc[kSums - 1][e] : __shfl_xor_sync(0xffffffffu, even, 16);
+        word[2 * e] = __byte_perm(even, odd, 0x5410);
+        word[2 * e + 1] = __byte_perm(even, odd, 0x7632);
       }
-      uint32_t keep[2] = {0u, 0u};         // codes of tokens that get no row
-      if (n < kPage) {
+      uint32_t keep = 0u;                  // codes of tokens that get no row
+      if (!whole) {
 #pragma unroll
-        for (int t = 0; t < kPage; ++t)
-          if (t < first || t >= first + n) keep[t >> 3] |= 15u << kv4_shift(t & 7);
+        for (int t = 0; t < kHalf; ++t)
+          if (t < lo || t >= hi) keep |= 15u << kv4_shift(t);
       }
-      uint4* at = reinterpret_cast<uint4*>(rec + col * 64);
       if (sub == 0) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          uint4 o = make_uint4(acc[0][2 * e], acc[1][2 * e], acc[0][2 * e + 1], acc[1][2 * e + 1]);
-          if (n < kPage)
-            o = make_uint4((o.x & ~keep[0]) | (old[e].x & keep[0]), (o.y & ~keep[1]) | (old[e].y & keep[1]),
-                           (o.z & ~keep[0]) | (old[e].z & keep[0]), (o.w & ~keep[1]) | (old[e].w & keep[1]));
-          at[e] = o;
-        }
+        for (int e = 0; e < 8; ++e) words[2 * e] = (word[e] & ~keep) | (old[e] & keep);
       }
     }
   }
@@ -333,7 +327,7 @@ cudaError_t launch_kv4_append(const Kv4RowsParams& p, int dim, cudaStream_t st) 
   // accepted path); for prompts sixteen, of which one begins a page.
   const int window = (long long)p.max_rows * p.num_layers <= 4 * kSMs ? 1 : kPage;
   // enough CTAs per window for one page's tasks, a warp each
-  const int share = (2 * p.heads + kRowsWarps - 1) / kRowsWarps;
+  const int share = (4 * p.heads + kRowsWarps - 1) / kRowsWarps;
   const dim3 grid((p.max_rows + window - 1) / window, p.num_layers, share);
   if (dim == 256)
     kv4_append_kernel<256><<<grid, kRowsThreads, 0, st>>>(p, window);
