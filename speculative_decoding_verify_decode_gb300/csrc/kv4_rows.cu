@@ -106,6 +106,7 @@ __global__ void __launch_bounds__(kRowsThreads, 6) kv4_append_kernel(const Kv4Ro
   const int head = combo >> 2, half = combo & 1;      // tokens 0..7 of the page, or 8..15
   const bool is_v = combo & 2;
   const int col = lane % kLanes, sub = lane / kLanes;
+  pdl_wait();
   // The window's entries and the 16 behind it, one a lane: every warp finds its groups for itself, in one latency.
   int slot = -1, src = -1, prev = -1;
   if (r_base + lane < p.max_rows) {
@@ -329,11 +330,8 @@ cudaError_t launch_kv4_append(const Kv4RowsParams& p, int dim, cudaStream_t st) 
   // enough CTAs per window for one page's tasks, a warp each
   const int share = (4 * p.heads + kRowsWarps - 1) / kRowsWarps;
   const dim3 grid((p.max_rows + window - 1) / window, p.num_layers, share);
-  if (dim == 256)
-    kv4_append_kernel<256><<<grid, kRowsThreads, 0, st>>>(p, window);
-  else
-    kv4_append_kernel<128><<<grid, kRowsThreads, 0, st>>>(p, window);
-  return cudaGetLastError();
+  return dim == 256 ? launch_pdl(kv4_append_kernel<256>, grid, dim3(kRowsThreads), 0, st, p, window)
+                    : launch_pdl(kv4_append_kernel<128>, grid, dim3(kRowsThreads), 0, st, p, window);
 }
 
 cudaError_t launch_kv4_read(const Kv4RowsParams& p, int dim, cudaStream_t st) {
