@@ -50,14 +50,14 @@ constexpr int kTile = kTileTokens;     // tokens of a product's M
 constexpr float kRise = 16.0f;         // log2 of the weight beyond which a reference moves
 constexpr float kLog2e = 1.4426950408889634f;
 
-template <int NQ, int WG, int MH, bool MOD>
+template <int NQ, int VW, int MH, bool MOD>
 struct Kv4Small {
-  static constexpr int kBars = 64;
+  static constexpr int kBars = 56;
   float m[NQ];             // the column's reference, negated: -m
   float alpha[NQ];         // rescale factor of the current tile; 1 / l in the epilogue
   float slope[MOD ? NQ : 4];   // distance bias of the column, base 2
   float red[4][NQ];        // per lane quarter: column maxima of a tile; column sums in the epilogue
-  alignas(16) uint2 vs[WG * 4][MH][64];       // per V warp: scales of a tile's token pairs, and -24 times them
+  alignas(16) uint2 vs[VW][MH][64];           // per V warp: scales of a tile's token pairs, and -24 times them
   unsigned long long anc[kMaxNodes];          // bit r: node r is on the node's root path; in the draft CTA then turned
                                               // round, bit n: node n sees the row
   uint64_t bar[kBars];
@@ -83,18 +83,30 @@ struct Kv4 {
   // dims one CTA with two groups is faster (64 sequences of 1 to 32768 tokens 427 us against 463).
   static constexpr int kCtas = kv4_ctas(NQ, D);
   static constexpr int WG = NQ == 16 && kCtas == 1 ? 2 : 1;
-  static constexpr int kWarps = NG * 4, kThreads = (kWarps + WG * 8 + 4) * 32;
+  // 144 columns: tensor memory has room for short slots only, and one S buffer, so the widening of K is waited for.  Each of
+  // its two slots has a group of four warps of its own, which widens its next values before the slot is free, and the
+  // products of QK go before those of PV (tree of 23 over 131072 tokens 97 -> 91 us; the other widths gain nothing by it).
+  static constexpr int KG = NQ < 144 ? 1 : 2;
+  static constexpr int kWarps = NG * 4, kWideK = WG * KG * 4, kWideV = WG * 4, kThreads = (kWarps + kWideK + kWideV + 4) * 32;
+  // Registers of the launch, and the roles' shares of them.
+  static constexpr int kLaunchRegs = 65536 / kCtas / kThreads / 8 * 8;
+  static constexpr int kRegsSoft = kCtas == 2 ? 88 : NG == 3 ? 104 : 136;
+  static constexpr int kRegsWide = kCtas == 2 ? 64 : NG == 3 ? 48 : 72;
+  static constexpr int kRegsRest = kCtas == 2 ? 40 : NG == 3 ? 40 : 56;
+  static_assert(kWarps * kRegsSoft + (kWideK + kWideV) * kRegsWide + 4 * kRegsRest <= kThreads / 32 * kLaunchRegs, "registers");
   static constexpr int kSmemBytes = kCtas == 2 ? 115712 : 232448;   // dynamic shared memory a CTA can have
   static constexpr int kTmem = 512 / kCtas;
   static constexpr int MH = D / 128;                      // 128-dim blocks
-  using Small = Kv4Small<NQ, WG, MH, MOD>;
+  using Small = Kv4Small<NQ, kWideV, MH, MOD>;
   // Tiles that pass the softmax together: what a turn costs beyond them (barriers, the references' check, bookkeeping)
   // is as much as sixteen columns of a tile or two.
     static constexpr int T = NQ == 16 && kCtas == 1 ? 4 : NQ <= 48 ? 2 : 1;
   static constexpr int NS = NQ <= 96 ? 2 : 1;             // S buffers in tensor memory
   // Widened operands: slots of SW elements a lane, two to a column.
-    static constexpr int SW = NQ < 144 ? 128 : D == 128 ? 64 : 32;
+  static constexpr int SW = NQ < 144 ? 128 : D == 128 ? 64 : 32;
   static constexpr int kSlotCols = SW / 2;
+  // Short slots: the first values are widened before their slot is waited for.
+  static constexpr bool kEarly = SW < 128;
   static constexpr int kColO = NS * T * NQ, kColA = kColO + MH * NQ;
   static constexpr int kSlotsLeft = (kTmem - kColA) / kSlotCols / WG;
   static constexpr int KA = kSlotsLeft / 2 > 1 && D / SW > 1 ? 2 : 1, VA = kSlotsLeft - KA > 1 && kTile / SW * MH > 1 ? 2 : 1;
@@ -111,6 +123,7 @@ struct Kv4 {
   static constexpr int kPageStride = kJoint ? 2 * kRecord : kRecord, kSlotBytes = 8 * kPageStride;
   static constexpr size_t kRingBytes = (size_t)(kJoint ? KS : KS + VS) * WG * kSlotBytes;
   static constexpr size_t kSmem = (size_t)kQBytes + 2 * kPBytes + kRingBytes + sizeof(Small);
+  static_assert(KG == 1 || KA == KG, "a slot for each group");
   static_assert(KS * WG >= 2 && VS * WG >= 2, "rings of two tiles at least");
   static_assert(kColA + WG * (KA + VA) * kSlotCols <= kTmem, "tensor memory");
   static_assert(KU * KA * SW == D && VU * VA * SW == kTile * MH, "slots of a tile");
@@ -247,14 +260,14 @@ template <int D, int NG, int CC, bool MOD>
 __global__ void __launch_bounds__(Kv4<D, NG, CC, MOD>::kThreads, Kv4<D, NG, CC, MOD>::kCtas)
 kv4_attn_kernel(const Kv4AttnParams p, const BatchDesc bd) {
   using K = Kv4<D, NG, CC, MOD>;
-  constexpr int NQ = K::NQ, MH = K::MH, NS = K::NS, KS = K::KS, VS = K::VS, KA = K::KA, VA = K::VA, SW = K::SW, WG = K::WG,
+  constexpr int NQ = K::NQ, MH = K::MH, NS = K::NS, KS = K::KS, VS = K::VS, KA = K::KA, VA = K::VA, SW = K::SW, WG = K::WG, KG = K::KG,
                 T = K::T;
   constexpr int kWarps = K::kWarps, kAllThreads = K::kThreads;      // softmax warps; all threads
-  constexpr int kWarpWideK = kWarps, kWarpWideV = kWarps + WG * 4, kWarpK = kWarps + WG * 8, kWarpV = kWarpK + 1,
+  constexpr int kWarpWideK = kWarps, kWarpWideV = kWarps + K::kWideK, kWarpK = kWarpWideV + K::kWideV, kWarpV = kWarpK + 1,
                 kWarpQK = kWarpK + 2;
   using Sm = typename K::Small;
   constexpr int B_KF = 0, B_KE = B_KF + KS * WG, B_VF = K::kJoint ? B_KF : B_KE + KS * WG, B_VE = K::kJoint ? B_KE : B_VF + VS * WG,
-                B_AKF = B_VE + VS * WG, B_AKE = B_AKF + KA * WG, B_AVF = B_AKE + KA * WG, B_AVE = B_AVF + VA * WG, B_SF = B_AVE + VA * WG, B_SE = B_SF + NS, B_PF = B_SE + NS,
+                B_AKF = B_VE + VS * WG, B_AKE = B_AKF + KA * WG, B_AVF = B_AKE + KA * WG, B_AVE = B_AVF + VA * WG, B_SF = B_AVE + VA * WG, B_SE = B_SF + 2, B_PF = B_SE + NS,
                 B_OD = B_PF + 2, B_Q = B_OD + 2, B_G = B_Q + 1;
   constexpr int kNumBars = B_G + NG;
   static_assert(kNumBars <= Sm::kBars, "barriers");
@@ -276,15 +289,13 @@ kv4_attn_kernel(const Kv4AttnParams p, const BatchDesc bd) {
     const int L = p.ctx_lens[b];
     return L < 0 ? 0 : min(L, p.max_pages * kPage);
   };
-  if (tid == 0) {
-#pragma unroll 1
-    for (int i = 0; i < kNumBars; ++i) {
-      const bool empties = (i >= B_KE && i < B_KE + KS * WG) || (i >= B_VE && i < B_VE + VS * WG);
-      const bool by_four = (i >= B_AKF && i < B_AKE) || (i >= B_AVF && i < B_AVE) || i >= B_G;
-      const bool by_softmax = (i >= B_SE && i < B_SE + NS) || i == B_PF || i == B_PF + 1;
-      mbar_init(smem_u32(&sm->bar[i]), by_softmax ? (uint32_t)kWarps : empties ? (K::kJoint ? 8u : 4u) : by_four ? 4u : 1u);
-    }
-    sm->abort = 0;
+  if (tid < kNumBars) {
+    const int i = tid;
+    const bool k_empty = i >= B_KE && i < B_KE + KS * WG, v_empty = i >= B_VE && i < B_VE + VS * WG;     // both where the ring is joint
+    const bool by_four = (i >= B_AKF && i < B_AKE) || (i >= B_AVF && i < B_AVE) || i >= B_G;
+    const bool by_softmax = (i >= B_SE && i < B_SE + NS) || i == B_PF || i == B_PF + 1;
+    mbar_init(smem_u32(&sm->bar[i]), by_softmax ? (uint32_t)kWarps : k_empty || v_empty ? (k_empty ? 4u * KG : 0u) + (v_empty ? 4u : 0u) : by_four ? 4u : 1u);
+    if (i == 0) sm->abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   // Launched as a programmatic dependent: everything above touches no global memory; here the previous kernel's writes
@@ -457,11 +468,8 @@ kv4_attn_kernel(const Kv4AttnParams p, const BatchDesc bd) {
   // A position that some query sees: from the root's oldest visible one on.
   auto first_seen = [&](int L) { return p.window > 0 ? L - p.window + 1 : 0; };
 
-  // The block is launched with 61440 registers (768 x 80, 640 x 96): the softmax warps take 112 (three groups) or 136 each,
-  // the widening ones 56 or 72, the others 32 or 56.
   if (warp >= kWarpK) {
-    if (K::kCtas == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-    else if (NG == 3) asm volatile("setmaxnreg.dec.sync.aligned.u32 32;"); else asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(K::kRegsRest));
     if (warp <= kWarpV) {
       // ---------------------------------------------------------- producers (where the ring is joint, the first alone)
       // Page ids come a group of four tiles at a time (lane l: page l % 8 of the group's l / 8), two groups ahead of
@@ -552,7 +560,7 @@ kv4_attn_kernel(const Kv4AttnParams p, const BatchDesc bd) {
     } else if (warp == kWarpQK) {
       // ---------------------------------------------------------- QK issuer
       Ring s_ring;
-      int np = 0, turn = 0;
+      int np = 0, it = 0, turn = 0;
       uint32_t phase = 0;            // of a group's slots: a bit each
       bool ok = true;
       const uint64_t q_desc = sw128_desc(smem_u32(sQ), 16, 1024);
@@ -594,7 +602,7 @@ kv4_attn_kernel(const Kv4AttnParams p, const BatchDesc bd) {
                       umma_ta<2>(d, a0, b, idesc, k > 0 ? 1u : 0u);
                   }
                   umma_commit(empty + 8 * s);
-                  if (s == KA - 1 && k == K::KU - 1 && j == n - 1) umma_commit(bar(B_SF + s_ring.at));
+                  if (s == KA - 1 && k == K::KU - 1 && j == n - 1) umma_commit(bar(B_SF + (NS == 2 ? s_ring.at : it & 1)));
                 }
                 __syncwarp();
               }
@@ -604,6 +612,7 @@ kv4_attn_kernel(const Kv4AttnParams p, const BatchDesc bd) {
             turn = turn + 1 == WG ? 0 : turn + 1;
           }
           s_ring.next(NS);
+          ++it;
         }
       }
     } else {
@@ -626,6 +635,10 @@ kv4_attn_kernel(const Kv4AttnParams p, const BatchDesc bd) {
         for (int i = pc.first, n; i < end && ok; i += n, ++it) {
           n = min(T, end - i);
           ok = __all_sync(0xffffffffu, wait(B_PF + (it & 1), it >> 1));
+          // With one S buffer the next QK has waited for the same softmax, and the softmax waits for it: it goes first, and this
+          // PV beside that softmax.  (Two barriers in turn, so that the one after the next cannot complete unseen: its
+          // softmax needs this PV.)
+          if (NS == 1 && i + n < end) ok = __all_sync(0xffffffffu, wait(B_SF + ((it + 1) & 1), (it + 1) >> 1)) && ok;
           uint64_t b = it & 1 ? p_desc1 : p_desc0;
 #pragma unroll 1
           for (int j = 0; j < n && ok; ++j, b += kTile) {
@@ -672,11 +685,11 @@ kv4_attn_kernel(const Kv4AttnParams p, const BatchDesc bd) {
   } else if (warp >= kWarpWideK) {
     // ------------------------------------------------------------ the widening warps
     // After an expired wait no other one waits, and they run through.
-    if (K::kCtas == 2) { } else
-    if (NG == 3) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;"); else asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (K::kRegsWide < K::kLaunchRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(K::kRegsWide));
     const bool is_k = warp < kWarpWideV;
     const int quarter = warp & 3, row = quarter * 32 + lane;
-    const int group = (warp - (is_k ? kWarpWideK : kWarpWideV)) >> 2;
+    const int of_four = (warp - (is_k ? kWarpWideK : kWarpWideV)) >> 2;
+    const int group = is_k ? of_four / KG : of_four, part = is_k ? of_four % KG : 0;     // whose tiles, and which slot of K's
     const uint32_t a_base = tmem + ((uint32_t)(quarter * 32) << 16) + K::kColA + (is_k ? group * KA : KA * WG + group * VA) * K::kSlotCols;
     const uint32_t a_full = bar(is_k ? B_AKF + group * KA : B_AVF + group * VA), a_empty = bar(is_k ? B_AKE + group * KA : B_AVE + group * VA);
     const int n_ring = is_k ? KS : VS, b_full = (is_k ? B_KF : B_VF) + group * n_ring, b_empty = (is_k ? B_KE : B_VE) + group * n_ring;
@@ -712,6 +725,7 @@ kv4_attn_kernel(const Kv4AttnParams p, const BatchDesc bd) {
 #pragma unroll 1
           for (int n = 0; n < (is_k ? K::KU * KA : K::VU * VA); ++n) {
             const int s = n % (is_k ? KA : VA), k = n / (is_k ? KA : VA);
+            if (KG == 2 && is_k && s != part) continue;
             slot_free(s, (is_k ? K::KU : K::VU) % 2 == 0 ? k & 1 : odd ^ (k & 1));
             if (is_k) {
               const uint4* src = reinterpret_cast<const uint4*>(p.k_new + (long long)(q0 + min(row, n_nodes - 1)) * p.k_stride + pc.g * D);
@@ -756,24 +770,35 @@ kv4_attn_kernel(const Kv4AttnParams p, const BatchDesc bd) {
           const uint8_t* rec = buf + ring.at * K::kSlotBytes + (row >> 4) * K::kPageStride;
           const uint8_t* words = rec + (row & 15) * 16;
           uint16_t* sc = reinterpret_cast<uint16_t*>(const_cast<uint8_t*>(rec) + kv4_codes(D) + (row & 15) * (D / 16));
-          bool odd_scale = false;      // one with bits that do not count, or beyond the largest
+          // of this group's blocks: with bits that do not count, or beyond the largest
+          auto mine_of = [&](int e) {      // blocks 2 e and 2 e + 1
+            return KG == 1 ? ~0u : SW == 32 ? 0xffffu << (16 * part) : (e * 64 / SW) % 2 == part ? ~0u : 0u;
+          };
+          bool odd_scale = false;
 #pragma unroll
           for (int e = 0; e < D / 64; ++e) {
-            const uint32_t two = reinterpret_cast<const uint32_t*>(sc)[e], most = kKv4BadScale - 1u | (kKv4BadScale - 1u) << 16;
+            const uint32_t two = reinterpret_cast<const uint32_t*>(sc)[e] & mine_of(e), most = kKv4BadScale - 1u | (kKv4BadScale - 1u) << 16;
             odd_scale |= (two & 0x00070007u) != 0u || __vmaxu2(two & 0x7fff7fffu, most) != most;
           }
-          if (odd_scale) {             // rare: put right in place (nobody else reads this token's)
+          if (odd_scale) {             // rare: put right in place (nobody else reads these)
             bool bad = false;
 #pragma unroll 1
-            for (int e = 0; e < D / 64; ++e) reinterpret_cast<uint32_t*>(sc)[e] = kv4_sane(reinterpret_cast<uint32_t*>(sc)[e], bad);
+            for (int e = 0; e < D / 32; ++e) {
+              if ((mine_of(e >> 1) >> (16 * (e & 1)) & 1u) == 0u) continue;
+              sc[e] = (uint16_t)kv4_sane(sc[e], bad);
+            }
             fence_async_smem();
             if (bad && t0 + row < pc.L && t0 + row >= seen) report(p.dev_status, SD_DEV_BAD_SCALE);
           }
+          if (KG == 2) {
+            words += part * (SW / 32) * (kPage * 16);
+            sc += part * (SW / 32);
+          }
 #pragma unroll 1
-          for (int n = 0; n < K::KU * KA; ++n) {
+          for (int n = KG == 2 ? part : 0; n < K::KU * KA; n += KG) {
             const int s = n % KA, k = n / KA;
             const uint32_t to = a_base + s * K::kSlotCols;
-            slot_free(s, K::KU % 2 == 0 ? k & 1 : odd ^ (k & 1));
+            if (!K::kEarly) slot_free(s, K::KU % 2 == 0 ? k & 1 : odd ^ (k & 1));
 #pragma unroll 1
             for (int h = 0; h < SW / 32; ++h) {
               const uint4 w = *reinterpret_cast<const uint4*>(words);
@@ -784,7 +809,12 @@ kv4_attn_kernel(const Kv4AttnParams p, const BatchDesc bd) {
               uint32_t x[16];
 #pragma unroll
               for (int e = 0; e < 16; ++e) x[e] = kv4_pair(ww[e >> 2], e & 3, sv, less);
+              if (K::kEarly && h == 0) slot_free(s, K::KU % 2 == 0 ? k & 1 : odd ^ (k & 1));
               tmem_st16u(to + h * 16, x);
+            }
+            if (KG == 2) {
+              words += (KG - 1) * (SW / 32) * (kPage * 16);
+              sc += (KG - 1) * (SW / 32);
             }
             slot_done(s);
           }
@@ -814,10 +844,11 @@ kv4_attn_kernel(const Kv4AttnParams p, const BatchDesc bd) {
             const __nv_bfloat162 less = kv4_less(kv4_scale2(s2));
             vs[mb * 64 + pair] = make_uint2(s2, *reinterpret_cast<const uint32_t*>(&less));
           }
+          __syncwarp();
 #pragma unroll 1
           for (int n = 0; n < K::VU * VA; ++n) {
             const int s = n % VA, k = n / VA, mb = n % MH, ts = n / MH;      // 128-dim block mb of SW tokens
-            slot_free(s, K::VU % 2 == 0 ? k & 1 : odd ^ (k & 1));
+            if (!K::kEarly) slot_free(s, K::VU % 2 == 0 ? k & 1 : odd ^ (k & 1));
             const uint8_t* words = pages + ts * (SW / 16) * K::kPageStride + (mb * 128 + row) * 8;
             const uint4* sl_at = reinterpret_cast<const uint4*>(vs + mb * 64 + ts * (SW / 2));
             const uint32_t to = a_base + s * K::kSlotCols;
@@ -832,6 +863,7 @@ kv4_attn_kernel(const Kv4AttnParams p, const BatchDesc bd) {
                 x[e] = kv4_pair(word, e & 3, kv4_scale2(sl.x), kv4_scale2(sl.y));
                 x[e + 1] = kv4_pair(word, (e & 3) + 1, kv4_scale2(sl.z), kv4_scale2(sl.w));
               }
+              if (K::kEarly && h == 0) slot_free(s, K::VU % 2 == 0 ? k & 1 : odd ^ (k & 1));
               tmem_st16u(to + h * 16, x);
             }
             slot_done(s);
@@ -845,8 +877,7 @@ kv4_attn_kernel(const Kv4AttnParams p, const BatchDesc bd) {
     }
   } else {
     // ------------------------------------------------------------ softmax warps
-    if (K::kCtas == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 88;");
-    else if (NG == 3) asm volatile("setmaxnreg.inc.sync.aligned.u32 112;"); else asm volatile("setmaxnreg.inc.sync.aligned.u32 136;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(K::kRegsSoft));
     const int group = warp >> 2, quarter = warp & 3;
     const int row = quarter * 32 + lane;                       // token row of S; dim (mod 128) of O^T
     const uint32_t lane_addr = (uint32_t)(quarter * 32) << 16;
@@ -867,7 +898,9 @@ kv4_attn_kernel(const Kv4AttnParams p, const BatchDesc bd) {
       const bool has_draft = pc.first == 0;
       // ---------------------------------------------------------- staging: Q and the tree
       // (the previous piece's products have all finished: its last scores and its last O were waited for)
-      if (tid < n_nodes) {
+      // the tree, where something goes by it: the draft block, a window's depths, a bias
+      const bool needs_tree = has_draft || MOD || p.window > 0;
+      if (needs_tree && tid < n_nodes) {
         const int up = p.parents[q0 + tid];
         sm->par[tid] = (int8_t)(up < -1 || up >= kMaxNodes ? -2 : up);
         sm->wild[tid] = 0;
@@ -875,7 +908,7 @@ kv4_attn_kernel(const Kv4AttnParams p, const BatchDesc bd) {
       {
         constexpr int LPR = D / 8, RPW = 32 / LPR;                     // lanes per row, rows per warp and load
         constexpr int U = (NQ + kWarps * RPW - 1) / (kWarps * RPW);    // a warp's query rows, RPW at a time
-        constexpr int UB = U < 4 ? U : 4;                              // of them in flight
+        constexpr int UB = U < 12 ? U : 12;                            // of them in flight
         const int sub = lane / LPR, ch = lane % LPR;                   // 8-value chunk of the row
         const int n_q = nc * 16;
         const float inv_hpc = 1.0f / (float)hpc;
@@ -921,7 +954,7 @@ kv4_attn_kernel(const Kv4AttnParams p, const BatchDesc bd) {
         if (MOD) sm->slope[q] = p.slopes != nullptr && q < rows ? p.slopes[head0 + q % hpc] * kLog2e : 0.f;
       }
       // the tree: root paths and depths
-      if (tid < n_nodes) {
+      if (needs_tree && tid < n_nodes) {
         unsigned long long a = 1ull << tid;
         int d = 0;
         bool good = sm->par[tid] >= -1 && (tid > 0 || sm->par[0] == -1);
@@ -978,7 +1011,7 @@ kv4_attn_kernel(const Kv4AttnParams p, const BatchDesc bd) {
         // Scores that are more than a multiple of the product are formed first and put back in its place.
         const bool formed = MOD || masked;
         const float mul = formed ? 1.f : fac;
-        wait_full(B_SF, s_ring);
+        if (NS == 2) wait_full(B_SF, s_ring); else wait(B_SF + (it & 1), it >> 1);
         __syncwarp();
         tc_fence_after();
         const uint32_t s_addr = tmem + lane_addr + s_ring.at * T * NQ + col0;

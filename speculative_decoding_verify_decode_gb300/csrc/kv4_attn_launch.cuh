@@ -2,6 +2,8 @@
 // kind is a translation unit of its own, so that they compile side by side.
 #pragma once
 
+#include <atomic>
+
 #include "common.cuh"
 #include "kernels.h"
 
@@ -21,7 +23,16 @@ namespace {
 template <int NG, int CC>
 cudaError_t launch_kv4_cols(const Kv4AttnParams& p, const BatchDesc& bd, cudaStream_t st) {
   using K = Kv4<SDV_KV4_DIM, NG, CC, SDV_KV4_MOD != 0>;
-  auto kernel = kv4_attn_kernel<SDV_KV4_DIM, NG, CC, SDV_KV4_MOD != 0>;
+  const auto kernel = kv4_attn_kernel<SDV_KV4_DIM, NG, CC, SDV_KV4_MOD != 0>;
+  // The roles share out the registers of the launch: with fewer than these they would wait for one another.
+  static std::atomic<int> regs{0};
+  if (regs.load() == 0) {
+    cudaFuncAttributes a;
+    const cudaError_t asked = cudaFuncGetAttributes(&a, kernel);
+    if (asked != cudaSuccess) return asked;
+    regs.store(a.numRegs);
+  }
+  if (regs.load() < K::kLaunchRegs) return cudaErrorLaunchOutOfResources;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)K::kSmem);
   if (e != cudaSuccess) return e;
   return launch_pdl(kernel, dim3(p.grid), dim3(K::kThreads), K::kSmem, st, p, bd);
