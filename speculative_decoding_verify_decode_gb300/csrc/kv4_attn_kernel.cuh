@@ -101,9 +101,9 @@ struct Kv4 {
   // Tiles that pass the softmax together: what a turn costs beyond them (barriers, the references' check, bookkeeping)
   // is as much as sixteen columns of a tile or two.
     static constexpr int T = NQ == 16 && kCtas == 1 ? 4 : NQ <= 48 ? 2 : 1;
-  static constexpr int NS = NQ <= 96 ? 2 : 1;             // S buffers in tensor memory
+  static constexpr int NS = NQ <= 96 || D == 128 ? 2 : 1; // S buffers in tensor memory
   // Widened operands: slots of SW elements a lane, two to a column.
-  static constexpr int SW = NQ < 144 ? 128 : D == 128 ? 64 : 32;
+  static constexpr int SW = NQ < 144 ? 128 : 32;
   static constexpr int kSlotCols = SW / 2;
   // Short slots: the first values are widened before their slot is waited for.
   static constexpr bool kEarly = SW < 128;
@@ -204,6 +204,14 @@ __device__ __forceinline__ float fast_rcp(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+// tcgen05.wait::ld, with the values that it was waited for (whose uses then cannot come before it).
+__device__ __forceinline__ void wait_scores(float (&v)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]), "+f"(v[8]),
+                 "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15])
+               :
+               : "memory");
 }
 // Maxima of 16 values over the warp's lanes: lane L ends with that of value L % 16.
 __device__ __forceinline__ float warp_max16(const float (&v)[16], int lane) {
@@ -771,8 +779,9 @@ kv4_attn_kernel(const Kv4AttnParams p, const BatchDesc bd) {
           const uint8_t* words = rec + (row & 15) * 16;
           uint16_t* sc = reinterpret_cast<uint16_t*>(const_cast<uint8_t*>(rec) + kv4_codes(D) + (row & 15) * (D / 16));
           // of this group's blocks: with bits that do not count, or beyond the largest
+          static_assert(KG == 1 || SW == 32, "every second block");
           auto mine_of = [&](int e) {      // blocks 2 e and 2 e + 1
-            return KG == 1 ? ~0u : SW == 32 ? 0xffffu << (16 * part) : (e * 64 / SW) % 2 == part ? ~0u : 0u;
+            return KG == 1 ? ~0u : 0xffffu << (16 * part);
           };
           bool odd_scale = false;
 #pragma unroll
@@ -1085,45 +1094,52 @@ kv4_attn_kernel(const Kv4AttnParams p, const BatchDesc bd) {
         // warp's would pass 2^kRise waits for that
         uint32_t missed = 0;
         uint8_t* const p_row = sP + (it & 1) * K::kPBytes + c_first * 2 * T * kTile * 16 + row * 16;
-        auto scored = [&](int c, const float (&a)[16], float (&d)[16]) {     // exponents; their maximum
+        auto scored = [&](int c, float (&a)[16]) {     // exponents in place of the scores; their maximum
           float most = -INFINITY;
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const float4 m = *reinterpret_cast<const float4*>(&sm->m[col0 + c * 16 + 4 * k]);
             const float2 d0 = fma2(make_float2(a[4 * k], a[4 * k + 1]), make_float2(mul, mul), make_float2(m.x, m.y));
             const float2 d1 = fma2(make_float2(a[4 * k + 2], a[4 * k + 3]), make_float2(mul, mul), make_float2(m.z, m.w));
-            d[4 * k] = d0.x; d[4 * k + 1] = d0.y; d[4 * k + 2] = d1.x; d[4 * k + 3] = d1.y;
+            a[4 * k] = d0.x; a[4 * k + 1] = d0.y; a[4 * k + 2] = d1.x; a[4 * k + 3] = d1.y;
             most = fmaxf(fmaxf(most, fmaxf(d0.x, d0.y)), fmaxf(d1.x, d1.y));
           }
           return most;
         };
-        auto weigh = [&](float2 (&total)[8], int j, int c, const float (&d)[16], float add) {
+        auto weigh = [&](int j, int c, float (&d)[16]) {     // weights in place of the exponents, and into P
           uint32_t w[8];
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
-            const float2 e = make_float2(fast_exp2(d[2 * k]), fast_exp2(d[2 * k + 1]));
-            total[k] = fma2(e, make_float2(add, add), total[k]);
-            const __nv_bfloat162 h = __floats2bfloat162_rn(e.x, e.y);
+            d[2 * k] = fast_exp2(d[2 * k]);
+            d[2 * k + 1] = fast_exp2(d[2 * k + 1]);
+            const __nv_bfloat162 h = __floats2bfloat162_rn(d[2 * k], d[2 * k + 1]);
             w[k] = *reinterpret_cast<const uint32_t*>(&h);
           }
           uint8_t* at = p_row + j * kTile * 16 + c * 2 * T * kTile * 16;
           *reinterpret_cast<uint4*>(at) = make_uint4(w[0], w[1], w[2], w[3]);
           *reinterpret_cast<uint4*>(at + T * kTile * 16) = make_uint4(w[4], w[5], w[6], w[7]);
         };
+        auto add_up = [&](float2 (&total)[8], const float (&e)[16]) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) total[k] = add2(make_float2(e[2 * k], e[2 * k + 1]), total[k]);
+        };
         const uint32_t all = (1u << mine) - 1u;
         // (into the buffer that the PV before the last has left)
         if (it >= 2) spin(B_OD + (it & 1), (it >> 1) - 1);
         if (settled) {
+          // (whether a chunk's weights count is asked when they are there)
 #pragma unroll 1
           for (int j = 0; j < subs; ++j) {
 #pragma unroll
             for (int c = 0; c < CC; ++c) {
               if (c >= mine) break;
-              float a[16], d[16];
-              tmem_ld16(s_addr + j * NQ + c * 16, a);
-              tmem_wait_ld();
-              if (__any_sync(0xffffffffu, scored(c, a, d) > kRise)) missed |= 1u << (j * CC + c);
-              else weigh(sum[c], j, c, d, 1.f);
+              float x[16];
+              tmem_ld16(s_addr + j * NQ + c * 16, x);
+              wait_scores(x);
+              const bool over = __any_sync(0xffffffffu, scored(c, x) > kRise);
+              weigh(j, c, x);
+              if (over) missed |= 1u << (j * CC + c);
+              else add_up(sum[c], x);
             }
           }
         } else {
@@ -1196,11 +1212,12 @@ kv4_attn_kernel(const Kv4AttnParams p, const BatchDesc bd) {
 #pragma unroll
             for (int c = 0; c < CC; ++c) {
               if (!((todo >> c) & 1u)) continue;
-              float a[16], d[16];
-              tmem_ld16(s_addr + j * NQ + c * 16, a);
-              tmem_wait_ld();
-              scored(c, a, d);
-              weigh(sum[c], j, c, d, (missed >> (j * CC + c)) & 1u ? 1.f : 0.f);
+              float x[16];
+              tmem_ld16(s_addr + j * NQ + c * 16, x);
+              wait_scores(x);
+              scored(c, x);
+              weigh(j, c, x);
+              if ((missed >> (j * CC + c)) & 1u) add_up(sum[c], x);
             }
           }
         }
