@@ -132,7 +132,7 @@ size_t sd_kv4_attn_workspace_size(const sd_shape* shape);
  *               that may run at the same time need one each.
  *
  * Numerics: keys, values and queries enter the products as they are (bf16);
- * softmax weights are rounded to bf16 (2^-9 of themselves), their sum is not;
+ * softmax weights are rounded to bf16 (by at most 2^-8 of themselves), their sum is not;
  * scores, statistics, sums and the partial outputs of split sequences are fp32.
  * A page id out of range sets SD_DEV_BAD_PAGE and its tokens count as zeros; a
  * scale beyond SD_KV4_MAX_SCALE (infinities and NaN too) sets SD_DEV_BAD_SCALE

@@ -18,10 +18,13 @@
 // written and read at four times its size.  The cache's records are laid out for it: K's
 // words go along a token's dims, V's along a dim's tokens, so neither is transposed.
 //
-// What bounds it.  Bytes: 9 D / 8 a token and KV head, read once per CTA column part.
-// Beside that, per 128-token tile of 256 dims: 32 products of M = 128, N = NQ, K = 16
-// (2304 cycles at 144 columns), and the widening, some 900 warp instructions
-// on each of the four schedulers, against 1570 cycles of HBM time.
+// What bounds it.  Bytes: 9 D / 8 a token and KV head for K and as many for V, read once per CTA column part: 1570 cycles
+// a tile of 256 dims at an SM's share of HBM.  Single tokens (16 columns): the instructions of the widening, some 1000
+// a tile and scheduler, half of them integer ones of two cycles (64 sequences of 1 to 32768 tokens, 128 dims: 390 us where
+// the bytes take 207; of 1 to 16384, 256 dims: 191 of 104).  144 columns of 256 dims: 32 products of 81 cycles, then the chain
+// S -> softmax -> S, as there is one S buffer and 1152 cycles of exponentials (a tile takes 4700 cycles; a tree of 23 over
+// 131072 tokens 89 us of 22).  Between them, 96 columns: 3300 cycles a tile.  A piece costs as much as three to five tiles
+// more: query rows and the tree are staged, the first references are taken, partial outputs are stored.
 //
 // Work split, line of units, pieces and merge: as in kv8_attn_kernel.cuh.
 //
@@ -29,10 +32,10 @@
 //   S[128 tok][NQ]     = K_tile . Q^T          A from tensor memory, Q K-major in shared memory
 //   O^T[D][NQ]        += V_tile^T . P^T        M = 128 dims a product, P MN-major in shared memory
 // Warps: NG groups of four softmax warps (lane quarter = warp % 4, CC chunks of 16 columns a
-// group; thread = token row), four that widen K, four that widen V, then one each that loads K,
-// loads V, issues QK, issues PV.  The softmax reads S twice, first for the columns whose
-// reference must move, then for the weights: its sums are all it holds
-// (48 registers at CC = 3), and masked or capped scores go back to S in between.
+// group; thread = token row), WG groups of KG x 4 that widen K and of four that widen V, then one each that loads K,
+// loads V, issues QK, issues PV.  The softmax reads its scores once: it forms weights with the references that there are,
+// and where one is beyond 2^kRise, or there is none yet, the group moves these columns' references and forms them anew.
+// Masked, capped or biased scores are formed first and go back to S.
 // Every wait on a barrier is bounded; on expiry the kernel reports
 // SD_DEV_TIMEOUT and runs out.
 #pragma once
@@ -99,10 +102,11 @@ struct Kv4 {
   static constexpr int MH = D / 128;                      // 128-dim blocks
   using Small = Kv4Small<NQ, kWideV, MH, MOD>;
   // Tiles that pass the softmax together: what a turn costs beyond them (barriers, the references' check, bookkeeping)
-  // is as much as sixteen columns of a tile or two.
-    static constexpr int T = NQ == 16 && kCtas == 1 ? 4 : NQ <= 48 ? 2 : 1;
+  // is as much as sixteen columns of a tile or two (64 sequences, 128 dims: one tile 560 us, four 427).
+  static constexpr int T = NQ == 16 && kCtas == 1 ? 4 : NQ <= 48 ? 2 : 1;
   static constexpr int NS = NQ <= 96 || D == 128 ? 2 : 1; // S buffers in tensor memory
-  // Widened operands: slots of SW elements a lane, two to a column.
+  // Widened operands: slots of SW elements a lane, two to a column.  One long slot beats two short ones, whose handshakes
+  // cost more than their overlap gives (8 chains of 5 nodes: 64 elements 39 us, 128 36); 144 columns leave no room for it.
   static constexpr int SW = NQ < 144 ? 128 : 32;
   static constexpr int kSlotCols = SW / 2;
   // Short slots: the first values are widened before their slot is waited for.

@@ -31,6 +31,7 @@ SD_DEV_BAD_SCALE = 256
 SD_DEV_BAD_SLOT = 512
 SD_DEV_NOT_FINITE = 1024
 SD_DEV_BAD_POSITION = 2048
+SD_LOGPROBS_MAX_TOP = 32
 MAX_NODES = 64
 MAX_BATCH = 256
 MAX_LAYERS = 64

@@ -263,6 +263,8 @@ class Kv4Step(Kv8Step):
 
     def __init__(self, cache: Kv4Cache, q_indptr, vocab: int, num_q_heads: int = 24, window: int = 0, softcap: float = 0.0,
                  slopes=None, max_path: int | None = None, top: int = 0):
+        if not 0 <= top <= min(int(vocab), native.SD_LOGPROBS_MAX_TOP):
+            raise ValueError(f"top is 0..{min(int(vocab), native.SD_LOGPROBS_MAX_TOP)}")
         super().__init__(cache, q_indptr, vocab, num_q_heads, window, softcap, slopes, max_path)
         self.top, total, dev = int(top), int(self.q_indptr[-1]), cache.device
         layers, _, heads, dim = self._geometry()

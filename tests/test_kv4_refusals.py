@@ -274,6 +274,11 @@ def test_cache_and_step_hold_what_the_calls_need():
     assert c.kv.shape == (3, 12, 2, 2, 1152) and c.kv.dtype == torch.uint8 and c.free_list.tolist() == list(range(11, -1, -1))
     s = Kv4Step(c, [0, 3, 7], 1000, num_q_heads=8, top=5)
     assert s.out.shape == (3, 7, 8, 128) and s.top_ids.shape == (7, 5) and s.q_turned.shape == (3, 7, 8, 128)
+    for top in (-1, 33):
+        with pytest.raises(ValueError):
+            Kv4Step(c, [0, 3, 7], 1000, num_q_heads=8, top=top)
+    with pytest.raises(ValueError):
+        Kv4Step(c, [0, 3, 7], 4, num_q_heads=8, top=5)
     assert s.k_turned.shape == (3, 7, 2, 128) and s.attn_ws.numel() == native.sd_kv4_attn_workspace_size(s.shape)
 
 
@@ -287,8 +292,8 @@ def test_struct_and_constants_match_the_headers(tmp_path):
     src = tmp_path / "a.c"
     src.write_text('#include <stddef.h>\n#include <stdio.h>\n#include "sd_kv4.h"\n#include "sd_rope.h"\n#include "sd_logprobs.h"\n'
                    f'int main(void) {{ printf("%zu", sizeof(sd_rope_shape)); {offs} {more}'
-                   ' printf(" %d %d %d", SD_LOGITS_F32, SD_LOGITS_BF16, SD_LOGITS_F16); return 0; }\n')
+                   ' printf(" %d %d %d %d", SD_LOGITS_F32, SD_LOGITS_BF16, SD_LOGITS_F16, SD_LOGPROBS_MAX_TOP); return 0; }\n')
     subprocess.run(["gcc", "-std=c11", "-I", inc, str(src), "-o", str(tmp_path / "a")], check=True)
     got = [int(x) for x in subprocess.run([str(tmp_path / "a")], check=True, capture_output=True, text=True).stdout.split()]
     assert got == [ctypes.sizeof(native.SdRopeShape)] + [getattr(native.SdRopeShape, n).offset for n in names] + \
-        [getattr(native, b) for b in bits] + [1, 0, 1, 2]
+        [getattr(native, b) for b in bits] + [1, 0, 1, 2, native.SD_LOGPROBS_MAX_TOP]
