@@ -8,7 +8,8 @@ namespace sdv {
 namespace {
 
 // Query columns of a CTA: as many heads of a KV group as fit, so that the cache is read and widened as few times as
-// can be.
+// can be (trees whose 124 to 138 columns fit one part, against two parts of 62 to 72: 23 nodes over 131072 tokens 90 us and
+// 114, 31 nodes over 20001 with capped scores 37 and 46).
 struct Kv4Plan {
   int hpc, hparts;   // query heads of a KV group per CTA, and CTA parts per group
   int nq;            // query columns of the kernel instance

@@ -324,9 +324,7 @@ __global__ void __launch_bounds__(kRowsThreads) kv4_read_kernel(const Kv4RowsPar
 
 cudaError_t launch_kv4_append(const Kv4RowsParams& p, int dim, cudaStream_t st) {
   if (p.max_rows == 0) return cudaSuccess;
-  // Rows per CTA: a row of its own while that fills the machine about twice over at most (single tokens of a batch, an
-  // accepted path); for prompts sixteen, of which one begins a page.
-  const int window = (long long)p.max_rows * p.num_layers <= 4 * kSMs ? 1 : kPage;
+  const int window = kPage;      // rows of a CTA, of which one or two begin a page
   // enough CTAs per window for one page's tasks, a warp each
   const int share = (4 * p.heads + kRowsWarps - 1) / kRowsWarps;
   const dim3 grid((p.max_rows + window - 1) / window, p.num_layers, share);

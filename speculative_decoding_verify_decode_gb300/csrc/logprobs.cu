@@ -418,7 +418,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_piece_kernel(const Log
     }
   };
   // Where a row is one long stream, the tile after the next is asked for into L2, as the registers hold one (2047 rows of
-  // 151936 144 -> 131 us; four tiles on 132; for rows in three pieces 63 -> 64).
+  // 151936 144 -> 131 us; four tiles on 132; rows in pieces gain nothing).
   auto ahead = [&](int at) {
     if (VEC && p.pieces == 1 && t == 0 && at < end) {
       const uint32_t bytes = (uint32_t)min(kTile, end - at) * (uint32_t)sizeof(T) & ~15u;
@@ -650,11 +650,12 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_join_kernel(const Logprob
   finish_row<T>(p, sh, row, st, bad, given);
 }
 
-// Pieces of a row (of whole 4096-logit groups, whatever the type): one while the rows make three waves of CTAs, else so
-// many that there is about one wave, and none smaller than a group.
+// Pieces of a row (of whole 4096-logit groups, whatever the type): one from a row per SM on, below that as many as fill the
+// machine once (151936 fp32 logits with 5 alternatives, 500 rows: one piece 52 us, three 63; 250 rows: one 30, two 34; 100
+// rows: six 20 us, seven 23; 64 rows: nine 17, ten 18).
 int pieces_of(int rows, int vocab, int* piece) {
-  const int groups = (vocab + kGroup - 1) / kGroup, wave = 4 * kSMs;
-  int n = rows >= 3 * wave ? 1 : rows > wave / 2 ? (2 * wave + rows - 1) / rows : (wave + rows - 1) / rows;
+  const int groups = (vocab + kGroup - 1) / kGroup;
+  int n = rows >= kSMs ? 1 : 4 * kSMs / rows;
   n = n < groups ? n : groups;
   n = n < kMaxPieces ? n : kMaxPieces;
   if (n * kMaxGroups < groups) n = (groups + kMaxGroups - 1) / kMaxGroups;      // (at most 16)
