@@ -14,7 +14,7 @@
 // consecutive dims: four lanes are a block, two shuffles its maximum.  K's words go through
 // shared memory (a row's lie 256 bytes apart), so that its record leaves in
 // 16-byte pieces; V's codes add up in halves of a word, two dims at a time.  Every warp finds its rows in the slot map for
-// itself.  2 bytes read and 9/16 written a value, and some 15 instructions, which bound it: 8191 rows of 4 heads of 256
+// itself.  2 bytes read and 9/16 written a value, and some 18 instructions, which bound it: 8191 rows of 4 heads of 256
 // dims take 16 us where their bytes take 6.4 (whole pages a warp, 128 registers: 17.6); 6 rows of 16 layers take 3.4, of
 // which a launch is 2.
 //
