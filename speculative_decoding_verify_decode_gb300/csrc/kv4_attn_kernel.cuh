@@ -51,6 +51,7 @@ namespace {
 
 constexpr int kTile = kTileTokens;     // tokens of a product's M
 constexpr float kRise = 16.0f;         // log2 of the weight beyond which a reference moves
+constexpr float kLarge = 67108864.0f;  // 2^26: a reference beyond which scores are rounded before it is taken off (see `large`)
 constexpr float kLog2e = 1.4426950408889634f;
 
 template <int NQ, int VW, int MH, bool MOD>
@@ -71,6 +72,7 @@ struct Kv4Small {
   int8_t depth[kMaxNodes];
   int8_t wild[kMaxNodes];  // the node's key or value holds a NaN or an infinity
   alignas(16) int flag[3][2][4];   // [group][tile parity][lane quarter]: chunks where a weight passes 2^kRise
+  int large[3];                    // [group]
   uint32_t tmem;
   int abort;
 };
@@ -966,6 +968,7 @@ kv4_attn_kernel(const Kv4AttnParams p, const BatchDesc bd) {
         sm->m[q] = q < nc * 16 ? 0.f : -1e30f;     // no reference yet; columns past those in use: below everything
         if (MOD) sm->slope[q] = p.slopes != nullptr && q < rows ? p.slopes[head0 + q % hpc] * kLog2e : 0.f;
       }
+      if (tid < 3) sm->large[tid] = 0;
       // the tree: root paths and depths
       if (needs_tree && tid < n_nodes) {
         unsigned long long a = 1ull << tid;
@@ -1014,6 +1017,10 @@ kv4_attn_kernel(const Kv4AttnParams p, const BatchDesc bd) {
       const float fac = p.scale * kLog2e;
       // Until a tile that every column sees something of has passed, columns may have no reference.
       bool settled = false;
+      // score times factor less reference is one fma, exact but for its one rounding; so what the maximum itself comes to is
+      // what its product lost when it became the reference: up to 2^4 at references of 2^28, and beyond every exponent where
+      // cache or queries are huge.  From kLarge on the product is rounded first, tile by tile: the maximum is 0 again.
+      bool large = false;
       const int end = pc.first + pc.tiles;
 #pragma unroll 1
       for (int i = pc.first, subs; i < end; i += subs, ++it) {
@@ -1098,13 +1105,13 @@ kv4_attn_kernel(const Kv4AttnParams p, const BatchDesc bd) {
         // warp's would pass 2^kRise waits for that
         uint32_t missed = 0;
         uint8_t* const p_row = sP + (it & 1) * K::kPBytes + c_first * 2 * T * kTile * 16 + row * 16;
-        auto scored = [&](int c, float (&a)[16]) {     // exponents in place of the scores; their maximum
+        auto scored = [&](int c, float (&a)[16], float by) {     // exponents in place of the scores; their maximum
           float most = -INFINITY;
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const float4 m = *reinterpret_cast<const float4*>(&sm->m[col0 + c * 16 + 4 * k]);
-            const float2 d0 = fma2(make_float2(a[4 * k], a[4 * k + 1]), make_float2(mul, mul), make_float2(m.x, m.y));
-            const float2 d1 = fma2(make_float2(a[4 * k + 2], a[4 * k + 3]), make_float2(mul, mul), make_float2(m.z, m.w));
+            const float2 d0 = fma2(make_float2(a[4 * k], a[4 * k + 1]), make_float2(by, by), make_float2(m.x, m.y));
+            const float2 d1 = fma2(make_float2(a[4 * k + 2], a[4 * k + 3]), make_float2(by, by), make_float2(m.z, m.w));
             a[4 * k] = d0.x; a[4 * k + 1] = d0.y; a[4 * k + 2] = d1.x; a[4 * k + 3] = d1.y;
             most = fmaxf(fmaxf(most, fmaxf(d0.x, d0.y)), fmaxf(d1.x, d1.y));
           }
@@ -1130,7 +1137,7 @@ kv4_attn_kernel(const Kv4AttnParams p, const BatchDesc bd) {
         const uint32_t all = (1u << mine) - 1u;
         // (into the buffer that the PV before the last has left)
         if (it >= 2) spin(B_OD + (it & 1), (it >> 1) - 1);
-        if (settled) {
+        if (settled && !large) {
           // (whether a chunk's weights count is asked when they are there)
 #pragma unroll 1
           for (int j = 0; j < subs; ++j) {
@@ -1140,7 +1147,7 @@ kv4_attn_kernel(const Kv4AttnParams p, const BatchDesc bd) {
               float x[16];
               tmem_ld16(s_addr + j * NQ + c * 16, x);
               wait_scores(x);
-              const bool over = __any_sync(0xffffffffu, scored(c, x) > kRise);
+              const bool over = __any_sync(0xffffffffu, scored(c, x, mul) > kRise);
               weigh(j, c, x);
               if (over) missed |= 1u << (j * CC + c);
               else add_up(sum[c], x);
@@ -1187,8 +1194,10 @@ kv4_attn_kernel(const Kv4AttnParams p, const BatchDesc bd) {
             if (now == 0.f && mt != -INFINITY) now = 1e-30f;
             sm->alpha[q] = old == 0.f ? 1.f : fast_exp2(old - now);
             sm->m[q] = -now;
+            if (fabsf(now) > kLarge) sm->large[group] = 1;
           }
           sync_group();
+          large = sm->large[group] != 0;
           // O belongs to the previous tile's PV until it has finished
           if (!fresh) spin(B_OD + ((it - 1) & 1), (it - 1) >> 1);
           tc_fence_after();
@@ -1219,7 +1228,11 @@ kv4_attn_kernel(const Kv4AttnParams p, const BatchDesc bd) {
               float x[16];
               tmem_ld16(s_addr + j * NQ + c * 16, x);
               wait_scores(x);
-              scored(c, x);
+              if (large) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) x[e] = __fmul_rn(x[e], mul);
+              }
+              scored(c, x, large ? 1.f : mul);
               weigh(j, c, x);
               if ((missed >> (j * CC + c)) & 1u) add_up(sum[c], x);
             }

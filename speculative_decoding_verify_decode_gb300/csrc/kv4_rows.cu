@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(kRowsThreads, 6) kv4_append_kernel(const Kv4Ro
   pdl_wait();
   // The window's entries and the 16 behind it, one a lane: every warp finds its groups for itself, in one latency.
   int slot = -1, src = -1, prev = -1;
-  if (r_base + lane < p.max_rows) {
+  if (lane < p.max_rows - r_base) {
     slot = p.slots[r_base + lane];
     src = p.rows != nullptr ? p.rows[r_base + lane] : r_base + lane;
   }

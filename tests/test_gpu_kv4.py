@@ -602,3 +602,38 @@ def test_append_and_read_on_another_stream_and_in_a_graph():
         want = kv4.append(cache, np64(k), np64(v), slots)
         np.testing.assert_array_equal(dev.cpu().numpy(), want)
         np.testing.assert_array_equal(np64(k_out)[3], kv4.values(want)[0][0, :, 10])
+
+
+@pytest.mark.parametrize("heads", [(24, 4, 256), (8, 2, 128)], ids=["d256", "d128"])
+@pytest.mark.parametrize("q_power,k_power", [(0, 100), (60, 30), (0, 30), (20, 10), (100, 0), (12, 12)])
+@pytest.mark.parametrize("nodes", [1, 23])
+def test_scores_so_large_that_one_key_is_left(nodes, q_power, k_power, heads):
+    """Scores of 2^24 to 2^110: softmax leaves the largest alone (its nearest rival is farther off than fp32's rounding of
+    either, else the column is passed over), so the output is that key's value, which bf16 holds exactly."""
+    c = Case([chain(nodes), chain(nodes)], [700, 5], heads, seed=31, spread=0.0)
+    c.q = (c.q.float() * 2.0 ** q_power).bfloat16()
+    c.scales["k"] = c.scales["k"] * 2.0 ** k_power
+    c.kn = (c.kn.float() * 2.0 ** k_power).bfloat16()
+    c.upload().call()
+    torch.cuda.synchronize()
+    assert int(c.status) == 0
+    got, lse = np64(c.out[:-1]), np64(c.lse)
+    assert np.isfinite(got).all() and np.isfinite(lse).all()
+    k, v = kv4.values(c.cache())
+    q, kn, vn, seen = np64(c.q), np64(c.kn), np64(c.vn), 0
+    for b in range(2):
+        pages = c.table[b, :-(-int(c.ctx[b]) // PAGE)]
+        for j in range(nodes):
+            r = c.indptr[b] + j
+            for h in range(c.hq):
+                g = h // (c.hq // c.hkv)
+                flat = lambda x, new: np.concatenate([x[pages, g].reshape(-1, c.dim)[:c.ctx[b]], new[c.indptr[b]:r + 1, g]])
+                keys, vals = flat(k, kn), flat(v, vn)
+                s = keys @ q[r, h] * c.dim ** -0.5
+                top = np.argmax(s)
+                off = 2.0 ** -20 * np.abs(keys).max() * np.abs(q[r, h]).sum() * c.dim ** -0.5 + 2.0 ** -22 * np.abs(s[top])
+                if np.sort(s)[-2] + 2 * off + 40 < s[top]:        # e^-40 of all others is nothing
+                    seen += 1
+                    np.testing.assert_array_equal(got[r, h], vals[top])
+                    assert abs(lse[r, h] - s[top]) <= off + 2.0 ** -20 * np.abs(s[top])
+    assert seen > 10
