@@ -319,3 +319,26 @@ def test_scales_of_logits_and_temperatures(rows, dtype, size, temperature):
     x, out, status = run((x * size).to(dtype), tokens=torch.randint(9001, (rows, 4), generator=gen), top=7, temperature=temperature, dtype=dtype)
     assert status == 0
     check(x, out, rows=[0, rows - 1, rows // 2], temperature=temperature)
+
+
+@pytest.mark.parametrize("rows,vocab,top", [(160, (1 << 21) + 5, 20), (1, (1 << 24) - 3, 32), (1, 1 << 24, 0), (200, 1, 1), (3, 31, 31)])
+def test_the_largest_and_smallest_vocabularies(rows, vocab, top):
+    """Rows in one piece of more than 4096 segments, the most logits there can be, and next to none."""
+    gen = torch.Generator(device="cuda").manual_seed(rows)
+    x = (torch.randn(rows, vocab, generator=gen, device="cuda") * 3).bfloat16()
+    tokens = torch.randint(vocab, (rows, 2), generator=gen, device="cuda")
+    out = run(x, tokens=tokens, top=top)[1]
+    for r in {0, rows // 2, rows - 1}:
+        z = x[r].double()
+        lse = torch.logsumexp(z, 0)
+        # sums: 2^-21, and the exponentials 2^-22 + 64 * 2^-23 (see the head of this file); the logarithm and the difference fp32
+        tol = 2.0 ** -21 + 2.0 ** -22 + 2.0 ** -17 + 2.0 ** -22 * (float(lse.abs()) + float(z.abs().max()))
+        assert abs(float(out["lse"][r]) - float(lse)) <= tol
+        assert torch.all((out["logprobs"][r].double() - (z[tokens[r]] - lse)).abs() <= tol)
+        p = (z - lse).exp()
+        h = -float((p * (z - lse)).sum())
+        assert abs(float(out["entropy"][r]) - h) <= tol + h * (2.0 ** -20 + 2.0 ** -17)
+        if top:
+            order = torch.sort(x[r].float(), descending=True, stable=True)[1][:top]
+            assert torch.equal(out["top_ids"][r].long(), order)
+            assert torch.all((out["top_logprobs"][r].double() - (z[order] - lse)).abs() <= tol)
