@@ -94,13 +94,13 @@ __device__ __forceinline__ float fast_rcp(float x) {
 }
 
 template <int D>
-__global__ void __launch_bounds__(kRowsThreads, 6) kv4_append_kernel(const Kv4RowsParams p, const int window) {
+__global__ void __launch_bounds__(kRowsThreads, 6) kv4_append_kernel(const Kv4RowsParams p) {
   constexpr int kLanes = D / 8;            // lanes per row (8 values each)
   constexpr int kRowsAtOnce = 32 / kLanes; // rows a warp touches per step
   constexpr int kHalf = kPage / 2, kSteps = kHalf / kRowsAtOnce;
   constexpr int kBlocks = D / kKv4Block;
   __shared__ __align__(16) uint32_t s_k[kRowsWarps][kHalf * D / 8];
-  const int layer = blockIdx.y, r_base = blockIdx.x * window;
+  const int layer = blockIdx.y, r_base = blockIdx.x * kPage;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int combo = blockIdx.z * kRowsWarps + warp;
   if (combo >= 4 * p.heads) return;
@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(kRowsThreads, 6) kv4_append_kernel(const Kv4Ro
   const bool is_v = combo & 2;
   const int col = lane % kLanes, sub = lane / kLanes;
   pdl_wait();
-  // The window's entries and the 16 behind it, one a lane: every warp finds its groups for itself, in one latency.
+  // Sixteen entries, and the 16 behind them, one a lane: every warp finds its groups for itself, in one latency.
   int slot = -1, src = -1, prev = -1;
   if (lane < p.max_rows - r_base) {
     slot = p.slots[r_base + lane];
@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(kRowsThreads, 6) kv4_append_kernel(const Kv4Ro
   const int up = __shfl_up_sync(0xffffffffu, slot, 1);
   if (lane > 0) prev = up;
   bool lead = false;
-  if (lane < window) {
+  if (lane < kPage) {
     if (slot < -1 || slot / kPage >= p.num_pool_pages) {
       if (layer == 0 && combo == 0) report(p.dev_status, SD_DEV_BAD_SLOT);
     } else if (slot >= 0) {
@@ -244,7 +244,6 @@ __global__ void __launch_bounds__(kRowsThreads, 6) kv4_append_kernel(const Kv4Ro
 
 template <int D>
 __global__ void __launch_bounds__(kRowsThreads) kv4_read_kernel(const Kv4RowsParams p) {
-  constexpr int window = kReadRows;
   constexpr int kLanes = D / 8, kRowsAtOnce = 32 / kLanes, kBlocks = D / kKv4Block;
   const int layer = blockIdx.y, lane = threadIdx.x & 31;
   const int combo = blockIdx.z * kRowsWarps + (threadIdx.x >> 5);
@@ -252,7 +251,7 @@ __global__ void __launch_bounds__(kRowsThreads) kv4_read_kernel(const Kv4RowsPar
   if (combo >= 2 * p.heads) return;
   const int head = combo >> 1;
   const bool is_v = combo & 1;
-  const int r0 = blockIdx.x * window, n = min(window, p.max_rows - r0);
+  const int r0 = blockIdx.x * kReadRows, n = min(kReadRows, p.max_rows - r0);
   int mine = -1;
   if (lane < n) {
     mine = p.slots[r0 + lane];
@@ -267,7 +266,7 @@ __global__ void __launch_bounds__(kRowsThreads) kv4_read_kernel(const Kv4RowsPar
   const size_t page_bytes = (size_t)p.heads * 2 * kv4_record(D);
   bool bad = false;
   if (!is_v) {
-    constexpr int kSteps = window / kRowsAtOnce;
+    constexpr int kSteps = kReadRows / kRowsAtOnce;
     uint32_t w[kSteps], s[kSteps];
 #pragma unroll
     for (int k = 0; k < kSteps; ++k) {
@@ -326,19 +325,17 @@ __global__ void __launch_bounds__(kRowsThreads) kv4_read_kernel(const Kv4RowsPar
 
 cudaError_t launch_kv4_append(const Kv4RowsParams& p, int dim, cudaStream_t st) {
   if (p.max_rows == 0) return cudaSuccess;
-  const int window = kPage;      // rows of a CTA, of which one or two begin a page
-  // enough CTAs per window for one page's tasks, a warp each
+  // a warp for each half page, K or V and head of sixteen entries, of which one or two begin a page
   const int share = (4 * p.heads + kRowsWarps - 1) / kRowsWarps;
-  const dim3 grid((p.max_rows + window - 1) / window, p.num_layers, share);
-  return dim == 256 ? launch_pdl(kv4_append_kernel<256>, grid, dim3(kRowsThreads), 0, st, p, window)
-                    : launch_pdl(kv4_append_kernel<128>, grid, dim3(kRowsThreads), 0, st, p, window);
+  const dim3 grid((p.max_rows - 1) / kPage + 1, p.num_layers, share);
+  return dim == 256 ? launch_pdl(kv4_append_kernel<256>, grid, dim3(kRowsThreads), 0, st, p)
+                    : launch_pdl(kv4_append_kernel<128>, grid, dim3(kRowsThreads), 0, st, p);
 }
 
 cudaError_t launch_kv4_read(const Kv4RowsParams& p, int dim, cudaStream_t st) {
   if (p.max_rows == 0) return cudaSuccess;
-  constexpr int window = kReadRows;
   const int share = (2 * p.heads + kRowsWarps - 1) / kRowsWarps;
-  const dim3 grid((p.max_rows + window - 1) / window, p.num_layers, share);
+  const dim3 grid((p.max_rows - 1) / kReadRows + 1, p.num_layers, share);
   return dim == 256 ? launch_pdl(kv4_read_kernel<256>, grid, dim3(kRowsThreads), 0, st, p)
                     : launch_pdl(kv4_read_kernel<128>, grid, dim3(kRowsThreads), 0, st, p);
 }
