@@ -20,8 +20,8 @@
 //
 // What bounds it.  Bytes: 9 D / 8 a token and KV head for K and as many for V, read once per CTA column part: 1570 cycles
 // a tile of 256 dims at an SM's share of HBM.  Single tokens (16 columns): the instructions of the widening, some 1000
-// a tile and scheduler, half of them integer ones of two cycles (64 sequences of 1 to 32768 tokens, 128 dims: 390 us where
-// the bytes take 207; of 1 to 16384, 256 dims: 191 of 104).  144 columns of 256 dims: 32 products of 81 cycles, then the chain
+// a tile and scheduler, half of them integer ones of two cycles (64 sequences of 1 to 32768 tokens, 128 dims: 382 us where
+// the bytes take 207; of 1 to 16384, 256 dims: 190 of 104).  144 columns of 256 dims: 32 products of 81 cycles, then the chain
 // S -> softmax -> S, as there is one S buffer and 1152 cycles of exponentials (a tile takes 4700 cycles; a tree of 23 over
 // 131072 tokens 89 us of 22).  Between them, 96 columns: 3300 cycles a tile.  A piece costs as much as three to five tiles
 // more: query rows and the tree are staged, the first references are taken, partial outputs are stored.
@@ -312,6 +312,11 @@ kv4_attn_kernel(const Kv4AttnParams p, const BatchDesc bd) {
     if (i == 0) sm->abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  if (warp == kWarpQK) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sm->tmem)),
+                 "n"(K::kTmem));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
   // Launched as a programmatic dependent: everything above touches no global memory; here the previous kernel's writes
   // become visible.
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -394,11 +399,6 @@ kv4_attn_kernel(const Kv4AttnParams p, const BatchDesc bd) {
       if (tid < bd.batch) sm->cum[tid + 1] = incl;
     }
   }
-  if (warp == kWarpQK) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sm->tmem)),
-                 "n"(K::kTmem));
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
-  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -414,16 +414,18 @@ kv4_attn_kernel(const Kv4AttnParams p, const BatchDesc bd) {
   // The piece that begins at unit u.
   auto piece_at = [&](int u) {
     Piece pc;
-    int lo = 0, hi = bd.batch - 1;
+    int lo = 0;      // sequences that end at or before u
 #pragma unroll 1
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (sm->cum[mid] <= u) lo = mid; else hi = mid - 1;
+    for (int b = 0; b < bd.batch; b += 32) {
+      const bool before = b + lane < bd.batch - 1 && sm->cum[b + lane + 1] <= u;
+      const int n = __popc(__ballot_sync(0xffffffffu, before));
+      lo += n;
+      if (n < 32) break;
     }
     const int line = (sm->cum[lo + 1] - sm->cum[lo]) / parts;     // units of one of the sequence's segments
     const int rem = u - sm->cum[lo], s = rem / line, at = rem - s * line;
     pc.b = lo;
-    pc.g = s / p.hparts;
+    pc.g = p.hparts == 1 ? s : s / p.hparts;
     pc.c = s - pc.g * p.hparts;
     pc.seg = lo * parts + s;
     pc.L = ctx_of(lo);
@@ -438,15 +440,9 @@ kv4_attn_kernel(const Kv4AttnParams p, const BatchDesc bd) {
       pc.tiles = pc.span = min(line - at, u_end - u);
     }
     pc.whole = pc.tiles == pc.nt + 1;
-    // the same for every lane, and known to be
-    pc.b = __shfl_sync(0xffffffffu, pc.b, 0);
-    pc.g = __shfl_sync(0xffffffffu, pc.g, 0);
-    pc.c = __shfl_sync(0xffffffffu, pc.c, 0);
+    // the same for every lane, and known to be (all nine of them shuffled: 64 sequences 388 us against 383)
     pc.first = __shfl_sync(0xffffffffu, pc.first, 0);
     pc.tiles = __shfl_sync(0xffffffffu, pc.tiles, 0);
-    pc.L = __shfl_sync(0xffffffffu, pc.L, 0);
-    pc.base = __shfl_sync(0xffffffffu, pc.base, 0);
-    pc.nt = __shfl_sync(0xffffffffu, pc.nt, 0);
     pc.span = __shfl_sync(0xffffffffu, pc.span, 0);
     return pc;
   };
