@@ -312,14 +312,15 @@ kv4_attn_kernel(const Kv4AttnParams p, const BatchDesc bd) {
     if (i == 0) sm->abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  // Launched as a programmatic dependent: everything above touches no global memory; here the previous kernel's writes
+  // become visible.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // (not before: the kernels that this one waits for may still want tensor memory)
   if (warp == kWarpQK) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sm->tmem)),
                  "n"(K::kTmem));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
-  // Launched as a programmatic dependent: everything above touches no global memory; here the previous kernel's writes
-  // become visible.
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (bd.batch <= 32) {
     int per, extra;
     // a sequence per lane, every warp for itself
