@@ -157,3 +157,60 @@ def test_a_rotating_append_into_the_bf16_cache_then_its_attention():
     spread = (s @ vals.abs()).transpose(0, 1)
     # bf16 output and bf16 weights, half a step each, and 2^-8 more for scores and sums in fp32
     assert torch.all((out.double() - ref).abs() <= 2.0 ** -8 * ref.abs() + 2.0 ** -7 * spread)
+
+
+def test_all_the_attentions_one_after_the_other():
+    """bf16, 4-bit and 8-bit attention, rotation, appends and log probabilities in one stream and one graph, each launched while
+    the one before drains: the same bits as alone."""
+    from test_gpu_kv4 import Case
+    from test_gpu_kv8 import Case as Case8
+    heads, dim, rng = (24, 4, 256), 256, np.random.default_rng(11)
+    small, wide = Case([chain(1)], [700], heads, seed=1).upload(), Case([tree(2, 22), chain(2)], [9000, 40], heads, seed=2).upload()
+    eight = Case8([tree(3, 12)], [3000], heads, seed=3).upload()
+    pages, nodes = 40, 9
+    kc, vc = bf16(rng, pages, 4, 16, dim).cuda(), bf16(rng, pages, 4, 16, dim).cuda()
+    q, kn, vn = bf16(rng, nodes, 24, dim).cuda(), bf16(rng, nodes, 4, dim).cuda(), bf16(rng, nodes, 4, dim).cuda()
+    shape = native.Shape([0, nodes], pages, pages, num_q_heads=24, num_kv_heads=4, head_dim=dim)
+    out16, status = torch.empty_like(q), torch.zeros(1, dtype=torch.int32, device="cuda")
+    ws16 = torch.empty(max(16, native.sd_verify_attn_workspace_size(shape)), dtype=torch.uint8, device="cuda")
+    table, ctx, par = cu([range(pages)], torch.int32), cu([pages * 16 - 3], torch.int32), cu(chain(nodes), torch.int32)
+    rot, pos = rope_table(1024, 64), cu(range(nodes), torch.int32)
+    q_turned, k_turned = torch.empty_like(q), torch.empty_like(kn)
+    logits = torch.randn(5, 20000, device="cuda")
+    ids, best, entropy = torch.empty(5, 8, dtype=torch.int32, device="cuda"), torch.empty(5, 8, device="cuda"), torch.empty(5, device="cuda")
+    lp_ws = torch.empty(native.sd_logprobs_workspace_size(5, 20000, 8), dtype=torch.uint8, device="cuda")
+    cache = torch.zeros(1, *native.kv4_cache_shape(4, 4, dim), dtype=torch.uint8, device="cuda")
+    slots = cu(range(16, 16 + nodes), torch.int32)
+    calls = [
+        lambda: native.sd_verify_attn(shape, q, kc, vc, kn, vn, table, ctx, par, out16, workspace=ws16, dev_status=status),
+        lambda: wide.call(),
+        lambda: native.sd_rope_append(rot, pos, q=q, k=kn, q_out=q_turned, k_out=k_turned, dev_status=status),
+        lambda: small.call(),
+        lambda: native.sd_kv4_append(cache, k_turned[None], vn[None], slots, dev_status=status),
+        lambda: eight.call(),
+        lambda: native.sd_logprobs(logits, None, None, ids, best, entropy, workspace=lp_ws, dev_status=status),
+    ]
+    outs = [out16, wide.out, q_turned, small.out, cache, eight.out, best]
+    want = []
+    for call, out in zip(calls, outs):
+        call()
+        torch.cuda.synchronize()
+        want.append(out.clone())
+    order = [0, 1, 3, 1, 0, 3, 2, 4, 1, 5, 3, 6, 0, 2, 5, 1, 6, 4, 3, 0]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for i in order:
+            calls[i]()
+    for how in (lambda: [calls[i]() for i in order], graph.replay, graph.replay):
+        for i, out in enumerate(outs):
+            if i not in (2, 4):
+                out.fill_(7)
+        how()
+        torch.cuda.synchronize()
+        for i, (got, ref) in enumerate(zip(outs, want)):
+            if i in (1, 3):
+                got, ref = got[:-1], ref[:-1]
+            if i == 5:
+                got, ref = got[:eight.indptr[-1]], ref[:eight.indptr[-1]]
+            assert torch.equal(got, ref), i
+        assert int(status) == 0 and int(wide.status) == 0 and int(small.status) == 0
