@@ -640,9 +640,29 @@ def _kv4_layers(cache_layers):
 def _kv4_rows(cache_layers, k_layers, v_layers, slots, names):
     """Checked arguments of sd_kv4_append and sd_kv4_read: sizes, addresses (the array keeps them alive), stride, rows."""
     dev = slots.get_device()
-    n, cache = _kv4_layers(cache_layers)
     if slots.dim() != 1:
         raise ValueError("slots is one-dimensional")
+    try:
+        # the usual case, a tensor each with a leading layer dimension: in one go (the checks are half of a small call)
+        n, pool, heads, two, width = cache_layers.shape
+        shape = k_layers.shape
+        each, row = pool * heads * 2 * width, 2 * shape[1] * shape[2] * shape[3]
+        if len(shape) == 4 and each and row and n and two == 2 and width == 9 * shape[3] and shape[2] == heads and shape[0] == n \
+                and v_layers.shape == shape and cache_layers.dtype is _U8 \
+                and k_layers.dtype is torch.bfloat16 and v_layers.dtype is torch.bfloat16 \
+                and cache_layers.get_device() == dev and k_layers.get_device() == dev and v_layers.get_device() == dev \
+                and cache_layers.is_contiguous() and k_layers.is_contiguous() and v_layers.is_contiguous():
+            at = cache_layers.data_ptr()
+            ptrs = array("Q", range(at, at + each * n, each))
+            at = k_layers.data_ptr()
+            ptrs.extend(range(at, at + row * n, row))
+            at = v_layers.data_ptr()
+            ptrs.extend(range(at, at + row * n, row))
+            at = ptrs.buffer_info()[0]
+            return ptrs, (n, heads, shape[3], 16, pool, at, at + 8 * n, at + 16 * n, 0), shape[1], dev
+    except (AttributeError, ValueError, IndexError):
+        pass
+    n, cache = _kv4_layers(cache_layers)
     pool, heads, dim = cache[0], cache[1], cache[3] // 9
     ptrs = array("Q")      # the three arrays of n addresses, one behind the other
     _put_layers(ptrs, cache_layers, n, "cache", _U8, cache, pool * heads * 18 * dim, dev)

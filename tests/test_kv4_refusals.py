@@ -225,6 +225,18 @@ def test_binding_refuses_wrong_cache_tensors():
             native.sd_kv4_read(args[0], args[3], args[1], args[2])
     with pytest.raises(ValueError):
         native.sd_kv4_read([cache], _i32(5), [new], [new.clone()])
+    # one tensor with a leading layer dimension each
+    stack, rows = cache[None], new[None]
+    for c, k, v in [(stack, rows, rows[:, :5]), (stack, rows[..., None], rows[..., None]), (stack, rows[:, :, :3], rows[:, :, :3]),
+                    (stack[..., :-9], rows, rows), (stack, rows.float(), rows.float()), (stack.int(), rows, rows), (stack, new, new),
+                    (cache, rows, rows), (stack[:0], rows[:0], rows[:0]), (stack.transpose(1, 2), rows, rows),
+                    (stack, rows.transpose(1, 2), rows.transpose(1, 2)), (torch.cat([stack, stack]), rows, rows)]:
+        with pytest.raises(ValueError):
+            native.sd_kv4_append(c, k, v, _i32(6))
+        with pytest.raises(ValueError):
+            native.sd_kv4_read(c, _i32(6), k, v)
+    with pytest.raises(ValueError, match="CUDA"):
+        native.sd_kv4_append(stack, rows, rows, _i32(6))
     with pytest.raises(ValueError, match="CUDA"):
         native.sd_kv4_append(*ok)
     s = _shape((0, 6), pool=8, max_pages=3)
