@@ -342,3 +342,29 @@ def test_the_largest_and_smallest_vocabularies(rows, vocab, top):
             order = torch.sort(x[r].float(), descending=True, stable=True)[1][:top]
             assert torch.equal(out["top_ids"][r].long(), order)
             assert torch.all((out["top_logprobs"][r].double() - (z[order] - lse)).abs() <= tol)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("rows,vocab", [(200, 20008), (200, 20001), (6, 20008)])
+def test_one_value_that_is_none_anywhere(rows, vocab, dtype):
+    """A NaN of either sign or a +infinity at any place of a row makes that row none, and no other; values behind the last row
+    and between rows that lie apart are not looked at."""
+    gen = torch.Generator().manual_seed(rows)
+    wide = torch.full((rows, vocab + 24), math.nan)
+    wide[:, :vocab] = torch.randn(rows, vocab, generator=gen) * 4
+    wide[:, 7] = -math.inf
+    bad = {r: [math.nan, -math.nan, math.inf][r % 3] for r in range(0, rows, 2)}
+    where = {r: (r * 997 + 3) % vocab if 0 < r < rows - 2 else (0 if r == 0 else vocab - 1) for r in bad}
+    for r, v in bad.items():
+        wide[r, where[r]] = v
+    x = wide.to(dtype).cuda()[:, :vocab]
+    tokens = torch.tensor([[7, 1 + r] for r in range(rows)])
+    x, out, status = run(x, tokens, 6, dtype=dtype)
+    assert status == native.SD_DEV_NAN_LOGITS
+    for r in bad:
+        values = torch.cat([out["lse"][r:r + 1], out["entropy"][r:r + 1], out["logprobs"][r], out["top_logprobs"][r]])
+        assert torch.isnan(values).all() and torch.all(out["top_ids"][r] == -1), r
+    good = [r for r in range(rows) if r not in bad]
+    assert torch.isfinite(out["lse"][good]).all() and torch.isfinite(out["entropy"][good]).all()
+    assert torch.all(out["logprobs"][good, 0] == -math.inf)
+    check(x, out, rows=good[:2] + good[-2:])
