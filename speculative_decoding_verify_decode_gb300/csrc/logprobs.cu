@@ -19,7 +19,7 @@
 // (maximum, then the smaller index) hold all of the set: what lies in another one has `top` maxima before it.
 // They are looked through again (most of it comes from L2), for logits that reach a bar that `top` keys reach for certain:
 // the last of those maxima, or the smallest over the warps of the ceil(top / warps)-th largest of the threads' maxima,
-// whichever is more.  (With a list and a bar that followed the stream, and a barrier for each 4096 logits, 2047 rows of
+// whichever is more; of a segment `top` at most go on where more than 64 reach it.  (With a list and a bar that followed the stream, and a barrier for each 4096 logits, 2047 rows of
 // 151936 with 20 alternatives took 217 us, now 131.)
 //
 // Bound by HBM for many rows without alternatives (1824 rows of 151936 bf16 logits 88 us, 0.93 of the copy rate); with 20 of
@@ -376,6 +376,49 @@ struct Quick {
   }
 };
 
+// A warp's segment of which many logits are in question (sorted ones, or many alike): of those that `pass` marks (a bit each of a
+// lane's, value j * kVec + k at v + j * 32 * kVec + k) the `top` largest, of equal ones the first.  The largest number that as
+// many reach is found bit by bit.  (Not in line: it would cost the stream its registers.)
+template <typename T>
+__device__ __noinline__ uint32_t segment_top(const T* x, int v, uint32_t pass, int top) {
+  constexpr int kVec = Load<T>::kVec;
+  const int lane = threadIdx.x & 31;
+  uint32_t o[kPer], least = 0u;
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) o[e] = (pass >> e) & 1u ? order_of(value_of(x[v + e / kVec * (32 * kVec) + e % kVec])) : 0u;
+#pragma unroll 1
+  for (uint32_t bit = 0x80000000u; bit != 0u; bit >>= 1) {
+    const uint32_t with = least | bit;
+    int more = 0;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) more += o[e] >= with ? 1 : 0;
+    if (__reduce_add_sync(0xffffffffu, more) >= top) least = with;
+  }
+  uint32_t equal = 0u;
+  pass = 0u;
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) {
+    pass |= o[e] > least ? 1u << e : 0u;
+    equal |= o[e] == least ? 1u << e : 0u;
+  }
+  int left = top - __reduce_add_sync(0xffffffffu, __popc(pass));
+#pragma unroll 1
+  for (int j = 0; j < kPer / kVec; ++j) {
+    uint32_t here = equal >> (j * kVec) & ((1u << kVec) - 1u);
+    const int n = __popc(here);
+    int upto = n;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int up = __shfl_up_sync(0xffffffffu, upto, d);
+      if (lane >= d) upto += up;
+    }
+    int mine = left - (upto - n);      // of the equal ones, for this lane and those behind it
+    for (; here != 0u && mine > 0; here &= here - 1u, --mine) pass |= (here & (0u - here)) << (j * kVec);
+    left -= __shfl_sync(0xffffffffu, upto, 31);
+  }
+  return pass;
+}
+
 // VEC: the rows start on 16 bytes and so does every 16-byte piece of them.
 template <typename T, bool TOP, bool VEC>
 __global__ void __launch_bounds__(kLpThreads, 4) logprobs_piece_kernel(const LogprobsParams p) {
@@ -503,14 +546,18 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_piece_kernel(const Log
   quick.into(st);
   if (TOP) {
     const int segments = (end - begin + kSegment - 1) / kSegment;
-    // a bar from the threads' maxima: `top` of them at least are no smaller
-    const uint32_t jth = warp_jth(most != most ? 0u : order_of(most), (p.top + kLpWarps - 1) / kLpWarps);
-    if (lane == 0) sh.thread_bar[warp] = jth;
+    // a bar from the threads' maxima, of the warps whose threads all have logits (the first in any case): `top` of them at
+    // least are no smaller, or it is -infinity
+    const int full = max(1, min(kLpWarps, (end - begin) / kSegment));
+    if (warp < full) {
+      const uint32_t jth = warp_jth(most != most ? 0u : order_of(most), (p.top + full - 1) / full);
+      if (lane == 0) sh.thread_bar[warp] = jth;
+    }
     if (t == 0) sh.n = 0;
     __syncthreads();
     uint32_t bar = sh.thread_bar[0];
 #pragma unroll
-    for (int w = 1; w < kLpWarps; ++w) bar = min(bar, sh.thread_bar[w]);
+    for (int w = 1; w < kLpWarps; ++w) bar = w < full ? min(bar, sh.thread_bar[w]) : bar;
     // the segments that reach it: about twice `top`, if not all the same
     for (int i = t; i < segments; i += kLpThreads) {
       const uint32_t o = order_of(sh.top_of[i]);
@@ -544,43 +591,13 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_piece_kernel(const Log
         const int v = at + e / kVec * (32 * kVec) + e % kVec;
         return key_of(value_of(x[v]), v);
       };
-      int count = __reduce_add_sync(0xffffffffu, __popc(pass));
-      if (count > 64) {
-        // (sorted logits: all of a segment) a bar of its own, from the threads' maxima as above
-        float own = -INFINITY;
-#pragma unroll
-        for (int e = 0; e < kPer; ++e) own = (pass >> e) & 1u ? fmaxf(own, y[e]) : own;
-        own = order_value(warp_jth(pass != 0u ? order_of(own) : order_of(-INFINITY), p.top));
-#pragma unroll
-        for (int e = 0; e < kPer; ++e) pass &= y[e] >= own ? ~0u : ~(1u << e);
-        count = __reduce_add_sync(0xffffffffu, __popc(pass));
+      if (__reduce_add_sync(0xffffffffu, __popc(pass)) > 64) pass = segment_top<T>(x, at, pass, p.top);
+#pragma unroll 1
+      for (; pass != 0; pass &= pass - 1u) {
+        const Key k = key(__ffs(pass) - 1);
+        sh.list[atomicAdd(&sh.n, 1)] = k;
       }
-      if (count <= 64) {
-#pragma unroll 1
-        for (; pass != 0; pass &= pass - 1u) {
-          const Key k = key(__ffs(pass) - 1);
-          sh.list[atomicAdd(&sh.n, 1)] = k;
-        }
-        __syncwarp();
-      } else {
-        // many alike: the segment's best, one by one, as many as there can be in the set
-#pragma unroll 1
-        for (int k = 0; k < p.top && __any_sync(0xffffffffu, pass != 0); ++k) {
-          Key best = 0;
-#pragma unroll 1
-          for (uint32_t left = pass; left != 0; left &= left - 1u) {
-            const Key c = key(__ffs(left) - 1);
-            best = c > best ? c : best;
-          }
-          const uint32_t hi = __reduce_max_sync(0xffffffffu, (uint32_t)(best >> 32));
-          const uint32_t lo = __reduce_max_sync(0xffffffffu, (uint32_t)(best >> 32) == hi ? (uint32_t)best : 0u);
-          if (best == ((Key)hi << 32 | lo)) {
-            sh.list[atomicAdd(&sh.n, 1)] = best;
-            const int off = (int)~lo - at;        // j * 32 kVec + k
-            pass &= ~(1u << (off / (32 * kVec) * kVec + off % (32 * kVec)));
-          }
-        }
-      }
+      __syncwarp();
     }
     __syncthreads();
     const int n = sh.n;

@@ -368,3 +368,23 @@ def test_one_value_that_is_none_anywhere(rows, vocab, dtype):
     assert torch.isfinite(out["lse"][good]).all() and torch.isfinite(out["entropy"][good]).all()
     assert torch.all(out["logprobs"][good, 0] == -math.inf)
     check(x, out, rows=good[:2] + good[-2:])
+
+
+@pytest.mark.parametrize("top", [1, 7, 31, 32])
+@pytest.mark.parametrize("vocab", [512, 700, 4600, 8500, 32000])
+@pytest.mark.parametrize("kind", ["normal", "rising", "falling", "two", "steps"])
+def test_alternatives_of_pieces_that_end_inside_a_segment(kind, vocab, top):
+    """The set and its order, where the last piece of a row has a few warps' logits only, and where many logits are equal."""
+    gen = torch.Generator().manual_seed(vocab + top)
+    x = torch.randn(3, vocab, generator=gen) * 4
+    if kind in ("rising", "falling"):
+        x = torch.sort(x, 1, descending=kind == "falling")[0]
+    elif kind == "two":
+        x = (x > 3).float()
+    elif kind == "steps":
+        x = torch.floor(torch.sort(x, 1)[0] * 2)
+    for dtype in (torch.float32, torch.float16):
+        y, out, status = run(x.to(dtype), top=top, dtype=dtype)
+        assert status == 0
+        order = torch.sort(y.float(), dim=1, descending=True, stable=True)[1][:, :top]
+        assert torch.equal(out["top_ids"].long(), order)
