@@ -20,7 +20,7 @@
 // They are looked through again (most of it comes from L2), for logits that reach a bar that `top` keys reach for certain:
 // the last of those maxima, or the smallest over the warps of the ceil(top / warps)-th largest of the threads' maxima,
 // whichever is more; of a segment `top` at most go on where more than 64 reach it.  (With a list and a bar that followed the stream, and a barrier for each 4096 logits, 2047 rows of
-// 151936 with 20 alternatives took 217 us, now 131.)
+// 151936 with 20 alternatives took 217 us, now 132.)
 //
 // Bound by HBM for many rows without alternatives (1824 rows of 151936 bf16 logits 88 us, 0.93 of the copy rate); with 20 of
 // them by what follows a row's stream, which the other three rows of an SM hide in part (115 us).  A fifth row
