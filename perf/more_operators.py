@@ -451,26 +451,22 @@ def _plain_rope(s, case):
 
 
 def _plain_logprobs(s, case):
-    """Differences from each row's maximum, whose own term is exactly 1; what the others add in 64 bits, since next to 1
-    it may be far below 32 bits' steps."""
-    x = s["logits"].float()
-    m = x.amax(1, keepdim=True)
-    d = (x - m) / case["temperature"]
-    e = torch.exp(d)
-    rest = e.sum(1, keepdim=True, dtype=torch.float64) - 1
-    log_sum = torch.log1p(rest)
-    entropy = (log_sum - e.mul_(d).sum(1, keepdim=True, dtype=torch.float64) / (1 + rest)).float()[:, 0]
-    lse = (m.double() / case["temperature"] + log_sum).float()[:, 0]
-    given = None if s["given"] is None else (d.gather(1, s["given"].long()) - log_sum).float()
+    z = s["logits"].float() / case["temperature"]
+    m = z.amax(1, keepdim=True)
+    e = torch.exp(z - m)
+    total = e.sum(1, keepdim=True)
+    lse = m + torch.log(total)
+    entropy = (torch.log(total) - (e * (z - m)).sum(1, keepdim=True) / total)[:, 0]
+    given = None if s["given"] is None else z.gather(1, s["given"].long()) - lse
     if not case["top"]:
-        return given, None, None, entropy, lse
+        return given, None, None, entropy, lse[:, 0]
     del e
     # largest first, ties by the lower index: one whole number for both (the bits of a float order as it does)
-    bits = (x + 0.0).view(torch.int32).long()
+    bits = (s["logits"].float() + 0.0).view(torch.int32).long()
     key = torch.where(bits >= 0, bits, (bits & 0x7fffffff).neg()) * (1 << 20)
     key = key - torch.arange(case["vocab"], device=DEVICE)
     ids = key.topk(case["top"], 1)[1]
-    return given, ids.int(), (d.gather(1, ids) - log_sum).float(), entropy, lse
+    return given, ids.int(), z.gather(1, ids) - lse, entropy, lse[:, 0]
 
 
 # ------------------------------------------------------------------------------------------ in 64 bits
