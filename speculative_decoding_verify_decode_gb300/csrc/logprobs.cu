@@ -82,7 +82,8 @@ struct Stats {
 
 struct LpShared {
   Key list[kListMax];
-  int n;             // keys in the list
+  int n;             // keys in the list of segments, or of a join
+  int found;         // keys of the segments' logits: a word of its own, as n is read where no barrier follows before this counts
   int segment[SD_LOGPROBS_MAX_TOP];
   int count;         // of a search
   uint32_t warp_bar[kLpWarps], thread_bar[kLpWarps];
@@ -553,7 +554,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_piece_kernel(const Log
       const uint32_t jth = warp_jth(most != most ? 0u : order_of(most), (p.top + full - 1) / full);
       if (lane == 0) sh.thread_bar[warp] = jth;
     }
-    if (t == 0) sh.n = 0;
+    if (t == 0) sh.n = sh.found = 0;
     __syncthreads();
     uint32_t bar = sh.thread_bar[0];
 #pragma unroll
@@ -571,7 +572,6 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_piece_kernel(const Log
       bar = max(bar, (uint32_t)(sh.list[p.top - 1] >> 32));
     }
     if (t < taken) sh.segment[t] = (int)~(uint32_t)sh.list[t];
-    if (t == 0) sh.n = 0;
     __syncthreads();
     const float reach = order_value(bar);
 #pragma unroll 1
@@ -595,12 +595,12 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_piece_kernel(const Log
 #pragma unroll 1
       for (; pass != 0; pass &= pass - 1u) {
         const Key k = key(__ffs(pass) - 1);
-        sh.list[atomicAdd(&sh.n, 1)] = k;
+        sh.list[atomicAdd(&sh.found, 1)] = k;
       }
       __syncwarp();
     }
     __syncthreads();
-    const int n = sh.n;
+    const int n = sh.found;
     cut_list(sh, n, p.top);
     // a piece with fewer than `top` keys (the last of a row, or one with NaN): the rest sort behind everything
     for (int i = min(n, p.top) + t; i < p.top; i += kLpThreads) sh.list[i] = 0;
