@@ -134,7 +134,11 @@ size_t sd_kv4_attn_workspace_size(const sd_shape* shape);
  * Numerics: keys, values and queries enter the products as they are (bf16);
  * softmax weights are rounded to bf16 (by at most 2^-8 of themselves), their sum is not;
  * scores, statistics, sums and the partial outputs of split sequences are fp32
- * (a score beyond its range, 3.4e38, makes its row NaN).
+ * (a score beyond its range, 3.4e38, makes its row NaN).  Values are summed up before
+ * they are divided by the sum of the weights, and a weight may come to 2^16 before
+ * a row's reference moves: for a row of n keys (L_b + depth + 1) no sum passes
+ * fp32's range while n times the largest |v| is below 2^112 = 5e33; beyond that
+ * an output may be an infinity or NaN although the mean itself is not.
  * A page id out of range sets SD_DEV_BAD_PAGE and its tokens count as zeros; a
  * scale beyond SD_KV4_MAX_SCALE (infinities and NaN too) sets SD_DEV_BAD_SCALE
  * and counts as 0 (at tokens that no query sees it is not looked at).  What lies at masked
