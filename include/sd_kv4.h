@@ -70,7 +70,8 @@ extern "C" {
  * So m itself is held to half a unit of 5 bits, every other value within
  * |s| / 2, except that what is nearest to +8 s is held as 7 s (and that
  * magnitudes beyond 8 SD_KV4_MAX_SCALE = 1.12e38 saturate).  Infinities are
- * held as the end of the block's range on their side, NaN as 0; both set
+ * held as the end of the block's range on their side (as 0 where no finite value
+ * of the block reaches 2^-100, whose scale is 0), NaN as 0; both set
  * SD_DEV_NOT_FINITE.  Tokens of a page that get no row are left as they were.
  *
  *   num_layers                 1..SD_MAX_LAYERS

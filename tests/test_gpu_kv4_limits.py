@@ -1,12 +1,13 @@
-"""The ends of what include/sd_kv4.h promises: values as large as the attention's sums can hold."""
+"""The ends of what include/sd_kv4.h promises: values as large as the attention's sums can hold, infinities in an append."""
 import numpy as np
 import pytest
 import torch
 
 import oracle.kv4_oracle as kv4
+from speculative_decoding_verify_decode_gb300 import native
 
 from gpu_helpers import ensure_built
-from test_gpu_kv4 import Case, chain
+from test_gpu_kv4 import Case, chain, filled, run_append
 
 pytestmark = pytest.mark.gpu
 
@@ -45,3 +46,30 @@ def test_values_as_large_as_sums_can_hold(nodes, heads):
     assert int(c.status) == 0
     c.check(only={(0, 0), (nodes - 1, 3), (77 * nodes, 1), (batch * nodes - 1, 2)})
     assert torch.isfinite(c.out[:-1]).all() and torch.isfinite(c.lse).all()
+
+
+def test_infinities_in_blocks_without_a_range():
+    """Blocks of infinities, NaN and values below 2^-100 are held as 0; from 2^-100 on infinities are the ends of the range."""
+    inf, nan = float("inf"), float("nan")
+    x = torch.zeros(16, 2, 128)
+    b = x.unflatten(2, (-1, 32))
+    b[0, 0] = inf
+    b[1, 0] = -inf
+    b[2, 0, :, ::2], b[2, 0, :, 1::2] = inf, nan
+    b[3, 0, 0, 5], b[3, 0, 1, 31], b[3, 0, 2, 0] = inf, -inf, nan                      # others 0
+    b[4, 0] = 2.0 ** -101
+    b[4, 0, :, 7], b[4, 0, :, 8] = inf, -inf
+    b[5, 0] = -2.0 ** -101 * (2 - 2.0 ** -7)
+    b[5, 0, 1, 3] = inf
+    b[6, 0] = 2.0 ** -100
+    b[6, 0, :, 7], b[6, 0, :, 8] = inf, -inf
+    b[7, 0] = -2.0 ** -100
+    b[7, 0, 2, 7], b[7, 0, 3, 8] = inf, nan
+    x = x.bfloat16().cuda()
+    cache = filled(np.random.default_rng(3), 2, 2, 128)
+    status, got = run_append(cache, x, x.flip(0).contiguous(), list(range(16)))
+    assert status == native.SD_DEV_NOT_FINITE
+    k = kv4.values(got[0])[0][0, 0]
+    assert not k[:6].any()
+    np.testing.assert_array_equal(k[6].reshape(4, 32)[:, 6:9], np.tile([2.0 ** -100, 2.0 ** -100, -0.875 * 2.0 ** -100], (4, 1)))
+    assert k[7, 64 + 7] == 0.875 * 2.0 ** -100 and k[7, 96 + 8] == 0.0
