@@ -27,7 +27,9 @@ extern "C" {
 #define SD_LOGPROBS_MAX_GIVEN 64
 #define SD_LOGPROBS_MAX_VOCAB (1 << 24)
 
-/* Bytes of workspace sd_logprobs needs (0 on bad arguments). */
+/* Bytes of workspace sd_logprobs needs for a call of these sizes (0 on bad arguments, and where rows are not cut into pieces).
+ * Few rows are cut into more pieces than many, so fewer rows may need more: one workspace for calls of several sizes is as
+ * large as the largest need among them. */
 size_t sd_logprobs_workspace_size(int num_rows, int vocab, int top);
 
 /*

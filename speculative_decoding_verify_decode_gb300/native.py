@@ -781,6 +781,7 @@ _LOGITS = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 
 
 def sd_logprobs_workspace_size(num_rows: int, vocab: int, top: int) -> int:
+    """Bytes for a call of these sizes; fewer rows may need more (they are cut into more pieces)."""
     return int(load().sd_logprobs_workspace_size(int(num_rows), int(vocab), int(top)))
 
 
