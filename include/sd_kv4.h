@@ -135,7 +135,10 @@ size_t sd_kv4_attn_workspace_size(const sd_shape* shape);
  * Numerics: keys, values and queries enter the products as they are (bf16);
  * softmax weights are rounded to bf16 (by at most 2^-8 of themselves), their sum is not;
  * scores, statistics, sums and the partial outputs of split sequences are fp32
- * (a score beyond its range, 3.4e38, makes its row NaN).  Values are summed up before
+ * (a score beyond its range, 3.4e38, makes its row NaN).  The sum of weighted values
+ * runs in the tensor core, which cuts off towards zero: over n keys in one CTA it is
+ * off by up to n * 2^-27 of the sum of weight times |v| (values of one sign by 0.0007
+ * of themselves over 131072 keys, by 0.006 over 2^20).  Values are summed up before
  * they are divided by the sum of the weights, and a weight may come to 2^16 before
  * a row's reference moves: for a row of n keys (L_b + depth + 1) no sum passes
  * fp32's range while n times the largest |v| is below 2^112 = 5e33; beyond that

@@ -48,6 +48,42 @@ def test_values_as_large_as_sums_can_hold(nodes, heads):
     assert torch.isfinite(c.out[:-1]).all() and torch.isfinite(c.lse).all()
 
 
+@pytest.mark.parametrize("heads,nodes", [((4, 1, 256), 1), ((4, 1, 128), 1), ((6, 1, 256), 5), ((6, 1, 128), 23)])
+def test_sums_over_a_million_keys(heads, nodes):
+    """Values of one sign over 2^20 keys, in pieces of nearly as many: sums lose 16 keys' step by step at most 2^-23 of themselves.
+    The context is 64 pages again and again, so that the reference is a sum over those.  Tolerance as in test_gpu_kv4.py."""
+    batch, L, pages = 152, 1 << 20, 64
+    hq, hkv, dim = heads
+    c = Case([chain(nodes)] * batch, [pages * 16] + [0] * (batch - 1), heads, seed=23, size=0.5, spread=0.0)
+    rng = np.random.default_rng(23)
+    c.codes["v"], c.scales["v"] = rng.integers(9, 16, c.codes["v"].shape), np.abs(c.scales["v"])
+    c.vn = c.vn.abs()
+    table = torch.from_numpy(c.table[0, :pages].copy()).cuda()
+    c.ctx[:] = L
+    c.table = np.full((batch, 1), -1, np.int32)
+    c.upload()
+    c.d["page_table"] = table.repeat(L // (16 * pages))[None].repeat(batch, 1).contiguous()
+    c.shape = native.Shape(c.indptr, L // 16, len(c.codes["k"]), num_q_heads=hq, num_kv_heads=hkv, head_dim=dim)
+    c.ws = torch.empty(native.sd_kv4_attn_workspace_size(c.shape), dtype=torch.uint8, device="cuda")
+    c.call()
+    torch.cuda.synchronize()
+    assert int(c.status) == 0
+    k, v = (torch.from_numpy(x[c.d["page_table"][0, :pages].cpu().numpy(), 0].reshape(-1, dim)).cuda() for x in kv4.values(c.cache()))
+    last = torch.arange(1, batch + 1, device="cuda") * nodes - 1              # the nodes that see all of their sequence's
+    q, kn, vn = (c.d[x].double() for x in ("q", "k_new", "v_new"))
+    kn, vn = (x[:, 0].unflatten(0, (batch, nodes)) for x in (kn, vn))
+    s = torch.cat([torch.einsum("bhd,kd->bhk", q[last], k), torch.einsum("bhd,bkd->bhk", q[last], kn)], 2) * dim ** -0.5
+    s[:, :, :16 * pages] += np.log(L / (16 * pages))
+    p = torch.softmax(s, 2)
+    ref = torch.einsum("bhk,kd->bhd", p[:, :, :16 * pages], v) + torch.einsum("bhk,bkd->bhd", p[:, :, 16 * pages:], vn)
+    ds = c.score_error()
+    assert ds < 0.25
+    bound = (2.0 ** -8 + 2.0 ** -8 + 2 * np.expm1(ds) + (L + nodes) * 2.0 ** -27 + 2.0 ** -18) * ref       # ref > 0: it is the spread as well
+    assert torch.all((c.out[:-1][last].double() - ref).abs() <= bound)
+    lse = torch.logsumexp(s, 2)
+    assert torch.all((c.lse[last].double() - lse).abs() <= ds + 2.0 ** -20 * (lse.abs() + 1))
+
+
 def test_infinities_in_blocks_without_a_range():
     """Blocks of infinities, NaN and values below 2^-100 are held as 0; from 2^-100 on infinities are the ends of the range."""
     inf, nan = float("inf"), float("nan")
