@@ -8,7 +8,9 @@
 // (c - 8) s is exactly a bf16 value, so the products are those of a bf16 cache
 // that holds what the codes stand for.  m is the first tile's maximum, and moves
 // (with O and l rescaled) only when a weight passes 2^kRise: fp32 sums and bf16
-// weights are as exact at 2^16 as at 1.
+// weights are as exact at 2^16 as at 1.  Weights are bf16 because both operands of
+// a kind::f16 product have one type, and V's values need bf16's exponents: outputs
+// are off by 0.0018 to 0.0023 of their size, 0.0017 of it the output's own rounding.
 //
 // Where the widened operand goes.  A tile's 128 tokens x D dims (or D dims x 128
 // tokens of V^T) are the MMA's A operand, which may lie in tensor memory with a row
@@ -18,12 +20,12 @@
 // written and read at four times its size.  The cache's records are laid out for it: K's
 // words go along a token's dims, V's along a dim's tokens, so neither is transposed.
 //
-// What bounds it.  Bytes: 9 D / 8 a token and KV head for K and as many for V, read once per CTA column part: 1570 cycles
+// What bounds it.  Bytes: 9 D / 16 a token and KV head for K and as many for V, read once per CTA column part: 1570 cycles
 // a tile of 256 dims at an SM's share of HBM.  Single tokens (16 columns): the instructions of the widening, some 1000
 // a tile and scheduler, half of them integer ones of two cycles (64 sequences of 1 to 32768 tokens, 128 dims: 382 us where
-// the bytes take 207; of 1 to 16384, 256 dims: 190 of 104).  144 columns of 256 dims: 32 products of 81 cycles, then the chain
+// the bytes take 207; of 1 to 16384, 256 dims: 188 of 104).  144 columns of 256 dims: 32 products of 81 cycles, then the chain
 // S -> softmax -> S, as there is one S buffer and 1152 cycles of exponentials (a tile takes 4700 cycles; a tree of 23 over
-// 131072 tokens 89 us of 22).  Between them, 96 columns: 3300 cycles a tile.  A piece costs as much as three to five tiles
+// 131072 tokens 89.5 us, where its operations take 38 and its bytes 22).  Between them, 96 columns: 3300 cycles a tile.  A piece costs as much as three to five tiles
 // more: query rows and the tree are staged, the first references are taken, partial outputs are stored.
 //
 // Work split, line of units, pieces and merge: as in kv8_attn_kernel.cuh.
